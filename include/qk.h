@@ -52,7 +52,7 @@
 extern "C" {
 #endif
 
-#define QK_ABI_VERSION 7
+#define QK_ABI_VERSION 8
 
 /* element types */
 #define QK_F32 0
@@ -62,6 +62,10 @@ extern "C" {
 /* weight layouts */
 #define QK_B_KN 0 /* b is [k][n], n contiguous (the default) */
 #define QK_B_NK 1 /* b is [n][k], k contiguous */
+
+/* 8-bit code formats of the norm's output and of the cache */
+#define QK_CODE_I8 0  /* int8, symmetric [-127, 127] */
+#define QK_CODE_FP8 1 /* float8_e4m3fn */
 
 /* GEMM kernel choice for qk_gemm_i8_scaled_ex */
 #define QK_KERNEL_AUTO 0 /* by shape: decode GEMV for m <= 8, MFMA tiles otherwise */
@@ -470,6 +474,131 @@ int qk_gemm_i8_asym(int m, int n, int k, const int8_t *a, const int32_t *zero_po
                     const int8_t *b, const int32_t *wsum, int32_t *c, const float *scale_a,
                     const float *scale_b, float output_scale, void *out, int out_dtype,
                     int b_layout, hipStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Root-mean-square norm with an 8-bit output                          */
+/* ------------------------------------------------------------------ */
+/*
+ * The norm that stands before a linear layer, with the addition to the
+ * residual stream before it and the per-token quantization behind it, in one
+ * launch:
+ *   r[i][j]  = x[i][j] + residual[i][j]        (binary32; r = x without residual)
+ *   inv[i]   = 1 / sqrt(sum_j r^2 / k + eps)   (binary64, rounded to binary32)
+ *   y[i][j]  = (r[i][j] * inv[i]) * weight[j]  (binary32, two roundings)
+ *   scale[i] = max(max_j |y|, 1e-12f) / qmax   (binary32 division; qmax 127 or 448)
+ *   q[i][j]  = clamp(rint(y / scale), -127, 127), or e4m3fn(y / scale)
+ *   residual_out[i][j] = r rounded to dtype, nearest even
+ * x, residual, residual_out  [m][k] of dtype (QK_F32, QK_BF16, QK_F16), rows
+ *          ldx, ldr, ldo >= k elements apart.  residual NULL: no addition,
+ *          residual_out is ignored; otherwise residual_out is required and
+ *          may be residual or x itself (with the same row stride).
+ * weight   [k] of weight_dtype: dtype or QK_F32.
+ * code     QK_CODE_I8 or QK_CODE_FP8;  q [m][k] dense;  scale [m].
+ * A row whose max |y| is not finite (or whose sum is not) has that maximum as
+ * its scale and codes 0.  k == 0 gives scale = 1e-12f / qmax.  Any alignment
+ * of the element type, any k up to 2^30.
+ * Errors: negative size, row stride below k, unknown type, negative or NaN eps, NULL
+ * (QK_ERR_INVALID_VALUE); k above 2^30, misaligned (QK_ERR_UNSUPPORTED).
+ */
+int qk_rms_norm_quant(int m, int k, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                      const void *weight, int dtype, int weight_dtype, double eps, int code,
+                      void *residual_out, int64_t ldo, void *q, float *scale, hipStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Paged 8-bit key/value cache                                         */
+/* ------------------------------------------------------------------ */
+/*
+ * The cache is a pool of blocks of `block` positions (16, 32, 64 or 128):
+ *   k_cache  [blocks][kv_heads][block][dim] codes
+ *   v_cache  [blocks][kv_heads][dim][block] codes (positions innermost)
+ *   k_scale, v_scale  [blocks][kv_heads] float: value = code * scale
+ * code is QK_CODE_I8 or QK_CODE_FP8; dim a multiple of 16 from 16 to 256.  A
+ * sequence's position p lies in block table[s * ldt + p / block] at
+ * p % block.  The caller hands out blocks; no block may belong to two
+ * sequences of one write.
+ *
+ * Contents of device arrays (tables, lengths, row offsets) cannot be checked on the
+ * host: the kernels check every index taken from them and touch nothing
+ * outside the buffers.  A write or read drops rows whose sequence, table entry or
+ * block number is out of range; the attention gives NaN where a table entry
+ * it needs is out of range.
+ */
+
+/*
+ * Quantises a call's new tokens into the cache.  Sequence s's tokens are rows
+ * cu[s] .. cu[s + 1] - 1 of k and v (cu: seqs + 1 nondecreasing ints from 0
+ * to tokens), at positions start[s] and on.  Per block and head, K and V
+ * apart, with new tokens N in the block:
+ *   need  = max(max over N |x|, 1e-12f) / qmax           (binary32 division)
+ *   scale = need, or max(scale before, need) if start[s] lies inside the
+ *           block (earlier tokens of the sequence are in it)
+ *   new codes     Q(x / scale)
+ *   earlier codes Q((c * scale before) / scale) where the scale grew
+ * with Q as in qk_quant_per_token / qk_quant_per_token_fp8 (exact binary32
+ * quotient, nearest even).  Other positions of the block keep their bytes.
+ * A non-finite scale (infinity or NaN among the tokens) comes with codes 0:
+ * the block reads as NaN until it is begun anew.  Writing the same tokens
+ * twice changes nothing the second time.
+ *   k, v  [tokens][kv_heads][dim] of dtype, rows ldk and ldv >= kv_heads *
+ *         dim elements apart (slices of one projection's output).
+ *   table [seqs][width] int, row stride ldt;  start [seqs];  cu [seqs + 1].
+ * Errors: negative size, unknown type, code or block size, dim not a multiple
+ * of 16 or out of range, short stride, NULL (QK_ERR_INVALID_VALUE); caches
+ * not 16-byte aligned, others not aligned to their type, or more than 2^31
+ * workgroups (QK_ERR_UNSUPPORTED).
+ */
+int qk_kv_cache_write(int seqs, int tokens, int kv_heads, int dim, const void *k, int64_t ldk,
+                      const void *v, int64_t ldv, int dtype, void *k_cache, void *v_cache,
+                      float *k_scale, float *v_scale, int blocks, int block, int code,
+                      const int *table, int64_t ldt, int width, const int *start, const int *cu,
+                      hipStream_t stream);
+
+/*
+ * Reads positions back: rows cu[s] .. cu[s + 1] - 1 of k and v receive code *
+ * scale (binary32, rounded to dtype) of positions start[s] and on.  Arguments
+ * and errors as qk_kv_cache_write, with k and v written and the cache read.
+ */
+int qk_kv_cache_read(int seqs, int tokens, int kv_heads, int dim, void *k, int64_t ldk, void *v,
+                     int64_t ldv, int dtype, const void *k_cache, const void *v_cache,
+                     const float *k_scale, const float *v_scale, int blocks, int block, int code,
+                     const int *table, int64_t ldt, int width, const int *start, const int *cu,
+                     hipStream_t stream);
+
+/*
+ * Attention over the cache, causal, for any mix of single tokens, several
+ * tokens and prompts.  Sequence s holds lens[s] positions, the last of them
+ * its rows of q: row i of its n rows stands at position p = lens[s] - n + i and
+ * sees positions j <= p, and with window > 0 only p - window < j.
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,  k and v as the cache reads
+ *   lse = log sum_j exp(scale * q . k_j)
+ * A row that sees nothing (lens[s] < n) gives out = 0 and lse = -infinity.
+ * Query head h uses kv head h / (heads / kv_heads).
+ *   q    [tokens][heads][dim] of dtype (QK_BF16 or QK_F16), rows ldq >= heads *
+ *        dim elements apart.
+ *   lens [seqs] int;  cu [seqs + 1] int, or NULL when every sequence has one
+ *        row (tokens == seqs).
+ *   max_q   at least every sequence's number of rows (any such bound; a tight one
+ *           saves work).
+ *   max_kv  a bound on lens, held to width * block; a length above it counts as it.
+ *   out  [tokens][heads][dim] of dtype, dense;  lse [tokens][heads] float or
+ *        NULL.
+ *   workspace  qk_kv_attention_workspace_size(...) bytes, 256-byte aligned, any contents;
+ *        calls that can run at the same time must not share one.  NULL when
+ *        the size is 0.
+ * Scores, maxima, sums and outputs are held in binary32; codes enter the
+ * products exactly, probabilities rounded to 11 bits.
+ * Errors: as qk_kv_cache_write; heads not a multiple of kv_heads, cu NULL with tokens !=
+ * seqs, scale not finite, negative window or bound, max_q < 1 (QK_ERR_INVALID_VALUE);
+ * workspace missing, misaligned or short (QK_ERR_WORKSPACE).
+ */
+size_t qk_kv_attention_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim,
+                                      int max_kv, int window);
+int qk_kv_attention(int seqs, int tokens, int heads, int kv_heads, int dim, const void *q,
+                    int64_t ldq, int dtype, const void *k_cache, const void *v_cache,
+                    const float *k_scale, const float *v_scale, int blocks, int block, int code,
+                    const int *table, int64_t ldt, int width, const int *lens, const int *cu,
+                    int max_q, int max_kv, float scale, int window, void *out, float *lse,
+                    void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,87 @@
+"""Host-side refusals of the norm, cache and attention entry points.  None of
+these calls launches a kernel."""
+import ctypes
+
+import pytest
+
+import w8a8_int8_quantized_qk_amd as qk
+from tests.test_abi import FAKE, FAKE_ODD, NULL, _header_constants
+
+C = _header_constants()
+INVALID, UNSUP, WS = C["QK_ERR_INVALID_VALUE"], C["QK_ERR_UNSUPPORTED"], C["QK_ERR_WORKSPACE"]
+
+
+def call(fn, defaults, **kw):
+    args = dict(defaults)
+    assert set(kw) <= set(args)
+    args.update(kw)
+    return fn(*args.values())
+
+
+NORM = dict(m=4, k=64, x=FAKE, ldx=64, residual=FAKE, ldr=64, weight=FAKE, dtype=1, weight_dtype=1, eps=1e-6, code=0,
+            residual_out=FAKE, ldo=64, q=FAKE, scale=FAKE, stream=NULL)
+ROWS = dict(seqs=2, tokens=5, kv_heads=2, dim=64, k=FAKE, ldk=128, v=FAKE, ldv=128, dtype=1, k_cache=FAKE, v_cache=FAKE,
+            k_scale=FAKE, v_scale=FAKE, blocks=4, block=16, code=0, table=FAKE, ldt=3, width=3, start=FAKE, cu=FAKE,
+            stream=NULL)
+ATTEND = dict(seqs=2, tokens=5, heads=4, kv_heads=2, dim=64, q=FAKE, ldq=256, dtype=1, k_cache=FAKE, v_cache=FAKE, k_scale=FAKE,
+              v_scale=FAKE, blocks=4, block=16, code=0, table=FAKE, ldt=3, width=3, lens=FAKE, cu=FAKE, max_q=5, max_kv=48,
+              scale=0.125, window=0, out=FAKE, lse=NULL, workspace=NULL, workspace_bytes=0, stream=NULL)
+
+
+def test_constants():
+    assert (C["QK_CODE_I8"], C["QK_CODE_FP8"]) == (qk.CODE_I8, qk.CODE_FP8)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(m=-1), INVALID), (dict(k=-1), INVALID), (dict(dtype=3), INVALID), (dict(weight_dtype=2), INVALID),
+    (dict(dtype=0, weight_dtype=1), INVALID), (dict(code=2), INVALID), (dict(eps=-1e-9), INVALID),
+    (dict(eps=float("nan")), INVALID), (dict(x=NULL), INVALID), (dict(weight=NULL), INVALID), (dict(q=NULL), INVALID),
+    (dict(scale=NULL), INVALID), (dict(residual_out=NULL), INVALID), (dict(ldx=63), INVALID), (dict(ldr=63), INVALID),
+    (dict(ldo=63), INVALID), (dict(x=FAKE_ODD), UNSUP), (dict(residual=FAKE_ODD), UNSUP), (dict(weight=FAKE_ODD), UNSUP),
+    (dict(scale=FAKE_ODD), UNSUP), (dict(k=(1 << 30) + 1, ldx=1 << 31, ldr=1 << 31, ldo=1 << 31), UNSUP),
+    (dict(m=0, x=NULL, q=NULL, scale=NULL), 0),
+])
+def test_norm(kw, status):
+    assert call(qk.library().qk_rms_norm_quant, NORM, **kw) == status
+
+
+CACHE = [
+    (dict(seqs=-1), INVALID), (dict(tokens=-1), INVALID), (dict(kv_heads=0), INVALID), (dict(dim=24), INVALID),
+    (dict(dim=0), INVALID), (dict(dim=272), INVALID), (dict(block=8), INVALID), (dict(block=48), INVALID),
+    (dict(block=256), INVALID), (dict(code=7), INVALID), (dict(blocks=-1), INVALID), (dict(blocks=0), INVALID),
+    (dict(width=-1), INVALID), (dict(ldt=2), INVALID), (dict(table=NULL), INVALID), (dict(k_cache=NULL), INVALID),
+    (dict(v_cache=NULL), INVALID), (dict(k_scale=NULL), INVALID), (dict(v_scale=NULL), INVALID),
+    (dict(k_cache=ctypes.c_void_p(0x100008)), UNSUP), (dict(v_cache=FAKE_ODD), UNSUP), (dict(table=FAKE_ODD), UNSUP),
+    (dict(cu=FAKE_ODD), UNSUP), (dict(seqs=0), 0), (dict(tokens=0), 0),
+]
+
+
+@pytest.mark.parametrize("name", ["qk_kv_cache_write", "qk_kv_cache_read"])
+@pytest.mark.parametrize("kw,status", CACHE + [
+    (dict(dtype=3), INVALID), (dict(k=NULL), INVALID), (dict(v=NULL), INVALID), (dict(ldk=127), INVALID), (dict(ldv=127), INVALID),
+    (dict(start=NULL), INVALID), (dict(cu=NULL), INVALID), (dict(k=FAKE_ODD), UNSUP), (dict(start=FAKE_ODD), UNSUP),
+])
+def test_rows(name, kw, status):
+    assert call(getattr(qk.library(), name), ROWS, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", CACHE + [
+    (dict(dtype=0), INVALID), (dict(heads=3), INVALID), (dict(heads=0), INVALID), (dict(q=NULL), INVALID), (dict(out=NULL), INVALID),
+    (dict(ldq=255), INVALID), (dict(lens=NULL), INVALID), (dict(cu=NULL), INVALID), (dict(max_q=0), INVALID),
+    (dict(max_kv=-1), INVALID), (dict(window=-1), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(q=FAKE_ODD), UNSUP), (dict(out=FAKE_ODD), UNSUP), (dict(lens=FAKE_ODD), UNSUP),
+    (dict(lse=FAKE_ODD), UNSUP),
+    (dict(ldt=1000, width=1000, max_kv=16000), WS),
+    (dict(ldt=1000, width=1000, max_kv=16000, workspace=FAKE, workspace_bytes=64), WS),
+    (dict(ldt=1000, width=1000, max_kv=16000, workspace=ctypes.c_void_p(0x100010), workspace_bytes=1 << 30), WS),
+])
+def test_attention(kw, status):
+    assert call(qk.library().qk_kv_attention, ATTEND, **kw) == status
+
+
+def test_attention_workspace_size():
+    assert qk.kv_attention_workspace_size(1, 1, 4, 2, 64, 64) == 0            # one piece: nothing to join
+    assert qk.kv_attention_workspace_size(1, 1, 4, 2, 64, 100000) > 0
+    assert qk.kv_attention_workspace_size(0, 1, 4, 2, 64, 100000) == 0
+    assert qk.kv_attention_workspace_size(1, 1, 4, 3, 64, 100000) == 0        # refused shapes need none
+    assert qk.kv_attention_workspace_size(1, 1, 4, 2, 64, 100000, 100) == 0   # a window bounds the range

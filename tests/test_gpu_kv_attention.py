@@ -1,0 +1,274 @@
+"""GPU parity of the attention over the paged 8-bit cache against the plain
+implementation in binary64, within the bounds it derives (output rounding,
+probabilities in 11 bits, binary32 sums)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import w8a8_int8_quantized_qk_amd as qk
+from tests import plain_decoder as plain
+from tests.test_gpu_kv_cache import dev, random_cache
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    qk.library()
+
+
+class Setup:
+    """A cache of arbitrary bytes in which only the sequences' own positions
+    hold ordinary codes; unused table entries are -1."""
+
+    def __init__(self, seed, lens, counts, heads, kv_heads, dim, block, fp8, dtype, spread=1.0):
+        rng = self.rng = np.random.default_rng(seed)
+        self.lens, self.counts, self.fp8, self.dtype = lens, counts, fp8, dtype
+        self.table, blocks = plain.tables(rng, lens, block)
+        self.cache = random_cache(rng, blocks, kv_heads, dim, block, fp8)
+        top = 110.0 if fp8 else 36.0
+        for t in (self.cache.k, self.cache.v):
+            flat = t.view(torch.uint8).cpu().numpy()
+            for s, n in enumerate(lens):
+                for p in range(n):
+                    x = np.clip(rng.standard_normal((kv_heads, dim)).astype(np.float32) * top, -448 if fp8 else -127,
+                                448 if fp8 else 127)
+                    codes = plain.to_codes(x, fp8)
+                    if t is self.cache.k:
+                        flat[self.table[s][p // block], :, p % block] = codes
+                    else:
+                        flat[self.table[s][p // block], :, :, p % block] = codes
+            t.view(torch.uint8).copy_(dev(flat))
+        for t in (self.cache.k_scale, self.cache.v_scale):
+            t.copy_(dev((rng.uniform(0.3, 3.0, t.shape) / top).astype(np.float32)))
+        q = rng.standard_normal((sum(counts), heads, dim)).astype(np.float32) * spread
+        self.q = dev(q).to(plain.TORCH[dtype])
+
+    def run(self, **kw):
+        cu = None if all(c == 1 for c in self.counts) and not kw.pop("ragged", False) else dev(plain.offsets(self.counts))
+        kw.pop("ragged", None)
+        q = kw.pop("q", self.q)
+        return qk.kv_attention(q, self.cache, dev(self.table), dev(np.asarray(self.lens, np.int32)), cu, **kw)
+
+    def check(self, out, lse=None, window=0, scale=None):
+        host = plain.Cache(self.cache, self.fp8)
+        cu = plain.offsets(self.counts)
+        scale = self.q.shape[2] ** -0.5 if scale is None else scale
+        qf = plain.f32(self.q)
+        for s, n in enumerate(self.lens):
+            k, v = host.values(self.table[s], n)
+            r = slice(cu[s], cu[s + 1])
+            want, wl, bo, bl = plain.attention(qf[r], k, v, n, np.float64(np.float32(scale)), window)
+            ok = plain.within(out[r], want, bo)
+            assert ok.all(), f"sequence {s}: {(~ok).sum()} of {ok.size} outputs beyond the bound"
+            if lse is not None:
+                g = lse[r].cpu().numpy().astype(np.float64)
+                empty = np.isinf(wl)
+                assert np.array_equal(g[empty], wl[empty])
+                assert (np.abs(g[~empty] - wl[~empty]) <= bl[~empty]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("heads,kv_heads,dim,block", [(1, 1, 16, 16), (4, 2, 64, 32), (8, 1, 80, 64), (6, 2, 128, 16), (7, 1, 112, 128),
+                                                      (2, 2, 256, 64), (20, 1, 128, 64), (48, 3, 64, 16)])
+def test_single_tokens(heads, kv_heads, dim, block, dtype, fp8):
+    lens = [1, 2, 15, 16, 17, 63, 64, 65, 200, 0, 301]
+    t = Setup(heads * 7 + dim, lens, [1] * len(lens), heads, kv_heads, dim, block, fp8, dtype)
+    out, lse = t.run(return_lse=True)
+    t.check(out, lse)
+    again, lse2 = t.run(return_lse=True, ragged=True)
+    t.check(again, lse2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,dim,block,dtype", [(4, 2, 64, 16, "bf16"), (6, 2, 128, 64, "f16"), (3, 1, 256, 32, "bf16"),
+                                                            (5, 5, 48, 128, "bf16"), (17, 1, 96, 16, "f16")])
+def test_several_tokens_and_prompts(heads, kv_heads, dim, block, dtype, fp8):
+    # rows of a whole prompt, of its later part, single rows, none, and more rows than positions
+    lens = [40, 133, 1, 77, 90, 3, 0, 257]
+    counts = [40, 20, 1, 0, 5, 9, 2, 70]
+    t = Setup(dim + heads, lens, counts, heads, kv_heads, dim, block, fp8, dtype)
+    out, lse = t.run(return_lse=True)
+    t.check(out, lse)
+    assert not out[int(np.sum(counts[:5])):][:6].any()      # 9 rows over 3 positions: 6 see nothing
+    tight = t.run(max_q=max(counts), max_kv=max(lens))
+    assert torch.equal(tight, out)
+
+
+@pytest.mark.parametrize("window", [1, 5, 64, 100, 1000])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_window(window, fp8):
+    lens, counts = [300, 90, 64, 500], [1, 33, 64, 140]
+    t = Setup(window, lens, counts, 4, 2, 64, 16, fp8, "bf16")
+    # blocks before every window may have been given back: their entries are not read
+    for s, (n, c) in enumerate(zip(lens, counts)):
+        first = max(0, n - c - window + 1) // 16
+        t.table[s, :first] = -1
+    out, lse = t.run(window=window, return_lse=True)
+    ok = Setup(window, lens, counts, 4, 2, 64, 16, fp8, "bf16")
+    t.table = ok.table
+    t.check(out, lse, window=window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_cache_is_split(fp8, dtype):
+    t = Setup(11, [5000, 1, 2600, 700], [1, 1, 1, 1], 4, 2, 64, 64, fp8, dtype)
+    assert qk.kv_attention_workspace_size(4, 4, 4, 2, 64, 5056) > 0
+    out, lse = t.run(return_lse=True)
+    t.check(out, lse)
+    ws = torch.full((qk.kv_attention_workspace_size(4, 4, 4, 2, 64, 5056),), 255, dtype=torch.uint8, device=DEV)
+    own = t.run(workspace=ws)
+    assert torch.equal(own, out)
+    for _ in range(3):
+        assert torch.equal(t.run(), out)          # the same bits on every run
+
+
+def test_sharp_and_flat_rows():
+    # scores of several hundred, equal scores, a scale of zero, large and tiny queries
+    for spread, scale in ((300.0, None), (0.0, None), (1.0, 0.0), (1e30, 1e-30), (1e-30, 1e30), (1.0, -1.0)):
+        t = Setup(21, [700, 64, 33], [1, 3, 33], 4, 2, 128, 16, False, "bf16", spread)
+        out, lse = t.run(scale=scale, return_lse=True)
+        t.check(out, lse, scale=scale)
+
+
+def test_one_large_query_element():
+    # elements 2^20 and more below the row's largest still count
+    t = Setup(22, [100, 40], [1, 40], 4, 2, 64, 16, False, "bf16")
+    t.q[:, :, 0] = 4096.0
+    t.q[:, :, 1:] *= 2.0 ** -8
+    t.cache.k.view(torch.uint8)[:, :, :, 0] = 0
+    out, lse = t.run(return_lse=True)
+    t.check(out, lse)
+
+
+def test_scales_of_very_different_size():
+    t = Setup(23, [500, 130], [1, 70], 4, 2, 64, 16, False, "bf16")
+    s = np.clip(np.exp(t.rng.standard_normal(t.cache.v_scale.shape) * 8), 1e-13, 1e13)
+    t.cache.v_scale.copy_(dev(s.astype(np.float32)))
+    t.check(*t.run(return_lse=True))
+    # blocks of zeros with the guard's scale among ordinary ones
+    t = Setup(24, [500, 130], [1, 70], 4, 2, 64, 16, True, "bf16")
+    zero = t.table[0, 3]
+    t.cache.v.view(torch.uint8)[zero] = 0
+    t.cache.v_scale[zero] = float(np.float32(1e-12) / np.float32(448))
+    t.check(*t.run(return_lse=True))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_non_finite_values_reach_only_rows_that_see_them(fp8):
+    lens, counts = [80, 64], [40, 1]
+    t = Setup(31, lens, counts, 2, 1, 64, 16, fp8, "bf16")
+    clean, lse = t.run(return_lse=True)
+    t.check(clean, lse)
+    last = t.table[0, 4]                      # positions 64 to 79
+    t.cache.k_scale[last] = float("nan")
+    t.cache.v_scale[last] = float("nan")
+    for c in (t.cache.k, t.cache.v):
+        c.view(torch.uint8)[last] = 0
+    out = t.run()
+    blind = 64 - (80 - 40)                    # rows at positions below 64
+    assert torch.equal(out[:blind], clean[:blind]) and torch.equal(out[40:], clean[40:])
+    assert torch.isnan(out[blind:40]).all()
+    t.cache.v_scale[last] = float("inf")
+    t.cache.k_scale[last] = 1.0
+    out = t.run()
+    assert torch.equal(out[:blind], clean[:blind]) and torch.isnan(out[blind:40]).all()
+    # a query that is not finite spoils its own row and head alone
+    t = Setup(31, lens, counts, 2, 1, 64, 16, fp8, "bf16")
+    t.q[3, 1, 7] = float("nan")
+    t.q[9, 0, 0] = float("inf")
+    out = t.run()
+    assert torch.isnan(out[3, 1]).all() and torch.isnan(out[9, 0]).all()
+    out[3, 1] = clean[3, 1]
+    out[9, 0] = clean[9, 0]
+    assert torch.equal(out, clean)
+
+
+def test_table_entries_out_of_range_give_nan():
+    t = Setup(32, [80, 200], [1, 1], 2, 1, 64, 16, False, "bf16")
+    clean = t.run()
+    t.table[0, 2] = t.cache.k.shape[0]
+    out = t.run()
+    assert torch.isnan(out[0]).all() and torch.equal(out[1], clean[1])
+    t.table[0, 2] = -5
+    out = t.run()
+    assert torch.isnan(out[0]).all() and torch.equal(out[1], clean[1])
+
+
+def test_strided_queries_output_buffer_and_stream():
+    t = Setup(41, [150, 77, 9], [30, 1, 9], 6, 2, 64, 32, False, "bf16")
+    want = t.run()
+    wide = torch.zeros((t.q.shape[0], 6 * 64 + 129), dtype=t.q.dtype, device=DEV)
+    wide[:, 1:1 + 6 * 64] = t.q.flatten(1)
+    out = torch.empty_like(t.q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = t.run(q=wide[:, 1:1 + 6 * 64].unflatten(1, (6, 64)), out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    assert got is out and torch.equal(out, want)
+
+
+def test_many_sequences():
+    rng = np.random.default_rng(51)
+    counts = rng.integers(0, 4, 140).tolist()
+    lens = [int(c + rng.integers(0, 40)) for c in counts]
+    t = Setup(52, lens, counts, 4, 1, 32, 16, True, "f16")
+    t.check(*t.run(return_lse=True))
+
+
+def test_graph_replay():
+    t = Setup(61, [1300, 64, 700], [1, 1, 1], 4, 2, 64, 64, False, "bf16")
+    want = t.run().clone()
+    table, lens = dev(t.table), dev(np.asarray(t.lens, np.int32))
+    out = torch.empty_like(t.q)
+    ws = torch.empty(max(256, qk.kv_attention_workspace_size(3, 3, 4, 2, 64, table.shape[1] * 64)), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qk.kv_attention(t.q, t.cache, table, lens, out=out, workspace=ws)
+    for _ in range(4):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert torch.equal(t.run(), want)
+
+
+def test_refusals():
+    t = Setup(71, [20, 20], [1, 1], 4, 2, 64, 16, False, "bf16")
+    table, lens, cu = dev(t.table), dev(np.array([20, 20], np.int32)), dev(np.array([0, 1, 2], np.int32))
+    with pytest.raises(TypeError):
+        qk.kv_attention(t.q.float(), t.cache, table, lens)
+    with pytest.raises(ValueError):
+        qk.kv_attention(t.q[:, :3], t.cache, table, lens)
+    with pytest.raises(ValueError):
+        qk.kv_attention(t.q[:, :, :48], t.cache, table, lens)
+    with pytest.raises(ValueError):
+        qk.kv_attention(t.q[:1], t.cache, table, lens)
+    with pytest.raises(ValueError):
+        qk.kv_attention(t.q, t.cache, table[:1], lens)
+    with pytest.raises(TypeError):
+        qk.kv_attention(t.q, t.cache, table, lens.long())
+    with pytest.raises(ValueError):
+        qk.kv_attention(t.q, t.cache, table, lens, cu[:2])
+    with pytest.raises(qk.QKError):
+        qk.kv_attention(t.q, t.cache, table, lens, scale=float("inf"))
+    with pytest.raises(qk.QKError):
+        qk.kv_attention(t.q, t.cache, table, lens, window=-1)
+    with pytest.raises(qk.QKError):
+        qk.kv_attention(t.q, t.cache, table, lens, max_q=0)
+    big = dev(np.zeros((2, 4000), np.int32))
+    with pytest.raises(qk.QKError, match="WORKSPACE"):
+        qk.kv_attention(t.q, t.cache, big, lens, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        qk.new_kv_cache(4, 2, 64, block=48, device=DEV)
+    with pytest.raises(ValueError):
+        qk.new_kv_cache(4, 2, 72, device=DEV)

@@ -15,19 +15,28 @@ and its FP8 (float8_e4m3fn) counterpart:
   q, s     = quant_per_token_fp8(x, scale_ub)   # or silu_mul_quant_per_token_fp8(h)
   out      = gemm_fp8_scaled(q, w8, s, s_ch)     # binary32 accumulate + dequant
   out      = linear_fp8(x, w8, s_ch)
+and what a decoder layer has between its linears, 8 bit as well:
+  q, s, r  = rms_norm_quant(x, g, residual=r)    # r + x, norm, codes and scales
+  cache    = new_kv_cache(blocks, kv_heads, dim) # a paged INT8 or FP8 cache
+  kv_cache_write(cache, k, v, table, start, cu)  # quantised as it is written
+  out      = kv_attention(q, cache, table, lens) # attention over it
+  k, v     = kv_cache_read(cache, table, start, cu, tokens)
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
-ABI_VERSION = 7
+ABI_VERSION = 8
 F32, BF16, F16 = 0, 1, 2
 B_KN, B_NK = 0, 1
 KERNEL_AUTO, KERNEL_MFMA, KERNEL_GEMV = 0, 1, 2
+CODE_I8, CODE_FP8 = 0, 1
 QK_OK = 0
 SCRATCH_BYTES = 16777216  # static scratch of qk_linear_w8a8_noalloc, per GPU
 
@@ -47,7 +56,8 @@ EXPORTED = (
     "qk_silu_mul_quant_per_token_fp8", "qk_gemm_fp8_scaled", "qk_linear_fp8",
     "qk_gemm_i8_grouped", "qk_moe_gemm_i8_scaled", "qk_quant_static", "qk_silu_mul_quant_static",
     "qk_quant_static_fp8", "qk_silu_mul_quant_static_fp8", "qk_quant_per_token_asym",
-    "qk_weight_colsum", "qk_gemm_i8_asym",
+    "qk_weight_colsum", "qk_gemm_i8_asym", "qk_rms_norm_quant", "qk_kv_cache_write",
+    "qk_kv_cache_read", "qk_kv_attention_workspace_size", "qk_kv_attention",
 )
 
 
@@ -113,6 +123,17 @@ def _declare(lib):
     lib.qk_weight_colsum.restype = I
     lib.qk_gemm_i8_asym.argtypes = [I, I, I, P, P, P, P, P, P, P, F, P, I, I, P]
     lib.qk_gemm_i8_asym.restype = I
+    L, D = ctypes.c_int64, ctypes.c_double
+    lib.qk_rms_norm_quant.argtypes = [I, I, P, L, P, L, P, I, I, D, I, P, L, P, P, P]
+    lib.qk_rms_norm_quant.restype = I
+    for name in ("qk_kv_cache_write", "qk_kv_cache_read"):
+        getattr(lib, name).argtypes = [I, I, I, I, P, L, P, L, I, P, P, P, P, I, I, I, P, L, I, P, P, P]
+        getattr(lib, name).restype = I
+    lib.qk_kv_attention_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    lib.qk_kv_attention_workspace_size.restype = ctypes.c_size_t
+    lib.qk_kv_attention.argtypes = [I, I, I, I, I, P, L, I, P, P, P, P, I, I, I, P, L, I, P, P, I, I, F, I, P,
+                                    P, P, ctypes.c_size_t, P]
+    lib.qk_kv_attention.restype = I
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -751,3 +772,278 @@ def gemm_i8_asym(a: torch.Tensor, zero_point: torch.Tensor, b: torch.Tensor, wsu
     if not want_out:
         return c
     return (out, c) if return_acc else out
+
+
+# ---- the operators between a decoder layer's linears ----
+# These calls are short on the GPU, so their checks read each tensor attribute
+# once and pointers go to libqk as plain integers.
+
+def _raw_stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _rows(t: torch.Tensor, name: str, dtype, device, ndim: int) -> int:
+    """Check of a tensor of rows that may lie apart: returns the row stride.  The
+    dimensions after the first are dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+    inner = 1
+    for i in range(ndim - 1, 0, -1):
+        if stride[i] != inner and shape[i] != 1 and shape[0]:
+            raise ValueError(f"the rows of {name} must be dense")
+        inner *= shape[i]
+    if shape[0] <= 1:
+        return inner
+    if stride[0] < inner:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return stride[0]
+
+
+def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                   residual: torch.Tensor | None = None, fp8: bool = False,
+                   residual_out: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                   scale: torch.Tensor | None = None):
+    """Root-mean-square norm with 8-bit codes and per-token scales, one launch.
+
+    x [m, k] (fp32, bf16 or fp16), weight [k] of the same type or fp32.  With
+    residual [m, k] the norm is taken of r = x + residual, and r, rounded to
+    x's type, goes to residual_out (allocated when not given; may be residual
+    itself).  Rows of x, residual and residual_out may lie apart (slices).
+    Returns (q, scale), or (q, scale, residual_out) with a residual: q int8
+    (float8_e4m3fn when fp8) [m, k], scale fp32 [m], ready for gemm_i8_scaled
+    or gemm_fp8_scaled.
+    """
+    dt = x.dtype if isinstance(x, torch.Tensor) else None
+    if dt is not None and dt not in _IN_DTYPES:
+        raise TypeError(f"x dtype {dt} not supported")
+    dev = x.device if dt is not None else None
+    ldx = _rows(x, "x", dt, dev, 2)
+    m, k = x.shape
+    _need(weight, "weight", None, 1, dev)
+    if weight.dtype not in (dt, torch.float32):
+        raise TypeError(f"weight must be {dt} or fp32, got {weight.dtype}")
+    if weight.shape[0] != k:
+        raise ValueError("weight must be [k]")
+    ldr = ldo = 0
+    if residual is not None:
+        ldr = _rows(residual, "residual", dt, dev, 2)
+        residual_out = torch.empty((m, k), dtype=dt, device=dev) if residual_out is None else residual_out
+        ldo = _rows(residual_out, "residual_out", dt, dev, 2)
+        if residual.shape != x.shape or residual_out.shape != x.shape:
+            raise ValueError("residual and residual_out must be [m, k]")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    qdt = torch.float8_e4m3fn if fp8 else torch.int8
+    if q is None:
+        q = torch.empty((m, k), dtype=qdt, device=dev)
+    elif fp8:
+        _need_codes(q, "q", 2, dev)
+    else:
+        _need(q, "q", torch.int8, 2, dev)
+    if scale is None:
+        scale = torch.empty((m,), dtype=torch.float32, device=dev)
+    else:
+        _need(scale, "scale", torch.float32, 1, dev)
+    if q.shape != x.shape or scale.shape[0] != m:
+        raise ValueError("q must be [m, k] and scale [m]")
+    _check(library().qk_rms_norm_quant(
+        m, k, x.data_ptr(), ldx, 0 if residual is None else residual.data_ptr(), ldr, weight.data_ptr(),
+        _IN_DTYPES[dt], _IN_DTYPES[weight.dtype], eps, CODE_FP8 if fp8 else CODE_I8,
+        0 if residual is None else residual_out.data_ptr(), ldo, q.data_ptr(), scale.data_ptr(),
+        _raw_stream(dev)))
+    return (q, scale) if residual is None else (q, scale, residual_out)
+
+
+KV_BLOCKS = (16, 32, 64, 128)
+
+
+class KVCache(NamedTuple):
+    """A paged 8-bit key/value cache: k [blocks, kv_heads, block, dim] and v
+    [blocks, kv_heads, dim, block] codes (int8 or float8_e4m3fn), and one fp32
+    scale per block and head for either, [blocks, kv_heads]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def new_kv_cache(blocks: int, kv_heads: int, dim: int, block: int = 64, fp8: bool = False,
+                 device="cuda") -> KVCache:
+    """An empty cache (all codes and scales 0) of `blocks` blocks of `block`
+    positions (16, 32, 64 or 128); dim a multiple of 16 up to 256."""
+    if block not in KV_BLOCKS:
+        raise ValueError(f"block must be one of {KV_BLOCKS}")
+    if dim % 16 or not 16 <= dim <= 256:
+        raise ValueError("dim must be a multiple of 16 from 16 to 256")
+    if blocks < 0 or kv_heads < 1:
+        raise ValueError("blocks must not be negative, kv_heads at least 1")
+    dt = torch.float8_e4m3fn if fp8 else torch.int8
+    k = torch.zeros((blocks, kv_heads, block, dim), dtype=torch.int8, device=device).view(dt)
+    v = torch.zeros((blocks, kv_heads, dim, block), dtype=torch.int8, device=device).view(dt)
+    scales = [torch.zeros((blocks, kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(k, v, *scales)
+
+
+def _kv_args(cache: KVCache, table: torch.Tensor, seqs: int, device):
+    """Checks a cache and its block table; the arguments libqk takes for them."""
+    k, v, ks, vs = cache
+    if k.dim() != 4:
+        raise ValueError("cache.k must be [blocks, kv_heads, block, dim]")
+    blocks, heads, block, dim = k.shape
+    if v.shape != (blocks, heads, dim, block) or ks.shape != (blocks, heads) or vs.shape != (blocks, heads):
+        raise ValueError("cache.v must be [blocks, kv_heads, dim, block], the scales [blocks, kv_heads]")
+    if block not in KV_BLOCKS:
+        raise ValueError(f"block must be one of {KV_BLOCKS}")
+    if dim % 16 or not 16 <= dim <= 256:
+        raise ValueError("dim must be a multiple of 16 from 16 to 256")
+    dt = k.dtype
+    if dt not in (torch.int8, torch.float8_e4m3fn) or v.dtype != dt:
+        raise TypeError("cache codes must be int8 or float8_e4m3fn")
+    if ks.dtype != torch.float32 or vs.dtype != torch.float32:
+        raise TypeError("cache scales must be fp32")
+    for t, name in ((k, "cache.k"), (v, "cache.v"), (ks, "cache.k_scale"), (vs, "cache.v_scale")):
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    ldt = _rows(table, "table", torch.int32, device, 2)
+    if table.shape[0] != seqs:
+        raise ValueError(f"table must have one row for each of the {seqs} sequences")
+    return (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), blocks, block,
+            CODE_I8 if dt == torch.int8 else CODE_FP8, table.data_ptr(), ldt, table.shape[1])
+
+
+def _kv_rows(fn, cache: KVCache, k: torch.Tensor, v: torch.Tensor, table, start, cu):
+    dt = k.dtype if isinstance(k, torch.Tensor) else None
+    if dt is not None and dt not in _IN_DTYPES:
+        raise TypeError(f"k dtype {dt} not supported")
+    dev = k.device if dt is not None else None
+    ldk, ldv = _rows(k, "k", dt, dev, 3), _rows(v, "v", dt, dev, 3)
+    _need(start, "start", torch.int32, 1, dev)
+    _need(cu, "cu", torch.int32, 1, dev)
+    seqs = start.shape[0]
+    args = _kv_args(cache, table, seqs, dev)
+    if cu.shape[0] != seqs + 1:
+        raise ValueError("cu must have one entry more than start")
+    tokens, heads, dim = k.shape
+    if v.shape != k.shape or heads != cache[0].shape[1] or dim != cache[0].shape[3]:
+        raise ValueError("k and v must be [tokens, kv_heads, dim] of the cache's heads and dim")
+    _check(fn(seqs, tokens, heads, dim, k.data_ptr(), ldk, v.data_ptr(), ldv, _IN_DTYPES[dt], *args,
+              start.data_ptr(), cu.data_ptr(), _raw_stream(dev)))
+
+
+def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
+                   start: torch.Tensor, cu: torch.Tensor) -> KVCache:
+    """Quantise new tokens into the cache, one launch.
+
+    k, v [tokens, kv_heads, dim] (fp32, bf16 or fp16; rows may lie apart, as
+    slices of one projection); table int32 [seqs, width]: the blocks of each
+    sequence; start int32 [seqs]: its positions already in the cache; cu int32
+    [seqs + 1]: its rows of k and v.  A block's scale is set by the first write
+    into it and grows with later ones, which moves the earlier codes.  Returns
+    the cache, which is written in place.
+    """
+    _kv_rows(library().qk_kv_cache_write, cache, k, v, table, start, cu)
+    return cache
+
+
+def kv_cache_read(cache: KVCache, table: torch.Tensor, start: torch.Tensor, cu: torch.Tensor,
+                  tokens: int, dtype: torch.dtype = torch.bfloat16, k: torch.Tensor | None = None,
+                  v: torch.Tensor | None = None):
+    """Cached positions as (k, v), each [tokens, kv_heads, dim] of dtype.
+
+    Sequence s's positions start[s], start[s] + 1, ... go to rows cu[s] ..
+    cu[s + 1] - 1 of the outputs (allocated when not given); tokens is cu's
+    last entry, which the host knows.
+    """
+    heads, dim = cache[0].shape[1], cache[0].shape[3]
+    dev = cache[0].device
+    if k is None:
+        k = torch.empty((tokens, heads, dim), dtype=dtype, device=dev)
+    if v is None:
+        v = torch.empty((tokens, heads, dim), dtype=k.dtype, device=dev)
+    if k.shape[0] != tokens:
+        raise ValueError("k must have `tokens` rows")
+    _kv_rows(library().qk_kv_cache_read, cache, k, v, table, start, cu)
+    return k, v
+
+
+@functools.lru_cache(maxsize=4096)
+def kv_attention_workspace_size(seqs: int, tokens: int, heads: int, kv_heads: int, dim: int, max_kv: int,
+                                window: int = 0) -> int:
+    return int(library().qk_kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, max_kv, window))
+
+
+_attention_workspaces: dict = {}
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
+                 cu: torch.Tensor | None = None, scale: float | None = None, window: int = 0,
+                 max_q: int | None = None, max_kv: int | None = None, out: torch.Tensor | None = None,
+                 return_lse: bool = False, workspace: torch.Tensor | None = None):
+    """Causal attention of q [tokens, heads, dim] (bf16 or fp16; rows may lie
+    apart) over the cache.
+
+    lens int32 [seqs]: positions of each sequence in the cache, its rows of q
+    being the last of them; cu int32 [seqs + 1]: those rows, or None when every
+    sequence has one.  window > 0 limits a row to its last `window` positions.
+    scale defaults to dim ** -0.5.  max_q and max_kv are bounds that the host
+    knows on a sequence's rows and positions (by default all rows, and what the
+    table covers); tight ones save work.  Returns out [tokens, heads, dim], and
+    with return_lse the fp32 log-sum-exp [tokens, heads]; a row that sees no
+    position gives 0 and -inf.
+    """
+    dt = q.dtype if isinstance(q, torch.Tensor) else None
+    if dt is not None and dt not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"q dtype {dt} not supported")
+    dev = q.device if dt is not None else None
+    ldq = _rows(q, "q", dt, dev, 3)
+    tokens, heads, dim = q.shape
+    _need(lens, "lens", torch.int32, 1, dev)
+    seqs = lens.shape[0]
+    args = _kv_args(cache, table, seqs, dev)
+    kv_heads = cache[0].shape[1]
+    if dim != cache[0].shape[3] or heads % kv_heads:
+        raise ValueError("q must be [tokens, heads, dim] with heads a multiple of the cache's and its dim")
+    if cu is not None:
+        _need(cu, "cu", torch.int32, 1, dev)
+        if cu.shape[0] != seqs + 1:
+            raise ValueError("cu must have one entry more than lens")
+    elif tokens != seqs:
+        raise ValueError("without cu every sequence has one row")
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=dt, device=dev)
+    else:
+        _need(out, "out", dt, 3, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must be [tokens, heads, dim]")
+    lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
+    reach = args[9] * args[5]
+    max_kv = reach if max_kv is None else min(max_kv, reach)
+    max_q = (1 if cu is None else max(tokens, 1)) if max_q is None else max_q
+    stream = _raw_stream(dev)
+    if workspace is None:
+        need = kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, max_kv, window)
+        if need:
+            key = (dev, stream)
+            workspace = _attention_workspaces.get(key)
+            if workspace is None or workspace.numel() < need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                _attention_workspaces[key] = workspace
+    else:
+        _need(workspace, "workspace", None, None, dev)
+    _check(library().qk_kv_attention(
+        seqs, tokens, heads, kv_heads, dim, q.data_ptr(), ldq, _IN_DTYPES[dt], *args, lens.data_ptr(),
+        0 if cu is None else cu.data_ptr(), max_q, max_kv, dim ** -0.5 if scale is None else scale, window,
+        out.data_ptr(), lse.data_ptr() if return_lse else 0, 0 if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), stream))
+    return (out, lse) if return_lse else out

@@ -22,7 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqk.so")
 SOURCES = ["qk_api.hip", "quant.hip", "quant_static.hip", "gemm_mfma.hip", "gemm_wide.hip",
-           "gemm_spec.hip", "gemm_slice.hip", "gemv.hip"]
+           "gemm_spec.hip", "gemm_slice.hip", "gemv.hip", "norm_quant.hip", "kv_cache.hip",
+           "kv_attention.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -1,0 +1,359 @@
+// Root-mean-square norm with the residual's addition and an 8-bit output with
+// per-token scales, one launch, for gfx950.
+//
+// Per row of k elements (all binary32 unless stated):
+//   r      = x + residual                  (or x when there is no residual)
+//   inv    = RN32(1 / sqrt(sum r^2 / k + eps))   (the sum, the mean, the root
+//            and the division in binary64, rounded once)
+//   y      = (r * inv) * w
+//   scale  = max(max |y|, 1e-12) / qmax    qmax 127 (INT8) or 448 (FP8 e4m3fn)
+//   code   = rint(y / scale)  or  e4m3fn(y / scale)   (exact quotient)
+//   residual_out = r rounded to the type of x.
+// The norm works on the unrounded r; only what is stored is rounded.
+//
+// Why binary64 for one sum: every other step is one IEEE operation, so codes
+// and scales are reproducible bit for bit as long as inv is; a binary32 sum of
+// squares would change its last bits with the order of addition.  It costs a
+// conversion and a fused multiply-add per element, below the memory time.
+//
+// A row whose sum of squares or whose max |y| is not finite (an infinity or a
+// NaN among x, residual or w) gets that maximum's non-finite scale and codes
+// 0, so whatever the codes are multiplied into is NaN and not silently wrong.
+//
+// What bounds it: HBM, 2 reads and 1 write of the row's type plus the codes
+// (7 bytes per bf16 element).  A row's values stay in registers between the
+// two reductions, so x and the residual are read once.
+#include "quant_math.h"
+
+namespace qk {
+namespace {
+
+using qm::Elem;
+
+constexpr int kBlock = 256;
+constexpr int kMaxUnits = 8;  // units of P elements held per thread
+
+// 16 bytes at any alignment the element type allows (rows of odd widths)
+template <int ALIGN>
+struct __attribute__((packed, aligned(ALIGN))) Raw16 {
+  uint32_t w[4];
+};
+template <int ALIGN>
+struct __attribute__((packed, aligned(ALIGN))) Raw8 {
+  uint32_t w[2];
+};
+struct __attribute__((packed, aligned(1))) Raw4 {
+  uint32_t w;
+};
+
+template <int DT>
+__device__ __forceinline__ void load_full(const void* row, int u, float (&v)[Elem<DT>::kPerUnit]) {
+  using E = Elem<DT>;
+  const auto raw = *reinterpret_cast<const Raw16<E::kBytes>*>(static_cast<const char*>(row) +
+                                                              static_cast<size_t>(u) * 16);
+  E::unpack(make_uint4(raw.w[0], raw.w[1], raw.w[2], raw.w[3]), v);
+}
+
+// The P values of unit u of a row of k elements; those past the row's end are 0.
+template <int DT>
+__device__ __forceinline__ void load_values(const void* row, int k, int u,
+                                            float (&v)[Elem<DT>::kPerUnit]) {
+  constexpr int P = Elem<DT>::kPerUnit;
+  if ((u + 1) * P <= k) {
+    load_full<DT>(row, u, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < P; ++e) v[e] = u * P + e < k ? Elem<DT>::load(row, u * P + e) : 0.0f;
+  }
+}
+
+// The same for the weight, which is of the row's type or binary32.
+template <int DT>
+__device__ __forceinline__ void load_weight(const void* w, bool w_f32, int k, int u,
+                                            float (&v)[Elem<DT>::kPerUnit]) {
+  constexpr int P = Elem<DT>::kPerUnit;
+  if (DT == QK_F32 || !w_f32) {
+    load_values<DT>(w, k, u, v);
+  } else {
+    float a[4];
+#pragma unroll
+    for (int h = 0; h < P / 4; ++h) {
+      load_values<QK_F32>(w, k, u * (P / 4) + h, a);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[h * 4 + e] = a[e];
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t narrow_bits(float v) {
+  if constexpr (DT == QK_F32) return __float_as_uint(v);
+  if constexpr (DT == QK_BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  return __builtin_bit_cast(uint16_t, static_cast<_Float16>(qm::rounded_f32(v)));
+}
+
+template <int DT>
+__device__ __forceinline__ void store_values(void* row, int k, int u,
+                                             const float (&v)[Elem<DT>::kPerUnit]) {
+  using E = Elem<DT>;
+  constexpr int P = E::kPerUnit;
+  if ((u + 1) * P <= k) {
+    Raw16<E::kBytes> raw;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == QK_F32)
+        raw.w[i] = narrow_bits<DT>(v[i]);
+      else
+        raw.w[i] = qm::pack2_narrow<DT>(v[2 * i], v[2 * i + 1]);
+    }
+    *reinterpret_cast<Raw16<E::kBytes>*>(static_cast<char*>(row) + static_cast<size_t>(u) * 16) = raw;
+  } else {
+    for (int e = 0; u * P + e < k; ++e) {
+      if constexpr (DT == QK_F32)
+        static_cast<uint32_t*>(row)[u * P + e] = narrow_bits<DT>(v[e]);
+      else
+        static_cast<uint16_t*>(row)[u * P + e] = static_cast<uint16_t>(narrow_bits<DT>(v[e]));
+    }
+  }
+}
+
+// Four codes of values in units of the scale, packed little-endian.
+template <bool FP8>
+__device__ __forceinline__ uint32_t codes4(const float* y, float s, float r) {
+  if constexpr (FP8) {
+    return qm::pack4_fp8(qm::fp8_ratio_own(y[0], s, r), qm::fp8_ratio_own(y[1], s, r),
+                         qm::fp8_ratio_own(y[2], s, r), qm::fp8_ratio_own(y[3], s, r));
+  } else {
+    return qm::pack4_low_bytes(qm::code_word_dynamic(y[0], s, r), qm::code_word_dynamic(y[1], s, r),
+                               qm::code_word_dynamic(y[2], s, r), qm::code_word_dynamic(y[3], s, r));
+  }
+}
+
+template <int DT, bool FP8>
+__device__ __forceinline__ void store_row_codes(uint8_t* qrow, int k, int u, bool finite,
+                                                const float (&y)[Elem<DT>::kPerUnit], float s, float r) {
+  constexpr int P = Elem<DT>::kPerUnit;
+  uint32_t w[P / 4];
+#pragma unroll
+  for (int i = 0; i < P / 4; ++i) w[i] = finite ? codes4<FP8>(y + 4 * i, s, r) : 0u;
+  if ((u + 1) * P <= k) {
+    if constexpr (P == 8)
+      *reinterpret_cast<Raw8<1>*>(qrow + static_cast<size_t>(u) * P) = Raw8<1>{{w[0], w[1]}};
+    else
+      *reinterpret_cast<Raw4*>(qrow + static_cast<size_t>(u) * P) = Raw4{w[0]};
+  } else {
+    for (int e = 0; u * P + e < k; ++e)
+      qrow[u * P + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
+  }
+}
+
+struct NormParams {
+  int k;
+  const void* x;
+  int64_t ldx;  // row strides in elements
+  const void* residual;
+  int64_t ldr;
+  const void* weight;
+  int w_f32;
+  double eps;
+  void* r_out;
+  int64_t ldo;
+  uint8_t* q;
+  float* scale;
+};
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Sum over the row's threads: one wave, or four through LDS.
+template <int THREADS>
+__device__ __forceinline__ double row_sum(double v) {
+  v = wave_sum(v);
+  if constexpr (THREADS > 64) {
+    __shared__ double part[THREADS / 64];
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; ++w) v += part[w];
+  }
+  return v;
+}
+// Max of |y| as bit patterns: NaN orders above infinity, so it is kept.
+template <int THREADS>
+__device__ __forceinline__ float row_max_abs(float v) {
+  if constexpr (THREADS > 64)
+    return qm::block_max<THREADS>(v);
+  else
+    return qm::wave_max_nonneg(v);
+}
+
+__device__ __forceinline__ float max_abs_bits(float top, float y) {
+  return __uint_as_float(qm::max_u32(__float_as_uint(top), __float_as_uint(y) & 0x7fffffffu));
+}
+
+__device__ __forceinline__ float inverse_rms(double sum, int k, double eps) {
+  return static_cast<float>(1.0 / sqrt(sum / static_cast<double>(k) + eps));
+}
+
+// scale and r = RN(1 / scale) of a row; whether its codes are formed.
+template <bool FP8>
+__device__ __forceinline__ bool row_scale_of(float top, float& s, float& r) {
+  const bool finite = __float_as_uint(top) < 0x7f800000u;
+  if constexpr (FP8)
+    qm::row_scale_fp8(top, 0.0f, s, r);
+  else
+    qm::row_scale(top, s, r);
+  if (!finite) s = top;
+  return finite;
+}
+
+// A row in registers: THREADS threads (one wave, four rows per workgroup; or
+// one workgroup) with UPT units each.
+template <int DT, bool RES, bool FP8, int UPT, int THREADS>
+__global__ __launch_bounds__(kBlock) void norm_rows(NormParams p, int m) {
+  using E = Elem<DT>;
+  constexpr int P = E::kPerUnit;
+  const int t = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t row = THREADS == 64 ? static_cast<int64_t>(blockIdx.x) * (kBlock / 64) + (threadIdx.x >> 6)
+                                    : blockIdx.x;
+  if (row >= m) return;  // whole waves leave, and only in the variant without barriers
+  const int k = p.k, units = (k + P - 1) / P;
+  const char* xrow = static_cast<const char*>(p.x) + row * p.ldx * E::kBytes;
+  const char* rrow = RES ? static_cast<const char*>(p.residual) + row * p.ldr * E::kBytes : nullptr;
+
+  float v[UPT][P];
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < UPT; ++j) {
+    const int u = t + j * THREADS;
+    if (u < units) {
+      load_values<DT>(xrow, k, u, v[j]);
+      if constexpr (RES) {
+        float a[P];
+        load_values<DT>(rrow, k, u, a);
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[j][e] += a[e];
+      }
+#pragma unroll
+      for (int e = 0; e < P; ++e) sum = __builtin_fma(static_cast<double>(v[j][e]), static_cast<double>(v[j][e]), sum);
+    }
+  }
+  const float inv = inverse_rms(row_sum<THREADS>(sum), k, p.eps);
+
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < UPT; ++j) {
+    const int u = t + j * THREADS;
+    if (u < units) {
+      if constexpr (RES) store_values<DT>(static_cast<char*>(p.r_out) + row * p.ldo * E::kBytes, k, u, v[j]);
+      float w[P];
+      load_weight<DT>(p.weight, p.w_f32, k, u, w);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        v[j][e] = v[j][e] * inv * w[e];
+        if (u * P + e < k) top = max_abs_bits(top, v[j][e]);
+      }
+    }
+  }
+  top = row_max_abs<THREADS>(top);
+  float s, r;
+  const bool finite = row_scale_of<FP8>(top, s, r);
+  if (t == 0) p.scale[row] = s;
+#pragma unroll
+  for (int j = 0; j < UPT; ++j) {
+    const int u = t + j * THREADS;
+    if (u < units) store_row_codes<DT, FP8>(p.q + row * static_cast<int64_t>(k), k, u, finite, v[j], s, r);
+  }
+}
+
+// Rows longer than the registers hold: three passes over the row.  The
+// residual's sum is stored in the last one, by the thread that read it in
+// every pass, so it may replace the residual or x in place.
+template <int DT, bool RES, bool FP8>
+__global__ __launch_bounds__(kBlock) void norm_rows_long(NormParams p) {
+  using E = Elem<DT>;
+  constexpr int P = E::kPerUnit;
+  const int64_t row = blockIdx.x;
+  const int k = p.k, units = (k + P - 1) / P;
+  const char* xrow = static_cast<const char*>(p.x) + row * p.ldx * E::kBytes;
+  const char* rrow = RES ? static_cast<const char*>(p.residual) + row * p.ldr * E::kBytes : nullptr;
+  auto values = [&](int u, float(&v)[P]) {
+    load_values<DT>(xrow, k, u, v);
+    if constexpr (RES) {
+      float a[P];
+      load_values<DT>(rrow, k, u, a);
+#pragma unroll
+      for (int e = 0; e < P; ++e) v[e] += a[e];
+    }
+  };
+  double sum = 0.0;
+  for (int u = threadIdx.x; u < units; u += kBlock) {
+    float v[P];
+    values(u, v);
+#pragma unroll
+    for (int e = 0; e < P; ++e) sum = __builtin_fma(static_cast<double>(v[e]), static_cast<double>(v[e]), sum);
+  }
+  const float inv = inverse_rms(row_sum<kBlock>(sum), k, p.eps);
+  float top = 0.0f;
+  for (int u = threadIdx.x; u < units; u += kBlock) {
+    float v[P], w[P];
+    values(u, v);
+    load_weight<DT>(p.weight, p.w_f32, k, u, w);
+#pragma unroll
+    for (int e = 0; e < P; ++e)
+      if (u * P + e < k) top = max_abs_bits(top, v[e] * inv * w[e]);
+  }
+  top = row_max_abs<kBlock>(top);
+  float s, r;
+  const bool finite = row_scale_of<FP8>(top, s, r);
+  if (threadIdx.x == 0) p.scale[row] = s;
+  for (int u = threadIdx.x; u < units; u += kBlock) {
+    float v[P], w[P];
+    values(u, v);
+    if constexpr (RES) store_values<DT>(static_cast<char*>(p.r_out) + row * p.ldo * E::kBytes, k, u, v);
+    load_weight<DT>(p.weight, p.w_f32, k, u, w);
+#pragma unroll
+    for (int e = 0; e < P; ++e) v[e] = v[e] * inv * w[e];
+    store_row_codes<DT, FP8>(p.q + row * static_cast<int64_t>(k), k, u, finite, v, s, r);
+  }
+}
+
+template <int DT, bool RES, bool FP8>
+hipError_t dispatch(int m, const NormParams& p, hipStream_t stream) {
+  constexpr int P = Elem<DT>::kPerUnit;
+  const int units = p.k / P + (p.k % P != 0);
+  const dim3 block(kBlock), rows(static_cast<unsigned>(m)), quads((static_cast<unsigned>(m) + 3) / 4);
+  if (units <= 64) return launch(norm_rows<DT, RES, FP8, 1, 64>, quads, block, 0, stream, p, m);
+  if (units <= 128) return launch(norm_rows<DT, RES, FP8, 2, 64>, quads, block, 0, stream, p, m);
+  if (units <= kBlock) return launch(norm_rows<DT, RES, FP8, 1, kBlock>, rows, block, 0, stream, p, m);
+  if (units <= kBlock * 2) return launch(norm_rows<DT, RES, FP8, 2, kBlock>, rows, block, 0, stream, p, m);
+  if (units <= kBlock * 4) return launch(norm_rows<DT, RES, FP8, 4, kBlock>, rows, block, 0, stream, p, m);
+  if (units <= kBlock * kMaxUnits)
+    return launch(norm_rows<DT, RES, FP8, kMaxUnits, kBlock>, rows, block, 0, stream, p, m);
+  return launch(norm_rows_long<DT, RES, FP8>, rows, block, 0, stream, p);
+}
+
+template <int DT>
+hipError_t dispatch_dtype(const RmsNormQuantArgs& a, hipStream_t stream) {
+  const NormParams p{a.k,     a.x,      a.ldx, a.residual, a.ldr, a.weight, a.weight_f32,
+                     a.eps,   a.r_out,  a.ldo, a.q,        a.scale};
+  if (a.residual)
+    return a.fp8 ? dispatch<DT, true, true>(a.m, p, stream) : dispatch<DT, true, false>(a.m, p, stream);
+  return a.fp8 ? dispatch<DT, false, true>(a.m, p, stream) : dispatch<DT, false, false>(a.m, p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm_quant(const RmsNormQuantArgs& a, hipStream_t stream) {
+  switch (a.dtype) {
+    case QK_F32: return dispatch_dtype<QK_F32>(a, stream);
+    case QK_BF16: return dispatch_dtype<QK_BF16>(a, stream);
+    default: return dispatch_dtype<QK_F16>(a, stream);
+  }
+}
+
+}  // namespace qk

@@ -504,4 +504,135 @@ int qk_gemm_i8_asym(int m, int n, int k, const int8_t* a, const int32_t* zero_po
   return status_of(qk::launch_gemm_asym(g, zero_point, wsum, stream));
 }
 
+int qk_rms_norm_quant(int m, int k, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                      const void* weight, int dtype, int weight_dtype, double eps, int code,
+                      void* residual_out, int64_t ldo, void* q, float* scale, hipStream_t stream) {
+  if (m < 0 || k < 0 || !known_input_dtype(dtype)) return QK_ERR_INVALID_VALUE;
+  if (weight_dtype != dtype && weight_dtype != QK_F32) return QK_ERR_INVALID_VALUE;
+  if (code != QK_CODE_I8 && code != QK_CODE_FP8) return QK_ERR_INVALID_VALUE;
+  if (!(eps >= 0.0)) return QK_ERR_INVALID_VALUE;
+  if (m == 0) return QK_OK;
+  if (!scale || (k > 0 && (!x || !weight || !q || (residual && !residual_out)))) return QK_ERR_INVALID_VALUE;
+  if (ldx < k || (residual && (ldr < k || ldo < k))) return QK_ERR_INVALID_VALUE;
+  if (k > 1 << 30) return QK_ERR_UNSUPPORTED;
+  const uintptr_t e = dtype == QK_F32 ? 4 : 2;
+  if (!aligned(x, e) || !aligned(weight, weight_dtype == QK_F32 ? 4 : 2) || !aligned(scale, 4))
+    return QK_ERR_UNSUPPORTED;
+  if (residual && (!aligned(residual, e) || !aligned(residual_out, e))) return QK_ERR_UNSUPPORTED;
+  const qk::RmsNormQuantArgs a{m,        k,          x,        ldx, residual,
+                               ldr,      weight,     dtype,    weight_dtype == QK_F32,
+                               eps,      residual_out, ldo,    code == QK_CODE_FP8,
+                               static_cast<uint8_t*>(q), scale};
+  return status_of(qk::launch_rms_norm_quant(a, stream));
+}
+
+// Checks of the cache and its tables, the same for every call on it.
+static int kv_check(int seqs, int tokens, int kv_heads, int dim, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, int blocks, int block, int code,
+                    const int* table, int64_t ldt, int width, const int* lens) {
+  if (seqs < 0 || tokens < 0 || kv_heads < 1 || blocks < 0 || width < 0) return QK_ERR_INVALID_VALUE;
+  if (dim < 16 || dim > 256 || dim % 16 != 0) return QK_ERR_INVALID_VALUE;
+  if (block != 16 && block != 32 && block != 64 && block != 128) return QK_ERR_INVALID_VALUE;
+  if (code != QK_CODE_I8 && code != QK_CODE_FP8) return QK_ERR_INVALID_VALUE;
+  if (seqs == 0 || tokens == 0) return QK_OK;
+  if (ldt < width || !lens || (width > 0 && !table)) return QK_ERR_INVALID_VALUE;
+  if (blocks == 0 || !k_cache || !v_cache || !k_scale || !v_scale) return QK_ERR_INVALID_VALUE;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+      !aligned(table, 4) || !aligned(lens, 4))
+    return QK_ERR_UNSUPPORTED;
+  return QK_OK;
+}
+
+static qk::KvCacheView kv_view(int kv_heads, int dim, const void* k_cache, const void* v_cache,
+                               const float* k_scale, const float* v_scale, int blocks, int block, int code,
+                               const int* table, int64_t ldt, int width) {
+  return qk::KvCacheView{blocks,
+                         kv_heads,
+                         block,
+                         dim,
+                         code == QK_CODE_FP8,
+                         static_cast<uint8_t*>(const_cast<void*>(k_cache)),
+                         static_cast<uint8_t*>(const_cast<void*>(v_cache)),
+                         const_cast<float*>(k_scale),
+                         const_cast<float*>(v_scale),
+                         table,
+                         ldt,
+                         width};
+}
+
+// A grid beyond what a launch takes is an argument error here.
+static int status_of_cut(hipError_t e) {
+  return e == hipErrorInvalidConfiguration ? QK_ERR_UNSUPPORTED : status_of(e);
+}
+
+static int kv_rows(bool write, int seqs, int tokens, int kv_heads, int dim, void* k, int64_t ldk, void* v,
+                   int64_t ldv, int dtype, const void* k_cache, const void* v_cache, const float* k_scale,
+                   const float* v_scale, int blocks, int block, int code, const int* table, int64_t ldt,
+                   int width, const int* start, const int* cu, hipStream_t stream) {
+  if (!known_input_dtype(dtype)) return QK_ERR_INVALID_VALUE;
+  const int rc = kv_check(seqs, tokens, kv_heads, dim, k_cache, v_cache, k_scale, v_scale, blocks, block, code,
+                          table, ldt, width, start);
+  if (rc != QK_OK || seqs == 0 || tokens == 0) return rc;
+  const int64_t row = static_cast<int64_t>(kv_heads) * dim;
+  if (!k || !v || !cu || ldk < row || ldv < row) return QK_ERR_INVALID_VALUE;
+  const uintptr_t e = dtype == QK_F32 ? 4 : 2;
+  if (!aligned(k, e) || !aligned(v, e) || !aligned(cu, 4)) return QK_ERR_UNSUPPORTED;
+  const qk::KvCacheView c = kv_view(kv_heads, dim, k_cache, v_cache, k_scale, v_scale, blocks, block, code, table,
+                                    ldt, width);
+  const qk::KvRowsArgs a{seqs, tokens, dtype, start, cu, k, ldk, v, ldv};
+  return status_of_cut(write ? qk::launch_kv_cache_write(c, a, stream) : qk::launch_kv_cache_read(c, a, stream));
+}
+
+int qk_kv_cache_write(int seqs, int tokens, int kv_heads, int dim, const void* k, int64_t ldk,
+                      const void* v, int64_t ldv, int dtype, void* k_cache, void* v_cache,
+                      float* k_scale, float* v_scale, int blocks, int block, int code,
+                      const int* table, int64_t ldt, int width, const int* start, const int* cu,
+                      hipStream_t stream) {
+  return kv_rows(true, seqs, tokens, kv_heads, dim, const_cast<void*>(k), ldk, const_cast<void*>(v), ldv, dtype,
+                 k_cache, v_cache, k_scale, v_scale, blocks, block, code, table, ldt, width, start, cu, stream);
+}
+
+int qk_kv_cache_read(int seqs, int tokens, int kv_heads, int dim, void* k, int64_t ldk, void* v,
+                     int64_t ldv, int dtype, const void* k_cache, const void* v_cache,
+                     const float* k_scale, const float* v_scale, int blocks, int block, int code,
+                     const int* table, int64_t ldt, int width, const int* start, const int* cu,
+                     hipStream_t stream) {
+  return kv_rows(false, seqs, tokens, kv_heads, dim, k, ldk, v, ldv, dtype, k_cache, v_cache, k_scale, v_scale,
+                 blocks, block, code, table, ldt, width, start, cu, stream);
+}
+
+size_t qk_kv_attention_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim,
+                                      int max_kv, int window) {
+  if (seqs <= 0 || tokens <= 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads != 0 || dim < 16 ||
+      dim > 256 || max_kv < 0 || window < 0)
+    return 0;
+  return qk::kv_attention_workspace_bytes(seqs, tokens, heads, kv_heads, dim, max_kv, window);
+}
+
+int qk_kv_attention(int seqs, int tokens, int heads, int kv_heads, int dim, const void* q,
+                    int64_t ldq, int dtype, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, int blocks, int block, int code,
+                    const int* table, int64_t ldt, int width, const int* lens, const int* cu,
+                    int max_q, int max_kv, float scale, int window, void* out, float* lse,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (dtype != QK_BF16 && dtype != QK_F16) return QK_ERR_INVALID_VALUE;
+  if (kv_heads < 1 || heads < 1 || heads % kv_heads != 0) return QK_ERR_INVALID_VALUE;
+  if (max_q < 1 || max_kv < 0 || window < 0 || !(scale - scale == 0.0f)) return QK_ERR_INVALID_VALUE;
+  const int rc = kv_check(seqs, tokens, kv_heads, dim, k_cache, v_cache, k_scale, v_scale, blocks, block, code,
+                          table, ldt, width, lens);
+  if (rc != QK_OK || seqs == 0 || tokens == 0) return rc;
+  if (!q || !out || ldq < static_cast<int64_t>(heads) * dim || (!cu && tokens != seqs))
+    return QK_ERR_INVALID_VALUE;
+  if (!aligned(q, 2) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(cu, 4)) return QK_ERR_UNSUPPORTED;
+  const int64_t reach = static_cast<int64_t>(width) * block;
+  if (reach < max_kv) max_kv = static_cast<int>(reach);
+  const size_t need = qk::kv_attention_workspace_bytes(seqs, tokens, heads, kv_heads, dim, max_kv, window);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return QK_ERR_WORKSPACE;
+  const qk::KvCacheView c = kv_view(kv_heads, dim, k_cache, v_cache, k_scale, v_scale, blocks, block, code, table,
+                                    ldt, width);
+  const qk::KvAttentionArgs a{seqs, tokens, heads, dtype, q, ldq, lens, cu, max_q, max_kv, scale, window, out, lse,
+                              workspace, workspace_bytes};
+  return status_of_cut(qk::launch_kv_attention(c, a, stream));
+}
+
 }  // extern "C"

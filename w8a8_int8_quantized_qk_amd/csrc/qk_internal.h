@@ -157,4 +157,71 @@ struct GemvArgs {
 size_t gemv_workspace_bytes(int n);
 hipError_t launch_gemv(const GemvArgs& g, hipStream_t stream);
 
+// Root-mean-square norm with the residual's addition and 8-bit codes
+// (norm_quant.hip).  Row strides (ld*) in elements; residual and r_out may be
+// null together.
+struct RmsNormQuantArgs {
+  int m, k;
+  const void* x;
+  int64_t ldx;
+  const void* residual;
+  int64_t ldr;
+  const void* weight;
+  int dtype, weight_f32;
+  double eps;
+  void* r_out;
+  int64_t ldo;
+  bool fp8;
+  uint8_t* q;
+  float* scale;
+};
+hipError_t launch_rms_norm_quant(const RmsNormQuantArgs& a, hipStream_t stream);
+
+// A paged 8-bit key/value cache (qk.h, "Paged 8-bit key/value cache") and the
+// sequences that a call works on.
+struct KvCacheView {
+  int blocks, heads, block, dim;  // block: positions per block, 16 to 128
+  bool fp8;
+  uint8_t* k;  // [blocks][heads][block][dim]
+  uint8_t* v;  // [blocks][heads][dim][block]
+  float* k_scale;  // [blocks][heads]
+  float* v_scale;
+  const int* table;  // [seqs][width], row stride ldt
+  int64_t ldt;
+  int width;
+};
+// New tokens into the cache, and back (kv_cache.hip).  Sequence b's rows are
+// cu[b] .. cu[b + 1] of k and v, at positions start[b] and on; ldk and ldv are
+// the rows' strides in elements.
+struct KvRowsArgs {
+  int seqs, tokens, dtype;
+  const int* start;
+  const int* cu;
+  void* k;
+  int64_t ldk;
+  void* v;
+  int64_t ldv;
+};
+hipError_t launch_kv_cache_write(const KvCacheView& c, const KvRowsArgs& a, hipStream_t stream);
+hipError_t launch_kv_cache_read(const KvCacheView& c, const KvRowsArgs& a, hipStream_t stream);
+
+// Attention over the cache (kv_attention.hip).
+struct KvAttentionArgs {
+  int seqs, tokens, heads, dtype;
+  const void* q;  // [tokens][heads][dim], row stride ldq
+  int64_t ldq;
+  const int* lens;  // [seqs] positions in the cache
+  const int* cu;    // [seqs + 1] rows of each sequence, or null: one each
+  int max_q, max_kv;
+  float scale;
+  int window;
+  void* out;   // [tokens][heads][dim] dense
+  float* lse;  // [tokens][heads] or null
+  void* workspace;
+  size_t workspace_bytes;
+};
+size_t kv_attention_workspace_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_kv,
+                                    int window);
+hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, hipStream_t stream);
+
 }  // namespace qk

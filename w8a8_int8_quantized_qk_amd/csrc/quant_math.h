@@ -78,6 +78,26 @@ struct Elem<QK_F16> {
   }
 };
 
+// v itself, kept as a binary32 result of its own: without it the compiler may
+// merge the operation that made v with a conversion to binary16 behind it
+// (v_fma_mixlo_f16), which rounds once where the definition rounds twice.
+__device__ __forceinline__ float rounded_f32(float v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
+// Two values rounded to DT (a 16-bit type), nearest even, a in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2_narrow(float a, float b) {
+  if constexpr (DT == QK_BF16) {
+    typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, pair_t{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+  } else {
+    typedef _Float16 pair_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, pair_t{static_cast<_Float16>(rounded_f32(a)), static_cast<_Float16>(rounded_f32(b))});
+  }
+}
+
 // clamp(rint(x / s), -127, 127) with x / s formed from r = RN(1 / s).
 __device__ __forceinline__ int code_of(float x, float s, float r) {
   const float y = x * r;
