@@ -577,22 +577,26 @@ int qk_kv_cache_read(int seqs, int tokens, int kv_heads, int dim, void *k, int64
  *        dim elements apart.
  *   lens [seqs] int;  cu [seqs + 1] int, or NULL when every sequence has one
  *        row (tokens == seqs).
- *   max_q   at least every sequence's number of rows (any such bound; a tight one
- *           saves work).
+ *   max_q   a bound on every sequence's number of rows (a tight one saves work;
+ *           rows of a sequence with more may be left unwritten).
  *   max_kv  a bound on lens, held to width * block; a length above it counts as it.
  *   out  [tokens][heads][dim] of dtype, dense;  lse [tokens][heads] float or
  *        NULL.
- *   workspace  qk_kv_attention_workspace_size(...) bytes, 256-byte aligned, any contents;
- *        calls that can run at the same time must not share one.  NULL when
- *        the size is 0.
+ *   workspace  qk_kv_attention_workspace_size(...) bytes (ragged: whether cu is given;
+ *        max_kv as it is held), 256-byte aligned; NULL when the size is 0.  Its
+ *        first 64 KiB count arrivals: set to zero once by qk_workspace_init
+ *        before the first use, and again after a call that returned a HIP
+ *        launch error; every successful call leaves them zero, so one buffer
+ *        serves all calls issued in order on a stream.  Calls that can run at
+ *        the same time must not share one.
  * Scores, maxima, sums and outputs are held in binary32; codes enter the
  * products exactly, probabilities rounded to 11 bits.
  * Errors: as qk_kv_cache_write; heads not a multiple of kv_heads, cu NULL with tokens !=
  * seqs, scale not finite, negative window or bound, max_q < 1 (QK_ERR_INVALID_VALUE);
  * workspace missing, misaligned or short (QK_ERR_WORKSPACE).
  */
-size_t qk_kv_attention_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim,
-                                      int max_kv, int window);
+size_t qk_kv_attention_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim, int ragged,
+                                      int max_q, int max_kv, int window);
 int qk_kv_attention(int seqs, int tokens, int heads, int kv_heads, int dim, const void *q,
                     int64_t ldq, int dtype, const void *k_cache, const void *v_cache,
                     const float *k_scale, const float *v_scale, int blocks, int block, int code,

@@ -80,8 +80,10 @@ def test_attention(kw, status):
 
 
 def test_attention_workspace_size():
-    assert qk.kv_attention_workspace_size(1, 1, 4, 2, 64, 64) == 0            # one piece: nothing to join
-    assert qk.kv_attention_workspace_size(1, 1, 4, 2, 64, 100000) > 0
-    assert qk.kv_attention_workspace_size(0, 1, 4, 2, 64, 100000) == 0
-    assert qk.kv_attention_workspace_size(1, 1, 4, 3, 64, 100000) == 0        # refused shapes need none
-    assert qk.kv_attention_workspace_size(1, 1, 4, 2, 64, 100000, 100) == 0   # a window bounds the range
+    size = qk.kv_attention_workspace_size
+    assert size(1, 1, 4, 2, 64, 64) == 0                     # one piece: nothing to join
+    assert size(1, 1, 4, 2, 64, 100000) > 0
+    assert size(0, 1, 4, 2, 64, 100000) == 0
+    assert size(1, 1, 4, 3, 64, 100000) == 0                 # refused shapes need none
+    assert size(1, 1, 4, 2, 64, 100000, window=100) == 0     # a window bounds the range
+    assert size(1, 200, 4, 2, 64, 100000, ragged=True, max_q=200) > 0

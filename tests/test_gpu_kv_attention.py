@@ -76,7 +76,7 @@ class Setup:
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("heads,kv_heads,dim,block", [(1, 1, 16, 16), (4, 2, 64, 32), (8, 1, 80, 64), (6, 2, 128, 16), (7, 1, 112, 128),
-                                                      (2, 2, 256, 64), (20, 1, 128, 64), (48, 3, 64, 16)])
+                                                      (2, 2, 256, 64), (20, 1, 128, 64), (48, 3, 64, 16), (80, 1, 32, 16)])
 def test_single_tokens(heads, kv_heads, dim, block, dtype, fp8):
     lens = [1, 2, 15, 16, 17, 63, 64, 65, 200, 0, 301]
     t = Setup(heads * 7 + dim, lens, [1] * len(lens), heads, kv_heads, dim, block, fp8, dtype)
@@ -123,11 +123,24 @@ def test_long_cache_is_split(fp8, dtype):
     assert qk.kv_attention_workspace_size(4, 4, 4, 2, 64, 5056) > 0
     out, lse = t.run(return_lse=True)
     t.check(out, lse)
-    ws = torch.full((qk.kv_attention_workspace_size(4, 4, 4, 2, 64, 5056),), 255, dtype=torch.uint8, device=DEV)
+    ws = qk.new_workspace(qk.kv_attention_workspace_size(4, 4, 4, 2, 64, 5056), DEV)
+    ws[65536:] = 255                              # only the counters have to be zero, and they are zero again
     own = t.run(workspace=ws)
-    assert torch.equal(own, out)
+    assert torch.equal(own, out) and not ws[:65536].any()
     for _ in range(3):
         assert torch.equal(t.run(), out)          # the same bits on every run
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,fp8", [(4, 2, 128, False), (2, 2, 64, True), (3, 1, 256, True)])
+def test_prompt_tiles_are_split(heads, kv_heads, dim, fp8):
+    # a few rows behind a long cache: tiles of many columns whose positions are cut into chunks
+    lens, counts = [2500, 1900, 700, 50], [90, 1, 150, 50]
+    t = Setup(12 + dim, lens, counts, heads, kv_heads, dim, 32, fp8, "bf16")
+    assert qk.kv_attention_workspace_size(4, sum(counts), heads, kv_heads, dim, t.table.shape[1] * 32, 0, True, 150) > 0
+    out, lse = t.run(return_lse=True, max_q=150)
+    t.check(out, lse)
+    for _ in range(3):
+        assert torch.equal(t.run(max_q=150), out)
 
 
 def test_sharp_and_flat_rows():
@@ -229,7 +242,7 @@ def test_graph_replay():
     want = t.run().clone()
     table, lens = dev(t.table), dev(np.asarray(t.lens, np.int32))
     out = torch.empty_like(t.q)
-    ws = torch.empty(max(256, qk.kv_attention_workspace_size(3, 3, 4, 2, 64, table.shape[1] * 64)), dtype=torch.uint8, device=DEV)
+    ws = qk.new_workspace(qk.kv_attention_workspace_size(3, 3, 4, 2, 64, table.shape[1] * 64), DEV)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):

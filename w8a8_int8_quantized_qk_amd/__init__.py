@@ -129,7 +129,7 @@ def _declare(lib):
     for name in ("qk_kv_cache_write", "qk_kv_cache_read"):
         getattr(lib, name).argtypes = [I, I, I, I, P, L, P, L, I, P, P, P, P, I, I, I, P, L, I, P, P, P]
         getattr(lib, name).restype = I
-    lib.qk_kv_attention_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    lib.qk_kv_attention_workspace_size.argtypes = [I] * 9
     lib.qk_kv_attention_workspace_size.restype = ctypes.c_size_t
     lib.qk_kv_attention.argtypes = [I, I, I, I, I, P, L, I, P, P, P, P, I, I, I, P, L, I, P, P, I, I, F, I, P,
                                     P, P, ctypes.c_size_t, P]
@@ -979,8 +979,10 @@ def kv_cache_read(cache: KVCache, table: torch.Tensor, start: torch.Tensor, cu: 
 
 @functools.lru_cache(maxsize=4096)
 def kv_attention_workspace_size(seqs: int, tokens: int, heads: int, kv_heads: int, dim: int, max_kv: int,
-                                window: int = 0) -> int:
-    return int(library().qk_kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, max_kv, window))
+                                window: int = 0, ragged: bool = False, max_q: int = 1) -> int:
+    """Bytes of workspace of a kv_attention call (ragged: with cu); 0 if none."""
+    return int(library().qk_kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, ragged, max_q,
+                                                        max_kv, window))
 
 
 _attention_workspaces: dict = {}
@@ -998,7 +1000,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: tor
     sequence has one.  window > 0 limits a row to its last `window` positions.
     scale defaults to dim ** -0.5.  max_q and max_kv are bounds that the host
     knows on a sequence's rows and positions (by default all rows, and what the
-    table covers); tight ones save work.  Returns out [tokens, heads, dim], and
+    table covers); tight ones save work.  A workspace of one's own has
+    kv_attention_workspace_size(...) bytes and comes from new_workspace.  Returns out [tokens, heads, dim], and
     with return_lse the fp32 log-sum-exp [tokens, heads]; a row that sees no
     position gives 0 and -inf.
     """
@@ -1032,18 +1035,22 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: tor
     max_q = (1 if cu is None else max(tokens, 1)) if max_q is None else max_q
     stream = _raw_stream(dev)
     if workspace is None:
-        need = kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, max_kv, window)
+        need = kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, max_kv, window, cu is not None,
+                                           max_q)
         if need:
             key = (dev, stream)
             workspace = _attention_workspaces.get(key)
             if workspace is None or workspace.numel() < need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace = new_workspace(need, dev)
                 _attention_workspaces[key] = workspace
     else:
         _need(workspace, "workspace", None, None, dev)
-    _check(library().qk_kv_attention(
+    status = library().qk_kv_attention(
         seqs, tokens, heads, kv_heads, dim, q.data_ptr(), ldq, _IN_DTYPES[dt], *args, lens.data_ptr(),
         0 if cu is None else cu.data_ptr(), max_q, max_kv, dim ** -0.5 if scale is None else scale, window,
         out.data_ptr(), lse.data_ptr() if return_lse else 0, 0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), stream))
+        0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
+    if status != QK_OK and status < 1000:  # part of the call may have run: a fresh workspace next time
+        _attention_workspaces.pop((dev, stream), None)
+    _check(status)
     return (out, lse) if return_lse else out

@@ -3,7 +3,9 @@
 // sliding window, and grouped heads.
 //
 // The (row, head) pairs of a sequence that share a kv head are the columns of
-// a tile.  Scores are formed transposed, S^T = K Q^T: a lane then holds the
+// a tile: 16 in kv_attention_cols_kernel (sequences with up to 64 columns:
+// single tokens; bound by the cache's bytes), 128 in kv_attention_tile_kernel
+// (prompts; bound by the matrix cores and the exponentials).  Scores are formed transposed, S^T = K Q^T: a lane then holds the
 // scores of one column, so the running maximum, the sum and the rescaling of
 // the output are plain lane arithmetic, and the probabilities are already
 // where the second product, O^T = V^T P^T, wants them.  Its reduction index
@@ -32,23 +34,30 @@ using kv::half8_t;
 using kv::Raw16;
 
 typedef float float4_t __attribute__((ext_vector_type(4)));
+typedef float float16_t __attribute__((ext_vector_type(16)));
 
-constexpr int kCols = 16;       // columns of a tile
-constexpr int kGroup = 64;      // positions a wave takes at a time
+constexpr int kCols = 16;        // columns of a tile of kv_attention_cols_kernel
+constexpr int kSmall = 64;       // columns of a sequence that it takes (in tiles of 16)
+constexpr int kTileCols = 128;   // columns of a tile of kv_attention_tile_kernel
+constexpr int kGroup = 64;       // positions taken at a time
 constexpr int kWaves = 4;
 constexpr float kNone = -3.0e38f;  // a maximum over nothing
 constexpr float kLift = 14.0f;
+constexpr int kCounters = 16384;   // arrival counters at the front of the workspace
 
 struct Params {
   KvCacheView c;
   KvAttentionArgs a;
-  int group;      // heads per kv head
-  int chunk;      // positions per workgroup
-  int splits;     // chunks of the longest range
-  int cols;       // columns that the workspace holds per tile
-  float scale2;   // scale * log2(e)
-  float* part_o;  // [item][kv head][split][cols][dim]
-  float* part_ml; // [item][kv head][split][cols][2]
+  int block_shift;  // log2 of the cache's block
+  int group;        // heads per kv head
+  int tiles;        // cols kernel: tiles per sequence
+  int chunk;        // positions per workgroup
+  int splits;       // chunks of the longest range
+  int cols;         // columns that the workspace holds per tile
+  float scale2;     // scale * log2(e)
+  unsigned* arrived;  // [item][kv head], zero between calls (cols kernel)
+  float* part_o;      // [item][kv head][split][cols][dim]
+  float* part_ml;     // [item][kv head][split][cols][2]
 };
 
 // A tile's columns and the positions they see.
@@ -61,28 +70,12 @@ struct Tile {
   int splits;
 };
 
-__device__ __forceinline__ Tile find_tile(const Params& p, int64_t item) {
-  Tile t{};
-  int tile;
-  if (p.a.cu) {
-    t.seq = kv::find_sequence(item, p.a.cu, p.a.seqs, p.group, kCols, 1);
-    if (t.seq < 0) return t;
-    const int first = p.a.cu[t.seq];
-    t.rows = p.a.cu[t.seq + 1] - first;
-    if (first < 0 || t.rows <= 0 || t.rows > p.a.tokens - first) return t;
-    t.row0 = first;
-    tile = static_cast<int>(item - kv::item_base(first, p.group, kCols, 1, t.seq));
-  } else {
-    const int tiles = (p.group + kCols - 1) / kCols;
-    t.seq = static_cast<int>(item / tiles);
-    t.rows = 1;
-    t.row0 = t.seq;
-    tile = static_cast<int>(item - static_cast<int64_t>(t.seq) * tiles);
-  }
+// Columns col0 .. col0 + size of the sequence whose rows are already in t.
+__device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0, int size) {
   const int64_t all = static_cast<int64_t>(t.rows) * p.group;
-  t.col0 = tile * kCols;
-  if (t.col0 >= all) return t;
-  t.ncols = static_cast<int>(min(all - t.col0, static_cast<int64_t>(kCols)));
+  if (col0 >= all) return;
+  t.col0 = static_cast<int>(col0);
+  t.ncols = static_cast<int>(min(all - col0, static_cast<int64_t>(size)));
   t.len = min(max(p.a.lens[t.seq], 0), p.a.max_kv);  // max_kv is at most what the table covers
   const int first_pos = t.len - t.rows + t.col0 / p.group;
   const int last_pos = t.len - t.rows + (t.col0 + t.ncols - 1) / p.group;
@@ -90,6 +83,37 @@ __device__ __forceinline__ Tile find_tile(const Params& p, int64_t item) {
   t.lo = p.a.window > 0 ? max(first_pos - p.a.window + 1, 0) : 0;
   t.splits = t.hi > t.lo ? (t.hi - (t.lo & ~(kGroup - 1)) + p.chunk - 1) / p.chunk : 0;
   t.live = true;
+}
+
+// Rows of sequence t.seq; false if the offsets point outside.
+__device__ __forceinline__ bool set_rows(const Params& p, Tile& t) {
+  if (!p.a.cu) {
+    t.rows = 1;
+    t.row0 = t.seq;
+    return true;
+  }
+  const int first = p.a.cu[t.seq];
+  t.rows = p.a.cu[t.seq + 1] - first;
+  t.row0 = first;
+  return first >= 0 && t.rows > 0 && t.rows <= p.a.tokens - first;
+}
+
+// Tiles of 16 columns: item = sequence * tiles + tile; longer sequences are
+// the other kernel's.
+__device__ __forceinline__ Tile find_cols(const Params& p, unsigned item) {
+  Tile t{};
+  t.seq = static_cast<int>(item / static_cast<unsigned>(p.tiles));
+  if (!set_rows(p, t) || (p.a.cu && static_cast<int64_t>(t.rows) * p.group > kSmall)) return t;
+  set_range(p, t, static_cast<int64_t>(item - static_cast<unsigned>(t.seq) * p.tiles) * kCols, kCols);
+  return t;
+}
+
+// Tiles of 128 columns, laid over the ragged rows.
+__device__ __forceinline__ Tile find_tile(const Params& p, int64_t item) {
+  Tile t{};
+  t.seq = kv::find_sequence(item, p.a.cu, p.a.seqs, p.group, kTileCols, 1);
+  if (t.seq < 0 || !set_rows(p, t) || static_cast<int64_t>(t.rows) * p.group <= kSmall) return t;
+  set_range(p, t, (item - kv::item_base(t.row0, p.group, kTileCols, 1, t.seq)) * kTileCols, kTileCols);
   return t;
 }
 
@@ -97,7 +121,7 @@ __device__ __forceinline__ Tile find_tile(const Params& p, int64_t item) {
 // items.
 struct Place {
   int inner, head;
-  int64_t item;
+  unsigned item;
 };
 __device__ __forceinline__ Place place_of(const Params& p, int inner) {
   const unsigned b = blockIdx.x, r = b / static_cast<unsigned>(inner);
@@ -105,46 +129,64 @@ __device__ __forceinline__ Place place_of(const Params& p, int inner) {
   return Place{static_cast<int>(b - r * inner), static_cast<int>(r - item * p.c.heads), item};
 }
 
-// Max and sum over the four lanes that hold one column (lane ^ 16, ^ 32).
+// Max and sum over the lanes that hold one column: lane ^ 32, and lane ^ 16
+// where a column has four lanes.
+template <bool FOUR>
 __device__ __forceinline__ float column_max(float v) {
-  uint32_t b = __float_as_uint(v);
-  const auto r16 = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-  v = __builtin_fmaxf(__uint_as_float(r16[0]), __uint_as_float(r16[1]));
-  b = __float_as_uint(v);
-  const auto r32 = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return __builtin_fmaxf(__uint_as_float(r32[0]), __uint_as_float(r32[1]));
+  if constexpr (FOUR) {
+    const uint32_t b = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    v = __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  const uint32_t b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
+template <bool FOUR>
 __device__ __forceinline__ float column_sum(float v) {
-  uint32_t b = __float_as_uint(v);
-  const auto r16 = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-  v = __uint_as_float(r16[0]) + __uint_as_float(r16[1]);
-  b = __float_as_uint(v);
-  const auto r32 = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return __uint_as_float(r32[0]) + __uint_as_float(r32[1]);
+  if constexpr (FOUR) {
+    const uint32_t b = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  const uint32_t b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-template <int DT>
-__device__ __forceinline__ uint16_t narrow(float v) {
-  if constexpr (DT == QK_BF16)
-    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-  else
-    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+// A column's place among the query rows, and the positions it sees.
+struct Column {
+  bool valid;
+  int64_t out_row;  // row * heads + head, of out and lse
+  int64_t q_at;     // element offset of its query
+  int see_lo, see_hi;
+};
+__device__ __forceinline__ Column column_of(const Params& p, const Tile& t, int head, int k) {
+  Column c;
+  c.valid = k < t.ncols;
+  const int col = t.col0 + (c.valid ? k : 0), row = col / p.group;
+  const int h = head * p.group + col - row * p.group;
+  c.out_row = (t.row0 + row) * p.a.heads + h;
+  c.q_at = (t.row0 + row) * p.a.ldq + static_cast<int64_t>(h) * p.c.dim;
+  const int pos = t.len - t.rows + row;
+  c.see_lo = p.a.window > 0 ? max(pos - p.a.window + 1, 0) : 0;
+  c.see_hi = c.valid ? min(pos + 1, t.len) : 0;
+  return c;
 }
 
 // The column's query as the second operand of K Q^T, and the power of two
-// that undoes its scaling.  Lane (g, n) holds, for step 2 c + u, elements
-// 64 c + 16 g + 8 u + j: the order in which 16-byte loads bring K.
-template <int DT, int DP>
-__device__ __forceinline__ float load_query(const void* q, int64_t at, int dim, bool valid,
-                                            half8_t (&f)[DP / 32]) {
-  const int g = (threadIdx.x & 63) >> 4;
-  uint32_t raw[DP / 32][4];
+// that undoes its scaling.  at(i) is the element that the lane's i-th piece
+// of 8 begins with.
+template <int DT, int N, bool FOUR, typename At>
+__device__ __forceinline__ float load_query(const Params& p, const Column& c, At at, half8_t (&f)[N]) {
+  uint32_t raw[N][4];
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < DP / 32; ++i) {
-    const int d = 64 * (i >> 1) + 16 * g + 8 * (i & 1);
+  for (int i = 0; i < N; ++i) {
+    const int d = at(i);
     Raw16<2> w{{0, 0, 0, 0}};
-    if (valid && d < dim) w = *reinterpret_cast<const Raw16<2>*>(static_cast<const char*>(q) + (at + d) * 2);
+    if (c.valid && d < p.c.dim)
+      w = *reinterpret_cast<const Raw16<2>*>(static_cast<const char*>(p.a.q) + (c.q_at + d) * 2);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       raw[i][e] = w.w[e];
@@ -153,14 +195,14 @@ __device__ __forceinline__ float load_query(const void* q, int64_t at, int dim, 
   }
   if constexpr (DT == QK_F16) {
 #pragma unroll
-    for (int i = 0; i < DP / 32; ++i)
+    for (int i = 0; i < N; ++i)
       f[i] = __builtin_bit_cast(half8_t, make_uint4(raw[i][0], raw[i][1], raw[i][2], raw[i][3]));
     return 1.0f;
   } else {
-    const float amax = column_max(__uint_as_float(top << 16));
+    const float amax = column_max<FOUR>(__uint_as_float(top << 16));
     const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;  // NaN and infinity stay what they are
 #pragma unroll
-    for (int i = 0; i < DP / 32; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         f[i][2 * w] = static_cast<_Float16>(__builtin_amdgcn_ldexpf(qm::bf16_lo(raw[i][w]), 14 - e));
@@ -170,43 +212,105 @@ __device__ __forceinline__ float load_query(const void* q, int64_t at, int dim, 
   }
 }
 
+// Bytes of a 16-position piece of V past `have` positions as zeros: what lies
+// past a sequence's end may be any bytes, NaN codes among them, and a zero
+// probability would not silence those.
+__device__ __forceinline__ void keep_first(uint4& w, int have) {
+  uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = min(max(have - 4 * i, 0), 4);
+    v[i] &= b >= 4 ? 0xffffffffu : (1u << (8 * b)) - 1u;
+  }
+  w = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Partial results travel between workgroups of one launch, which may run on
+// dies with L2 caches of their own: device-scope accesses, which go past the
+// L2.  With those no cache has to be written back or invalidated; a store is
+// done once the wave's vmcnt says so.
+__device__ __forceinline__ void put2(float* at, float a, float b) {
+  const uint64_t v = static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(at), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 get2(const float* at) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(at), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l != 0.0f ? (m - kLift + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -__builtin_inff();
+}
+
+// Joins a tile's chunks in order: threads of one workgroup (`threads` of them,
+// a multiple of 64, this one being `tid`) over (column, pair of elements).
+template <int DT>
+__device__ __forceinline__ void join_chunks(const Params& p, const Tile& t, int head, int64_t slot, int splits,
+                                            int first, int ncols, int tid, int threads) {
+  constexpr int kAhead = 8;  // chunks whose loads are in flight together
+  const int pairs = p.c.dim >> 1;
+  for (int i = tid; i < ncols * pairs; i += threads) {
+    const int k = first + i / pairs, d = 2 * (i % pairs);
+    float m = kNone, l = 0.0f, a = 0.0f, b = 0.0f;
+    for (int s0 = 0; s0 < splits; s0 += kAhead) {
+      float2 ml[kAhead], o[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int64_t at = slot + static_cast<int64_t>(min(s0 + j, splits - 1)) * p.cols + k;
+        ml[j] = get2(p.part_ml + at * 2);
+        o[j] = get2(p.part_o + at * p.c.dim + d);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (s0 + j >= splits) break;
+        const float m_new = __builtin_fmaxf(m, ml[j].x);
+        const float f0 = __builtin_amdgcn_exp2f(m - m_new), f1 = __builtin_amdgcn_exp2f(ml[j].x - m_new);
+        m = m_new;
+        l = __builtin_fmaf(l, f0, ml[j].y * f1);
+        a = __builtin_fmaf(a, f0, o[j].x * f1);
+        b = __builtin_fmaf(b, f0, o[j].y * f1);
+      }
+    }
+    const int64_t out_row = column_of(p, t, head, k).out_row;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    *reinterpret_cast<kv::Raw4<2>*>(static_cast<char*>(p.a.out) + (out_row * p.c.dim + d) * 2) =
+        kv::Raw4<2>{qm::pack2_narrow<DT>(a * inv, b * inv)};
+    if (d == 0 && p.a.lse) p.a.lse[out_row] = lse_of(m, l);
+  }
+}
+
 // One workgroup: one tile of up to 16 columns, one kv head, one chunk of
 // positions.  Its four waves take groups of 64 positions in turn, each with a
 // maximum, a sum and an output of its own, and join them through LDS at the
-// end; nothing is shared before, so no wave waits for another.  A wave keeps a
-// group's K and V (16 KB at dim 128) on its way from memory while it works on
-// the group before.
+// end; nothing is shared before, so no wave waits for another.  K of the next
+// group is asked for as soon as the products with this one's have taken its
+// registers, V likewise, so a wave always has one of the two (8 KB at dim
+// 128) on its way.  The workgroup that arrives last at a tile joins its
+// chunks.
 template <int DT, bool FP8, int DP>
 __global__ __launch_bounds__(64 * kWaves) void kv_attention_cols_kernel(Params p) {
   constexpr int KC = DP / 64;  // 16-byte pieces of a K row per lane
   constexpr int VC = DP / 16;  // 16-row pieces of V
   __shared__ float lds_o[kWaves][kCols][DP + 4];
   __shared__ float lds_m[kWaves][kCols], lds_l[kWaves][kCols];
+  __shared__ unsigned lds_last;
 
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place at = place_of(p, p.splits);
   const int split = at.inner, head = at.head;
-  const int64_t item = at.item;
-  const Tile t = find_tile(p, item);
+  const Tile t = find_cols(p, at.item);
   if (!t.live) return;
-  const int dim = p.c.dim, P = p.c.block, group = p.group;
-  const int begin0 = t.lo & ~(kGroup - 1);
-  const int begin = begin0 + split * p.chunk, end = min(begin + p.chunk, t.hi);
+  const int dim = p.c.dim, P = p.c.block;
+  const int begin = (t.lo & ~(kGroup - 1)) + split * p.chunk, end = min(begin + p.chunk, t.hi);
   if (split > 0 && begin >= t.hi) return;  // split 0 stays, to write the rows that see nothing
 
-  // this lane's column
-  const int col = t.col0 + n;
-  const bool valid = n < t.ncols;
-  const int row = valid ? col / group : 0;
-  const int64_t qrow = t.row0 + row;
-  const int qhead = head * group + (valid ? col - row * group : 0);
-  const int pos = t.len - t.rows + row;
-  const int see_lo = p.a.window > 0 ? max(pos - p.a.window + 1, 0) : 0;
-  const int see_hi = valid ? min(pos + 1, t.len) : 0;
-
+  const Column col = column_of(p, t, head, n);
   half8_t qf[DP / 32];
-  const float unscale = load_query<DT, DP>(p.a.q, qrow * p.a.ldq + static_cast<int64_t>(qhead) * dim, dim, valid, qf);
+  // lane (g, n) holds, for step 2 c + u, elements 64 c + 16 g + 8 u + j: the
+  // order in which 16-byte loads bring K
+  const float unscale = load_query<DT, DP / 32, true>(
+      p, col, [&](int i) { return 64 * (i >> 1) + 16 * g + 8 * (i & 1); }, qf);
   const float c_col = unscale * p.scale2;
 
   float4_t o[VC];
@@ -216,244 +320,523 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_cols_kernel(Params p
 
   const int64_t head_bytes = static_cast<int64_t>(P) * dim;
   const int* const table = p.c.table + t.seq * p.c.ldt;
-  // The block that holds 16 positions from `at` on, held to the range of
-  // positions that are seen; entries outside the cache read block 0 and give
-  // NaN scales.
-  auto piece = [&](int at) { return min(max(at, t.lo & ~15), (t.hi - 1) & ~15); };
+  // 16 positions from `pos` on, held to the range of positions that are seen
+  // (every table entry that is read is a real one); a block number outside
+  // the cache reads block 0 and gives NaN scales
+  const int piece_lo = t.lo & ~15, piece_hi = (t.hi - 1) & ~15;
+  auto piece = [&](int pos) { return min(max(pos, piece_lo), piece_hi); };
+  auto in_pool = [&](int b) { return static_cast<unsigned>(b) < static_cast<unsigned>(p.c.blocks); };
 
-  for (int t0 = begin + wave * kGroup; t0 < end; t0 += kWaves * kGroup) {
-    // K: lane's row r = n of tile i is position t0 + 16 (r / 4) + 4 i + r % 4
-    const int kp = piece(t0 + 16 * (n >> 2)), vp = piece(t0 + 16 * g);
-    int kb = table[kp / P], vb = table[vp / P];
-    const bool bad = static_cast<unsigned>(vb) >= static_cast<unsigned>(p.c.blocks);
-    kb = static_cast<unsigned>(kb) < static_cast<unsigned>(p.c.blocks) ? kb : 0;
-    vb = bad ? 0 : vb;
-    const int64_t kt = static_cast<int64_t>(kb) * p.c.heads + head, vt = static_cast<int64_t>(vb) * p.c.heads + head;
-    const uint8_t* const krow = p.c.k + kt * head_bytes + static_cast<int64_t>((kp & (P - 1)) + (n & 3)) * dim + 16 * g;
-    const uint8_t* const vrow = p.c.v + vt * head_bytes + static_cast<int64_t>(n) * P + (vp & (P - 1));
-    uint4 kr[4][KC], vr[VC];
+  uint4 kr[4][KC], vr[VC];
+  float ks, vs;
+  // K: the lane's row n of tile i is position t0 + 16 (n / 4) + 4 i + n % 4
+  auto load_k = [&](int kp, int kb) {
+    const int64_t tile = static_cast<int64_t>(in_pool(kb) ? kb : 0) * p.c.heads + head;
+    const uint8_t* const row = p.c.k + tile * head_bytes + ((kp & (P - 1)) + (n & 3)) * dim + 16 * g;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
-        kr[i][c] = make_uint4(0, 0, 0, 0);
-        if (64 * c + 16 * g < dim) kr[i][c] = *reinterpret_cast<const uint4*>(krow + 4 * i * dim + 64 * c);
+        if (64 * c + 16 * g < dim)
+          kr[i][c] = *reinterpret_cast<const uint4*>(row + 4 * i * dim + 64 * c);
+        else
+          kr[i][c] = make_uint4(0, 0, 0, 0);
       }
+  };
+  auto load_v = [&](int vp, int vb) {
+    const int64_t tile = static_cast<int64_t>(in_pool(vb) ? vb : 0) * p.c.heads + head;
+    const uint8_t* row = p.c.v + tile * head_bytes + n * P + (vp & (P - 1));
 #pragma unroll
     for (int i = 0; i < VC; ++i) {
-      vr[i] = make_uint4(0, 0, 0, 0);
-      if (16 * i < dim) vr[i] = *reinterpret_cast<const uint4*>(vrow + static_cast<int64_t>(16 * i) * P);
+      if (16 * i < dim)
+        vr[i] = *reinterpret_cast<const uint4*>(row + 16 * i * P);
+      else
+        vr[i] = make_uint4(0, 0, 0, 0);
     }
-    float ks = p.c.k_scale[vt], vs = p.c.v_scale[vt];
-    if (bad) ks = vs = __builtin_nanf("");
+    ks = p.c.k_scale[tile];
+    vs = p.c.v_scale[tile];
+    if (!in_pool(vb)) ks = vs = __builtin_nanf("");
+  };
 
-    float4_t s[4];
+  constexpr int kStep = kWaves * kGroup;
+  int t0 = begin + wave * kGroup;
+  if (t0 < end) {
+    int kp = piece(t0 + 16 * (n >> 2)), vp = piece(t0 + 16 * g);
+    load_k(kp, table[kp >> p.block_shift]);
+    load_v(vp, table[vp >> p.block_shift]);
+    int kp1 = piece(t0 + kStep + 16 * (n >> 2)), vp1 = piece(t0 + kStep + 16 * g);
+    int kb1 = table[kp1 >> p.block_shift], vb1 = table[vp1 >> p.block_shift];
+    for (; t0 < end; t0 += kStep) {
+      const bool more = t0 + kStep < end;
+      float4_t s[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[i] = float4_t{0, 0, 0, 0};
+      for (int i = 0; i < 4; ++i) {
+        s[i] = float4_t{0, 0, 0, 0};
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        s[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[i][c].x, kr[i][c].y), qf[2 * c], s[i], 0, 0, 0);
-        s[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[i][c].z, kr[i][c].w), qf[2 * c + 1], s[i], 0, 0, 0);
-      }
-    }
-    const float c = c_col * ks, lvs = __builtin_amdgcn_logf(vs);
-    float top = kNone;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int spot = t0 + 16 * g + 4 * i + e;
-        const float y = __builtin_fmaf(s[i][e], c, lvs);
-        s[i][e] = spot >= see_lo && spot < see_hi ? y : -__builtin_inff();
-        top = __builtin_fmaxf(top, s[i][e]);
-      }
-    const float m_new = __builtin_fmaxf(m, column_max(top));
-    const float shrink = __builtin_amdgcn_exp2f(m - m_new);
-    m = m_new;
-    float sum = 0.0f;
-    half8_t pf[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float pr = __builtin_amdgcn_exp2f(s[i][e] - m + kLift);
-        sum += pr;
-        pf[i >> 1][4 * (i & 1) + e] = static_cast<_Float16>(pr);
-      }
-    // a lane that sees none of these positions must not meet their scale
-    l = l * shrink + (sum != 0.0f ? sum / vs : 0.0f);
-    if (FP8) {  // positions past the end may hold any bytes, NaN codes among them
-      const int have = min(t.len - vp, 16);
-      if (have < 16) {
-        uint32_t mask[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int b = min(max(have - 4 * w, 0), 4);
-          mask[w] = b >= 4 ? 0xffffffffu : (1u << (8 * b)) - 1u;
-        }
-#pragma unroll
-        for (int i = 0; i < VC; ++i) {
-          vr[i].x &= mask[0];
-          vr[i].y &= mask[1];
-          vr[i].z &= mask[2];
-          vr[i].w &= mask[3];
+        for (int c = 0; c < KC; ++c) {
+          s[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[i][c].x, kr[i][c].y), qf[2 * c], s[i], 0, 0, 0);
+          s[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[i][c].z, kr[i][c].w), qf[2 * c + 1], s[i], 0, 0, 0);
         }
       }
-    }
+      if (more) load_k(kp1, kb1);
+      const float c = c_col * ks, lvs = __builtin_amdgcn_logf(vs), inv_vs = 1.0f / vs;
+      const bool edge = t0 < t.lo || t0 + kGroup > t.len - t.rows;  // some column may not see all 64
+      float top = kNone;
 #pragma unroll
-    for (int i = 0; i < VC; ++i) {
-      o[i] *= shrink;
-      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[i].x, vr[i].y), pf[0], o[i], 0, 0, 0);
-      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[i].z, vr[i].w), pf[1], o[i], 0, 0, 0);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] = __builtin_fmaf(s[i][e], c, lvs);
+      if (edge || p.a.window > 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int spot = t0 + 16 * g + 4 * i + e;
+            s[i][e] = spot >= col.see_lo && spot < col.see_hi ? s[i][e] : -__builtin_inff();
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = __builtin_fmaxf(top, s[i][e]);
+      const float m_new = __builtin_fmaxf(m, column_max<true>(top));
+      const float shrink = __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+      float sum = 0.0f;
+      half8_t pf[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float pr = __builtin_amdgcn_exp2f(s[i][e] - (m - kLift));
+          sum += pr;
+          pf[i >> 1][4 * (i & 1) + e] = static_cast<_Float16>(pr);
+        }
+      // a lane that sees none of these positions must not meet their scale
+      l = __builtin_fmaf(l, shrink, sum != 0.0f ? sum * inv_vs : 0.0f);
+      if (FP8 && t0 + kGroup > t.len) {
+#pragma unroll
+        for (int i = 0; i < VC; ++i) keep_first(vr[i], t.len - vp);
+      }
+#pragma unroll
+      for (int i = 0; i < VC; ++i) {
+        o[i] *= shrink;
+        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[i].x, vr[i].y), pf[0], o[i], 0, 0, 0);
+        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[i].z, vr[i].w), pf[1], o[i], 0, 0, 0);
+      }
+      if (more) {
+        load_v(vp1, vb1);
+        vp = vp1;
+        kp1 = piece(t0 + 2 * kStep + 16 * (n >> 2));
+        vp1 = piece(t0 + 2 * kStep + 16 * g);
+        kb1 = table[kp1 >> p.block_shift];
+        vb1 = table[vp1 >> p.block_shift];
+      }
     }
   }
 
   // join the four waves
-  l = column_sum(l);
+  l = column_sum<true>(l);
   if (g == 0) {
     lds_m[wave][n] = m;
     lds_l[wave][n] = l;
   }
 #pragma unroll
   for (int i = 0; i < VC; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) lds_o[wave][n][16 * i + 4 * g + e] = o[i][e];
+    *reinterpret_cast<float4_t*>(&lds_o[wave][n][16 * i + 4 * g]) = o[i];
   __syncthreads();
 
-  const int64_t slot = ((item * p.c.heads + head) * p.splits + split) * p.cols;
-  for (int k = wave; k < t.ncols; k += kWaves) {
-    float mm = lds_m[0][k], ll = 0.0f, f[kWaves];
+  const unsigned tile_id = at.item * static_cast<unsigned>(p.c.heads) + head;
+  const int64_t slot = static_cast<int64_t>(tile_id) * p.splits * p.cols;
+  const bool whole = t.splits <= 1;
+  const int pairs = dim >> 1;
+  for (int i = threadIdx.x; i < t.ncols * pairs; i += 64 * kWaves) {
+    const int k = i / pairs, d = 2 * (i - k * pairs);
+    float mm = lds_m[0][k], ll = 0.0f, a = 0.0f, b = 0.0f;
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) mm = __builtin_fmaxf(mm, lds_m[w][k]);
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      f[w] = __builtin_amdgcn_exp2f(lds_m[w][k] - mm);
-      ll = __builtin_fmaf(lds_l[w][k], f[w], ll);
+      const float f = __builtin_amdgcn_exp2f(lds_m[w][k] - mm);
+      ll = __builtin_fmaf(lds_l[w][k], f, ll);
+      a = __builtin_fmaf(lds_o[w][k][d], f, a);
+      b = __builtin_fmaf(lds_o[w][k][d + 1], f, b);
     }
-    const int kc = t.col0 + k, kr = kc / group, kh = head * group + kc - kr * group;
-    const int64_t out_at = (t.row0 + kr) * p.a.heads + kh;
-    const bool last = t.splits <= 1;
-    const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
-    for (int d = lane; d < dim; d += 64) {
-      float v = 0.0f;
+    if (whole) {
+      const int64_t out_row = column_of(p, t, head, k).out_row;
+      const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
+      *reinterpret_cast<kv::Raw4<2>*>(static_cast<char*>(p.a.out) + (out_row * dim + d) * 2) =
+          kv::Raw4<2>{qm::pack2_narrow<DT>(a * inv, b * inv)};
+      if (d == 0 && p.a.lse) p.a.lse[out_row] = lse_of(mm, ll);
+    } else {
+      const int64_t part = slot + static_cast<int64_t>(split) * p.cols + k;
+      put2(p.part_o + part * dim + d, a, b);
+      if (d == 0) put2(p.part_ml + part * 2, mm, ll);
+    }
+  }
+  if (whole) return;
+
+  // every wave's stores are done before the workgroup counts as arrived
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned before = __hip_atomic_fetch_add(p.arrived + tile_id, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const bool last = before + 1 == static_cast<unsigned>(t.splits);
+    if (last) __hip_atomic_store(p.arrived + tile_id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    lds_last = last;
+  }
+  __syncthreads();
+  if (lds_last) join_chunks<DT>(p, t, head, slot, t.splits, 0, t.ncols, threadIdx.x, 64 * kWaves);
+}
+
+// One workgroup: one tile of 128 columns, one kv head, one chunk of positions
+// in steps of 64.  The four waves share K and V of a step through LDS, as
+// binary16 (each code is converted once per workgroup), and have 32 columns
+// each.  LDS is doubled: while a step is worked on, the next one's bytes come
+// from memory into registers and are written converted to the other half;
+// one barrier per step.  Rows of K lie in the order in which the first
+// product's result registers want them, 16-byte pieces of a row are
+// exchanged by its number so that eight consecutive rows fall on different
+// banks.
+template <int DT, bool FP8, int DP>
+__global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_tile_kernel(Params p) {
+  constexpr int KP = DP / 8;       // 16-byte pieces of a K row (8 binary16)
+  constexpr int NC = DP / 64;      // 16-byte loads per thread, of K and of V
+  constexpr int ND = DP / 32;      // 32-row pieces of V
+  constexpr int RB = DP / 16;      // 16-byte pieces of a row of codes
+  __shared__ __align__(16) _Float16 lds_k[2][kGroup * DP];
+  __shared__ __align__(16) _Float16 lds_v[2][DP * kGroup];
+  __shared__ __align__(16) float lds_s[2][3][4];  // of each 16 positions: k scale, log2 v scale, 1 / v scale
+
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Place at = place_of(p, p.splits);
+  const int split = at.inner, head = at.head;
+  const Tile t = find_tile(p, at.item);
+  if (!t.live) return;
+  const int dim = p.c.dim, P = p.c.block;
+  const int begin = (t.lo & ~(kGroup - 1)) + split * p.chunk, end = min(begin + p.chunk, t.hi);
+  if (split > 0 && begin >= t.hi) return;
+
+  const Column col = column_of(p, t, head, wave * 32 + n);
+  half8_t qf[DP / 16];
+  const float unscale = load_query<DT, DP / 16, false>(p, col, [&](int i) { return 16 * i + 8 * h; }, qf);
+  const float c_col = unscale * p.scale2;
+  // positions that all of this wave's columns see, and that any of them sees
+  const int w0 = wave * 32, w1 = min(wave * 32 + 31, t.ncols - 1);
+  const bool any = w0 < t.ncols;
+  const int pos0 = t.len - t.rows + (t.col0 + w0) / p.group, pos1 = t.len - t.rows + (t.col0 + max(w1, 0)) / p.group;
+  const int all_hi = min(pos0 + 1, t.len), any_hi = any ? min(pos1 + 1, t.len) : 0;
+  const int all_lo = p.a.window > 0 ? max(pos1 - p.a.window + 1, 0) : 0;
+  const int any_lo = p.a.window > 0 ? max(pos0 - p.a.window + 1, 0) : 0;
+
+  float16_t o[ND];
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v = __builtin_fmaf(lds_o[w][k][d], f[w], v);
-      if (last)
-        static_cast<uint16_t*>(p.a.out)[out_at * dim + d] = narrow<DT>(v * inv);
-      else
-        p.part_o[(slot + k) * dim + d] = v;
+  for (int i = 0; i < ND; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+  float m = kNone, l = 0.0f;
+
+  const int64_t head_bytes = static_cast<int64_t>(P) * dim;
+  const int* const table = p.c.table + t.seq * p.c.ldt;
+  const int piece_lo = t.lo & ~15, piece_hi = (t.hi - 1) & ~15;
+  auto piece = [&](int pos) { return min(max(pos, piece_lo), piece_hi); };
+  auto in_pool = [&](int b) { return static_cast<unsigned>(b) < static_cast<unsigned>(p.c.blocks); };
+
+  // What this thread brings of a step.  K: piece kd of rows krow(i); V: 16
+  // positions (the vs-th of four) of rows vrow(i).
+  const int kd = tid % RB, v4 = tid & 3;
+  auto krow = [&](int i) { return tid / RB + i * (64 * kWaves / RB); };
+  auto vrow = [&](int i) { return (tid >> 2) + i * (16 * kWaves); };
+  uint4 kr[NC], vr[NC];
+  float sk = 0.0f, sv = 0.0f;
+  int kb[NC], vb = 0;  // block numbers of the step to load
+  auto load_blocks = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) kb[i] = table[piece(t0 + (krow(i) & ~15)) >> p.block_shift];
+    vb = table[piece(t0 + 16 * v4) >> p.block_shift];
+  };
+  auto load_step = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int r = krow(i), pos = piece(t0 + (r & ~15)) + (r & 15);
+      const int64_t tile = static_cast<int64_t>(in_pool(kb[i]) ? kb[i] : 0) * p.c.heads + head;
+      kr[i] = make_uint4(0, 0, 0, 0);
+      if (16 * kd < dim)
+        kr[i] = *reinterpret_cast<const uint4*>(p.c.k + tile * head_bytes + (pos & (P - 1)) * dim + 16 * kd);
     }
-    if (lane == 0) {
-      if (!last) {
-        p.part_ml[(slot + k) * 2] = mm;
-        p.part_ml[(slot + k) * 2 + 1] = ll;
-      } else if (p.a.lse) {
-        p.a.lse[out_at] = ll != 0.0f ? (mm - kLift + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f : -__builtin_inff();
+    const int vp = piece(t0 + 16 * v4);
+    const int64_t tile = static_cast<int64_t>(in_pool(vb) ? vb : 0) * p.c.heads + head;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      vr[i] = make_uint4(0, 0, 0, 0);
+      if (vrow(i) < dim) {
+        vr[i] = *reinterpret_cast<const uint4*>(p.c.v + tile * head_bytes + vrow(i) * P + (vp & (P - 1)));
+        if (FP8 && t0 + kGroup > t.len) keep_first(vr[i], t.len - vp);
       }
     }
+    if (tid < 4) {
+      sk = p.c.k_scale[tile];
+      sv = p.c.v_scale[tile];
+      if (!in_pool(vb)) sk = sv = __builtin_nanf("");
+    }
+  };
+  auto put_step = [&](int buf) {
+    half8_t* const kl = reinterpret_cast<half8_t*>(lds_k[buf]);
+    half8_t* const vl = reinterpret_cast<half8_t*>(lds_v[buf]);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      // position 32 a + 16 b + 8 c + 4 d + e lies in row 32 a + 16 b + 8 d + 4 c + e
+      const int r = krow(i), row = (r & ~12) | ((r & 8) >> 1) | ((r & 4) << 1);
+      const int key = row & 7;
+      kl[row * KP + ((2 * kd) ^ key)] = kv::codes8_to_half<FP8>(kr[i].x, kr[i].y);
+      kl[row * KP + ((2 * kd + 1) ^ key)] = kv::codes8_to_half<FP8>(kr[i].z, kr[i].w);
+      const int d = vrow(i);
+      vl[d * 8 + ((2 * v4) ^ (d & 7))] = kv::codes8_to_half<FP8>(vr[i].x, vr[i].y);
+      vl[d * 8 + ((2 * v4 + 1) ^ (d & 7))] = kv::codes8_to_half<FP8>(vr[i].z, vr[i].w);
+    }
+    if (tid < 4) {
+      lds_s[buf][0][tid] = sk;
+      lds_s[buf][1][tid] = __builtin_amdgcn_logf(sv);
+      lds_s[buf][2][tid] = 1.0f / sv;
+    }
+  };
+
+  if (begin < end) {
+    load_blocks(begin);
+    load_step(begin);
+    if (begin + kGroup < end) load_blocks(begin + kGroup);
+    put_step(0);
   }
+  __syncthreads();
+  int buf = 0;
+  for (int t0 = begin; t0 < end; t0 += kGroup, buf ^= 1) {
+    const bool more = t0 + kGroup < end;
+    if (more) {
+      load_step(t0 + kGroup);
+      if (t0 + 2 * kGroup < end) load_blocks(t0 + 2 * kGroup);
+    }
+    if (t0 < any_hi && t0 + kGroup > any_lo) {
+      const half8_t* const kl = reinterpret_cast<const half8_t*>(lds_k[buf]);
+      const half8_t* const vl = reinterpret_cast<const half8_t*>(lds_v[buf]);
+      float16_t s[2];
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[a][e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+          s[a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[(32 * a + n) * KP + ((2 * i + h) ^ (n & 7))], qf[i], s[a], 0, 0, 0);
+      }
+      // register 8 b + e of s[a] is position 32 a + 16 b + 8 h + e
+      float top = kNone;
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float c = c_col * lds_s[buf][0][2 * a + b], lvs = lds_s[buf][1][2 * a + b];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[a][8 * b + e] = __builtin_fmaf(s[a][8 * b + e], c, lvs);
+        }
+      if (t0 + kGroup > all_hi || t0 < all_lo) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int spot = t0 + 32 * a + 16 * (e >> 3) + 8 * h + (e & 7);
+            s[a][e] = spot >= col.see_lo && spot < col.see_hi ? s[a][e] : -__builtin_inff();
+          }
+      }
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, s[a][e]);
+      const float m_new = __builtin_fmaxf(m, column_max<false>(top));
+      if (__any(m_new != m)) {
+        const float shrink = __builtin_amdgcn_exp2f(m - m_new);
+        m = m_new;
+        l *= shrink;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) o[i] *= shrink;
+      }
+      half8_t pf[4];
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float pr = __builtin_amdgcn_exp2f(s[a][8 * b + e] - (m - kLift));
+            sum += pr;
+            pf[2 * a + b][e] = static_cast<_Float16>(pr);
+          }
+          // a lane that sees none of these positions must not meet their scale
+          l += sum != 0.0f ? sum * lds_s[buf][2][2 * a + b] : 0.0f;
+        }
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int s4 = 0; s4 < 4; ++s4)
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[(32 * i + n) * 8 + ((2 * s4 + h) ^ (n & 7))], pf[s4], o[i], 0, 0, 0);
+    }
+    if (more) put_step(buf ^ 1);
+    __syncthreads();
+  }
+
+  if (!col.valid) return;
+  l = column_sum<false>(l);
+  // register 4 q + e of o[i] is element 32 i + 8 q + 4 h + e
+  if (t.splits <= 1) {
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int d = 32 * i + 8 * q + 4 * h;
+        if (d < dim)
+          *reinterpret_cast<kv::Raw8<2>*>(static_cast<char*>(p.a.out) + (col.out_row * dim + d) * 2) =
+              kv::Raw8<2>{{qm::pack2_narrow<DT>(o[i][4 * q] * inv, o[i][4 * q + 1] * inv),
+                           qm::pack2_narrow<DT>(o[i][4 * q + 2] * inv, o[i][4 * q + 3] * inv)}};
+      }
+    if (h == 0 && p.a.lse) p.a.lse[col.out_row] = lse_of(m, l);
+    return;
+  }
+  const int64_t part = ((static_cast<int64_t>(at.item) * p.c.heads + head) * p.splits + split) * p.cols + wave * 32 + n;
+#pragma unroll
+  for (int i = 0; i < ND; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int d = 32 * i + 8 * q + 4 * h;
+      if (d < dim)
+        *reinterpret_cast<float4_t*>(p.part_o + part * dim + d) =
+            float4_t{o[i][4 * q], o[i][4 * q + 1], o[i][4 * q + 2], o[i][4 * q + 3]};
+    }
+  if (h == 0) *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(m, l);
 }
 
-// Joins the chunks of a tile: one wave per column.
-template <int DT, int DP>
-__global__ __launch_bounds__(64) void kv_attention_join_kernel(Params p) {
-  const Place at = place_of(p, p.cols);
-  const int k = at.inner, head = at.head;
-  const int64_t item = at.item;
-  const Tile t = find_tile(p, item);
-  if (!t.live || t.splits <= 1 || k >= t.ncols) return;
-  const int lane = threadIdx.x, dim = p.c.dim;
-  const int64_t slot = (item * p.c.heads + head) * p.splits;
-  const int splits = min(t.splits, p.splits);
-  float m = kNone;
-  for (int s = lane; s < splits; s += 64) m = __builtin_fmaxf(m, p.part_ml[((slot + s) * p.cols + k) * 2]);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
-  float l = 0.0f, v[DP / 64];
-#pragma unroll
-  for (int i = 0; i < DP / 64; ++i) v[i] = 0.0f;
-  for (int s = 0; s < splits; ++s) {
-    const int64_t part = (slot + s) * p.cols + k;
-    const float f = __builtin_amdgcn_exp2f(p.part_ml[part * 2] - m);
-    l = __builtin_fmaf(p.part_ml[part * 2 + 1], f, l);
-#pragma unroll
-    for (int i = 0; i < DP / 64; ++i)
-      if (lane + 64 * i < dim) v[i] = __builtin_fmaf(p.part_o[part * dim + lane + 64 * i], f, v[i]);
-  }
-  const int kc = t.col0 + k, kr = kc / p.group, kh = head * p.group + kc - kr * p.group;
-  const int64_t out_at = (t.row0 + kr) * p.a.heads + kh;
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-  for (int i = 0; i < DP / 64; ++i)
-    if (lane + 64 * i < dim) static_cast<uint16_t*>(p.a.out)[out_at * dim + lane + 64 * i] = narrow<DT>(v[i] * inv);
-  if (lane == 0 && p.a.lse)
-    p.a.lse[out_at] = l != 0.0f ? (m - kLift + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -__builtin_inff();
+// Joins the chunks of tiles of 128 columns, 8 columns per workgroup.
+template <int DT>
+__global__ __launch_bounds__(256) void kv_attention_join_kernel(Params p) {
+  const Place at = place_of(p, kTileCols / 8);
+  const Tile t = find_tile(p, at.item);
+  const int first = at.inner * 8;
+  if (!t.live || t.splits <= 1 || first >= t.ncols) return;
+  const int64_t slot = (static_cast<int64_t>(at.item) * p.c.heads + at.head) * p.splits * p.cols;
+  join_chunks<DT>(p, t, at.head, slot, t.splits, first, min(8, t.ncols - first), threadIdx.x, 256);
 }
 
-// How a call is cut: tiles, chunks of positions, workspace.
-struct Plan {
-  int64_t items;
-  int chunk, splits, cols;
-  size_t bytes;
+// How a call is cut: which kernels run, their tiles and chunks of positions.
+struct Cut {
+  int64_t items;  // 0: the kernel is not needed
+  int tiles, chunk, splits, cols;
+  size_t bytes;   // of partial results
 };
 
-Plan plan_of(int seqs, int tokens, int heads, int kv_heads, int dim, bool ragged, int max_kv, int window) {
-  Plan pl{};
-  const int group = heads / kv_heads;
-  pl.items = ragged ? kv::item_base(tokens, group, kCols, 1, seqs)
-                    : static_cast<int64_t>(seqs) * ((group + kCols - 1) / kCols);
+Cut chunked(int64_t items, int tiles, int kv_heads, int dim, int cols, int max_kv, int window, int rows, int wanted,
+            int least, int most) {
+  Cut c{items, tiles, 0, 0, cols, 0};
+  if (items == 0) return c;
   // positions that one tile can see, from a multiple of 64 on
   int64_t range = max_kv;
-  if (window > 0) range = std::min<int64_t>(range, static_cast<int64_t>(window) + kCols);
-  range += kGroup;
-  const int64_t tiles = std::max<int64_t>(1, pl.items * kv_heads);
-  // about 1024 workgroups (four per CU), chunks of 256 positions at least
-  int64_t chunk = (range * tiles + 1023) / 1024;
-  chunk = std::max<int64_t>(256, (chunk + 255) / 256 * 256);
-  chunk = std::min<int64_t>(chunk, (range + 255) / 256 * 256);
-  pl.chunk = static_cast<int>(std::min<int64_t>(chunk, 1 << 30));
-  pl.splits = static_cast<int>((range + pl.chunk - 1) / pl.chunk);
-  pl.cols = ragged ? kCols : std::min(group, kCols);
-  if (pl.splits > 1)
-    pl.bytes = static_cast<size_t>(pl.items) * kv_heads * pl.splits * pl.cols * (dim + 2) * sizeof(float);
-  return pl;
+  if (window > 0) range = std::min<int64_t>(range, static_cast<int64_t>(window) + rows);
+  range = (range + 2 * kGroup - 1) / kGroup * kGroup;
+  const int64_t all = items * kv_heads;
+  int64_t chunk = (range * all + wanted - 1) / wanted;
+  chunk = std::min<int64_t>(std::max<int64_t>((chunk + least - 1) / least * least, least), most);
+  if (chunk > range || all > kCounters) chunk = range;
+  c.chunk = static_cast<int>(std::min<int64_t>(chunk, 1 << 30));
+  c.splits = static_cast<int>((range + c.chunk - 1) / c.chunk);
+  if (c.splits > 1) c.bytes = static_cast<size_t>(all) * c.splits * cols * (dim + 2) * sizeof(float);
+  return c;
+}
+
+// Tiles of 16 columns, for sequences of at most kSmall columns.
+Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window) {
+  const int64_t most = ragged ? std::min<int64_t>(static_cast<int64_t>(max_q) * group, kSmall) : group;
+  if (ragged && group > kSmall) return Cut{};  // every sequence is the other kernel's
+  const int tiles = static_cast<int>((most + kCols - 1) / kCols);
+  return chunked(static_cast<int64_t>(seqs) * tiles, tiles, kv_heads, dim, static_cast<int>(std::min<int64_t>(most, kCols)),
+                 max_kv, window, kCols, 2048, 256, 1024);
+}
+
+// Tiles of 128 columns, for the others.
+Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window) {
+  if (!ragged || static_cast<int64_t>(max_q) * group <= kSmall) return Cut{};
+  return chunked(kv::item_base(tokens, group, kTileCols, 1, seqs), 1, kv_heads, dim, kTileCols, max_kv, window, kTileCols,
+                 512, 512, 1 << 30);
 }
 
 template <int DT, bool FP8, int DP>
-hipError_t go(const Params& p, int64_t items, hipStream_t stream) {
-  const int64_t tiles = items * p.c.heads;
-  if (tiles * std::max(p.splits, p.cols) > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const dim3 grid(static_cast<unsigned>(tiles * p.splits));
-  hipError_t e = launch(kv_attention_cols_kernel<DT, FP8, DP>, grid, dim3(64 * kWaves), 0, stream, p);
-  if (e != hipSuccess || p.splits <= 1) return e;
-  return launch(kv_attention_join_kernel<DT, DP>, dim3(static_cast<unsigned>(tiles * p.cols)), dim3(64), 0, stream, p);
+hipError_t go(const Params& base, const Cut& cc, const Cut& ct, hipStream_t stream) {
+  if (cc.items) {
+    Params p = base;
+    p.tiles = cc.tiles;
+    p.chunk = cc.chunk;
+    p.splits = cc.splits;
+    p.cols = cc.cols;
+    const int64_t all = cc.items * p.c.heads;
+    p.part_ml = p.part_o + all * cc.splits * cc.cols * p.c.dim;
+    const hipError_t e = launch(kv_attention_cols_kernel<DT, FP8, DP>, dim3(static_cast<unsigned>(all * cc.splits)),
+                                dim3(64 * kWaves), 0, stream, p);
+    if (e != hipSuccess) return e;
+  }
+  if (ct.items) {
+    Params p = base;
+    p.chunk = ct.chunk;
+    p.splits = ct.splits;
+    p.cols = ct.cols;
+    p.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(base.part_o) + (cc.bytes + 255) / 256 * 256);
+    const int64_t all = ct.items * p.c.heads;
+    p.part_ml = p.part_o + all * ct.splits * ct.cols * p.c.dim;
+    hipError_t e = launch(kv_attention_tile_kernel<DT, FP8, DP>, dim3(static_cast<unsigned>(all * ct.splits)),
+                          dim3(64 * kWaves), 0, stream, p);
+    if (e != hipSuccess || ct.splits <= 1) return e;
+    return launch(kv_attention_join_kernel<DT>, dim3(static_cast<unsigned>(all * (kTileCols / 8))), dim3(256), 0, stream, p);
+  }
+  return hipSuccess;
 }
 
 template <int DT, bool FP8>
-hipError_t by_dim(const Params& p, int64_t items, hipStream_t stream) {
-  if (p.c.dim <= 64) return go<DT, FP8, 64>(p, items, stream);
-  if (p.c.dim <= 128) return go<DT, FP8, 128>(p, items, stream);
-  return go<DT, FP8, 256>(p, items, stream);
+hipError_t by_dim(const Params& p, const Cut& cc, const Cut& ct, hipStream_t stream) {
+  if (p.c.dim <= 64) return go<DT, FP8, 64>(p, cc, ct, stream);
+  if (p.c.dim <= 128) return go<DT, FP8, 128>(p, cc, ct, stream);
+  return go<DT, FP8, 256>(p, cc, ct, stream);
+}
+
+size_t bytes_of(const Cut& cc, const Cut& ct) {
+  if (cc.bytes == 0 && ct.bytes == 0) return 0;
+  return kCounters * sizeof(unsigned) + (cc.bytes + 255) / 256 * 256 + ct.bytes;
 }
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_kv,
-                                    int window) {
-  // enough for either form of the call
-  return std::max(plan_of(seqs, tokens, heads, kv_heads, dim, true, max_kv, window).bytes,
-                  plan_of(seqs, tokens, heads, kv_heads, dim, false, max_kv, window).bytes);
+size_t kv_attention_workspace_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, bool ragged, int max_q,
+                                    int max_kv, int window) {
+  const int group = heads / kv_heads;
+  return bytes_of(cut_cols(seqs, group, kv_heads, dim, ragged, max_q, max_kv, window),
+                  cut_tile(seqs, tokens, group, kv_heads, dim, ragged, max_q, max_kv, window));
 }
 
 hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, hipStream_t stream) {
-  const Plan pl = plan_of(a.seqs, a.tokens, a.heads, c.heads, c.dim, a.cu != nullptr, a.max_kv, a.window);
-  Params p{c, a, a.heads / c.heads, pl.chunk, pl.splits, pl.cols, a.scale * 1.4426950408889634f, nullptr, nullptr};
-  p.part_o = static_cast<float*>(a.workspace);
-  p.part_ml = p.part_o + static_cast<size_t>(pl.items) * c.heads * pl.splits * pl.cols * c.dim;
-  if (a.dtype == QK_BF16)
-    return c.fp8 ? by_dim<QK_BF16, true>(p, pl.items, stream) : by_dim<QK_BF16, false>(p, pl.items, stream);
-  return c.fp8 ? by_dim<QK_F16, true>(p, pl.items, stream) : by_dim<QK_F16, false>(p, pl.items, stream);
+  const int group = a.heads / c.heads;
+  const bool ragged = a.cu != nullptr;
+  const Cut cc = cut_cols(a.seqs, group, c.heads, c.dim, ragged, a.max_q, a.max_kv, a.window);
+  const Cut ct = cut_tile(a.seqs, a.tokens, group, c.heads, c.dim, ragged, a.max_q, a.max_kv, a.window);
+  const int64_t limit = 0x7fffffff;
+  if (cc.items * c.heads * std::max(cc.splits, 1) > limit ||
+      ct.items * c.heads * std::max(ct.splits, kTileCols / 8) > limit)
+    return hipErrorInvalidConfiguration;
+  Params p{};
+  p.c = c;
+  p.a = a;
+  while (1 << p.block_shift < c.block) ++p.block_shift;
+  p.group = group;
+  p.scale2 = a.scale * 1.4426950408889634f;
+  p.arrived = static_cast<unsigned*>(a.workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounters * sizeof(unsigned));
+  if (a.dtype == QK_BF16) return c.fp8 ? by_dim<QK_BF16, true>(p, cc, ct, stream) : by_dim<QK_BF16, false>(p, cc, ct, stream);
+  return c.fp8 ? by_dim<QK_F16, true>(p, cc, ct, stream) : by_dim<QK_F16, false>(p, cc, ct, stream);
 }
 
 }  // namespace qk

@@ -220,8 +220,8 @@ struct KvAttentionArgs {
   void* workspace;
   size_t workspace_bytes;
 };
-size_t kv_attention_workspace_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_kv,
-                                    int window);
+size_t kv_attention_workspace_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, bool ragged, int max_q,
+                                    int max_kv, int window);
 hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, hipStream_t stream);
 
 }  // namespace qk
