@@ -24,6 +24,7 @@
 // p / v_scale in binary32 from the unrounded p.  Rounding p to 11 bits is the
 // only rounding below binary32 before the output's.
 #include <algorithm>
+#include <cmath>
 
 #include "kv_common.h"
 
@@ -43,6 +44,7 @@ constexpr int kGroup = 64;       // positions taken at a time
 constexpr int kWaves = 4;
 constexpr float kNone = -3.0e38f;  // a maximum over nothing
 constexpr float kLift = 14.0f;
+constexpr int kJoinHere = 16;      // most chunks that a tile's last workgroup joins
 constexpr int kCounters = 16384;   // arrival counters at the front of the workspace
 
 struct Params {
@@ -51,10 +53,14 @@ struct Params {
   int block_shift;  // log2 of the cache's block
   int group;        // heads per kv head
   int tiles;        // cols kernel: tiles per sequence
+  unsigned items;
+  int small;        // tile kernel: columns of a sequence that the other kernel takes
   int chunk;        // positions per workgroup
   int splits;       // chunks of the longest range
   int cols;         // columns that the workspace holds per tile
-  float scale2;     // scale * log2(e)
+  float scale2;     // |scale| * log2(e)
+  uint32_t flip;    // sign bits that turn q where the scale is negative
+  bool join_later;  // cols kernel: the chunks are joined by a launch of their own
   unsigned* arrived;  // [item][kv head], zero between calls (cols kernel)
   float* part_o;      // [item][kv head][split][cols][dim]
   float* part_ml;     // [item][kv head][split][cols][2]
@@ -112,7 +118,7 @@ __device__ __forceinline__ Tile find_cols(const Params& p, unsigned item) {
 __device__ __forceinline__ Tile find_tile(const Params& p, int64_t item) {
   Tile t{};
   t.seq = kv::find_sequence(item, p.a.cu, p.a.seqs, p.group, kTileCols, 1);
-  if (t.seq < 0 || !set_rows(p, t) || static_cast<int64_t>(t.rows) * p.group <= kSmall) return t;
+  if (t.seq < 0 || !set_rows(p, t) || static_cast<int64_t>(t.rows) * p.group <= p.small) return t;
   set_range(p, t, (item - kv::item_base(t.row0, p.group, kTileCols, 1, t.seq)) * kTileCols, kTileCols);
   return t;
 }
@@ -189,7 +195,7 @@ __device__ __forceinline__ float load_query(const Params& p, const Column& c, At
       w = *reinterpret_cast<const Raw16<2>*>(static_cast<const char*>(p.a.q) + (c.q_at + d) * 2);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      raw[i][e] = w.w[e];
+      raw[i][e] = w.w[e] ^ p.flip;
       top = qm::max_u32(top, qm::max_u32(w.w[e] & 0x7fffu, (w.w[e] >> 16) & 0x7fffu));
     }
   }
@@ -242,15 +248,50 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l != 0.0f ? (m - kLift + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -__builtin_inff();
 }
 
-// Joins a tile's chunks in order: threads of one workgroup (`threads` of them,
-// a multiple of 64, this one being `tid`) over (column, pair of elements).
+// One step of the running softmax over a lane's scores of one column: N
+// pieces of E raw scores s, whose exponents are y = s c + b with c >= 0 and
+// b = log2 v_scale per piece.  Leaves p = 2^(y - m + 14) in s and returns the
+// factor by which what was summed before shrinks.  The maximum is taken of the
+// raw scores and the product with c merged into the exponent: one fused
+// multiply-add, one max, one exponential and one addition per score.
+template <int N, int E, bool FOUR>
+__device__ __forceinline__ float softmax_step(float (&s)[N][E], const float (&c)[N], const float (&b)[N],
+                                              const float (&inv_vs)[N], float& m, float& l) {
+  float top = kNone;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float t = s[i][0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) t = __builtin_fmaxf(t, s[i][e]);
+    top = __builtin_fmaxf(top, __builtin_fmaf(t, c[i], b[i]));
+  }
+  const float m_new = __builtin_fmaxf(m, column_max<FOUR>(top));
+  const float shrink = __builtin_amdgcn_exp2f(m - m_new);
+  m = m_new;
+  l *= shrink;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float off = b[i] - (m_new - kLift);
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      s[i][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][e], c[i], off));
+      sum += s[i][e];
+    }
+    l = __builtin_fmaf(sum, inv_vs[i], l);
+  }
+  return shrink;
+}
+
+// Joins a tile's chunks in order, by the workgroup that arrived last: threads
+// over (column, pair of elements).
 template <int DT>
-__device__ __forceinline__ void join_chunks(const Params& p, const Tile& t, int head, int64_t slot, int splits,
-                                            int first, int ncols, int tid, int threads) {
+__device__ __forceinline__ void join_chunks(const Params& p, const Tile& t, int head, int64_t slot) {
   constexpr int kAhead = 8;  // chunks whose loads are in flight together
   const int pairs = p.c.dim >> 1;
-  for (int i = tid; i < ncols * pairs; i += threads) {
-    const int k = first + i / pairs, d = 2 * (i % pairs);
+  const int splits = t.splits;
+  for (int i = threadIdx.x; i < t.ncols * pairs; i += 64 * kWaves) {
+    const int k = i / pairs, d = 2 * (i - k * pairs);
     float m = kNone, l = 0.0f, a = 0.0f, b = 0.0f;
     for (int s0 = 0; s0 < splits; s0 += kAhead) {
       float2 ml[kAhead], o[kAhead];
@@ -288,7 +329,7 @@ __device__ __forceinline__ void join_chunks(const Params& p, const Tile& t, int 
 // 128) on its way.  The workgroup that arrives last at a tile joins its
 // chunks.
 template <int DT, bool FP8, int DP>
-__global__ __launch_bounds__(64 * kWaves) void kv_attention_cols_kernel(Params p) {
+__global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : DP > 64 ? 3 : 4) void kv_attention_cols_kernel(Params p) {
   constexpr int KC = DP / 64;  // 16-byte pieces of a K row per lane
   constexpr int VC = DP / 16;  // 16-row pieces of V
   __shared__ float lds_o[kWaves][kCols][DP + 4];
@@ -320,19 +361,20 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_cols_kernel(Params p
 
   const int64_t head_bytes = static_cast<int64_t>(P) * dim;
   const int* const table = p.c.table + t.seq * p.c.ldt;
-  // 16 positions from `pos` on, held to the range of positions that are seen
-  // (every table entry that is read is a real one); a block number outside
-  // the cache reads block 0 and gives NaN scales
-  const int piece_lo = t.lo & ~15, piece_hi = (t.hi - 1) & ~15;
-  auto piece = [&](int pos) { return min(max(pos, piece_lo), piece_hi); };
+  // Table entries are read at any position that the table has, whether seen or
+  // not, so that they need not wait for the lengths; a block number outside
+  // the cache reads block 0.  Where such a position is seen its scales are
+  // NaN; elsewhere scores are masked, and bytes of V that may be NaN codes
+  // become zeros.
+  auto entry = [&](int pos) { return table[min(pos >> p.block_shift, p.c.width - 1)]; };
   auto in_pool = [&](int b) { return static_cast<unsigned>(b) < static_cast<unsigned>(p.c.blocks); };
 
   uint4 kr[4][KC], vr[VC];
   float ks, vs;
   // K: the lane's row n of tile i is position t0 + 16 (n / 4) + 4 i + n % 4
-  auto load_k = [&](int kp, int kb) {
+  auto load_k = [&](int t0, int kb) {
     const int64_t tile = static_cast<int64_t>(in_pool(kb) ? kb : 0) * p.c.heads + head;
-    const uint8_t* const row = p.c.k + tile * head_bytes + ((kp & (P - 1)) + (n & 3)) * dim + 16 * g;
+    const uint8_t* const row = p.c.k + tile * head_bytes + (((t0 + 16 * (n >> 2)) & (P - 1)) + (n & 3)) * dim + 16 * g;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -343,9 +385,9 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_cols_kernel(Params p
           kr[i][c] = make_uint4(0, 0, 0, 0);
       }
   };
-  auto load_v = [&](int vp, int vb) {
+  auto load_v = [&](int t0, int vb) {
     const int64_t tile = static_cast<int64_t>(in_pool(vb) ? vb : 0) * p.c.heads + head;
-    const uint8_t* row = p.c.v + tile * head_bytes + n * P + (vp & (P - 1));
+    const uint8_t* const row = p.c.v + tile * head_bytes + n * P + ((t0 + 16 * g) & (P - 1));
 #pragma unroll
     for (int i = 0; i < VC; ++i) {
       if (16 * i < dim)
@@ -359,80 +401,69 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_cols_kernel(Params p
   };
 
   constexpr int kStep = kWaves * kGroup;
-  int t0 = begin + wave * kGroup;
-  if (t0 < end) {
-    int kp = piece(t0 + 16 * (n >> 2)), vp = piece(t0 + 16 * g);
-    load_k(kp, table[kp >> p.block_shift]);
-    load_v(vp, table[vp >> p.block_shift]);
-    int kp1 = piece(t0 + kStep + 16 * (n >> 2)), vp1 = piece(t0 + kStep + 16 * g);
-    int kb1 = table[kp1 >> p.block_shift], vb1 = table[vp1 >> p.block_shift];
-    for (; t0 < end; t0 += kStep) {
-      const bool more = t0 + kStep < end;
-      float4_t s[4];
+  int kb1 = 0, vb1 = 0;  // block numbers of the next group
+  auto next_blocks = [&](int t0) {
+    kb1 = entry(t0 + 16 * (n >> 2));
+    vb1 = entry(t0 + 16 * g);
+  };
+  // the group at t0, whose K and V are in registers or on their way; `more`:
+  // ask for the next group's
+  auto group = [&](int t0, auto more) {
+    float4_t acc[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[i] = float4_t{0, 0, 0, 0};
+    for (int i = 0; i < 4; ++i) {
+      acc[i] = float4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          s[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[i][c].x, kr[i][c].y), qf[2 * c], s[i], 0, 0, 0);
-          s[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[i][c].z, kr[i][c].w), qf[2 * c + 1], s[i], 0, 0, 0);
-        }
-      }
-      if (more) load_k(kp1, kb1);
-      const float c = c_col * ks, lvs = __builtin_amdgcn_logf(vs), inv_vs = 1.0f / vs;
-      const bool edge = t0 < t.lo || t0 + kGroup > t.len - t.rows;  // some column may not see all 64
-      float top = kNone;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = __builtin_fmaf(s[i][e], c, lvs);
-      if (edge || p.a.window > 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int spot = t0 + 16 * g + 4 * i + e;
-            s[i][e] = spot >= col.see_lo && spot < col.see_hi ? s[i][e] : -__builtin_inff();
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = __builtin_fmaxf(top, s[i][e]);
-      const float m_new = __builtin_fmaxf(m, column_max<true>(top));
-      const float shrink = __builtin_amdgcn_exp2f(m - m_new);
-      m = m_new;
-      float sum = 0.0f;
-      half8_t pf[2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float pr = __builtin_amdgcn_exp2f(s[i][e] - (m - kLift));
-          sum += pr;
-          pf[i >> 1][4 * (i & 1) + e] = static_cast<_Float16>(pr);
-        }
-      // a lane that sees none of these positions must not meet their scale
-      l = __builtin_fmaf(l, shrink, sum != 0.0f ? sum * inv_vs : 0.0f);
-      if (FP8 && t0 + kGroup > t.len) {
-#pragma unroll
-        for (int i = 0; i < VC; ++i) keep_first(vr[i], t.len - vp);
-      }
-#pragma unroll
-      for (int i = 0; i < VC; ++i) {
-        o[i] *= shrink;
-        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[i].x, vr[i].y), pf[0], o[i], 0, 0, 0);
-        o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[i].z, vr[i].w), pf[1], o[i], 0, 0, 0);
-      }
-      if (more) {
-        load_v(vp1, vb1);
-        vp = vp1;
-        kp1 = piece(t0 + 2 * kStep + 16 * (n >> 2));
-        vp1 = piece(t0 + 2 * kStep + 16 * g);
-        kb1 = table[kp1 >> p.block_shift];
-        vb1 = table[vp1 >> p.block_shift];
+      for (int c = 0; c < KC; ++c) {
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[i][c].x, kr[i][c].y), qf[2 * c], acc[i], 0, 0, 0);
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[i][c].z, kr[i][c].w), qf[2 * c + 1], acc[i], 0, 0, 0);
       }
     }
+    if constexpr (decltype(more)::value) load_k(t0 + kStep, kb1);
+    float s[1][16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[0][i] = acc[i >> 2][i & 3];
+    float c[1] = {c_col * ks}, bias[1] = {__builtin_amdgcn_logf(vs)}, inv_vs[1] = {__builtin_amdgcn_rcpf(vs)};
+    if (t0 < t.lo || t0 + kGroup > t.len - t.rows || p.a.window > 0) {  // some column may not see all 64
+      const int at = t0 + 16 * g;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool seen = at + i >= col.see_lo && at + i < col.see_hi;
+        s[0][i] = seen ? __builtin_fmaf(s[0][i], c[0], bias[0]) : -__builtin_inff();
+      }
+      c[0] = 1.0f;
+      bias[0] = 0.0f;
+      // a lane that sees none of these positions must not meet their scale
+      if (at + 16 <= col.see_lo || at >= col.see_hi) inv_vs[0] = 0.0f;
+    }
+    const float shrink = softmax_step<1, 16, true>(s, c, bias, inv_vs, m, l);
+    half8_t pf[2];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) pf[i >> 3][i & 7] = static_cast<_Float16>(s[0][i]);
+    if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) {
+      const int have = t0 + 16 * g + 16 > t.lo ? t.len - (t0 + 16 * g) : 0;
+#pragma unroll
+      for (int i = 0; i < VC; ++i) keep_first(vr[i], have);
+    }
+#pragma unroll
+    for (int i = 0; i < VC; ++i) {
+      o[i] *= shrink;
+      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[i].x, vr[i].y), pf[0], o[i], 0, 0, 0);
+      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[i].z, vr[i].w), pf[1], o[i], 0, 0, 0);
+    }
+    if constexpr (decltype(more)::value) {
+      load_v(t0 + kStep, vb1);
+      next_blocks(t0 + 2 * kStep);
+    }
+  };
+  int t0 = begin + wave * kGroup;
+  if (t0 < end) {
+    next_blocks(t0);
+    load_k(t0, kb1);
+    load_v(t0, vb1);
+    next_blocks(t0 + kStep);
+    for (; t0 + kStep < end; t0 += kStep) group(t0, std::true_type{});
+    group(t0, std::false_type{});
   }
 
   // join the four waves
@@ -474,7 +505,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_cols_kernel(Params p
       if (d == 0) put2(p.part_ml + part * 2, mm, ll);
     }
   }
-  if (whole) return;
+  if (whole || p.join_later) return;
 
   // every wave's stores are done before the workgroup counts as arrived
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -486,7 +517,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_cols_kernel(Params p
     lds_last = last;
   }
   __syncthreads();
-  if (lds_last) join_chunks<DT>(p, t, head, slot, t.splits, 0, t.ncols, threadIdx.x, 64 * kWaves);
+  if (lds_last) join_chunks<DT>(p, t, head, slot);
 }
 
 // One workgroup: one tile of 128 columns, one kv head, one chunk of positions
@@ -510,7 +541,8 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
 
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Place at = place_of(p, p.splits);
+  Place at = place_of(p, p.splits);
+  at.item = p.items - 1 - at.item;  // later rows see more: the longest work first
   const int split = at.inner, head = at.head;
   const Tile t = find_tile(p, at.item);
   if (!t.live) return;
@@ -539,47 +571,45 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
 
   const int64_t head_bytes = static_cast<int64_t>(P) * dim;
   const int* const table = p.c.table + t.seq * p.c.ldt;
-  const int piece_lo = t.lo & ~15, piece_hi = (t.hi - 1) & ~15;
-  auto piece = [&](int pos) { return min(max(pos, piece_lo), piece_hi); };
+  auto entry = [&](int pos) { return table[min(pos >> p.block_shift, p.c.width - 1)]; };  // as above
   auto in_pool = [&](int b) { return static_cast<unsigned>(b) < static_cast<unsigned>(p.c.blocks); };
 
   // What this thread brings of a step.  K: piece kd of rows krow(i); V: 16
-  // positions (the vs-th of four) of rows vrow(i).
-  const int kd = tid % RB, v4 = tid & 3;
+  // positions of rows lane + 64 i.  Either way a wave's rows lie in one piece of
+  // 16 positions, so block numbers and addresses of tiles are scalar.
+  const int kd = tid % RB;
   auto krow = [&](int i) { return tid / RB + i * (64 * kWaves / RB); };
-  auto vrow = [&](int i) { return (tid >> 2) + i * (16 * kWaves); };
+  auto kpart = [&](int i) { return __builtin_amdgcn_readfirstlane(krow(i) >> 4); };
   uint4 kr[NC], vr[NC];
   float sk = 0.0f, sv = 0.0f;
   int kb[NC], vb = 0;  // block numbers of the step to load
   auto load_blocks = [&](int t0) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) kb[i] = table[piece(t0 + (krow(i) & ~15)) >> p.block_shift];
-    vb = table[piece(t0 + 16 * v4) >> p.block_shift];
+    for (int i = 0; i < NC; ++i) kb[i] = entry(t0 + 16 * kpart(i));
+    vb = entry(t0 + 16 * wave);
   };
   auto load_step = [&](int t0) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int r = krow(i), pos = piece(t0 + (r & ~15)) + (r & 15);
+      const int pos = (t0 + 16 * kpart(i)) & (P - 1);
       const int64_t tile = static_cast<int64_t>(in_pool(kb[i]) ? kb[i] : 0) * p.c.heads + head;
+      const uint8_t* const from = p.c.k + tile * head_bytes + pos * dim;
       kr[i] = make_uint4(0, 0, 0, 0);
-      if (16 * kd < dim)
-        kr[i] = *reinterpret_cast<const uint4*>(p.c.k + tile * head_bytes + (pos & (P - 1)) * dim + 16 * kd);
+      if (16 * kd < dim) kr[i] = *reinterpret_cast<const uint4*>(from + static_cast<unsigned>((krow(i) & 15) * dim + 16 * kd));
     }
-    const int vp = piece(t0 + 16 * v4);
+    const int vp = t0 + 16 * wave;
     const int64_t tile = static_cast<int64_t>(in_pool(vb) ? vb : 0) * p.c.heads + head;
+    const uint8_t* const from = p.c.v + tile * head_bytes + (vp & (P - 1));
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       vr[i] = make_uint4(0, 0, 0, 0);
-      if (vrow(i) < dim) {
-        vr[i] = *reinterpret_cast<const uint4*>(p.c.v + tile * head_bytes + vrow(i) * P + (vp & (P - 1)));
-        if (FP8 && t0 + kGroup > t.len) keep_first(vr[i], t.len - vp);
+      if (lane + 64 * i < dim) {
+        vr[i] = *reinterpret_cast<const uint4*>(from + static_cast<unsigned>((lane + 64 * i) * P));
+        if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) keep_first(vr[i], vp + 16 > t.lo ? t.len - vp : 0);
       }
     }
-    if (tid < 4) {
-      sk = p.c.k_scale[tile];
-      sv = p.c.v_scale[tile];
-      if (!in_pool(vb)) sk = sv = __builtin_nanf("");
-    }
+    sk = in_pool(vb) ? p.c.k_scale[tile] : __builtin_nanf("");
+    sv = in_pool(vb) ? p.c.v_scale[tile] : __builtin_nanf("");
   };
   auto put_step = [&](int buf) {
     half8_t* const kl = reinterpret_cast<half8_t*>(lds_k[buf]);
@@ -591,14 +621,14 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
       const int key = row & 7;
       kl[row * KP + ((2 * kd) ^ key)] = kv::codes8_to_half<FP8>(kr[i].x, kr[i].y);
       kl[row * KP + ((2 * kd + 1) ^ key)] = kv::codes8_to_half<FP8>(kr[i].z, kr[i].w);
-      const int d = vrow(i);
-      vl[d * 8 + ((2 * v4) ^ (d & 7))] = kv::codes8_to_half<FP8>(vr[i].x, vr[i].y);
-      vl[d * 8 + ((2 * v4 + 1) ^ (d & 7))] = kv::codes8_to_half<FP8>(vr[i].z, vr[i].w);
+      const int d = lane + 64 * i;
+      vl[d * 8 + ((2 * wave) ^ (d & 7))] = kv::codes8_to_half<FP8>(vr[i].x, vr[i].y);
+      vl[d * 8 + ((2 * wave + 1) ^ (d & 7))] = kv::codes8_to_half<FP8>(vr[i].z, vr[i].w);
     }
-    if (tid < 4) {
-      lds_s[buf][0][tid] = sk;
-      lds_s[buf][1][tid] = __builtin_amdgcn_logf(sv);
-      lds_s[buf][2][tid] = 1.0f / sv;
+    if (lane == 0) {
+      lds_s[buf][0][wave] = sk;
+      lds_s[buf][1][wave] = __builtin_amdgcn_logf(sv);
+      lds_s[buf][2][wave] = __builtin_amdgcn_rcpf(sv);
     }
   };
 
@@ -619,61 +649,51 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
     if (t0 < any_hi && t0 + kGroup > any_lo) {
       const half8_t* const kl = reinterpret_cast<const half8_t*>(lds_k[buf]);
       const half8_t* const vl = reinterpret_cast<const half8_t*>(lds_v[buf]);
-      float16_t s[2];
+      float16_t acc[2];
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[a][e] = 0.0f;
+        for (int e = 0; e < 16; ++e) acc[a][e] = 0.0f;
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i)
-          s[a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[(32 * a + n) * KP + ((2 * i + h) ^ (n & 7))], qf[i], s[a], 0, 0, 0);
+          acc[a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[(32 * a + n) * KP + ((2 * i + h) ^ (n & 7))], qf[i], acc[a], 0, 0, 0);
       }
-      // register 8 b + e of s[a] is position 32 a + 16 b + 8 h + e
-      float top = kNone;
+      // register 8 b + e of acc[a] is position 32 a + 16 b + 8 h + e
+      float s[4][8], c[4], bias[4], inv_vs[4];
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+      for (int b = 0; b < 4; ++b) {
+        c[b] = c_col * lds_s[buf][0][b];
+        bias[b] = lds_s[buf][1][b];
+        inv_vs[b] = lds_s[buf][2][b];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const float c = c_col * lds_s[buf][0][2 * a + b], lvs = lds_s[buf][1][2 * a + b];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[a][8 * b + e] = __builtin_fmaf(s[a][8 * b + e], c, lvs);
-        }
+        for (int e = 0; e < 8; ++e) s[b][e] = acc[b >> 1][8 * (b & 1) + e];
+      }
       if (t0 + kGroup > all_hi || t0 < all_lo) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+        for (int b = 0; b < 4; ++b) {
+          const int first = t0 + 16 * b;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int spot = t0 + 32 * a + 16 * (e >> 3) + 8 * h + (e & 7);
-            s[a][e] = spot >= col.see_lo && spot < col.see_hi ? s[a][e] : -__builtin_inff();
+          for (int e = 0; e < 8; ++e) {
+            const int spot = first + 8 * h + e;
+            s[b][e] = spot >= col.see_lo && spot < col.see_hi ? __builtin_fmaf(s[b][e], c[b], bias[b]) : -__builtin_inff();
           }
+          c[b] = 1.0f;
+          bias[b] = 0.0f;
+          // a column that sees none of these positions must not meet their scale
+          if (first + 16 <= col.see_lo || first >= col.see_hi) inv_vs[b] = 0.0f;
+        }
       }
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, s[a][e]);
-      const float m_new = __builtin_fmaxf(m, column_max<false>(top));
-      if (__any(m_new != m)) {
-        const float shrink = __builtin_amdgcn_exp2f(m - m_new);
-        m = m_new;
-        l *= shrink;
+      const float m_old = m;
+      const float shrink = softmax_step<4, 8, false>(s, c, bias, inv_vs, m, l);
+      if (__any(m != m_old)) {
 #pragma unroll
         for (int i = 0; i < ND; ++i) o[i] *= shrink;
       }
       half8_t pf[4];
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+      for (int b = 0; b < 4; ++b)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float sum = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float pr = __builtin_amdgcn_exp2f(s[a][8 * b + e] - (m - kLift));
-            sum += pr;
-            pf[2 * a + b][e] = static_cast<_Float16>(pr);
-          }
-          // a lane that sees none of these positions must not meet their scale
-          l += sum != 0.0f ? sum * lds_s[buf][2][2 * a + b] : 0.0f;
-        }
+        for (int e = 0; e < 8; ++e) pf[b][e] = static_cast<_Float16>(s[b][e]);
 #pragma unroll
       for (int i = 0; i < ND; ++i)
 #pragma unroll
@@ -715,15 +735,98 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
   if (h == 0) *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(m, l);
 }
 
-// Joins the chunks of tiles of 128 columns, 8 columns per workgroup.
+// Sums chunks first .. last of one column into (m, l, v): the whole wave, four
+// elements per lane.
+__device__ __forceinline__ void sum_chunks(const Params& p, int64_t slot, int first, int last, float& m, float& l,
+                                           float4_t& v) {
+  const int lane = threadIdx.x & 63, dim = p.c.dim;
+  m = kNone;
+  l = 0.0f;
+  v = float4_t{0, 0, 0, 0};
+  constexpr int kAhead = 8;  // chunks whose loads are in flight together
+  for (int s0 = first; s0 < last; s0 += kAhead) {
+    float2 ml[kAhead];
+    float4_t o[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t part = slot + static_cast<int64_t>(min(s0 + j, last - 1)) * p.cols;
+      ml[j] = *reinterpret_cast<const float2*>(p.part_ml + part * 2);
+      o[j] = float4_t{0, 0, 0, 0};
+      if (4 * lane < dim) o[j] = *reinterpret_cast<const float4_t*>(p.part_o + part * dim + 4 * lane);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (s0 + j >= last) break;
+      const float m_new = __builtin_fmaxf(m, ml[j].x);
+      const float f0 = __builtin_amdgcn_exp2f(m - m_new), f1 = __builtin_amdgcn_exp2f(ml[j].x - m_new);
+      m = m_new;
+      l = __builtin_fmaf(l, f0, ml[j].y * f1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(v[e], f0, o[j][e] * f1);
+    }
+  }
+}
+
 template <int DT>
-__global__ __launch_bounds__(256) void kv_attention_join_kernel(Params p) {
-  const Place at = place_of(p, kTileCols / 8);
+__device__ __forceinline__ void store_row(const Params& p, int64_t out_row, float m, float l, const float4_t& v) {
+  const int lane = threadIdx.x & 63;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  if (4 * lane < p.c.dim)
+    *reinterpret_cast<kv::Raw8<2>*>(static_cast<char*>(p.a.out) + (out_row * p.c.dim + 4 * lane) * 2) =
+        kv::Raw8<2>{{qm::pack2_narrow<DT>(v[0] * inv, v[1] * inv), qm::pack2_narrow<DT>(v[2] * inv, v[3] * inv)}};
+  if (lane == 0 && p.a.lse) p.a.lse[out_row] = lse_of(m, l);
+}
+
+// Joins chunks in a launch of its own.  Many chunks of few columns: one
+// workgroup per column, its waves a quarter of the chunks each.
+template <int DT>
+__global__ __launch_bounds__(64 * kWaves) void kv_attention_join_cols_kernel(Params p) {
+  __shared__ float lds_o[kWaves][256];
+  __shared__ float lds_m[kWaves], lds_l[kWaves];
+  const Place at = place_of(p, p.cols);
+  const Tile t = find_cols(p, at.item);
+  if (!t.live || t.splits <= 1 || at.inner >= t.ncols) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t slot = (static_cast<int64_t>(at.item) * p.c.heads + at.head) * p.splits * p.cols + at.inner;
+  const int each = (t.splits + kWaves - 1) / kWaves, first = wave * each;
+  float m, l;
+  float4_t v;
+  sum_chunks(p, slot, first, min(first + each, t.splits), m, l, v);
+  if (lane == 0) {
+    lds_m[wave] = m;
+    lds_l[wave] = l;
+  }
+  *reinterpret_cast<float4_t*>(&lds_o[wave][4 * lane]) = v;
+  __syncthreads();
+  if (wave != 0) return;
+  for (int w = 1; w < kWaves; ++w) m = __builtin_fmaxf(m, lds_m[w]);
+  l = 0.0f;
+  v = float4_t{0, 0, 0, 0};
+  for (int w = 0; w < kWaves; ++w) {
+    const float f = __builtin_amdgcn_exp2f(lds_m[w] - m);
+    l = __builtin_fmaf(lds_l[w], f, l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(lds_o[w][4 * lane + e], f, v[e]);
+  }
+  store_row<DT>(p, column_of(p, t, at.head, at.inner).out_row, m, l, v);
+}
+
+// Few chunks of many columns: one workgroup per 16 columns, four per wave.
+template <int DT>
+__global__ __launch_bounds__(64 * kWaves) void kv_attention_join_tile_kernel(Params p) {
+  const Place at = place_of(p, kTileCols / kCols);
   const Tile t = find_tile(p, at.item);
-  const int first = at.inner * 8;
-  if (!t.live || t.splits <= 1 || first >= t.ncols) return;
+  if (!t.live || t.splits <= 1) return;
   const int64_t slot = (static_cast<int64_t>(at.item) * p.c.heads + at.head) * p.splits * p.cols;
-  join_chunks<DT>(p, t, at.head, slot, t.splits, first, min(8, t.ncols - first), threadIdx.x, 256);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int i = 0; i < kCols / kWaves; ++i) {
+    const int k = at.inner * kCols + wave * (kCols / kWaves) + i;
+    if (k >= t.ncols) return;
+    float m, l;
+    float4_t v;
+    sum_chunks(p, slot + k, 0, t.splits, m, l, v);
+    store_row<DT>(p, column_of(p, t, at.head, k).out_row, m, l, v);
+  }
 }
 
 // How a call is cut: which kernels run, their tiles and chunks of positions.
@@ -754,10 +857,11 @@ Cut chunked(int64_t items, int tiles, int kv_heads, int dim, int cols, int max_k
 // Tiles of 16 columns, for sequences of at most kSmall columns.
 Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window) {
   const int64_t most = ragged ? std::min<int64_t>(static_cast<int64_t>(max_q) * group, kSmall) : group;
-  if (ragged && group > kSmall) return Cut{};  // every sequence is the other kernel's
+  // wide groups, and a call of one long sequence, are the other kernel's alone
+  if (ragged && (group > kSmall || (seqs == 1 && max_q * static_cast<int64_t>(group) > kSmall))) return Cut{};
   const int tiles = static_cast<int>((most + kCols - 1) / kCols);
   return chunked(static_cast<int64_t>(seqs) * tiles, tiles, kv_heads, dim, static_cast<int>(std::min<int64_t>(most, kCols)),
-                 max_kv, window, kCols, 2048, 256, 1024);
+                 max_kv, window, kCols, 1024, 256, 2048);
 }
 
 // Tiles of 128 columns, for the others.
@@ -775,15 +879,21 @@ hipError_t go(const Params& base, const Cut& cc, const Cut& ct, hipStream_t stre
     p.chunk = cc.chunk;
     p.splits = cc.splits;
     p.cols = cc.cols;
+    p.join_later = cc.splits > kJoinHere;
     const int64_t all = cc.items * p.c.heads;
     p.part_ml = p.part_o + all * cc.splits * cc.cols * p.c.dim;
-    const hipError_t e = launch(kv_attention_cols_kernel<DT, FP8, DP>, dim3(static_cast<unsigned>(all * cc.splits)),
-                                dim3(64 * kWaves), 0, stream, p);
+    hipError_t e = launch(kv_attention_cols_kernel<DT, FP8, DP>, dim3(static_cast<unsigned>(all * cc.splits)),
+                          dim3(64 * kWaves), 0, stream, p);
+    if (e == hipSuccess && p.join_later)
+      e = launch(kv_attention_join_cols_kernel<DT>, dim3(static_cast<unsigned>(all * cc.cols)), dim3(64 * kWaves), 0,
+                 stream, p);
     if (e != hipSuccess) return e;
   }
   if (ct.items) {
     Params p = base;
     p.chunk = ct.chunk;
+    p.items = static_cast<unsigned>(ct.items);
+    p.small = cc.items ? kSmall : 0;
     p.splits = ct.splits;
     p.cols = ct.cols;
     p.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(base.part_o) + (cc.bytes + 255) / 256 * 256);
@@ -792,7 +902,8 @@ hipError_t go(const Params& base, const Cut& cc, const Cut& ct, hipStream_t stre
     hipError_t e = launch(kv_attention_tile_kernel<DT, FP8, DP>, dim3(static_cast<unsigned>(all * ct.splits)),
                           dim3(64 * kWaves), 0, stream, p);
     if (e != hipSuccess || ct.splits <= 1) return e;
-    return launch(kv_attention_join_kernel<DT>, dim3(static_cast<unsigned>(all * (kTileCols / 8))), dim3(256), 0, stream, p);
+    return launch(kv_attention_join_tile_kernel<DT>, dim3(static_cast<unsigned>(all * (kTileCols / kCols))), dim3(64 * kWaves), 0,
+                  stream, p);
   }
   return hipSuccess;
 }
@@ -824,15 +935,16 @@ hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, h
   const Cut cc = cut_cols(a.seqs, group, c.heads, c.dim, ragged, a.max_q, a.max_kv, a.window);
   const Cut ct = cut_tile(a.seqs, a.tokens, group, c.heads, c.dim, ragged, a.max_q, a.max_kv, a.window);
   const int64_t limit = 0x7fffffff;
-  if (cc.items * c.heads * std::max(cc.splits, 1) > limit ||
-      ct.items * c.heads * std::max(ct.splits, kTileCols / 8) > limit)
+  if (cc.items * c.heads * std::max(cc.splits, kCols) > limit ||
+      ct.items * c.heads * std::max(ct.splits, kTileCols / kCols) > limit)
     return hipErrorInvalidConfiguration;
   Params p{};
   p.c = c;
   p.a = a;
   while (1 << p.block_shift < c.block) ++p.block_shift;
   p.group = group;
-  p.scale2 = a.scale * 1.4426950408889634f;
+  p.scale2 = std::fabs(a.scale) * 1.4426950408889634f;
+  p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
   p.arrived = static_cast<unsigned*>(a.workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounters * sizeof(unsigned));
   if (a.dtype == QK_BF16) return c.fp8 ? by_dim<QK_BF16, true>(p, cc, ct, stream) : by_dim<QK_BF16, false>(p, cc, ct, stream);
