@@ -218,6 +218,14 @@ __device__ __forceinline__ float load_query(const Params& p, const Column& c, At
   }
 }
 
+// A wave-uniform element of an array that the kernel does not write, through
+// the scalar cache: it has a counter of its own, so that waiting for a block
+// number does not mean waiting for the keys and values asked for before it.
+__device__ __forceinline__ int scalar_load(const int* p, int i) {
+  typedef const __attribute__((address_space(4))) int* constant_t;
+  return reinterpret_cast<constant_t>(reinterpret_cast<uintptr_t>(p))[__builtin_amdgcn_readfirstlane(i)];
+}
+
 // Bytes of a 16-position piece of V past `have` positions as zeros: what lies
 // past a sequence's end may be any bytes, NaN codes among them, and a zero
 // probability would not silence those.
@@ -323,13 +331,10 @@ __device__ __forceinline__ void join_chunks(const Params& p, const Tile& t, int 
 // One workgroup: one tile of up to 16 columns, one kv head, one chunk of
 // positions.  Its four waves take groups of 64 positions in turn, each with a
 // maximum, a sum and an output of its own, and join them through LDS at the
-// end; nothing is shared before, so no wave waits for another.  K of the next
-// group is asked for as soon as the products with this one's have taken its
-// registers, V likewise, so a wave always has one of the two (8 KB at dim
-// 128) on its way.  The workgroup that arrives last at a tile joins its
-// chunks.
+// end; nothing is shared before, so no wave waits for another.  The workgroup
+// that arrives last at a tile joins its chunks.
 template <int DT, bool FP8, int DP>
-__global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : DP > 64 ? 3 : 4) void kv_attention_cols_kernel(Params p) {
+__global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_cols_kernel(Params p) {
   constexpr int KC = DP / 64;  // 16-byte pieces of a K row per lane
   constexpr int VC = DP / 16;  // 16-row pieces of V
   __shared__ float lds_o[kWaves][kCols][DP + 4];
@@ -339,7 +344,11 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : DP > 64 ? 3 : 4) void k
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place at = place_of(p, p.splits);
-  const int split = at.inner, head = at.head;
+  // Workgroups go round the eight dies in turn, and early chunks have work in
+  // every sequence, late ones in few: the chunks are turned by the tile's
+  // number so that no die gets the same one of each (64 requests of up to 8192
+  // positions in four chunks: 153 us without, 128 with).
+  const int head = at.head, split = static_cast<int>((at.inner + at.item + head) % static_cast<unsigned>(p.splits));
   const Tile t = find_cols(p, at.item);
   if (!t.live) return;
   const int dim = p.c.dim, P = p.c.block;
@@ -366,64 +375,84 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : DP > 64 ? 3 : 4) void k
   // the cache reads block 0.  Where such a position is seen its scales are
   // NaN; elsewhere scores are masked, and bytes of V that may be NaN codes
   // become zeros.
-  auto entry = [&](int pos) { return table[min(pos >> p.block_shift, p.c.width - 1)]; };
+  auto entry = [&](int pos) { return scalar_load(table, min(pos >> p.block_shift, p.c.width - 1)); };
   auto in_pool = [&](int b) { return static_cast<unsigned>(b) < static_cast<unsigned>(p.c.blocks); };
 
-  uint4 kr[4][KC], vr[VC];
-  float ks, vs;
+  // Up to dim 128 the next group's K and V are asked for before this one is
+  // worked on; beyond, the registers hold one of each, and the next K is asked
+  // for when the scores are done, the next V at the end.
+  constexpr int kSets = DP > 128 ? 1 : 2;
+  uint4 kr[kSets][4][KC], vr[kSets][VC];
+  float ks[kSets], vs[kSets];
+  // The blocks of the next group's four pieces of 16 positions.
+  int nb0 = 0, nb1 = 0, nb2 = 0, nb3 = 0;
+  auto next_blocks = [&](int t0) {
+    nb0 = entry(t0);
+    nb1 = entry(t0 + 16);
+    nb2 = entry(t0 + 32);
+    nb3 = entry(t0 + 48);
+  };
+  auto pick = [&](int j) {
+    const int lo = j & 1 ? nb1 : nb0, hi = j & 1 ? nb3 : nb2;
+    return j & 2 ? hi : lo;
+  };
+  auto tile_of = [&](int b) { return static_cast<int64_t>(in_pool(b) ? b : 0) * p.c.heads + head; };
+  // Elements past dim come from the front of the row: K's meet zeros of the
+  // query there, V's rows past dim are not stored.
+  int kpart[KC];
+#pragma unroll
+  for (int c = 0; c < KC; ++c) kpart[c] = 64 * c + 16 * g < dim ? 64 * c + 16 * g : 0;
   // K: the lane's row n of tile i is position t0 + 16 (n / 4) + 4 i + n % 4
-  auto load_k = [&](int t0, int kb) {
-    const int64_t tile = static_cast<int64_t>(in_pool(kb) ? kb : 0) * p.c.heads + head;
-    const uint8_t* const row = p.c.k + tile * head_bytes + (((t0 + 16 * (n >> 2)) & (P - 1)) + (n & 3)) * dim + 16 * g;
+  auto load_k = [&](int t0, auto half) {
+    constexpr int S = decltype(half)::value % kSets;
+    const uint8_t* const row =
+        p.c.k + tile_of(pick(n >> 2)) * head_bytes + (((t0 + 16 * (n >> 2)) & (P - 1)) + (n & 3)) * dim;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        if (64 * c + 16 * g < dim)
-          kr[i][c] = *reinterpret_cast<const uint4*>(row + 4 * i * dim + 64 * c);
-        else
-          kr[i][c] = make_uint4(0, 0, 0, 0);
-      }
+      for (int c = 0; c < KC; ++c) kr[S][i][c] = *reinterpret_cast<const uint4*>(row + 4 * i * dim + kpart[c]);
   };
-  auto load_v = [&](int t0, int vb) {
-    const int64_t tile = static_cast<int64_t>(in_pool(vb) ? vb : 0) * p.c.heads + head;
-    const uint8_t* const row = p.c.v + tile * head_bytes + n * P + ((t0 + 16 * g) & (P - 1));
+  auto load_scales = [&](auto half) {
+    constexpr int S = decltype(half)::value % kSets;
+    const int b = pick(g);
+    ks[S] = p.c.k_scale[tile_of(b)];
+    vs[S] = p.c.v_scale[tile_of(b)];
+    if (!in_pool(b)) ks[S] = vs[S] = __builtin_nanf("");
+  };
+  auto load_v = [&](int t0, auto half) {
+    constexpr int S = decltype(half)::value % kSets;
+    const uint8_t* const row = p.c.v + tile_of(pick(g)) * head_bytes + n * P + ((t0 + 16 * g) & (P - 1));
 #pragma unroll
-    for (int i = 0; i < VC; ++i) {
-      if (16 * i < dim)
-        vr[i] = *reinterpret_cast<const uint4*>(row + 16 * i * P);
-      else
-        vr[i] = make_uint4(0, 0, 0, 0);
-    }
-    ks = p.c.k_scale[tile];
-    vs = p.c.v_scale[tile];
-    if (!in_pool(vb)) ks = vs = __builtin_nanf("");
+    for (int i = 0; i < VC; ++i) vr[S][i] = *reinterpret_cast<const uint4*>(row + (16 * i < dim ? 16 * i : 0) * P);
   };
 
   constexpr int kStep = kWaves * kGroup;
-  int kb1 = 0, vb1 = 0;  // block numbers of the next group
-  auto next_blocks = [&](int t0) {
-    kb1 = entry(t0 + 16 * (n >> 2));
-    vb1 = entry(t0 + 16 * g);
-  };
   // the group at t0, whose K and V are in registers or on their way; `more`:
   // ask for the next group's
-  auto group = [&](int t0, auto more) {
+  auto group = [&](int t0, auto half, auto more) {
+    constexpr int S = decltype(half)::value % kSets;
+    constexpr std::integral_constant<int, 1 - decltype(half)::value> other{};
+    if constexpr (decltype(more)::value && kSets == 2) {
+      load_scales(other);
+      load_k(t0 + kStep, other);
+      load_v(t0 + kStep, other);
+      next_blocks(t0 + 2 * kStep);
+    }
     float4_t acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       acc[i] = float4_t{0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[i][c].x, kr[i][c].y), qf[2 * c], acc[i], 0, 0, 0);
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[i][c].z, kr[i][c].w), qf[2 * c + 1], acc[i], 0, 0, 0);
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[S][i][c].x, kr[S][i][c].y), qf[2 * c], acc[i], 0, 0, 0);
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[S][i][c].z, kr[S][i][c].w), qf[2 * c + 1], acc[i], 0, 0, 0);
       }
     }
-    if constexpr (decltype(more)::value) load_k(t0 + kStep, kb1);
+    if constexpr (decltype(more)::value && kSets == 1) load_k(t0 + kStep, other);
     float s[1][16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[0][i] = acc[i >> 2][i & 3];
-    float c[1] = {c_col * ks}, bias[1] = {__builtin_amdgcn_logf(vs)}, inv_vs[1] = {__builtin_amdgcn_rcpf(vs)};
+    float c[1] = {c_col * ks[S]}, bias[1] = {__builtin_amdgcn_logf(vs[S])}, inv_vs[1] = {__builtin_amdgcn_rcpf(vs[S])};
     if (t0 < t.lo || t0 + kGroup > t.len - t.rows || p.a.window > 0) {  // some column may not see all 64
       const int at = t0 + 16 * g;
 #pragma unroll
@@ -443,27 +472,47 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : DP > 64 ? 3 : 4) void k
     if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) {
       const int have = t0 + 16 * g + 16 > t.lo ? t.len - (t0 + 16 * g) : 0;
 #pragma unroll
-      for (int i = 0; i < VC; ++i) keep_first(vr[i], have);
+      for (int i = 0; i < VC; ++i) keep_first(vr[S][i], have);
+    }
+    if (__any(shrink != 1.0f)) {
+#pragma unroll
+      for (int i = 0; i < VC; ++i) o[i] *= shrink;
     }
 #pragma unroll
     for (int i = 0; i < VC; ++i) {
-      o[i] *= shrink;
-      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[i].x, vr[i].y), pf[0], o[i], 0, 0, 0);
-      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[i].z, vr[i].w), pf[1], o[i], 0, 0, 0);
+      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[S][i].x, vr[S][i].y), pf[0], o[i], 0, 0, 0);
+      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[S][i].z, vr[S][i].w), pf[1], o[i], 0, 0, 0);
     }
-    if constexpr (decltype(more)::value) {
-      load_v(t0 + kStep, vb1);
+    if constexpr (decltype(more)::value && kSets == 1) {
+      load_scales(other);
+      load_v(t0 + kStep, other);
       next_blocks(t0 + 2 * kStep);
     }
   };
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
   int t0 = begin + wave * kGroup;
   if (t0 < end) {
     next_blocks(t0);
-    load_k(t0, kb1);
-    load_v(t0, vb1);
+    load_scales(even);
+    load_k(t0, even);
+    load_v(t0, even);
     next_blocks(t0 + kStep);
-    for (; t0 + kStep < end; t0 += kStep) group(t0, std::true_type{});
-    group(t0, std::false_type{});
+    if constexpr (kSets == 1) {
+      for (; t0 + kStep < end; t0 += kStep) group(t0, even, std::true_type{});
+      group(t0, even, std::false_type{});
+    } else {
+      for (; t0 + 2 * kStep < end; t0 += 2 * kStep) {
+        group(t0, even, std::true_type{});
+        group(t0 + kStep, odd, std::true_type{});
+      }
+      if (t0 + kStep < end) {
+        group(t0, even, std::true_type{});
+        group(t0 + kStep, odd, std::false_type{});
+      } else {
+        group(t0, even, std::false_type{});
+      }
+    }
   }
 
   // join the four waves
@@ -523,9 +572,9 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : DP > 64 ? 3 : 4) void k
 // One workgroup: one tile of 128 columns, one kv head, one chunk of positions
 // in steps of 64.  The four waves share K and V of a step through LDS, as
 // binary16 (each code is converted once per workgroup), and have 32 columns
-// each.  LDS is doubled: while a step is worked on, the next one's bytes come
-// from memory into registers and are written converted to the other half;
-// one barrier per step.  Rows of K lie in the order in which the first
+// each.  LDS is doubled: while a step is worked on, the next one's bytes are
+// written converted to the other half, and those of the one after it come
+// from memory into registers; one barrier per step.  Rows of K lie in the order in which the first
 // product's result registers want them, 16-byte pieces of a row are
 // exchanged by its number so that eight consecutive rows fall on different
 // banks.
@@ -571,137 +620,161 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
 
   const int64_t head_bytes = static_cast<int64_t>(P) * dim;
   const int* const table = p.c.table + t.seq * p.c.ldt;
-  auto entry = [&](int pos) { return table[min(pos >> p.block_shift, p.c.width - 1)]; };  // as above
+  auto entry = [&](int pos) { return scalar_load(table, min(pos >> p.block_shift, p.c.width - 1)); };  // as above
   auto in_pool = [&](int b) { return static_cast<unsigned>(b) < static_cast<unsigned>(p.c.blocks); };
 
   // What this thread brings of a step.  K: piece kd of rows krow(i); V: 16
   // positions of rows lane + 64 i.  Either way a wave's rows lie in one piece of
   // 16 positions, so block numbers and addresses of tiles are scalar.
-  const int kd = tid % RB;
+  // Elements past dim come from the front of the row and rows past dim from
+  // the last: they meet zeros of the query, or are not stored.
+  const int kd = tid % RB, kcol = 16 * kd < dim ? 16 * kd : 0;
   auto krow = [&](int i) { return tid / RB + i * (64 * kWaves / RB); };
   auto kpart = [&](int i) { return __builtin_amdgcn_readfirstlane(krow(i) >> 4); };
-  uint4 kr[NC], vr[NC];
-  float sk = 0.0f, sv = 0.0f;
+  // Up to dim 128 two steps are on their way, so that a load has a whole step
+  // to arrive; beyond, the registers hold one.
+  constexpr int kSets = DP > 128 ? 1 : 2;
+  uint4 kr[kSets][NC], vr[kSets][NC];
+  float sk[kSets], sv[kSets];
   int kb[NC], vb = 0;  // block numbers of the step to load
   auto load_blocks = [&](int t0) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) kb[i] = entry(t0 + 16 * kpart(i));
     vb = entry(t0 + 16 * wave);
   };
-  auto load_step = [&](int t0) {
+  auto load_step = [&](int t0, auto half) {
+    constexpr int S = decltype(half)::value % kSets;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int pos = (t0 + 16 * kpart(i)) & (P - 1);
       const int64_t tile = static_cast<int64_t>(in_pool(kb[i]) ? kb[i] : 0) * p.c.heads + head;
       const uint8_t* const from = p.c.k + tile * head_bytes + pos * dim;
-      kr[i] = make_uint4(0, 0, 0, 0);
-      if (16 * kd < dim) kr[i] = *reinterpret_cast<const uint4*>(from + static_cast<unsigned>((krow(i) & 15) * dim + 16 * kd));
+      kr[S][i] = *reinterpret_cast<const uint4*>(from + static_cast<unsigned>((krow(i) & 15) * dim + kcol));
     }
-    const int vp = t0 + 16 * wave;
     const int64_t tile = static_cast<int64_t>(in_pool(vb) ? vb : 0) * p.c.heads + head;
-    const uint8_t* const from = p.c.v + tile * head_bytes + (vp & (P - 1));
+    const uint8_t* const from = p.c.v + tile * head_bytes + ((t0 + 16 * wave) & (P - 1));
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      vr[i] = make_uint4(0, 0, 0, 0);
-      if (lane + 64 * i < dim) {
-        vr[i] = *reinterpret_cast<const uint4*>(from + static_cast<unsigned>((lane + 64 * i) * P));
-        if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) keep_first(vr[i], vp + 16 > t.lo ? t.len - vp : 0);
-      }
+      vr[S][i] = *reinterpret_cast<const uint4*>(from + static_cast<unsigned>(min(lane + 64 * i, dim - 1) * P));
     }
-    sk = in_pool(vb) ? p.c.k_scale[tile] : __builtin_nanf("");
-    sv = in_pool(vb) ? p.c.v_scale[tile] : __builtin_nanf("");
+    sk[S] = p.c.k_scale[tile];
+    sv[S] = p.c.v_scale[tile];
+    if (!in_pool(vb)) sk[S] = sv[S] = __builtin_nanf("");
   };
-  auto put_step = [&](int buf) {
-    half8_t* const kl = reinterpret_cast<half8_t*>(lds_k[buf]);
-    half8_t* const vl = reinterpret_cast<half8_t*>(lds_v[buf]);
+  // the step at t0 into half H of LDS
+  auto put_step = [&](int t0, auto half) {
+    constexpr int H = decltype(half)::value, S = H % kSets;
+    half8_t* const kl = reinterpret_cast<half8_t*>(lds_k[H]);
+    half8_t* const vl = reinterpret_cast<half8_t*>(lds_v[H]);
+    if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) {
+      const int have = t0 + 16 * wave + 16 > t.lo ? t.len - (t0 + 16 * wave) : 0;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) keep_first(vr[S][i], have);
+    }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       // position 32 a + 16 b + 8 c + 4 d + e lies in row 32 a + 16 b + 8 d + 4 c + e
       const int r = krow(i), row = (r & ~12) | ((r & 8) >> 1) | ((r & 4) << 1);
       const int key = row & 7;
-      kl[row * KP + ((2 * kd) ^ key)] = kv::codes8_to_half<FP8>(kr[i].x, kr[i].y);
-      kl[row * KP + ((2 * kd + 1) ^ key)] = kv::codes8_to_half<FP8>(kr[i].z, kr[i].w);
+      kl[row * KP + ((2 * kd) ^ key)] = kv::codes8_to_half<FP8>(kr[S][i].x, kr[S][i].y);
+      kl[row * KP + ((2 * kd + 1) ^ key)] = kv::codes8_to_half<FP8>(kr[S][i].z, kr[S][i].w);
       const int d = lane + 64 * i;
-      vl[d * 8 + ((2 * wave) ^ (d & 7))] = kv::codes8_to_half<FP8>(vr[i].x, vr[i].y);
-      vl[d * 8 + ((2 * wave + 1) ^ (d & 7))] = kv::codes8_to_half<FP8>(vr[i].z, vr[i].w);
+      vl[d * 8 + ((2 * wave) ^ (d & 7))] = kv::codes8_to_half<FP8>(vr[S][i].x, vr[S][i].y);
+      vl[d * 8 + ((2 * wave + 1) ^ (d & 7))] = kv::codes8_to_half<FP8>(vr[S][i].z, vr[S][i].w);
     }
     if (lane == 0) {
-      lds_s[buf][0][wave] = sk;
-      lds_s[buf][1][wave] = __builtin_amdgcn_logf(sv);
-      lds_s[buf][2][wave] = __builtin_amdgcn_rcpf(sv);
+      lds_s[H][0][wave] = sk[S];
+      lds_s[H][1][wave] = __builtin_amdgcn_logf(sv[S]);
+      lds_s[H][2][wave] = __builtin_amdgcn_rcpf(sv[S]);
     }
   };
-
-  if (begin < end) {
-    load_blocks(begin);
-    load_step(begin);
-    if (begin + kGroup < end) load_blocks(begin + kGroup);
-    put_step(0);
-  }
-  __syncthreads();
-  int buf = 0;
-  for (int t0 = begin; t0 < end; t0 += kGroup, buf ^= 1) {
-    const bool more = t0 + kGroup < end;
-    if (more) {
-      load_step(t0 + kGroup);
-      if (t0 + 2 * kGroup < end) load_blocks(t0 + 2 * kGroup);
+  // the step at t0, in half H of LDS
+  auto work = [&](int t0, auto half) {
+    constexpr int H = decltype(half)::value;
+    if (t0 >= any_hi || t0 + kGroup <= any_lo) return;
+    const half8_t* const kl = reinterpret_cast<const half8_t*>(lds_k[H]);
+    const half8_t* const vl = reinterpret_cast<const half8_t*>(lds_v[H]);
+    float16_t acc[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i)
+        acc[a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[(32 * a + n) * KP + ((2 * i + h) ^ (n & 7))], qf[i], acc[a], 0, 0, 0);
     }
-    if (t0 < any_hi && t0 + kGroup > any_lo) {
-      const half8_t* const kl = reinterpret_cast<const half8_t*>(lds_k[buf]);
-      const half8_t* const vl = reinterpret_cast<const half8_t*>(lds_v[buf]);
-      float16_t acc[2];
+    // register 8 b + e of acc[a] is position 32 a + 16 b + 8 h + e
+    float s[4][8], c[4], bias[4], inv_vs[4];
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
+    for (int b = 0; b < 4; ++b) {
+      c[b] = c_col * lds_s[H][0][b];
+      bias[b] = lds_s[H][1][b];
+      inv_vs[b] = lds_s[H][2][b];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[a][e] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < DP / 16; ++i)
-          acc[a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[(32 * a + n) * KP + ((2 * i + h) ^ (n & 7))], qf[i], acc[a], 0, 0, 0);
-      }
-      // register 8 b + e of acc[a] is position 32 a + 16 b + 8 h + e
-      float s[4][8], c[4], bias[4], inv_vs[4];
+      for (int e = 0; e < 8; ++e) s[b][e] = acc[b >> 1][8 * (b & 1) + e];
+    }
+    if (t0 + kGroup > all_hi || t0 < all_lo) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        c[b] = c_col * lds_s[buf][0][b];
-        bias[b] = lds_s[buf][1][b];
-        inv_vs[b] = lds_s[buf][2][b];
+        const int first = t0 + 16 * b;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[b][e] = acc[b >> 1][8 * (b & 1) + e];
-      }
-      if (t0 + kGroup > all_hi || t0 < all_lo) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int first = t0 + 16 * b;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int spot = first + 8 * h + e;
-            s[b][e] = spot >= col.see_lo && spot < col.see_hi ? __builtin_fmaf(s[b][e], c[b], bias[b]) : -__builtin_inff();
-          }
-          c[b] = 1.0f;
-          bias[b] = 0.0f;
-          // a column that sees none of these positions must not meet their scale
-          if (first + 16 <= col.see_lo || first >= col.see_hi) inv_vs[b] = 0.0f;
+        for (int e = 0; e < 8; ++e) {
+          const int spot = first + 8 * h + e;
+          s[b][e] = spot >= col.see_lo && spot < col.see_hi ? __builtin_fmaf(s[b][e], c[b], bias[b]) : -__builtin_inff();
         }
+        c[b] = 1.0f;
+        bias[b] = 0.0f;
+        // a column that sees none of these positions must not meet their scale
+        if (first + 16 <= col.see_lo || first >= col.see_hi) inv_vs[b] = 0.0f;
       }
-      const float m_old = m;
-      const float shrink = softmax_step<4, 8, false>(s, c, bias, inv_vs, m, l);
-      if (__any(m != m_old)) {
-#pragma unroll
-        for (int i = 0; i < ND; ++i) o[i] *= shrink;
-      }
-      half8_t pf[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) pf[b][e] = static_cast<_Float16>(s[b][e]);
-#pragma unroll
-      for (int i = 0; i < ND; ++i)
-#pragma unroll
-        for (int s4 = 0; s4 < 4; ++s4)
-          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[(32 * i + n) * 8 + ((2 * s4 + h) ^ (n & 7))], pf[s4], o[i], 0, 0, 0);
     }
-    if (more) put_step(buf ^ 1);
+    const float m_old = m;
+    const float shrink = softmax_step<4, 8, false>(s, c, bias, inv_vs, m, l);
+    if (__any(m != m_old)) {
+#pragma unroll
+      for (int i = 0; i < ND; ++i) o[i] *= shrink;
+    }
+    half8_t pf[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) pf[b][e] = static_cast<_Float16>(s[b][e]);
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int s4 = 0; s4 < 4; ++s4)
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[(32 * i + n) * 8 + ((2 * s4 + h) ^ (n & 7))], pf[s4], o[i], 0, 0, 0);
+  };
+  // One step: ask for a later one, work on this one, write the next.
+  auto step = [&](int t0, auto half) {
+    constexpr int H = decltype(half)::value;
+    using Same = std::integral_constant<int, H>;
+    using Other = std::integral_constant<int, 1 - H>;
+    if (t0 + kSets * kGroup < end) {
+      load_step(t0 + kSets * kGroup, std::integral_constant<int, (H + kSets) % 2>{});
+      load_blocks(t0 + (kSets + 1) * kGroup);
+    }
+    work(t0, Same{});
+    if (t0 + kGroup < end) put_step(t0 + kGroup, Other{});
     __syncthreads();
+  };
+
+  using Even = std::integral_constant<int, 0>;
+  using Odd = std::integral_constant<int, 1>;
+  if (begin < end) {
+    load_blocks(begin);
+    load_step(begin, Even{});
+    load_blocks(begin + kGroup);
+    if (kSets > 1 && begin + kGroup < end) {
+      load_step(begin + kGroup, Odd{});
+      load_blocks(begin + 2 * kGroup);
+    }
+    put_step(begin, Even{});
+  }
+  __syncthreads();
+  for (int t0 = begin; t0 < end; t0 += 2 * kGroup) {
+    step(t0, Even{});
+    if (t0 + kGroup < end) step(t0 + kGroup, Odd{});
   }
 
   if (!col.valid) return;
@@ -836,17 +909,16 @@ struct Cut {
   size_t bytes;   // of partial results
 };
 
-Cut chunked(int64_t items, int tiles, int kv_heads, int dim, int cols, int max_kv, int window, int rows, int wanted,
-            int least, int most) {
-  Cut c{items, tiles, 0, 0, cols, 0};
-  if (items == 0) return c;
-  // positions that one tile can see, from a multiple of 64 on
+// The positions that one tile can see, from a multiple of 64 on.
+int64_t range_of(int max_kv, int window, int rows) {
   int64_t range = max_kv;
   if (window > 0) range = std::min<int64_t>(range, static_cast<int64_t>(window) + rows);
-  range = (range + 2 * kGroup - 1) / kGroup * kGroup;
+  return (range + 2 * kGroup - 1) / kGroup * kGroup;
+}
+
+Cut cut_of(int64_t items, int tiles, int kv_heads, int dim, int cols, int64_t range, int64_t chunk) {
+  Cut c{items, tiles, 0, 0, cols, 0};
   const int64_t all = items * kv_heads;
-  int64_t chunk = (range * all + wanted - 1) / wanted;
-  chunk = std::min<int64_t>(std::max<int64_t>((chunk + least - 1) / least * least, least), most);
   if (chunk > range || all > kCounters) chunk = range;
   c.chunk = static_cast<int>(std::min<int64_t>(chunk, 1 << 30));
   c.splits = static_cast<int>((range + c.chunk - 1) / c.chunk);
@@ -854,21 +926,43 @@ Cut chunked(int64_t items, int tiles, int kv_heads, int dim, int cols, int max_k
   return c;
 }
 
-// Tiles of 16 columns, for sequences of at most kSmall columns.
+// Tiles of 16 columns, for sequences of at most kSmall columns.  One workgroup
+// per CU keeps HBM busy, and every further chunk costs a start (about 3.5 us)
+// and its part of the join, so tiles are cut until there are 256 workgroups;
+// where there are that many tiles, only so that ragged lengths even out.
+// Measured (dim 128, us in 1 / 2 / 4 / 8 / 16 / 32 / 64 chunks): 16 tiles of
+// 121344 positions 652 / 336 / 178 / 105 / 89 / 91 / 96; 8 of 32768 172 / 92 /
+// 51 / 31 / 22 / 20 / 22; 128 of 7936 54 / 41 / 44 / 45 / 49; 512 of up to 8192
+// 131 / 139 / 128 / 128; 512 of 4096 94 / 102 / 109 / 113.
 Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window) {
   const int64_t most = ragged ? std::min<int64_t>(static_cast<int64_t>(max_q) * group, kSmall) : group;
   // wide groups, and a call of one long sequence, are the other kernel's alone
   if (ragged && (group > kSmall || (seqs == 1 && max_q * static_cast<int64_t>(group) > kSmall))) return Cut{};
   const int tiles = static_cast<int>((most + kCols - 1) / kCols);
-  return chunked(static_cast<int64_t>(seqs) * tiles, tiles, kv_heads, dim, static_cast<int>(std::min<int64_t>(most, kCols)),
-                 max_kv, window, kCols, 1024, 256, 2048);
+  const int64_t items = static_cast<int64_t>(seqs) * tiles;
+  // beside long sequences the others are mostly single tokens
+  const bool mixed = ragged && static_cast<int64_t>(max_q) * group > kSmall;
+  const int64_t live = (mixed ? static_cast<int64_t>(seqs) * ((group + kCols - 1) / kCols) : items) * kv_heads;
+  const int64_t range = range_of(max_kv, window, kCols);
+  int64_t chunks = 1;
+  if (range > 1024 && live < 256) chunks = 256 / live;
+  if (range > 6144 && live >= 256) chunks = (range + 2047) / 2048;
+  constexpr int64_t kStep = kWaves * kGroup;
+  const int64_t chunk = ((range + chunks - 1) / chunks + kStep - 1) / kStep * kStep;
+  return cut_of(items, tiles, kv_heads, dim, static_cast<int>(std::min<int64_t>(most, kCols)), range, chunk);
 }
 
-// Tiles of 128 columns, for the others.
+// Tiles of 128 columns, for the others: chunks only where there are too few
+// tiles for the CUs (two workgroups fit on one, one beyond dim 128).
 Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window) {
   if (!ragged || static_cast<int64_t>(max_q) * group <= kSmall) return Cut{};
-  return chunked(kv::item_base(tokens, group, kTileCols, 1, seqs), 1, kv_heads, dim, kTileCols, max_kv, window, kTileCols,
-                 512, 512, 1 << 30);
+  const int64_t cols = static_cast<int64_t>(tokens) * group;
+  const int64_t live = (cols / kTileCols + std::min<int64_t>(seqs, cols / kTileCols) / 2) * kv_heads;
+  const int64_t range = range_of(max_kv, window, kTileCols), wanted = dim > 128 ? 256 : 512;
+  int64_t chunk = range;
+  if (live < 192 && range > 512) chunk = ((range * live + wanted - 1) / wanted + 255) / 256 * 256;
+  return cut_of(kv::item_base(tokens, group, kTileCols, 1, seqs), 1, kv_heads, dim, kTileCols, range,
+                std::max<int64_t>(chunk, 256));
 }
 
 template <int DT, bool FP8, int DP>
