@@ -79,6 +79,26 @@ def test_attention(kw, status):
     assert call(qk.library().qk_kv_attention, ATTEND, **kw) == status
 
 
+def test_binding_refuses_on_the_host():
+    import torch
+    x, w = torch.zeros(2, 16), torch.zeros(16)
+    with pytest.raises(ValueError, match="x must be a GPU tensor"):
+        qk.rms_norm_quant(x, w)
+    with pytest.raises(TypeError, match="x must be a torch.Tensor"):
+        qk.rms_norm_quant([1.0], w)
+    cache = qk.new_kv_cache(2, 1, 16, 16, device="cpu")
+    with pytest.raises(ValueError, match="k must be a GPU tensor"):
+        qk.kv_cache_write(cache, x, x, x, x, x)
+    with pytest.raises(ValueError, match="GPU"):
+        qk.kv_cache_read(cache, x, x, x, 2)
+    with pytest.raises(TypeError):
+        qk.kv_cache_read(cache, x, x, x, 2, torch.float64)
+    with pytest.raises(ValueError, match="q must be a GPU tensor"):
+        qk.kv_attention(x, cache, x, x)
+    with pytest.raises(TypeError):
+        qk.kv_attention(None, cache, x, x)
+
+
 def test_attention_workspace_size():
     size = qk.kv_attention_workspace_size
     assert size(1, 1, 4, 2, 64, 64) == 0                     # one piece: nothing to join

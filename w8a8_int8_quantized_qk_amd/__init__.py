@@ -2,8 +2,9 @@
 
 Every step runs in the HIP kernels of ``libqk.so`` (built for gfx950 by
 ``build.py``); this module only checks tensors, passes raw device pointers
-and the current HIP stream through the C ABI of ``include/qk.h``, and raises
-on a nonzero status.  PyTorch provides device memory and streams.  There is no
+and the current HIP stream through the C ABI of ``include/qk.h`` (by ctypes,
+for the short calls between the linears by the C++ module ``_qkbind``), and
+raises on a nonzero status.  PyTorch provides device memory and streams.  There is no
 fallback: if the library is missing or was built for another ABI, every call
 raises.
 
@@ -25,7 +26,6 @@ and what a decoder layer has between its linears, 8 bit as well:
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 from typing import NamedTuple
@@ -775,37 +775,38 @@ def gemm_i8_asym(a: torch.Tensor, zero_point: torch.Tensor, b: torch.Tensor, wsu
 
 
 # ---- the operators between a decoder layer's linears ----
-# These calls are short on the GPU, so their checks read each tensor attribute
-# once and pointers go to libqk as plain integers.
-
-def _raw_stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+# These calls are short on the GPU: their checks and allocations are in C++
+# (csrc/bind.cpp, the module _qkbind) and raise the same exceptions.
+_bound = None
 
 
-def _rows(t: torch.Tensor, name: str, dtype, device, ndim: int) -> int:
-    """Check of a tensor of rows that may lie apart: returns the row stride.  The
-    dimensions after the first are dense."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != ndim:
-        raise ValueError(f"{name} must have {ndim} dimensions")
-    inner = 1
-    for i in range(ndim - 1, 0, -1):
-        if stride[i] != inner and shape[i] != 1 and shape[0]:
-            raise ValueError(f"the rows of {name} must be dense")
-        inner *= shape[i]
-    if shape[0] <= 1:
-        return inner
-    if stride[0] < inner:
-        raise ValueError(f"the rows of {name} must not overlap")
-    return stride[0]
+def _workspace_on(nbytes: int, index: int) -> torch.Tensor:
+    return new_workspace(nbytes, torch.device("cuda", index))
+
+
+def _bind_to(lib: ctypes.CDLL):
+    """The module _qkbind, with its calls going to `lib`."""
+    try:
+        from . import _qkbind
+    except ImportError as e:
+        raise ImportError(
+            f"{os.path.join(_HERE, '_qkbind.so')} is missing or was built for another torch: build it with "
+            "`python -m w8a8_int8_quantized_qk_amd.build` (or __graft_entry__.build())") from e
+    names = ("qk_rms_norm_quant", "qk_kv_cache_write", "qk_kv_cache_read", "qk_kv_attention_workspace_size",
+             "qk_kv_attention")
+    _qkbind.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names), _check,
+                 torch._C._cuda_getCurrentRawStream, _workspace_on)
+    return _qkbind
+
+
+def _bind():
+    global _bound
+    if _bound is None:
+        lib = library()
+        with _lock:
+            if _bound is None:
+                _bound = _bind_to(lib)
+    return _bound
 
 
 def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -822,45 +823,7 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     (float8_e4m3fn when fp8) [m, k], scale fp32 [m], ready for gemm_i8_scaled
     or gemm_fp8_scaled.
     """
-    dt = x.dtype if isinstance(x, torch.Tensor) else None
-    if dt is not None and dt not in _IN_DTYPES:
-        raise TypeError(f"x dtype {dt} not supported")
-    dev = x.device if dt is not None else None
-    ldx = _rows(x, "x", dt, dev, 2)
-    m, k = x.shape
-    _need(weight, "weight", None, 1, dev)
-    if weight.dtype not in (dt, torch.float32):
-        raise TypeError(f"weight must be {dt} or fp32, got {weight.dtype}")
-    if weight.shape[0] != k:
-        raise ValueError("weight must be [k]")
-    ldr = ldo = 0
-    if residual is not None:
-        ldr = _rows(residual, "residual", dt, dev, 2)
-        residual_out = torch.empty((m, k), dtype=dt, device=dev) if residual_out is None else residual_out
-        ldo = _rows(residual_out, "residual_out", dt, dev, 2)
-        if residual.shape != x.shape or residual_out.shape != x.shape:
-            raise ValueError("residual and residual_out must be [m, k]")
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    qdt = torch.float8_e4m3fn if fp8 else torch.int8
-    if q is None:
-        q = torch.empty((m, k), dtype=qdt, device=dev)
-    elif fp8:
-        _need_codes(q, "q", 2, dev)
-    else:
-        _need(q, "q", torch.int8, 2, dev)
-    if scale is None:
-        scale = torch.empty((m,), dtype=torch.float32, device=dev)
-    else:
-        _need(scale, "scale", torch.float32, 1, dev)
-    if q.shape != x.shape or scale.shape[0] != m:
-        raise ValueError("q must be [m, k] and scale [m]")
-    _check(library().qk_rms_norm_quant(
-        m, k, x.data_ptr(), ldx, 0 if residual is None else residual.data_ptr(), ldr, weight.data_ptr(),
-        _IN_DTYPES[dt], _IN_DTYPES[weight.dtype], eps, CODE_FP8 if fp8 else CODE_I8,
-        0 if residual is None else residual_out.data_ptr(), ldo, q.data_ptr(), scale.data_ptr(),
-        _raw_stream(dev)))
-    return (q, scale) if residual is None else (q, scale, residual_out)
+    return _bind().rms_norm_quant(x, weight, eps, residual, fp8, residual_out, q, scale)
 
 
 KV_BLOCKS = (16, 32, 64, 128)
@@ -893,54 +856,6 @@ def new_kv_cache(blocks: int, kv_heads: int, dim: int, block: int = 64, fp8: boo
     return KVCache(k, v, *scales)
 
 
-def _kv_args(cache: KVCache, table: torch.Tensor, seqs: int, device):
-    """Checks a cache and its block table; the arguments libqk takes for them."""
-    k, v, ks, vs = cache
-    if k.dim() != 4:
-        raise ValueError("cache.k must be [blocks, kv_heads, block, dim]")
-    blocks, heads, block, dim = k.shape
-    if v.shape != (blocks, heads, dim, block) or ks.shape != (blocks, heads) or vs.shape != (blocks, heads):
-        raise ValueError("cache.v must be [blocks, kv_heads, dim, block], the scales [blocks, kv_heads]")
-    if block not in KV_BLOCKS:
-        raise ValueError(f"block must be one of {KV_BLOCKS}")
-    if dim % 16 or not 16 <= dim <= 256:
-        raise ValueError("dim must be a multiple of 16 from 16 to 256")
-    dt = k.dtype
-    if dt not in (torch.int8, torch.float8_e4m3fn) or v.dtype != dt:
-        raise TypeError("cache codes must be int8 or float8_e4m3fn")
-    if ks.dtype != torch.float32 or vs.dtype != torch.float32:
-        raise TypeError("cache scales must be fp32")
-    for t, name in ((k, "cache.k"), (v, "cache.v"), (ks, "cache.k_scale"), (vs, "cache.v_scale")):
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    ldt = _rows(table, "table", torch.int32, device, 2)
-    if table.shape[0] != seqs:
-        raise ValueError(f"table must have one row for each of the {seqs} sequences")
-    return (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), blocks, block,
-            CODE_I8 if dt == torch.int8 else CODE_FP8, table.data_ptr(), ldt, table.shape[1])
-
-
-def _kv_rows(fn, cache: KVCache, k: torch.Tensor, v: torch.Tensor, table, start, cu):
-    dt = k.dtype if isinstance(k, torch.Tensor) else None
-    if dt is not None and dt not in _IN_DTYPES:
-        raise TypeError(f"k dtype {dt} not supported")
-    dev = k.device if dt is not None else None
-    ldk, ldv = _rows(k, "k", dt, dev, 3), _rows(v, "v", dt, dev, 3)
-    _need(start, "start", torch.int32, 1, dev)
-    _need(cu, "cu", torch.int32, 1, dev)
-    seqs = start.shape[0]
-    args = _kv_args(cache, table, seqs, dev)
-    if cu.shape[0] != seqs + 1:
-        raise ValueError("cu must have one entry more than start")
-    tokens, heads, dim = k.shape
-    if v.shape != k.shape or heads != cache[0].shape[1] or dim != cache[0].shape[3]:
-        raise ValueError("k and v must be [tokens, kv_heads, dim] of the cache's heads and dim")
-    _check(fn(seqs, tokens, heads, dim, k.data_ptr(), ldk, v.data_ptr(), ldv, _IN_DTYPES[dt], *args,
-              start.data_ptr(), cu.data_ptr(), _raw_stream(dev)))
-
-
 def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
                    start: torch.Tensor, cu: torch.Tensor) -> KVCache:
     """Quantise new tokens into the cache, one launch.
@@ -952,8 +867,7 @@ def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torc
     into it and grows with later ones, which moves the earlier codes.  Returns
     the cache, which is written in place.
     """
-    _kv_rows(library().qk_kv_cache_write, cache, k, v, table, start, cu)
-    return cache
+    return _bind().kv_cache_write(cache, k, v, table, start, cu)
 
 
 def kv_cache_read(cache: KVCache, table: torch.Tensor, start: torch.Tensor, cu: torch.Tensor,
@@ -965,27 +879,16 @@ def kv_cache_read(cache: KVCache, table: torch.Tensor, start: torch.Tensor, cu: 
     cu[s + 1] - 1 of the outputs (allocated when not given); tokens is cu's
     last entry, which the host knows.
     """
-    heads, dim = cache[0].shape[1], cache[0].shape[3]
-    dev = cache[0].device
-    if k is None:
-        k = torch.empty((tokens, heads, dim), dtype=dtype, device=dev)
-    if v is None:
-        v = torch.empty((tokens, heads, dim), dtype=k.dtype, device=dev)
-    if k.shape[0] != tokens:
-        raise ValueError("k must have `tokens` rows")
-    _kv_rows(library().qk_kv_cache_read, cache, k, v, table, start, cu)
-    return k, v
+    if dtype not in _IN_DTYPES:
+        raise TypeError(f"dtype {dtype} not supported")
+    return _bind().kv_cache_read(cache, table, start, cu, tokens, _IN_DTYPES[dtype], k, v)
 
 
-@functools.lru_cache(maxsize=4096)
 def kv_attention_workspace_size(seqs: int, tokens: int, heads: int, kv_heads: int, dim: int, max_kv: int,
                                 window: int = 0, ragged: bool = False, max_q: int = 1) -> int:
     """Bytes of workspace of a kv_attention call (ragged: with cu); 0 if none."""
     return int(library().qk_kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, ragged, max_q,
                                                         max_kv, window))
-
-
-_attention_workspaces: dict = {}
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
@@ -1005,52 +908,5 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: tor
     with return_lse the fp32 log-sum-exp [tokens, heads]; a row that sees no
     position gives 0 and -inf.
     """
-    dt = q.dtype if isinstance(q, torch.Tensor) else None
-    if dt is not None and dt not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"q dtype {dt} not supported")
-    dev = q.device if dt is not None else None
-    ldq = _rows(q, "q", dt, dev, 3)
-    tokens, heads, dim = q.shape
-    _need(lens, "lens", torch.int32, 1, dev)
-    seqs = lens.shape[0]
-    args = _kv_args(cache, table, seqs, dev)
-    kv_heads = cache[0].shape[1]
-    if dim != cache[0].shape[3] or heads % kv_heads:
-        raise ValueError("q must be [tokens, heads, dim] with heads a multiple of the cache's and its dim")
-    if cu is not None:
-        _need(cu, "cu", torch.int32, 1, dev)
-        if cu.shape[0] != seqs + 1:
-            raise ValueError("cu must have one entry more than lens")
-    elif tokens != seqs:
-        raise ValueError("without cu every sequence has one row")
-    if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=dt, device=dev)
-    else:
-        _need(out, "out", dt, 3, dev)
-        if out.shape != q.shape:
-            raise ValueError("out must be [tokens, heads, dim]")
-    lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
-    reach = args[9] * args[5]
-    max_kv = reach if max_kv is None else min(max_kv, reach)
-    max_q = (1 if cu is None else max(tokens, 1)) if max_q is None else max_q
-    stream = _raw_stream(dev)
-    if workspace is None:
-        need = kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, max_kv, window, cu is not None,
-                                           max_q)
-        if need:
-            key = (dev, stream)
-            workspace = _attention_workspaces.get(key)
-            if workspace is None or workspace.numel() < need:
-                workspace = new_workspace(need, dev)
-                _attention_workspaces[key] = workspace
-    else:
-        _need(workspace, "workspace", None, None, dev)
-    status = library().qk_kv_attention(
-        seqs, tokens, heads, kv_heads, dim, q.data_ptr(), ldq, _IN_DTYPES[dt], *args, lens.data_ptr(),
-        0 if cu is None else cu.data_ptr(), max_q, max_kv, dim ** -0.5 if scale is None else scale, window,
-        out.data_ptr(), lse.data_ptr() if return_lse else 0, 0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
-    if status != QK_OK and status < 1000:  # part of the call may have run: a fresh workspace next time
-        _attention_workspaces.pop((dev, stream), None)
-    _check(status)
-    return (out, lse) if return_lse else out
+    return _bind().kv_attention(q, cache, table, lens, cu, scale, window, max_q, max_kv, out, return_lse,
+                                workspace)
