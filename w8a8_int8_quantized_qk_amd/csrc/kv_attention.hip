@@ -77,12 +77,12 @@ struct Tile {
 };
 
 // Columns col0 .. col0 + size of the sequence whose rows are already in t.
-__device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0, int size) {
+__device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0, int size, int len) {
   const int64_t all = static_cast<int64_t>(t.rows) * p.group;
   if (col0 >= all) return;
   t.col0 = static_cast<int>(col0);
   t.ncols = static_cast<int>(min(all - col0, static_cast<int64_t>(size)));
-  t.len = min(max(p.a.lens[t.seq], 0), p.a.max_kv);  // max_kv is at most what the table covers
+  t.len = min(max(len, 0), p.a.max_kv);  // max_kv is at most what the table covers
   const int first_pos = t.len - t.rows + t.col0 / p.group;
   const int last_pos = t.len - t.rows + (t.col0 + t.ncols - 1) / p.group;
   t.hi = min(last_pos + 1, t.len);
@@ -91,35 +91,35 @@ __device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0
   t.live = true;
 }
 
-// Rows of sequence t.seq; false if the offsets point outside.
-__device__ __forceinline__ bool set_rows(const Params& p, Tile& t) {
-  if (!p.a.cu) {
-    t.rows = 1;
-    t.row0 = t.seq;
-    return true;
-  }
-  const int first = p.a.cu[t.seq];
-  t.rows = p.a.cu[t.seq + 1] - first;
-  t.row0 = first;
-  return first >= 0 && t.rows > 0 && t.rows <= p.a.tokens - first;
-}
-
 // Tiles of 16 columns: item = sequence * tiles + tile; longer sequences are
 // the other kernel's.
 __device__ __forceinline__ Tile find_cols(const Params& p, unsigned item) {
   Tile t{};
   t.seq = static_cast<int>(item / static_cast<unsigned>(p.tiles));
-  if (!set_rows(p, t) || (p.a.cu && static_cast<int64_t>(t.rows) * p.group > kSmall)) return t;
-  set_range(p, t, static_cast<int64_t>(item - static_cast<unsigned>(t.seq) * p.tiles) * kCols, kCols);
+  t.rows = 1;
+  t.row0 = t.seq;
+  if (p.a.cu) {
+    const int first = p.a.cu[t.seq];
+    t.rows = p.a.cu[t.seq + 1] - first;
+    t.row0 = first;
+    if (first < 0 || t.rows <= 0 || t.rows > p.a.tokens - first) return t;
+    if (static_cast<int64_t>(t.rows) * p.group > kSmall) return t;
+  }
+  set_range(p, t, static_cast<int64_t>(item - static_cast<unsigned>(t.seq) * p.tiles) * kCols, kCols,
+            p.a.lens[t.seq]);
   return t;
 }
 
 // Tiles of 128 columns, laid over the ragged rows.
 __device__ __forceinline__ Tile find_tile(const Params& p, int64_t item) {
   Tile t{};
-  t.seq = kv::find_sequence(item, p.a.cu, p.a.seqs, p.group, kTileCols, 1);
-  if (t.seq < 0 || !set_rows(p, t) || static_cast<int64_t>(t.rows) * p.group <= p.small) return t;
-  set_range(p, t, (item - kv::item_base(t.row0, p.group, kTileCols, 1, t.seq)) * kTileCols, kTileCols);
+  const kv::Owner o = kv::find_sequence(item, p.a.cu, p.a.lens, p.a.seqs, p.group, kTileCols, 1);
+  t.seq = o.seq;
+  t.rows = o.next - o.first;
+  t.row0 = o.first;
+  if (o.seq < 0 || o.first < 0 || t.rows <= 0 || t.rows > p.a.tokens - o.first) return t;
+  if (static_cast<int64_t>(t.rows) * p.group <= p.small) return t;
+  set_range(p, t, (item - kv::item_base(t.row0, p.group, kTileCols, 1, t.seq)) * kTileCols, kTileCols, o.value);
   return t;
 }
 
@@ -945,7 +945,7 @@ Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q,
   const int64_t live = (mixed ? static_cast<int64_t>(seqs) * ((group + kCols - 1) / kCols) : items) * kv_heads;
   const int64_t range = range_of(max_kv, window, kCols);
   int64_t chunks = 1;
-  if (range > 1024 && live < 256) chunks = 256 / live;
+  if (range > 640 && live < 256) chunks = 256 / live;
   if (range > 6144 && live >= 256) chunks = (range + 2047) / 2048;
   constexpr int64_t kStep = kWaves * kGroup;
   const int64_t chunk = ((range + chunks - 1) / chunks + kStep - 1) / kStep * kStep;

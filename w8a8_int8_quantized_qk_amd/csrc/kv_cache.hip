@@ -64,10 +64,9 @@ __device__ __forceinline__ Task find_task(const Params& p) {
   const int64_t item = ih / p.c.heads;
   t.head = static_cast<int>(ih - item * p.c.heads);
   if (item >= p.items) return t;
-  const int b = kv::find_sequence(item, p.a.cu, p.a.seqs, 1, p.c.block, 2);
-  if (b < 0) return t;
-  const int first = p.a.cu[b], n = p.a.cu[b + 1] - first, start = p.a.start[b];
-  if (first < 0 || n <= 0 || n > p.a.tokens - first || start < 0 || start > 0x7fffffff - n) return t;
+  const kv::Owner o = kv::find_sequence(item, p.a.cu, p.a.start, p.a.seqs, 1, p.c.block, 2);
+  const int b = o.seq, first = o.first, n = o.next - o.first, start = o.value;
+  if (b < 0 || first < 0 || n <= 0 || n > p.a.tokens - first || start < 0 || start > 0x7fffffff - n) return t;
   const int64_t at = start / p.c.block + (item - kv::item_base(first, 1, p.c.block, 2, b));
   const int64_t pos0 = at * p.c.block;
   if (pos0 >= static_cast<int64_t>(start) + n || at >= p.c.width) return t;
@@ -141,34 +140,43 @@ __global__ __launch_bounds__(512) void kv_write_kernel(Params p) {
   // keys: [unit][8 columns]; values: [4 pair + quarter][4 positions of either column]
   float x[NU > NC * 4 ? NU : NC * 4][8];
 
+  // Loads are unconditional, from the nearest row or column that there is, and
+  // what lies outside is masked afterwards: a load under a condition would be
+  // waited for on the spot.
   uint32_t top = 0;
   if (t.live) {
     if (!t.value) {
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        const int u = lane + 64 * i, r = (u * p.magic) >> 16, pos = p0 + r;
-        const int d = (u - r * (dim / 8)) * 8;
-        if (u < 2 * dim && pos >= t.lo && pos < t.hi) {
-          load8<DT>(p.a.k, (t.row + pos) * p.a.ldk + head0 + d, x[i]);
+        const int u = min(lane + 64 * i, 2 * dim - 1), r = (u * p.magic) >> 16;
+        const int d = (u - r * (dim / 8)) * 8, pos = min(max(p0 + r, t.lo), t.hi - 1);
+        load8<DT>(p.a.k, (t.row + pos) * p.a.ldk + head0 + d, x[i]);
+      }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = qm::max_u32(top, __float_as_uint(x[i][e]) & 0x7fffffffu);
-        }
+      for (int i = 0; i < NU; ++i) {
+        const int u = min(lane + 64 * i, 2 * dim - 1), pos = p0 + ((u * p.magic) >> 16);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = qm::max_u32(m, __float_as_uint(x[i][e]) & 0x7fffffffu);
+        top = qm::max_u32(top, pos >= t.lo && pos < t.hi ? m : 0u);
       }
     } else {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int d = 2 * (lane + 64 * c);
+        const int d = 2 * (lane + 64 * c), dc = d < dim ? d : 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int pos = p0 + i;
-          float a = 0.0f, b = 0.0f;
-          if (d < dim && pos >= t.lo && pos < t.hi)
-            load2<DT>(p.a.v, (t.row + pos) * p.a.ldv + head0 + d, a, b);
-          x[c * 4 + i / 4][i % 4] = a;
-          x[c * 4 + i / 4][4 + i % 4] = b;
-          top = qm::max_u32(top, qm::max_u32(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu));
+          const int pos = min(max(p0 + i, t.lo), t.hi - 1);
+          load2<DT>(p.a.v, (t.row + pos) * p.a.ldv + head0 + dc, x[c * 4 + i / 4][i % 4], x[c * 4 + i / 4][4 + i % 4]);
         }
       }
+      // every row that was loaded is one of the call's, so none needs a mask for
+      // the maximum: the nearest row only repeats
+#pragma unroll
+      for (int c = 0; c < 4 * NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = qm::max_u32(top, __float_as_uint(x[c][e]) & 0x7fffffffu);
+      if (p0 >= t.hi || p0 + 16 <= t.lo) top = 0;  // no new position among these 16
     }
   }
   float amax = qm::wave_max_nonneg(__uint_as_float(top));
@@ -203,26 +211,27 @@ __global__ __launch_bounds__(512) void kv_write_kernel(Params p) {
 
   if (!t.value) {
     uint8_t* const tile = p.c.k + t.tile * P * dim;
+    uint2 old[NU];
+    if (moves) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+        old[i] = *reinterpret_cast<const uint2*>(tile + static_cast<int64_t>(p0) * dim + min(lane + 64 * i, 2 * dim - 1) * 8);
+    }
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int u = lane + 64 * i, rr = (u * p.magic) >> 16, pos = p0 + rr;
-      if (u >= 2 * dim || pos >= t.hi) continue;
-      uint2* const at = reinterpret_cast<uint2*>(tile + static_cast<int64_t>(p0) * dim + u * 8);
+      if (u >= 2 * dim || pos >= t.hi || (pos < t.lo && !moves)) continue;
       uint2 w = make_uint2(0, 0);
-      if (pos >= t.lo) {
-        if (finite) {
+      if (finite) {
+        if (pos >= t.lo) {
           w.x = kv::codes4_of<FP8>(reinterpret_cast<const float(&)[4]>(x[i][0]), s, r);
           w.y = kv::codes4_of<FP8>(reinterpret_cast<const float(&)[4]>(x[i][4]), s, r);
+        } else {
+          w.x = moved4<FP8>(old[i].x, s0, s, r);
+          w.y = moved4<FP8>(old[i].y, s0, s, r);
         }
-        *at = w;
-      } else if (moves) {
-        if (finite) {
-          const uint2 old = *at;
-          w.x = moved4<FP8>(old.x, s0, s, r);
-          w.y = moved4<FP8>(old.y, s0, s, r);
-        }
-        *at = w;
       }
+      *reinterpret_cast<uint2*>(tile + static_cast<int64_t>(p0) * dim + u * 8) = w;
     }
   } else {
     if (p0 >= t.hi || (p0 + 16 <= t.lo && !moves)) return;  // nothing of these 16 positions changes
@@ -230,37 +239,40 @@ __global__ __launch_bounds__(512) void kv_write_kernel(Params p) {
     // byte masks of the 16 positions: new ones, earlier ones
     const int nlo = min(max(t.lo - p0, 0), 16), nhi = min(max(t.hi - p0, 0), 16);
     const bool whole = nlo == 0 && nhi == 16;
+    uint4 old[NC][2];
+    if (!whole) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int d = 2 * (lane + 64 * c);
+          old[c][h] = *reinterpret_cast<const uint4*>(tile + static_cast<int64_t>((d < dim ? d : 0) + h) * P);
+        }
+    }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int d = 2 * (lane + 64 * c);
       if (d >= dim) continue;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint4* const at = reinterpret_cast<uint4*>(tile + static_cast<int64_t>(d + h) * P);
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           w[i] = finite ? kv::codes4_of<FP8>(reinterpret_cast<const float(&)[4]>(x[c * 4 + i][4 * h]), s, r) : 0u;
         if (!whole) {
-          const uint4 old4 = *at;
-          const uint32_t old[4] = {old4.x, old4.y, old4.z, old4.w};
+          const uint32_t was[4] = {old[c][h].x, old[c][h].y, old[c][h].z, old[c][h].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t held = old[i];
-            if (moves) {
-              const uint32_t mv = finite ? moved4<FP8>(held, s0, s, r) : 0u;
-              const int e = min(max(nlo - 4 * i, 0), 4);  // earlier positions in this word
-              const uint32_t em = e >= 4 ? 0xffffffffu : (1u << (8 * e)) - 1u;
-              held = (mv & em) | (held & ~em);
-            }
+            // bytes of the word's earlier positions, and of those up to the new end
             const int f = min(max(nlo - 4 * i, 0), 4), g = min(max(nhi - 4 * i, 0), 4);
             const uint32_t below = f >= 4 ? 0xffffffffu : (1u << (8 * f)) - 1u;
             const uint32_t upto = g >= 4 ? 0xffffffffu : (1u << (8 * g)) - 1u;
-            const uint32_t nm = upto & ~below;
-            w[i] = (w[i] & nm) | (held & ~nm);
+            uint32_t held = was[i];
+            if (moves) held = ((finite ? moved4<FP8>(held, s0, s, r) : 0u) & below) | (held & ~below);
+            w[i] = (w[i] & upto & ~below) | (held & (below | ~upto));
           }
         }
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(tile + static_cast<int64_t>(d + h) * P) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }
@@ -297,11 +309,15 @@ __global__ __launch_bounds__(512) void kv_read_kernel(Params p) {
   if (!t.value) {
     const float s = p.c.k_scale[t.tile];
     const uint8_t* const tile = p.c.k + t.tile * P * dim + static_cast<int64_t>(p0) * dim;
+    uint2 codes[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+      codes[i] = *reinterpret_cast<const uint2*>(tile + min(lane + 64 * i, 2 * dim - 1) * 8);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int u = lane + 64 * i, r = (u * p.magic) >> 16, pos = p0 + r;
       if (u >= 2 * dim || pos < t.lo || pos >= t.hi) continue;
-      const uint2 w = *reinterpret_cast<const uint2*>(tile + u * 8);
+      const uint2 w = codes[i];
       float f[8];
       kv::codes4_to_float<FP8>(w.x, reinterpret_cast<float(&)[4]>(f[0]));
       kv::codes4_to_float<FP8>(w.y, reinterpret_cast<float(&)[4]>(f[4]));

@@ -32,21 +32,31 @@ __host__ __device__ __forceinline__ int64_t item_base(int64_t row, int mul, int 
   return row * mul / size + static_cast<int64_t>(extra) * b;
 }
 
-// The sequence that owns `item`: the number of bases at or below it, less
-// one.  The lanes of a wave look at 64 sequences at a time; the result is
-// uniform.  cu null: one row per sequence.
-__device__ __forceinline__ int find_sequence(int64_t item, const int* cu, int seqs, int mul, int size,
-                                             int extra) {
+// The sequence that owns `item`, its first row, the next one's, and its entry
+// of `each` (start or length): the last sequence whose base is at or below the
+// item.  The lanes of a wave look at 64 sequences at a time, each lane with its
+// sequence's numbers in hand, so that nothing has to be loaded again for the
+// one that is found; the result is uniform.  seq < 0: none.
+struct Owner {
+  int seq, first, next, value;
+};
+__device__ __forceinline__ Owner find_sequence(int64_t item, const int* cu, const int* each, int seqs, int mul,
+                                               int size, int extra) {
   const int lane = threadIdx.x & 63;
-  int found = 0;
+  Owner o{-1, 0, 0, 0};
   for (int b0 = 0; b0 < seqs; b0 += 64) {
-    const int b = b0 + lane;
-    const bool below = b < seqs && item_base(cu ? cu[b] : b, mul, size, extra, b) <= item;
+    const int b = min(b0 + lane, seqs - 1);
+    const int first = cu[b], next = cu[b + 1], value = each[b];
+    const bool below = b0 + lane < seqs && item_base(first, mul, size, extra, b) <= item;
     const int n = __popcll(__ballot(below));
-    found += n;
+    if (n == 0) break;
+    o.seq = b0 + n - 1;
+    o.first = __builtin_amdgcn_readlane(first, n - 1);
+    o.next = __builtin_amdgcn_readlane(next, n - 1);
+    o.value = __builtin_amdgcn_readlane(value, n - 1);
     if (n < 64) break;
   }
-  return found - 1;
+  return o;
 }
 
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));

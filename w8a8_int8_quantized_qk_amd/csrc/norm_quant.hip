@@ -211,12 +211,29 @@ __device__ __forceinline__ bool row_scale_of(float top, float& s, float& r) {
   return finite;
 }
 
+// 16 bytes of a row from element `at` on, as they are, and as values.
+template <int DT>
+__device__ __forceinline__ void raw_load(Raw16<Elem<DT>::kBytes>& r, const void* row, int at) {
+  r = *reinterpret_cast<const Raw16<Elem<DT>::kBytes>*>(static_cast<const char*>(row) +
+                                                        static_cast<size_t>(at) * Elem<DT>::kBytes);
+}
+template <int DT>
+__device__ __forceinline__ void raw_values(const Raw16<Elem<DT>::kBytes>& r, float* v) {
+  Elem<DT>::unpack(make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]), v);
+}
+
 // A row in registers: THREADS threads (one wave, four rows per workgroup; or
-// one workgroup) with UPT units each.
-template <int DT, bool RES, bool FP8, int UPT, int THREADS>
+// one workgroup) with UPT units each; k is at least one unit.  Every load is
+// unconditional and asked for before the first is used: a thread without a
+// unit loads the row's last elements, and a row's last, partial unit is moved
+// back to end with the row, so it computes the elements before it a second
+// time, with the same results; only the sum leaves them out.  W32: a binary32
+// weight beside a 16-bit row.
+template <int DT, bool RES, bool FP8, int UPT, int THREADS, bool W32>
 __global__ __launch_bounds__(kBlock) void norm_rows(NormParams p, int m) {
   using E = Elem<DT>;
   constexpr int P = E::kPerUnit;
+  constexpr int WT = W32 ? QK_F32 : DT, WN = P / Elem<WT>::kPerUnit;
   const int t = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int64_t row = THREADS == 64 ? static_cast<int64_t>(blockIdx.x) * (kBlock / 64) + (threadIdx.x >> 6)
                                     : blockIdx.x;
@@ -225,21 +242,41 @@ __global__ __launch_bounds__(kBlock) void norm_rows(NormParams p, int m) {
   const char* xrow = static_cast<const char*>(p.x) + row * p.ldx * E::kBytes;
   const char* rrow = RES ? static_cast<const char*>(p.residual) + row * p.ldr * E::kBytes : nullptr;
 
+  Raw16<E::kBytes> xr[UPT], rr[UPT];
+  Raw16<Elem<WT>::kBytes> wr[UPT][WN];
+  int at[UPT];
+#pragma unroll
+  for (int j = 0; j < UPT; ++j) {
+    at[j] = min((t + j * THREADS) * P, k - P);
+    raw_load<DT>(xr[j], xrow, at[j]);
+    if constexpr (RES) raw_load<DT>(rr[j], rrow, at[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < UPT; ++j)
+#pragma unroll
+    for (int h = 0; h < WN; ++h) raw_load<WT>(wr[j][h], p.weight, at[j] + h * (P / WN));
+
   float v[UPT][P];
   double sum = 0.0;
 #pragma unroll
   for (int j = 0; j < UPT; ++j) {
-    const int u = t + j * THREADS;
-    if (u < units) {
-      load_values<DT>(xrow, k, u, v[j]);
-      if constexpr (RES) {
-        float a[P];
-        load_values<DT>(rrow, k, u, a);
+    raw_values<DT>(xr[j], v[j]);
+    if constexpr (RES) {
+      float a[P];
+      raw_values<DT>(rr[j], a);
 #pragma unroll
-        for (int e = 0; e < P; ++e) v[j][e] += a[e];
-      }
+      for (int e = 0; e < P; ++e) v[j][e] += a[e];
+    }
+    const int first = (t + j * THREADS) * P;  // the unit's own elements begin here
+    if (first + P <= k) {
 #pragma unroll
       for (int e = 0; e < P; ++e) sum = __builtin_fma(static_cast<double>(v[j][e]), static_cast<double>(v[j][e]), sum);
+    } else {
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const double d = at[j] + e >= first ? static_cast<double>(v[j][e]) : 0.0;
+        sum = __builtin_fma(d, d, sum);
+      }
     }
   }
   const float inv = inverse_rms(row_sum<THREADS>(sum), k, p.eps);
@@ -247,16 +284,26 @@ __global__ __launch_bounds__(kBlock) void norm_rows(NormParams p, int m) {
   float top = 0.0f;
 #pragma unroll
   for (int j = 0; j < UPT; ++j) {
-    const int u = t + j * THREADS;
-    if (u < units) {
-      if constexpr (RES) store_values<DT>(static_cast<char*>(p.r_out) + row * p.ldo * E::kBytes, k, u, v[j]);
-      float w[P];
-      load_weight<DT>(p.weight, p.w_f32, k, u, w);
+    if constexpr (RES) {
+      if (t + j * THREADS < units) {
+        Raw16<E::kBytes> o;
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        v[j][e] = v[j][e] * inv * w[e];
-        if (u * P + e < k) top = max_abs_bits(top, v[j][e]);
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (DT == QK_F32)
+            o.w[i] = __float_as_uint(v[j][i]);
+          else
+            o.w[i] = qm::pack2_narrow<DT>(v[j][2 * i], v[j][2 * i + 1]);
+        }
+        *reinterpret_cast<Raw16<E::kBytes>*>(static_cast<char*>(p.r_out) + (row * p.ldo + at[j]) * E::kBytes) = o;
       }
+    }
+    float w[P];
+#pragma unroll
+    for (int h = 0; h < WN; ++h) raw_values<WT>(wr[j][h], w + h * (P / WN));
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      v[j][e] = v[j][e] * inv * w[e];
+      top = max_abs_bits(top, v[j][e]);
     }
   }
   top = row_max_abs<THREADS>(top);
@@ -265,12 +312,19 @@ __global__ __launch_bounds__(kBlock) void norm_rows(NormParams p, int m) {
   if (t == 0) p.scale[row] = s;
 #pragma unroll
   for (int j = 0; j < UPT; ++j) {
-    const int u = t + j * THREADS;
-    if (u < units) store_row_codes<DT, FP8>(p.q + row * static_cast<int64_t>(k), k, u, finite, v[j], s, r);
+    if (t + j * THREADS >= units) continue;
+    uint32_t c[P / 4];
+#pragma unroll
+    for (int i = 0; i < P / 4; ++i) c[i] = finite ? codes4<FP8>(v[j] + 4 * i, s, r) : 0u;
+    uint8_t* const q = p.q + row * static_cast<int64_t>(k) + at[j];
+    if constexpr (P == 8)
+      *reinterpret_cast<Raw8<1>*>(q) = Raw8<1>{{c[0], c[1]}};
+    else
+      *reinterpret_cast<Raw4*>(q) = Raw4{c[0]};
   }
 }
 
-// Rows longer than the registers hold: three passes over the row.  The
+// Rows longer than the registers hold, or shorter than a unit: three passes.  The
 // residual's sum is stored in the last one, by the thread that read it in
 // every pass, so it may replace the residual or x in place.
 template <int DT, bool RES, bool FP8>
@@ -322,19 +376,26 @@ __global__ __launch_bounds__(kBlock) void norm_rows_long(NormParams p) {
   }
 }
 
-template <int DT, bool RES, bool FP8>
+template <int DT, bool RES, bool FP8, bool W32>
 hipError_t dispatch(int m, const NormParams& p, hipStream_t stream) {
   constexpr int P = Elem<DT>::kPerUnit;
   const int units = p.k / P + (p.k % P != 0);
   const dim3 block(kBlock), rows(static_cast<unsigned>(m)), quads((static_cast<unsigned>(m) + 3) / 4);
-  if (units <= 64) return launch(norm_rows<DT, RES, FP8, 1, 64>, quads, block, 0, stream, p, m);
-  if (units <= 128) return launch(norm_rows<DT, RES, FP8, 2, 64>, quads, block, 0, stream, p, m);
-  if (units <= kBlock) return launch(norm_rows<DT, RES, FP8, 1, kBlock>, rows, block, 0, stream, p, m);
-  if (units <= kBlock * 2) return launch(norm_rows<DT, RES, FP8, 2, kBlock>, rows, block, 0, stream, p, m);
-  if (units <= kBlock * 4) return launch(norm_rows<DT, RES, FP8, 4, kBlock>, rows, block, 0, stream, p, m);
-  if (units <= kBlock * kMaxUnits)
-    return launch(norm_rows<DT, RES, FP8, kMaxUnits, kBlock>, rows, block, 0, stream, p, m);
-  return launch(norm_rows_long<DT, RES, FP8>, rows, block, 0, stream, p);
+  if (p.k < P || units > kBlock * kMaxUnits)
+    return launch(norm_rows_long<DT, RES, FP8>, rows, block, 0, stream, p);
+  if (units <= 64) return launch(norm_rows<DT, RES, FP8, 1, 64, W32>, quads, block, 0, stream, p, m);
+  if (units <= 128) return launch(norm_rows<DT, RES, FP8, 2, 64, W32>, quads, block, 0, stream, p, m);
+  if (units <= kBlock) return launch(norm_rows<DT, RES, FP8, 1, kBlock, W32>, rows, block, 0, stream, p, m);
+  if (units <= kBlock * 2) return launch(norm_rows<DT, RES, FP8, 2, kBlock, W32>, rows, block, 0, stream, p, m);
+  if (units <= kBlock * 4) return launch(norm_rows<DT, RES, FP8, 4, kBlock, W32>, rows, block, 0, stream, p, m);
+  return launch(norm_rows<DT, RES, FP8, kMaxUnits, kBlock, W32>, rows, block, 0, stream, p, m);
+}
+
+template <int DT, bool RES, bool FP8>
+hipError_t dispatch_weight(int m, const NormParams& p, hipStream_t stream) {
+  if constexpr (DT != QK_F32)
+    if (p.w_f32) return dispatch<DT, RES, FP8, true>(m, p, stream);
+  return dispatch<DT, RES, FP8, false>(m, p, stream);
 }
 
 template <int DT>
@@ -342,8 +403,8 @@ hipError_t dispatch_dtype(const RmsNormQuantArgs& a, hipStream_t stream) {
   const NormParams p{a.k,     a.x,      a.ldx, a.residual, a.ldr, a.weight, a.weight_f32,
                      a.eps,   a.r_out,  a.ldo, a.q,        a.scale};
   if (a.residual)
-    return a.fp8 ? dispatch<DT, true, true>(a.m, p, stream) : dispatch<DT, true, false>(a.m, p, stream);
-  return a.fp8 ? dispatch<DT, false, true>(a.m, p, stream) : dispatch<DT, false, false>(a.m, p, stream);
+    return a.fp8 ? dispatch_weight<DT, true, true>(a.m, p, stream) : dispatch_weight<DT, true, false>(a.m, p, stream);
+  return a.fp8 ? dispatch_weight<DT, false, true>(a.m, p, stream) : dispatch_weight<DT, false, false>(a.m, p, stream);
 }
 
 }  // namespace
