@@ -129,8 +129,8 @@ struct Place {
   int inner, head;
   unsigned item;
 };
-__device__ __forceinline__ Place place_of(const Params& p, int inner) {
-  const unsigned b = blockIdx.x, r = b / static_cast<unsigned>(inner);
+__device__ __forceinline__ Place place_of(const Params& p, unsigned b, int inner) {
+  const unsigned r = b / static_cast<unsigned>(inner);
   const unsigned item = r / static_cast<unsigned>(p.c.heads);
   return Place{static_cast<int>(b - r * inner), static_cast<int>(r - item * p.c.heads), item};
 }
@@ -328,22 +328,33 @@ __device__ __forceinline__ void join_chunks(const Params& p, const Tile& t, int 
   }
 }
 
+// The bodies share their kernel's dynamic LDS; this many binary16.  (Named in
+// the body that uses it: through a pointer from elsewhere the compiler keeps
+// fewer reads in flight, 69 against 64 us for a prompt of 1000 rows.)
+template <int DP>
+constexpr int kLdsHalves = 4 * kGroup * DP;
+
 // One workgroup: one tile of up to 16 columns, one kv head, one chunk of
 // positions.  Its four waves take groups of 64 positions in turn, each with a
 // maximum, a sum and an output of its own, and join them through LDS at the
 // end; nothing is shared before, so no wave waits for another.  The workgroup
 // that arrives last at a tile joins its chunks.
 template <int DT, bool FP8, int DP>
-__global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_cols_kernel(Params p) {
+__device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
+  // the waves' outputs, [wave][column][element], elements exchanged in fours by
+  // the column's number so that columns fall on different banks
+  extern __shared__ __align__(16) _Float16 lds_all[];
+  float* const lds_o = reinterpret_cast<float*>(lds_all);
+  __shared__ struct {
+    float m[kWaves][kCols], l[kWaves][kCols];
+    unsigned last;
+  } lds;
   constexpr int KC = DP / 64;  // 16-byte pieces of a K row per lane
   constexpr int VC = DP / 16;  // 16-row pieces of V
-  __shared__ float lds_o[kWaves][kCols][DP + 4];
-  __shared__ float lds_m[kWaves][kCols], lds_l[kWaves][kCols];
-  __shared__ unsigned lds_last;
 
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Place at = place_of(p, p.splits);
+  const Place at = place_of(p, block, p.splits);
   // Workgroups go round the eight dies in turn, and early chunks have work in
   // every sequence, late ones in few: the chunks are turned by the tile's
   // number so that no die gets the same one of each (64 requests of up to 8192
@@ -432,7 +443,7 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_co
   auto group = [&](int t0, auto half, auto more) {
     constexpr int S = decltype(half)::value % kSets;
     constexpr std::integral_constant<int, 1 - decltype(half)::value> other{};
-    if constexpr (decltype(more)::value && kSets == 2) {
+    if (kSets == 2 && more) {
       load_scales(other);
       load_k(t0 + kStep, other);
       load_v(t0 + kStep, other);
@@ -448,7 +459,7 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_co
         acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[S][i][c].z, kr[S][i][c].w), qf[2 * c + 1], acc[i], 0, 0, 0);
       }
     }
-    if constexpr (decltype(more)::value && kSets == 1) load_k(t0 + kStep, other);
+    if (kSets == 1 && more) load_k(t0 + kStep, other);
     float s[1][16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[0][i] = acc[i >> 2][i & 3];
@@ -483,7 +494,7 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_co
       o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[S][i].x, vr[S][i].y), pf[0], o[i], 0, 0, 0);
       o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(vr[S][i].z, vr[S][i].w), pf[1], o[i], 0, 0, 0);
     }
-    if constexpr (decltype(more)::value && kSets == 1) {
+    if (kSets == 1 && more) {
       load_scales(other);
       load_v(t0 + kStep, other);
       next_blocks(t0 + 2 * kStep);
@@ -499,8 +510,7 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_co
     load_v(t0, even);
     next_blocks(t0 + kStep);
     if constexpr (kSets == 1) {
-      for (; t0 + kStep < end; t0 += kStep) group(t0, even, std::true_type{});
-      group(t0, even, std::false_type{});
+      for (; t0 < end; t0 += kStep) group(t0, even, t0 + kStep < end);
     } else {
       for (; t0 + 2 * kStep < end; t0 += 2 * kStep) {
         group(t0, even, std::true_type{});
@@ -518,12 +528,12 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_co
   // join the four waves
   l = column_sum<true>(l);
   if (g == 0) {
-    lds_m[wave][n] = m;
-    lds_l[wave][n] = l;
+    lds.m[wave][n] = m;
+    lds.l[wave][n] = l;
   }
 #pragma unroll
   for (int i = 0; i < VC; ++i)
-    *reinterpret_cast<float4_t*>(&lds_o[wave][n][16 * i + 4 * g]) = o[i];
+    *reinterpret_cast<float4_t*>(lds_o + (wave * kCols + n) * DP + ((16 * i + 4 * g) ^ (4 * n))) = o[i];
   __syncthreads();
 
   const unsigned tile_id = at.item * static_cast<unsigned>(p.c.heads) + head;
@@ -532,15 +542,16 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_co
   const int pairs = dim >> 1;
   for (int i = threadIdx.x; i < t.ncols * pairs; i += 64 * kWaves) {
     const int k = i / pairs, d = 2 * (i - k * pairs);
-    float mm = lds_m[0][k], ll = 0.0f, a = 0.0f, b = 0.0f;
+    float mm = lds.m[0][k], ll = 0.0f, a = 0.0f, b = 0.0f;
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) mm = __builtin_fmaxf(mm, lds_m[w][k]);
+    for (int w = 1; w < kWaves; ++w) mm = __builtin_fmaxf(mm, lds.m[w][k]);
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const float f = __builtin_amdgcn_exp2f(lds_m[w][k] - mm);
-      ll = __builtin_fmaf(lds_l[w][k], f, ll);
-      a = __builtin_fmaf(lds_o[w][k][d], f, a);
-      b = __builtin_fmaf(lds_o[w][k][d + 1], f, b);
+      const float f = __builtin_amdgcn_exp2f(lds.m[w][k] - mm);
+      ll = __builtin_fmaf(lds.l[w][k], f, ll);
+      const float2 v = *reinterpret_cast<const float2*>(lds_o + (w * kCols + k) * DP + (d ^ (4 * k)));
+      a = __builtin_fmaf(v.x, f, a);
+      b = __builtin_fmaf(v.y, f, b);
     }
     if (whole) {
       const int64_t out_row = column_of(p, t, head, k).out_row;
@@ -563,10 +574,10 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_co
     const unsigned before = __hip_atomic_fetch_add(p.arrived + tile_id, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const bool last = before + 1 == static_cast<unsigned>(t.splits);
     if (last) __hip_atomic_store(p.arrived + tile_id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    lds_last = last;
+    lds.last = last;
   }
   __syncthreads();
-  if (lds_last) join_chunks<DT>(p, t, head, slot);
+  if (lds.last) join_chunks<DT>(p, t, head, slot);
 }
 
 // One workgroup: one tile of 128 columns, one kv head, one chunk of positions
@@ -579,18 +590,19 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_co
 // exchanged by its number so that eight consecutive rows fall on different
 // banks.
 template <int DT, bool FP8, int DP>
-__global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_tile_kernel(Params p) {
+__device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
+  extern __shared__ __align__(16) _Float16 lds_all[];
+  _Float16(*const lds_k)[kGroup * DP] = reinterpret_cast<_Float16(*)[kGroup * DP]>(lds_all);
+  _Float16(*const lds_v)[kGroup * DP] = lds_k + 2;
+  __shared__ __align__(16) float lds_s[2][3][4];  // of each 16 positions: k scale, log2 v scale, 1 / v scale
   constexpr int KP = DP / 8;       // 16-byte pieces of a K row (8 binary16)
   constexpr int NC = DP / 64;      // 16-byte loads per thread, of K and of V
   constexpr int ND = DP / 32;      // 32-row pieces of V
   constexpr int RB = DP / 16;      // 16-byte pieces of a row of codes
-  __shared__ __align__(16) _Float16 lds_k[2][kGroup * DP];
-  __shared__ __align__(16) _Float16 lds_v[2][DP * kGroup];
-  __shared__ __align__(16) float lds_s[2][3][4];  // of each 16 positions: k scale, log2 v scale, 1 / v scale
 
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  Place at = place_of(p, p.splits);
+  Place at = place_of(p, block, p.splits);
   at.item = p.items - 1 - at.item;  // later rows see more: the longest work first
   const int split = at.inner, head = at.head;
   const Tile t = find_tile(p, at.item);
@@ -643,7 +655,7 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
     vb = entry(t0 + 16 * wave);
   };
   auto load_step = [&](int t0, auto half) {
-    constexpr int S = decltype(half)::value % kSets;
+    const int S = half % kSets;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int pos = (t0 + 16 * kpart(i)) & (P - 1);
@@ -663,7 +675,7 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
   };
   // the step at t0 into half H of LDS
   auto put_step = [&](int t0, auto half) {
-    constexpr int H = decltype(half)::value, S = H % kSets;
+    const int H = half, S = H % kSets;
     half8_t* const kl = reinterpret_cast<half8_t*>(lds_k[H]);
     half8_t* const vl = reinterpret_cast<half8_t*>(lds_v[H]);
     if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) {
@@ -690,7 +702,7 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
   };
   // the step at t0, in half H of LDS
   auto work = [&](int t0, auto half) {
-    constexpr int H = decltype(half)::value;
+    const int H = half;
     if (t0 >= any_hi || t0 + kGroup <= any_lo) return;
     const half8_t* const kl = reinterpret_cast<const half8_t*>(lds_k[H]);
     const half8_t* const vl = reinterpret_cast<const half8_t*>(lds_v[H]);
@@ -700,8 +712,9 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[a][e] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < DP / 16; ++i)
+      for (int i = 0; i < DP / 16; ++i) {
         acc[a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[(32 * a + n) * KP + ((2 * i + h) ^ (n & 7))], qf[i], acc[a], 0, 0, 0);
+      }
     }
     // register 8 b + e of acc[a] is position 32 a + 16 b + 8 h + e
     float s[4][8], c[4], bias[4], inv_vs[4];
@@ -740,22 +753,20 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
 #pragma unroll
       for (int e = 0; e < 8; ++e) pf[b][e] = static_cast<_Float16>(s[b][e]);
 #pragma unroll
-    for (int i = 0; i < ND; ++i)
+    for (int i = 0; i < ND; ++i) {
 #pragma unroll
       for (int s4 = 0; s4 < 4; ++s4)
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[(32 * i + n) * 8 + ((2 * s4 + h) ^ (n & 7))], pf[s4], o[i], 0, 0, 0);
+    }
   };
   // One step: ask for a later one, work on this one, write the next.
-  auto step = [&](int t0, auto half) {
-    constexpr int H = decltype(half)::value;
-    using Same = std::integral_constant<int, H>;
-    using Other = std::integral_constant<int, 1 - H>;
+  auto step = [&](int t0, auto half, auto other) {
     if (t0 + kSets * kGroup < end) {
-      load_step(t0 + kSets * kGroup, std::integral_constant<int, (H + kSets) % 2>{});
+      load_step(t0 + kSets * kGroup, half);  // with one set there is no other
       load_blocks(t0 + (kSets + 1) * kGroup);
     }
-    work(t0, Same{});
-    if (t0 + kGroup < end) put_step(t0 + kGroup, Other{});
+    work(t0, half);
+    if (t0 + kGroup < end) put_step(t0 + kGroup, other);
     __syncthreads();
   };
 
@@ -772,9 +783,13 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
     put_step(begin, Even{});
   }
   __syncthreads();
-  for (int t0 = begin; t0 < end; t0 += 2 * kGroup) {
-    step(t0, Even{});
-    if (t0 + kGroup < end) step(t0 + kGroup, Odd{});
+  if constexpr (kSets == 1) {
+    for (int t0 = begin, half = 0; t0 < end; t0 += kGroup, half ^= 1) step(t0, half, half ^ 1);
+  } else {
+    for (int t0 = begin; t0 < end; t0 += 2 * kGroup) {
+      step(t0, Even{}, Odd{});
+      if (t0 + kGroup < end) step(t0 + kGroup, Odd{}, Even{});
+    }
   }
 
   if (!col.valid) return;
@@ -806,6 +821,27 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
             float4_t{o[i][4 * q], o[i][4 * q + 1], o[i][4 * q + 2], o[i][4 * q + 3]};
     }
   if (h == 0) *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(m, l);
+}
+
+template <int DT, bool FP8, int DP>
+__global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_cols_kernel(Params p) {
+  cols_body<DT, FP8, DP>(p, blockIdx.x);
+}
+template <int DT, bool FP8, int DP>
+__global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_tile_kernel(Params p) {
+  tile_body<DT, FP8, DP>(p, blockIdx.x);
+}
+// A call of both kinds of sequences in one launch, so that the two run side by
+// side: the first `tiles` workgroups (the longer ones) are tiles of 128
+// columns.  (16 requests of up to 4100 positions, one of them 509 rows: 30 us
+// one after the other, 21 together.)
+template <int DT, bool FP8, int DP>
+__global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_both_kernel(Params pt, Params pc,
+                                                                                         unsigned tiles) {
+  if (blockIdx.x < tiles)
+    tile_body<DT, FP8, DP>(pt, blockIdx.x);
+  else
+    cols_body<DT, FP8, DP>(pc, blockIdx.x - tiles);
 }
 
 // Sums chunks first .. last of one column into (m, l, v): the whole wave, four
@@ -856,7 +892,7 @@ template <int DT>
 __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_cols_kernel(Params p) {
   __shared__ float lds_o[kWaves][256];
   __shared__ float lds_m[kWaves], lds_l[kWaves];
-  const Place at = place_of(p, p.cols);
+  const Place at = place_of(p, blockIdx.x, p.cols);
   const Tile t = find_cols(p, at.item);
   if (!t.live || t.splits <= 1 || at.inner >= t.ncols) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -884,21 +920,36 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_cols_kernel(Par
   store_row<DT>(p, column_of(p, t, at.head, at.inner).out_row, m, l, v);
 }
 
-// Few chunks of many columns: one workgroup per 16 columns, four per wave.
+// Few chunks of many columns: four (row, head) pairs per wave, over the rows as
+// they lie, so that no workgroup is without rows.
 template <int DT>
 __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_tile_kernel(Params p) {
-  const Place at = place_of(p, kTileCols / kCols);
-  const Tile t = find_tile(p, at.item);
-  if (!t.live || t.splits <= 1) return;
-  const int64_t slot = (static_cast<int64_t>(at.item) * p.c.heads + at.head) * p.splits * p.cols;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int i = 0; i < kCols / kWaves; ++i) {
-    const int k = at.inner * kCols + wave * (kCols / kWaves) + i;
-    if (k >= t.ncols) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), heads = p.a.heads;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * 4;
+  int at_row = -1;
+  kv::Owner o{};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row64 = (first + i) / heads;
+    if (row64 >= p.a.tokens) return;
+    const int row = static_cast<int>(row64), h = static_cast<int>(first + i - row64 * heads);
+    if (row != at_row) o = kv::find_sequence(row, p.a.cu, p.a.lens, p.a.seqs, 1, 1, 0);
+    at_row = row;
+    Tile t{};
+    t.seq = o.seq;
+    t.row0 = o.first;
+    t.rows = o.next - o.first;
+    if (o.seq < 0 || o.first < 0 || row >= o.next || t.rows > p.a.tokens - o.first) continue;
+    if (static_cast<int64_t>(t.rows) * p.group <= p.small) continue;
+    const int head = h / p.group;
+    const int64_t col = static_cast<int64_t>(row - o.first) * p.group + h - head * p.group;
+    const int k = static_cast<int>(col % kTileCols);
+    set_range(p, t, col - k, kTileCols, o.value);
+    if (t.splits <= 1) continue;
+    const int64_t item = kv::item_base(o.first, p.group, kTileCols, 1, o.seq) + col / kTileCols;
     float m, l;
     float4_t v;
-    sum_chunks(p, slot + k, 0, t.splits, m, l, v);
-    store_row<DT>(p, column_of(p, t, at.head, k).out_row, m, l, v);
+    sum_chunks(p, (item * p.c.heads + head) * p.splits * p.cols + k, 0, t.splits, m, l, v);
+    store_row<DT>(p, static_cast<int64_t>(row) * heads + h, m, l, v);
   }
 }
 
@@ -967,39 +1018,40 @@ Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged
 
 template <int DT, bool FP8, int DP>
 hipError_t go(const Params& base, const Cut& cc, const Cut& ct, hipStream_t stream) {
-  if (cc.items) {
-    Params p = base;
-    p.tiles = cc.tiles;
-    p.chunk = cc.chunk;
-    p.splits = cc.splits;
-    p.cols = cc.cols;
-    p.join_later = cc.splits > kJoinHere;
-    const int64_t all = cc.items * p.c.heads;
-    p.part_ml = p.part_o + all * cc.splits * cc.cols * p.c.dim;
-    hipError_t e = launch(kv_attention_cols_kernel<DT, FP8, DP>, dim3(static_cast<unsigned>(all * cc.splits)),
-                          dim3(64 * kWaves), 0, stream, p);
-    if (e == hipSuccess && p.join_later)
-      e = launch(kv_attention_join_cols_kernel<DT>, dim3(static_cast<unsigned>(all * cc.cols)), dim3(64 * kWaves), 0,
-                 stream, p);
-    if (e != hipSuccess) return e;
+  Params pc = base, pt = base;
+  pc.tiles = cc.tiles;
+  pc.chunk = cc.chunk;
+  pc.splits = cc.splits;
+  pc.cols = cc.cols;
+  pc.join_later = cc.splits > kJoinHere;
+  const int64_t all_c = cc.items * base.c.heads, all_t = ct.items * base.c.heads;
+  pc.part_ml = pc.part_o + all_c * cc.splits * cc.cols * base.c.dim;
+  pt.chunk = ct.chunk;
+  pt.splits = ct.splits;
+  pt.cols = ct.cols;
+  pt.items = static_cast<unsigned>(ct.items);
+  pt.small = cc.items ? kSmall : 0;
+  pt.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(base.part_o) + (cc.bytes + 255) / 256 * 256);
+  pt.part_ml = pt.part_o + all_t * ct.splits * ct.cols * base.c.dim;
+  const unsigned blocks_c = static_cast<unsigned>(all_c * cc.splits), blocks_t = static_cast<unsigned>(all_t * ct.splits);
+  const dim3 block(64 * kWaves);
+  constexpr size_t lds_c = kWaves * kCols * DP * sizeof(float), lds_t = kLdsHalves<DP> * sizeof(_Float16);
+  static_assert(lds_c <= lds_t, "the larger serves both");
+  hipError_t e = hipSuccess;
+  if (cc.items && ct.items)
+    e = launch(kv_attention_both_kernel<DT, FP8, DP>, dim3(blocks_t + blocks_c), block, lds_t, stream, pt, pc,
+               blocks_t);
+  else if (cc.items)
+    e = launch(kv_attention_cols_kernel<DT, FP8, DP>, dim3(blocks_c), block, lds_c, stream, pc);
+  else if (ct.items)
+    e = launch(kv_attention_tile_kernel<DT, FP8, DP>, dim3(blocks_t), block, lds_t, stream, pt);
+  if (e == hipSuccess && cc.items && pc.join_later)
+    e = launch(kv_attention_join_cols_kernel<DT>, dim3(static_cast<unsigned>(all_c * cc.cols)), block, 0, stream, pc);
+  if (e == hipSuccess && ct.items && ct.splits > 1) {
+    const int64_t pairs = static_cast<int64_t>(base.a.tokens) * base.a.heads;
+    e = launch(kv_attention_join_tile_kernel<DT>, dim3(static_cast<unsigned>((pairs + 15) / 16)), block, 0, stream, pt);
   }
-  if (ct.items) {
-    Params p = base;
-    p.chunk = ct.chunk;
-    p.items = static_cast<unsigned>(ct.items);
-    p.small = cc.items ? kSmall : 0;
-    p.splits = ct.splits;
-    p.cols = ct.cols;
-    p.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(base.part_o) + (cc.bytes + 255) / 256 * 256);
-    const int64_t all = ct.items * p.c.heads;
-    p.part_ml = p.part_o + all * ct.splits * ct.cols * p.c.dim;
-    hipError_t e = launch(kv_attention_tile_kernel<DT, FP8, DP>, dim3(static_cast<unsigned>(all * ct.splits)),
-                          dim3(64 * kWaves), 0, stream, p);
-    if (e != hipSuccess || ct.splits <= 1) return e;
-    return launch(kv_attention_join_tile_kernel<DT>, dim3(static_cast<unsigned>(all * (kTileCols / kCols))), dim3(64 * kWaves), 0,
-                  stream, p);
-  }
-  return hipSuccess;
+  return e;
 }
 
 template <int DT, bool FP8>
@@ -1029,8 +1081,8 @@ hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, h
   const Cut cc = cut_cols(a.seqs, group, c.heads, c.dim, ragged, a.max_q, a.max_kv, a.window);
   const Cut ct = cut_tile(a.seqs, a.tokens, group, c.heads, c.dim, ragged, a.max_q, a.max_kv, a.window);
   const int64_t limit = 0x7fffffff;
-  if (cc.items * c.heads * std::max(cc.splits, kCols) > limit ||
-      ct.items * c.heads * std::max(ct.splits, kTileCols / kCols) > limit)
+  if (cc.items * c.heads * std::max(cc.splits, kCols) + ct.items * c.heads * ct.splits > limit ||
+      static_cast<int64_t>(a.tokens) * a.heads > limit * 16)
     return hipErrorInvalidConfiguration;
   Params p{};
   p.c = c;
