@@ -920,37 +920,31 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_cols_kernel(Par
   store_row<DT>(p, column_of(p, t, at.head, at.inner).out_row, m, l, v);
 }
 
-// Few chunks of many columns: four (row, head) pairs per wave, over the rows as
+// Few chunks of many columns: one (row, head) pair per wave, over the rows as
 // they lie, so that no workgroup is without rows.
 template <int DT>
 __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_tile_kernel(Params p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), heads = p.a.heads;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * 4;
-  int at_row = -1;
-  kv::Owner o{};
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row64 = (first + i) / heads;
-    if (row64 >= p.a.tokens) return;
-    const int row = static_cast<int>(row64), h = static_cast<int>(first + i - row64 * heads);
-    if (row != at_row) o = kv::find_sequence(row, p.a.cu, p.a.lens, p.a.seqs, 1, 1, 0);
-    at_row = row;
-    Tile t{};
-    t.seq = o.seq;
-    t.row0 = o.first;
-    t.rows = o.next - o.first;
-    if (o.seq < 0 || o.first < 0 || row >= o.next || t.rows > p.a.tokens - o.first) continue;
-    if (static_cast<int64_t>(t.rows) * p.group <= p.small) continue;
-    const int head = h / p.group;
-    const int64_t col = static_cast<int64_t>(row - o.first) * p.group + h - head * p.group;
-    const int k = static_cast<int>(col % kTileCols);
-    set_range(p, t, col - k, kTileCols, o.value);
-    if (t.splits <= 1) continue;
-    const int64_t item = kv::item_base(o.first, p.group, kTileCols, 1, o.seq) + col / kTileCols;
-    float m, l;
-    float4_t v;
-    sum_chunks(p, (item * p.c.heads + head) * p.splits * p.cols + k, 0, t.splits, m, l, v);
-    store_row<DT>(p, static_cast<int64_t>(row) * heads + h, m, l, v);
-  }
+  const int64_t pair = static_cast<int64_t>(blockIdx.x) * kWaves + wave, row64 = pair / heads;
+  if (row64 >= p.a.tokens) return;
+  const int row = static_cast<int>(row64), h = static_cast<int>(pair - row64 * heads);
+  const kv::Owner o = kv::find_sequence(row, p.a.cu, p.a.lens, p.a.seqs, 1, 1, 0);
+  Tile t{};
+  t.seq = o.seq;
+  t.row0 = o.first;
+  t.rows = o.next - o.first;
+  if (o.seq < 0 || o.first < 0 || row >= o.next || t.rows > p.a.tokens - o.first) return;
+  if (static_cast<int64_t>(t.rows) * p.group <= p.small) return;
+  const int head = h / p.group;
+  const int64_t col = static_cast<int64_t>(row - o.first) * p.group + h - head * p.group;
+  const int k = static_cast<int>(col % kTileCols);
+  set_range(p, t, col - k, kTileCols, o.value);
+  if (t.splits <= 1) return;
+  const int64_t item = kv::item_base(o.first, p.group, kTileCols, 1, o.seq) + col / kTileCols;
+  float m, l;
+  float4_t v;
+  sum_chunks(p, (item * p.c.heads + head) * p.splits * p.cols + k, 0, t.splits, m, l, v);
+  store_row<DT>(p, pair, m, l, v);
 }
 
 // How a call is cut: which kernels run, their tiles and chunks of positions.
@@ -1003,17 +997,20 @@ Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q,
   return cut_of(items, tiles, kv_heads, dim, static_cast<int>(std::min<int64_t>(most, kCols)), range, chunk);
 }
 
-// Tiles of 128 columns, for the others: chunks only where there are too few
-// tiles for the CUs (two workgroups fit on one, one beyond dim 128).
+// Tiles of 128 columns, for the others: chunks, of 512 positions or more, only
+// where there are too few tiles for the CUs (two workgroups fit on one, one
+// beyond dim 128) and the range is long.  Measured (us unsplit / split): 500
+// rows of 600 positions 24 / 35, 700 of 1400 47 / 30, 300 of 4000 123 / 38, 512
+// of 8192 220 / 112.
 Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window) {
   if (!ragged || static_cast<int64_t>(max_q) * group <= kSmall) return Cut{};
   const int64_t cols = static_cast<int64_t>(tokens) * group;
   const int64_t live = (cols / kTileCols + std::min<int64_t>(seqs, cols / kTileCols) / 2) * kv_heads;
   const int64_t range = range_of(max_kv, window, kTileCols), wanted = dim > 128 ? 256 : 512;
   int64_t chunk = range;
-  if (live < 192 && range > 512) chunk = ((range * live + wanted - 1) / wanted + 255) / 256 * 256;
+  if (live < 192 && range > 1024) chunk = ((range * live + wanted - 1) / wanted + 255) / 256 * 256;
   return cut_of(kv::item_base(tokens, group, kTileCols, 1, seqs), 1, kv_heads, dim, kTileCols, range,
-                std::max<int64_t>(chunk, 256));
+                std::max<int64_t>(chunk, 512));
 }
 
 template <int DT, bool FP8, int DP>
@@ -1049,7 +1046,7 @@ hipError_t go(const Params& base, const Cut& cc, const Cut& ct, hipStream_t stre
     e = launch(kv_attention_join_cols_kernel<DT>, dim3(static_cast<unsigned>(all_c * cc.cols)), block, 0, stream, pc);
   if (e == hipSuccess && ct.items && ct.splits > 1) {
     const int64_t pairs = static_cast<int64_t>(base.a.tokens) * base.a.heads;
-    e = launch(kv_attention_join_tile_kernel<DT>, dim3(static_cast<unsigned>((pairs + 15) / 16)), block, 0, stream, pt);
+    e = launch(kv_attention_join_tile_kernel<DT>, dim3(static_cast<unsigned>((pairs + kWaves - 1) / kWaves)), block, 0, stream, pt);
   }
   return e;
 }
@@ -1082,7 +1079,7 @@ hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, h
   const Cut ct = cut_tile(a.seqs, a.tokens, group, c.heads, c.dim, ragged, a.max_q, a.max_kv, a.window);
   const int64_t limit = 0x7fffffff;
   if (cc.items * c.heads * std::max(cc.splits, kCols) + ct.items * c.heads * ct.splits > limit ||
-      static_cast<int64_t>(a.tokens) * a.heads > limit * 16)
+      static_cast<int64_t>(a.tokens) * a.heads > limit)
     return hipErrorInvalidConfiguration;
   Params p{};
   p.c = c;
