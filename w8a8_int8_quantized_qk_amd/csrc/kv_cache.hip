@@ -278,21 +278,33 @@ __global__ __launch_bounds__(512) void kv_write_kernel(Params p) {
   }
 }
 
+// Stores of the rows read back: nontemporal, since what reads them next is far
+// behind (100003 positions of 8 heads: 129 us with ordinary stores, 119 so).
+template <int N, int ALIGN>
+__device__ __forceinline__ void store_words(char* p, const uint32_t (&w)[N]) {
+  typedef uint32_t words_t __attribute__((ext_vector_type(N), aligned(ALIGN)));
+  words_t v;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = w[i];
+  __builtin_nontemporal_store(v, reinterpret_cast<words_t*>(p));
+}
+
 template <int DT>
 __device__ __forceinline__ void store8(void* base, int64_t i, const float (&f)[8]) {
   using E = Elem<DT>;
   char* p = static_cast<char*>(base) + i * E::kBytes;
   if constexpr (DT == QK_F32) {
-    Raw16<4> w[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e / 4].w[e % 4] = __float_as_uint(f[e]);
-    reinterpret_cast<Raw16<4>*>(p)[0] = w[0];
-    reinterpret_cast<Raw16<4>*>(p)[1] = w[1];
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w[4] = {__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]), __float_as_uint(f[4 * h + 2]),
+                             __float_as_uint(f[4 * h + 3])};
+      store_words<4, 4>(p + 16 * h, w);
+    }
   } else {
-    Raw16<2> w;
+    uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w.w[e] = qm::pack2_narrow<DT>(f[2 * e], f[2 * e + 1]);
-    *reinterpret_cast<Raw16<2>*>(p) = w;
+    for (int e = 0; e < 4; ++e) w[e] = qm::pack2_narrow<DT>(f[2 * e], f[2 * e + 1]);
+    store_words<4, 2>(p, w);
   }
 }
 
@@ -347,9 +359,9 @@ __global__ __launch_bounds__(512) void kv_read_kernel(Params p) {
           char* const to = static_cast<char*>(p.a.v) +
                            ((t.row + pos) * p.a.ldv + head0 + d) * static_cast<int64_t>(Elem<DT>::kBytes);
           if constexpr (DT == QK_F32)
-            *reinterpret_cast<Raw8<4>*>(to) = Raw8<4>{{__float_as_uint(fa[e] * s), __float_as_uint(fb[e] * s)}};
+            store_words<2, 4>(to, {__float_as_uint(fa[e] * s), __float_as_uint(fb[e] * s)});
           else
-            *reinterpret_cast<Raw4<2>*>(to) = Raw4<2>{qm::pack2_narrow<DT>(fa[e] * s, fb[e] * s)};
+            store_words<1, 2>(to, {qm::pack2_narrow<DT>(fa[e] * s, fb[e] * s)});
         }
       }
     }
