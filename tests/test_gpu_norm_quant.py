@@ -149,3 +149,18 @@ def test_refusals():
         qk.rms_norm_quant(x, w, q=torch.empty((4, 64), dtype=torch.uint8, device=DEV))
     with pytest.raises(qk.QKError):
         qk.rms_norm_quant(x, w, eps=-1.0)
+
+
+@pytest.mark.parametrize("dtype,k,in_place", [(torch.bfloat16, 8195, True), (torch.float32, 4097, False)])
+def test_large_calls_give_what_their_rows_give(dtype, k, in_place):
+    # more than 160 MB read: past the caches; the same rows a few at a time go through them
+    m = 170_000_000 // (2 * k * dtype.itemsize)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn((m, k + 3), generator=g, device=DEV, dtype=torch.float32).to(dtype)[:, :k]
+    res = torch.randn((m, k), generator=g, device=DEV, dtype=torch.float32).to(dtype)
+    w = torch.rand((k,), generator=g, device=DEV, dtype=torch.float32).to(dtype)
+    rows = [0, 1, m // 2, m - 1]
+    want = qk.rms_norm_quant(x[rows], w, EPS, residual=res[rows])
+    got = qk.rms_norm_quant(x, w, EPS, residual=res, residual_out=res if in_place else None)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b[rows])

@@ -22,7 +22,10 @@
 //
 // What bounds it: HBM, 2 reads and 1 write of the row's type plus the codes
 // (7 bytes per bf16 element).  A row's values stay in registers between the
-// two reductions, so x and the residual are read once.
+// two reductions, so x and the residual are read once.  bf16 with a residual:
+// 8192 rows of 8192 in 73 us (6.4 TB/s), 2048 of 4096 in 11 us (5.3 TB/s); 8
+// rows of 4096 in 6 us, which is the launch and one row's chain of a load and
+// two reductions.
 #include "quant_math.h"
 
 namespace qk {
@@ -32,6 +35,15 @@ using qm::Elem;
 
 constexpr int kBlock = 256;
 constexpr int kMaxUnits = 8;  // units of P elements held per thread
+
+// Calls that read more than this pass the caches by.  What they read was
+// written too long ago to be in the 256 MB last-level cache, and filling that
+// cache costs.  Rows of 8192 bf16 elements with a residual, through the
+// caches / past them: 2048 rows (67 MB read) 19.3 / 23.5 us, 4096 (134 MB)
+// 40.1 / 40.5, 6144 (201 MB) 56.7 / 56.5, 8192 80.9 / 73.4, 16384 159 / 140.
+// The stored sum goes past them at every size: the next to read it is a whole
+// layer half away (512 rows 8.4 -> 7.6 us, 6144 rows 63.9 -> 56.7).
+constexpr double kReadOnceBytes = 160e6;
 
 // 16 bytes at any alignment the element type allows (rows of odd widths)
 template <int ALIGN>
@@ -160,6 +172,7 @@ struct NormParams {
   int64_t ldo;
   uint8_t* q;
   float* scale;
+  int once;  // x and residual are read past the caches
 };
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -217,6 +230,29 @@ __device__ __forceinline__ void raw_load(Raw16<Elem<DT>::kBytes>& r, const void*
   r = *reinterpret_cast<const Raw16<Elem<DT>::kBytes>*>(static_cast<const char*>(row) +
                                                         static_cast<size_t>(at) * Elem<DT>::kBytes);
 }
+// The same past the caches, and the store past them.
+typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+typedef words4 words4_16bit __attribute__((aligned(2)));
+typedef words4 words4_32bit __attribute__((aligned(4)));
+template <int DT>
+__device__ __forceinline__ void raw_load_once(Raw16<Elem<DT>::kBytes>& r, const void* row, int at) {
+  const char* from = static_cast<const char*>(row) + static_cast<size_t>(at) * Elem<DT>::kBytes;
+  words4 w;
+  if constexpr (DT == QK_F32)
+    w = __builtin_nontemporal_load(reinterpret_cast<const words4_32bit*>(from));
+  else
+    w = __builtin_nontemporal_load(reinterpret_cast<const words4_16bit*>(from));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.w[i] = w[i];
+}
+template <int DT>
+__device__ __forceinline__ void raw_store_once(void* to, const Raw16<Elem<DT>::kBytes>& r) {
+  const words4 w = {r.w[0], r.w[1], r.w[2], r.w[3]};
+  if constexpr (DT == QK_F32)
+    __builtin_nontemporal_store(w, static_cast<words4_32bit*>(to));
+  else
+    __builtin_nontemporal_store(w, static_cast<words4_16bit*>(to));
+}
 template <int DT>
 __device__ __forceinline__ void raw_values(const Raw16<Elem<DT>::kBytes>& r, float* v) {
   Elem<DT>::unpack(make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]), v);
@@ -246,10 +282,19 @@ __global__ __launch_bounds__(kBlock) void norm_rows(NormParams p, int m) {
   Raw16<Elem<WT>::kBytes> wr[UPT][WN];
   int at[UPT];
 #pragma unroll
-  for (int j = 0; j < UPT; ++j) {
-    at[j] = min((t + j * THREADS) * P, k - P);
-    raw_load<DT>(xr[j], xrow, at[j]);
-    if constexpr (RES) raw_load<DT>(rr[j], rrow, at[j]);
+  for (int j = 0; j < UPT; ++j) at[j] = min((t + j * THREADS) * P, k - P);
+  if (p.once) {
+#pragma unroll
+    for (int j = 0; j < UPT; ++j) {
+      raw_load_once<DT>(xr[j], xrow, at[j]);
+      if constexpr (RES) raw_load_once<DT>(rr[j], rrow, at[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < UPT; ++j) {
+      raw_load<DT>(xr[j], xrow, at[j]);
+      if constexpr (RES) raw_load<DT>(rr[j], rrow, at[j]);
+    }
   }
 #pragma unroll
   for (int j = 0; j < UPT; ++j)
@@ -294,7 +339,7 @@ __global__ __launch_bounds__(kBlock) void norm_rows(NormParams p, int m) {
           else
             o.w[i] = qm::pack2_narrow<DT>(v[j][2 * i], v[j][2 * i + 1]);
         }
-        *reinterpret_cast<Raw16<E::kBytes>*>(static_cast<char*>(p.r_out) + (row * p.ldo + at[j]) * E::kBytes) = o;
+        raw_store_once<DT>(static_cast<char*>(p.r_out) + (row * p.ldo + at[j]) * E::kBytes, o);
       }
     }
     float w[P];
@@ -400,8 +445,9 @@ hipError_t dispatch_weight(int m, const NormParams& p, hipStream_t stream) {
 
 template <int DT>
 hipError_t dispatch_dtype(const RmsNormQuantArgs& a, hipStream_t stream) {
-  const NormParams p{a.k,     a.x,      a.ldx, a.residual, a.ldr, a.weight, a.weight_f32,
-                     a.eps,   a.r_out,  a.ldo, a.q,        a.scale};
+  const double read = static_cast<double>(a.m) * a.k * Elem<DT>::kBytes * (a.residual ? 2 : 1);
+  const NormParams p{a.k,     a.x,      a.ldx, a.residual, a.ldr,   a.weight,            a.weight_f32,
+                     a.eps,   a.r_out,  a.ldo, a.q,        a.scale, read > kReadOnceBytes};
   if (a.residual)
     return a.fp8 ? dispatch_weight<DT, true, true>(a.m, p, stream) : dispatch_weight<DT, true, false>(a.m, p, stream);
   return a.fp8 ? dispatch_weight<DT, false, true>(a.m, p, stream) : dispatch_weight<DT, false, false>(a.m, p, stream);
