@@ -151,6 +151,26 @@ def test_sharp_and_flat_rows():
         t.check(out, lse, scale=scale)
 
 
+@pytest.mark.parametrize("step", [0.9, 1.7, 1.95, 6.0])
+@pytest.mark.parametrize("counts", [[1, 1], [60, 33]])
+def test_scores_that_keep_rising(step, counts):
+    # by `step` binary orders every 64 positions: the maximum that exponents are taken
+    # from may lag behind the true one
+    lens = [508, 300]
+    t = Setup(21, lens, counts, 4, 2, 64, 32, False, "f16")
+    flat = t.cache.k.view(torch.uint8).cpu().numpy()
+    for s, n in enumerate(lens):
+        for p in range(n):
+            codes = np.zeros(64, np.int8)
+            codes[0] = p // 4
+            flat[t.table[s][p // 32], :, p % 32] = codes.view(np.uint8)
+    t.cache.k.view(torch.uint8).copy_(dev(flat))
+    t.cache.k_scale.fill_(1.0)
+    t.q.fill_(step / 16 * 8 / 1.4427)
+    out, lse = t.run(return_lse=True)
+    t.check(out, lse)
+
+
 def test_one_large_query_element():
     # elements 2^20 and more below the row's largest still count
     t = Setup(22, [100, 40], [1, 40], 4, 2, 64, 16, False, "bf16")

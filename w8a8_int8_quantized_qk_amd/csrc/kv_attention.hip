@@ -5,10 +5,11 @@
 // The (row, head) pairs of a sequence that share a kv head are the columns of
 // a tile: 16 in kv_attention_cols_kernel (sequences with up to 64 columns:
 // single tokens; bound by the cache's bytes), 128 in kv_attention_tile_kernel
-// (prompts; bound by the matrix cores and the exponentials).  Scores are formed transposed, S^T = K Q^T: a lane then holds the
-// scores of one column, so the running maximum, the sum and the rescaling of
-// the output are plain lane arithmetic, and the probabilities are already
-// where the second product, O^T = V^T P^T, wants them.  Its reduction index
+// (prompts; bound by the matrix cores and the exponentials).  Scores are formed
+// transposed, S^T = K Q^T: a lane then holds the scores of one column, so the
+// running maximum, the sum and the rescaling of the output are plain lane
+// arithmetic, and the probabilities are already where the second product,
+// O^T = V^T P^T, wants them.  Its reduction index
 // is a position, and the order of positions is free as long as P and V agree:
 // the rows of K are taken in such an order that the scores a lane holds are
 // those of 16 consecutive positions, which is how V lies in the cache.
@@ -19,10 +20,10 @@
 // element to [2^14, 2^15): exact down to 2^-29 of it, and below that the error
 // is 2^-39 of it.  The block's scales never touch the codes: K's multiplies
 // the scores, and V's goes into the exponent, p = 2^(s + log2 v_scale - m + 14)
-// with m the running maximum of s + log2 v_scale, so that every p is at most
-// 2^14 and normal in binary16 down to 2^-28 of the largest.  The sum l adds
-// p / v_scale in binary32 from the unrounded p.  Rounding p to 11 bits is the
-// only rounding below binary32 before the output's.
+// with m at most 1.9 below the running maximum of s + log2 v_scale, so that
+// every p is below 2^15.9 and normal in binary16 down to 2^-28 of the largest.
+// The sum l adds p / v_scale in binary32 from the unrounded p.  Rounding p to
+// 11 bits is the only rounding below binary32 before the output's.
 #include <algorithm>
 #include <cmath>
 
@@ -44,6 +45,7 @@ constexpr int kGroup = 64;       // positions taken at a time
 constexpr int kWaves = 4;
 constexpr float kNone = -3.0e38f;  // a maximum over nothing
 constexpr float kLift = 14.0f;
+constexpr float kSlack = 1.9f;     // 2^(kLift + kSlack) < 65504
 constexpr int kJoinHere = 16;      // most chunks that a tile's last workgroup joins
 constexpr int kCounters = 16384;   // arrival counters at the front of the workspace
 
@@ -258,13 +260,15 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 // One step of the running softmax over a lane's scores of one column: N
 // pieces of E raw scores s, whose exponents are y = s c + b with c >= 0 and
-// b = log2 v_scale per piece.  Leaves p = 2^(y - m + 14) in s and returns the
-// factor by which what was summed before shrinks.  The maximum is taken of the
-// raw scores and the product with c merged into the exponent: one fused
-// multiply-add, one max, one exponential and one addition per score.
-template <int N, int E, bool FOUR>
-__device__ __forceinline__ float softmax_step(float (&s)[N][E], const float (&c)[N], const float (&b)[N],
-                                              const float (&inv_vs)[N], float& m, float& l) {
+// b = log2 v_scale per piece.  Leaves p = 2^(y - m + 14) in s.  m is raised to
+// the maximum only where that exceeds it by more than kSlack, so that most
+// steps find nothing to rescale; rescale(f) is called, for whole waves, where
+// what was summed before shrinks by f.  The maximum is taken of the raw scores
+// and the product with c merged into the exponent: one fused multiply-add,
+// one max, one exponential and one addition per score.
+template <int N, int E, bool FOUR, typename Rescale>
+__device__ __forceinline__ void softmax_step(float (&s)[N][E], const float (&c)[N], const float (&b)[N],
+                                             const float (&inv_vs)[N], float& m, float& l, Rescale rescale) {
   float top = kNone;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -273,13 +277,17 @@ __device__ __forceinline__ float softmax_step(float (&s)[N][E], const float (&c)
     for (int e = 1; e < E; ++e) t = __builtin_fmaxf(t, s[i][e]);
     top = __builtin_fmaxf(top, __builtin_fmaf(t, c[i], b[i]));
   }
-  const float m_new = __builtin_fmaxf(m, column_max<FOUR>(top));
-  const float shrink = __builtin_amdgcn_exp2f(m - m_new);
-  m = m_new;
-  l *= shrink;
+  top = column_max<FOUR>(top);
+  const bool grow = top > m + kSlack;
+  if (__any(grow)) {
+    const float m_new = grow ? top : m, shrink = __builtin_amdgcn_exp2f(m - m_new);
+    m = m_new;
+    l *= shrink;
+    rescale(shrink);
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float off = b[i] - (m_new - kLift);
+    const float off = b[i] - (m - kLift);
     float sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -288,7 +296,6 @@ __device__ __forceinline__ float softmax_step(float (&s)[N][E], const float (&c)
     }
     l = __builtin_fmaf(sum, inv_vs[i], l);
   }
-  return shrink;
 }
 
 // Joins a tile's chunks in order, by the workgroup that arrived last: threads
@@ -476,7 +483,10 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
       // a lane that sees none of these positions must not meet their scale
       if (at + 16 <= col.see_lo || at >= col.see_hi) inv_vs[0] = 0.0f;
     }
-    const float shrink = softmax_step<1, 16, true>(s, c, bias, inv_vs, m, l);
+    softmax_step<1, 16, true>(s, c, bias, inv_vs, m, l, [&](float shrink) {
+#pragma unroll
+      for (int i = 0; i < VC; ++i) o[i] *= shrink;
+    });
     half8_t pf[2];
 #pragma unroll
     for (int i = 0; i < 16; ++i) pf[i >> 3][i & 7] = static_cast<_Float16>(s[0][i]);
@@ -484,10 +494,6 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
       const int have = t0 + 16 * g + 16 > t.lo ? t.len - (t0 + 16 * g) : 0;
 #pragma unroll
       for (int i = 0; i < VC; ++i) keep_first(vr[S][i], have);
-    }
-    if (__any(shrink != 1.0f)) {
-#pragma unroll
-      for (int i = 0; i < VC; ++i) o[i] *= shrink;
     }
 #pragma unroll
     for (int i = 0; i < VC; ++i) {
@@ -585,10 +591,20 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
 // binary16 (each code is converted once per workgroup), and have 32 columns
 // each.  LDS is doubled: while a step is worked on, the next one's bytes are
 // written converted to the other half, and those of the one after it come
-// from memory into registers; one barrier per step.  Rows of K lie in the order in which the first
-// product's result registers want them, 16-byte pieces of a row are
-// exchanged by its number so that eight consecutive rows fall on different
-// banks.
+// from memory into registers; one barrier per step.  Rows of K lie in the order
+// in which the first product's result registers want them, 16-byte pieces of a
+// row are exchanged by its number so that eight consecutive rows fall on
+// different banks.
+//
+// 4096 rows of 32 heads on 8, dim 128, causal: 171 us, 800 TFLOP/s (a plain
+// binary16 matrix product of 8192^3 reaches 1280 here).  A wave's step is 1024
+// cycles of matrix instructions and some 300 vector instructions (64 codes
+// converted, 32 exponentials), of which the two waves of a SIMD overlap a part.
+// Measured beside it: 64 columns per wave, which halves the reads of LDS but
+// leaves one wave per SIMD, 319 us; the next step's conversion within the
+// first product 471 (registers spill); conversion before the products 175;
+// a raised wave priority during the products 176; rescaling at every new
+// maximum 176.
 template <int DT, bool FP8, int DP>
 __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   extern __shared__ __align__(16) _Float16 lds_all[];
@@ -636,42 +652,35 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   auto in_pool = [&](int b) { return static_cast<unsigned>(b) < static_cast<unsigned>(p.c.blocks); };
 
   // What this thread brings of a step.  K: piece kd of rows krow(i); V: 16
-  // positions of rows lane + 64 i.  Either way a wave's rows lie in one piece of
-  // 16 positions, so block numbers and addresses of tiles are scalar.
+  // positions of rows lane + 64 i.  Either way a wave brings the same 16
+  // positions, so one block number and one tile's address, both scalar, serve it.
   // Elements past dim come from the front of the row and rows past dim from
   // the last: they meet zeros of the query, or are not stored.
   const int kd = tid % RB, kcol = 16 * kd < dim ? 16 * kd : 0;
-  auto krow = [&](int i) { return tid / RB + i * (64 * kWaves / RB); };
-  auto kpart = [&](int i) { return __builtin_amdgcn_readfirstlane(krow(i) >> 4); };
+  auto krow = [&](int i) { return 16 * wave + lane / RB + i * (64 / RB); };
   // Up to dim 128 two steps are on their way, so that a load has a whole step
   // to arrive; beyond, the registers hold one.
   constexpr int kSets = DP > 128 ? 1 : 2;
   uint4 kr[kSets][NC], vr[kSets][NC];
   float sk[kSets], sv[kSets];
-  int kb[NC], vb = 0;  // block numbers of the step to load
-  auto load_blocks = [&](int t0) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i) kb[i] = entry(t0 + 16 * kpart(i));
-    vb = entry(t0 + 16 * wave);
-  };
+  int next_block = 0;  // of this wave's 16 positions of the step to load
+  auto load_block = [&](int t0) { next_block = entry(t0 + 16 * wave); };
   auto load_step = [&](int t0, auto half) {
     const int S = half % kSets;
+    const bool ok = in_pool(next_block);
+    const int64_t tile = static_cast<int64_t>(ok ? next_block : 0) * p.c.heads + head;
+    const int pos = (t0 + 16 * wave) & (P - 1);
+    const uint8_t* const from_k = p.c.k + tile * head_bytes + pos * dim;
+    const uint8_t* const from_v = p.c.v + tile * head_bytes + pos;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int pos = (t0 + 16 * kpart(i)) & (P - 1);
-      const int64_t tile = static_cast<int64_t>(in_pool(kb[i]) ? kb[i] : 0) * p.c.heads + head;
-      const uint8_t* const from = p.c.k + tile * head_bytes + pos * dim;
-      kr[S][i] = *reinterpret_cast<const uint4*>(from + static_cast<unsigned>((krow(i) & 15) * dim + kcol));
-    }
-    const int64_t tile = static_cast<int64_t>(in_pool(vb) ? vb : 0) * p.c.heads + head;
-    const uint8_t* const from = p.c.v + tile * head_bytes + ((t0 + 16 * wave) & (P - 1));
+    for (int i = 0; i < NC; ++i)
+      kr[S][i] = *reinterpret_cast<const uint4*>(from_k + static_cast<unsigned>((krow(i) & 15) * dim + kcol));
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      vr[S][i] = *reinterpret_cast<const uint4*>(from + static_cast<unsigned>(min(lane + 64 * i, dim - 1) * P));
-    }
+    for (int i = 0; i < NC; ++i)
+      vr[S][i] = *reinterpret_cast<const uint4*>(from_v + static_cast<unsigned>(min(lane + 64 * i, dim - 1) * P));
     sk[S] = p.c.k_scale[tile];
     sv[S] = p.c.v_scale[tile];
-    if (!in_pool(vb)) sk[S] = sv[S] = __builtin_nanf("");
+    if (!ok) sk[S] = sv[S] = __builtin_nanf("");
   };
   // the step at t0 into half H of LDS
   auto put_step = [&](int t0, auto half) {
@@ -741,12 +750,10 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
         if (first + 16 <= col.see_lo || first >= col.see_hi) inv_vs[b] = 0.0f;
       }
     }
-    const float m_old = m;
-    const float shrink = softmax_step<4, 8, false>(s, c, bias, inv_vs, m, l);
-    if (__any(m != m_old)) {
+    softmax_step<4, 8, false>(s, c, bias, inv_vs, m, l, [&](float shrink) {
 #pragma unroll
       for (int i = 0; i < ND; ++i) o[i] *= shrink;
-    }
+    });
     half8_t pf[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -763,7 +770,7 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   auto step = [&](int t0, auto half, auto other) {
     if (t0 + kSets * kGroup < end) {
       load_step(t0 + kSets * kGroup, half);  // with one set there is no other
-      load_blocks(t0 + (kSets + 1) * kGroup);
+      load_block(t0 + (kSets + 1) * kGroup);
     }
     work(t0, half);
     if (t0 + kGroup < end) put_step(t0 + kGroup, other);
@@ -773,12 +780,12 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   using Even = std::integral_constant<int, 0>;
   using Odd = std::integral_constant<int, 1>;
   if (begin < end) {
-    load_blocks(begin);
+    load_block(begin);
     load_step(begin, Even{});
-    load_blocks(begin + kGroup);
+    load_block(begin + kGroup);
     if (kSets > 1 && begin + kGroup < end) {
       load_step(begin + kGroup, Odd{});
-      load_blocks(begin + 2 * kGroup);
+      load_block(begin + 2 * kGroup);
     }
     put_step(begin, Even{});
   }
