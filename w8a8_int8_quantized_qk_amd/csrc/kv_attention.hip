@@ -336,8 +336,8 @@ __device__ __forceinline__ void join_chunks(const Params& p, const Tile& t, int 
 }
 
 // The bodies share their kernel's dynamic LDS; this many binary16.  (Named in
-// the body that uses it: through a pointer from elsewhere the compiler keeps
-// fewer reads in flight, 69 against 64 us for a prompt of 1000 rows.)
+// the body that uses it: through a pointer from elsewhere the compiler kept
+// fewer reads in flight, and a prompt of 1000 rows took 1.08 times as long.)
 template <int DP>
 constexpr int kLdsHalves = 4 * kGroup * DP;
 
@@ -346,6 +346,12 @@ constexpr int kLdsHalves = 4 * kGroup * DP;
 // maximum, a sum and an output of its own, and join them through LDS at the
 // end; nothing is shared before, so no wave waits for another.  The workgroup
 // that arrives last at a tile joins its chunks.
+//
+// 32 heads on 8, dim 128: 64 sequences of 1 to 8192 positions, INT8, 126 us
+// (5.0 TB/s; a plain copy reaches 4.9 and a read-only stream 6.1); two
+// sequences of about 115000, 64 heads, FP8, 88 us (5.4 TB/s); one of 771
+// positions 7 us: the launch, and a chain of table entry, keys, products and
+// join.
 template <int DT, bool FP8, int DP>
 __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
   // the waves' outputs, [wave][column][element], elements exchanged in fours by
@@ -593,10 +599,11 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
 // written converted to the other half, and those of the one after it come
 // from memory into registers; one barrier per step.  Rows of K lie in the order
 // in which the first product's result registers want them, 16-byte pieces of a
-// row are exchanged by its number so that eight consecutive rows fall on
-// different banks.
+// row are exchanged by its number so that consecutive rows fall on different
+// banks: 16 rows where a row of K has 16 pieces or more (eight only: 176 us for
+// 173 in the case below).
 //
-// 4096 rows of 32 heads on 8, dim 128, causal: 171 us, 800 TFLOP/s (a plain
+// 4096 rows of 32 heads on 8, dim 128, causal: 170-177 us, 790 TFLOP/s (a plain
 // binary16 matrix product of 8192^3 reaches 1280 here).  A wave's step is 1024
 // cycles of matrix instructions and some 300 vector instructions (64 codes
 // converted, 32 exponentials), of which the two waves of a SIMD overlap a part.
@@ -616,6 +623,7 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   constexpr int ND = DP / 32;      // 32-row pieces of V
   constexpr int RB = DP / 16;      // 16-byte pieces of a row of codes
 
+  auto key_k = [](int row) { return KP >= 16 ? row & 15 : (row >> 1) & 7; };
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   Place at = place_of(p, block, p.splits);
@@ -696,7 +704,7 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
     for (int i = 0; i < NC; ++i) {
       // position 32 a + 16 b + 8 c + 4 d + e lies in row 32 a + 16 b + 8 d + 4 c + e
       const int r = krow(i), row = (r & ~12) | ((r & 8) >> 1) | ((r & 4) << 1);
-      const int key = row & 7;
+      const int key = key_k(row);
       kl[row * KP + ((2 * kd) ^ key)] = kv::codes8_to_half<FP8>(kr[S][i].x, kr[S][i].y);
       kl[row * KP + ((2 * kd + 1) ^ key)] = kv::codes8_to_half<FP8>(kr[S][i].z, kr[S][i].w);
       const int d = lane + 64 * i;
@@ -722,7 +730,7 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
       for (int e = 0; e < 16; ++e) acc[a][e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) {
-        acc[a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[(32 * a + n) * KP + ((2 * i + h) ^ (n & 7))], qf[i], acc[a], 0, 0, 0);
+        acc[a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[(32 * a + n) * KP + ((2 * i + h) ^ key_k(n))], qf[i], acc[a], 0, 0, 0);
       }
     }
     // register 8 b + e of acc[a] is position 32 a + 16 b + 8 h + e
@@ -840,8 +848,8 @@ __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_ti
 }
 // A call of both kinds of sequences in one launch, so that the two run side by
 // side: the first `tiles` workgroups (the longer ones) are tiles of 128
-// columns.  (16 requests of up to 4100 positions, one of them 509 rows: 30 us
-// one after the other, 21 together.)
+// columns.  (16 requests of up to 4100 positions, one of them 509 rows, window
+// 1024: 37 us one after the other, 26 together.)
 template <int DT, bool FP8, int DP>
 __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_both_kernel(Params pt, Params pc,
                                                                                          unsigned tiles) {
