@@ -939,10 +939,10 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_cols_kernel(Par
 // they lie, so that no workgroup is without rows.
 template <int DT>
 __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_tile_kernel(Params p) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), heads = p.a.heads;
-  const int64_t pair = static_cast<int64_t>(blockIdx.x) * kWaves + wave, row64 = pair / heads;
-  if (row64 >= p.a.tokens) return;
-  const int row = static_cast<int>(row64), h = static_cast<int>(pair - row64 * heads);
+  const unsigned wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), heads = p.a.heads;
+  const unsigned pair = blockIdx.x * kWaves + wave, row_of = pair / heads;  // fewer than 2^31 pairs
+  if (row_of >= static_cast<unsigned>(p.a.tokens)) return;
+  const int row = static_cast<int>(row_of), h = static_cast<int>(pair - row_of * heads);
   const kv::Owner o = kv::find_sequence(row, p.a.cu, p.a.lens, p.a.seqs, 1, 1, 0);
   Tile t{};
   t.seq = o.seq;
