@@ -275,6 +275,34 @@ def test_graph_replay():
         assert torch.equal(t.run(), want)
 
 
+def test_graph_captured_before_any_eager_call_and_kept_past_larger_ones():
+    t = Setup(62, [1300, 64, 700], [1, 1, 1], 4, 2, 64, 64, False, "bf16")
+    big = Setup(63, [5000] * 4, [1] * 4, 16, 8, 64, 64, False, "bf16")
+    want, want_big = t.run().clone(), big.run().clone()
+    args = (t.q, t.cache, dev(t.table), dev(np.asarray(t.lens, np.int32)))
+    big_args = (big.q, big.cache, dev(big.table), dev(np.asarray(big.lens, np.int32)))
+    for warm in (False, True):
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            if warm:
+                qk.kv_attention(*args)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                out = qk.kv_attention(*args)
+                out_big = qk.kv_attention(*big_args)
+            for _ in range(3):
+                got = qk.kv_attention(*big_args)      # eager, on the same stream, with more workspace
+                g.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(got, want_big)
+                assert torch.equal(out, want) and torch.equal(out_big, want_big)
+                out.zero_()
+                out_big.zero_()
+        torch.cuda.current_stream().wait_stream(stream)
+
+
 def test_refusals():
     t = Setup(71, [20, 20], [1, 1], 4, 2, 64, 16, False, "bf16")
     table, lens, cu = dev(t.table), dev(np.array([20, 20], np.int32)), dev(np.array([0, 1, 2], np.int32))

@@ -780,8 +780,14 @@ def gemm_i8_asym(a: torch.Tensor, zero_point: torch.Tensor, b: torch.Tensor, wsu
 _bound = None
 
 
-def _workspace_on(nbytes: int, index: int) -> torch.Tensor:
-    return new_workspace(nbytes, torch.device("cuda", index))
+def _workspace_on(need: int, wanted: int, index: int):
+    """(a prepared workspace, whether later calls may use it).  In a capture its
+    preparation is part of the graph and has not run yet, so there it serves
+    its one call."""
+    device = torch.device("cuda", index)
+    with torch.cuda.device(device):
+        keep = not torch.cuda.is_current_stream_capturing()
+        return new_workspace(max(need, wanted) if keep else need, device), keep
 
 
 def _bind_to(lib: ctypes.CDLL):

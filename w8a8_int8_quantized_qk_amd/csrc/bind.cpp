@@ -19,6 +19,7 @@
 #include <cmath>
 #include <cstdint>
 #include <map>
+#include <memory>
 #include <string>
 #include <utility>
 
@@ -41,7 +42,7 @@ struct Lib {
 Lib lib;
 PyObject* py_check = nullptr;          // check(status): raises for a status other than 0
 PyObject* py_stream = nullptr;         // current stream of a device index, as a number
-PyObject* py_new_workspace = nullptr;  // new_workspace(bytes, device index)
+PyObject* py_new_workspace = nullptr;  // (bytes needed, bytes wanted, device index) -> (workspace, whether to keep it)
 
 // A Python exception on its way out; Raised: it is set already.
 struct Raise {
@@ -382,8 +383,9 @@ PyObject* kv_cache_read(PyObject* const* a, Py_ssize_t n) {
 
 // ---- attention ----
 
-// One prepared workspace per device and stream, kept until the process ends
-// (never destroyed: the device may be gone by then).
+// One prepared workspace per device and stream.  None is freed, not even one
+// that became too small: a captured graph may hold its address.  Each is at
+// least twice the one before, so together they are at most twice the last.
 std::map<std::pair<int, void*>, PyObject*>& workspaces() {
   static auto* all = new std::map<std::pair<int, void*>, PyObject*>;
   return *all;
@@ -437,6 +439,10 @@ PyObject* kv_attention(PyObject* const* a, Py_ssize_t n) {
   void* const stream = stream_of(dev);
   void* ws = nullptr;
   size_t bytes = 0;
+  struct Release {
+    void operator()(PyObject* o) const { Py_DECREF(o); }
+  };
+  std::unique_ptr<PyObject, Release> own;  // a workspace made for this call, until it is enqueued
   const std::pair<int, void*> key(dev.index(), stream);
   if (a[11] != Py_None) {
     const at::Tensor& t = tensor(a[11], "workspace");
@@ -447,15 +453,22 @@ PyObject* kv_attention(PyObject* const* a, Py_ssize_t n) {
   } else {
     const size_t need = lib.workspace(ns, nt, nh, c.heads, c.dim, ragged, static_cast<int>(max_q), static_cast<int>(max_kv), w);
     if (need > 0) {
-      PyObject*& kept = workspaces()[key];
-      if (!kept || THPVariable_Unpack(kept).nbytes() < need) {
-        PyObject* const fresh = PyObject_CallFunction(py_new_workspace, "ni", static_cast<Py_ssize_t>(need), static_cast<int>(dev.index()));
-        if (!fresh) throw Raised{};
-        Py_XDECREF(kept);
-        kept = fresh;
+      const auto at = workspaces().find(key);
+      PyObject* use = at != workspaces().end() ? at->second : nullptr;
+      const size_t had = use ? THPVariable_Unpack(use).nbytes() : 0;
+      if (had < need) {
+        PyObject* const made = PyObject_CallFunction(py_new_workspace, "nni", static_cast<Py_ssize_t>(need),
+                                                     static_cast<Py_ssize_t>(2 * had), static_cast<int>(dev.index()));
+        if (!made) throw Raised{};
+        use = PyTuple_GET_ITEM(made, 0);
+        if (PyTuple_GET_ITEM(made, 1) == Py_True) {
+          Py_INCREF(use);
+          workspaces()[key] = use;
+        }
+        own.reset(made);
       }
-      ws = THPVariable_Unpack(kept).data_ptr();
-      bytes = THPVariable_Unpack(kept).nbytes();
+      ws = THPVariable_Unpack(use).data_ptr();
+      bytes = THPVariable_Unpack(use).nbytes();
     }
   }
   const int status = lib.attention(
@@ -464,13 +477,7 @@ PyObject* kv_attention(PyObject* const* a, Py_ssize_t n) {
       c.table, c.ldt, c.width, static_cast<const int*>(lens.data_ptr()), cu, static_cast<int>(max_q),
       static_cast<int>(max_kv), scale, w, out.data_ptr(), want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, ws,
       bytes, stream);
-  if (status != 0 && status < 1000) {  // part of the call may have run: a fresh workspace next time
-    const auto at = workspaces().find(key);
-    if (at != workspaces().end()) {
-      Py_XDECREF(at->second);
-      workspaces().erase(at);
-    }
-  }
+  if (status != 0 && status < 1000) workspaces().erase(key);  // part of the call may have run: a fresh one next time
   check(status);
   PyObject* const oo = a[9] != Py_None ? same(a[9]) : wrapped(out);
   return want_lse ? tuple_of({oo, wrapped(lse)}) : oo;
