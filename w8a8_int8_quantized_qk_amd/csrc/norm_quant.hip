@@ -23,7 +23,7 @@
 // What bounds it: HBM, 2 reads and 1 write of the row's type plus the codes
 // (7 bytes per bf16 element).  A row's values stay in registers between the
 // two reductions, so x and the residual are read once.  bf16 with a residual:
-// 8192 rows of 8192 in 73 us (6.4 TB/s), 2048 of 4096 in 11 us (5.3 TB/s); 8
+// 8192 rows of 8192 in 72 us (6.5 TB/s), 2048 of 4096 in 11 us (5.3 TB/s); 8
 // rows of 4096 in 6 us, which is the launch and one row's chain of a load and
 // two reductions.
 #include "quant_math.h"
