@@ -131,6 +131,27 @@ def test_long_cache_is_split(fp8, dtype):
         assert torch.equal(t.run(), out)          # the same bits on every run
 
 
+@pytest.mark.parametrize("heads,kv_heads,counts,max_q", [(8, 8, [1, 16, 1, 1], 1), (8, 2, [3, 1, 1, 1], 1), (6, 2, [2, 2, 7, 21], 2)])
+def test_more_rows_than_max_q_stay_out_of_other_results(heads, kv_heads, counts, max_q):
+    # some sequences break the bound in a call that is cut into chunks: nothing is written outside the
+    # workspace, and the sequences that keep the bound get their results
+    lens = [5000, 4100, 700, 4990]
+    t = Setup(13, lens, counts, heads, kv_heads, 64, 64, False, "bf16")
+    args = (dev(t.table), dev(np.asarray(lens, np.int32)), dev(plain.offsets(counts)))
+    need = qk.kv_attention_workspace_size(4, sum(counts), heads, kv_heads, 64, t.table.shape[1] * 64, 0, True, max_q)
+    assert need > 0
+    room = torch.full((need + 65536,), 165, dtype=torch.uint8, device=DEV)
+    ws = room[:need]
+    qk.workspace_init(ws)
+    out = qk.kv_attention(t.q, t.cache, *args, max_q=max_q, workspace=ws)
+    assert (room[need:] == 165).all() and not ws[:65536].any()
+    host, cu = plain.Cache(t.cache, False), plain.offsets(counts)
+    for s in (s for s, n in enumerate(counts) if n <= max_q):
+        r = slice(cu[s], cu[s + 1])
+        want, _, bound, _ = plain.attention(plain.f32(t.q[r]), *host.values(t.table[s], lens[s]), lens[s], 0.125, 0)
+        assert plain.within(out[r], want, bound).all(), f"sequence {s}"
+
+
 @pytest.mark.parametrize("heads,kv_heads,dim,fp8", [(4, 2, 128, False), (2, 2, 64, True), (3, 1, 256, True)])
 def test_prompt_tiles_are_split(heads, kv_heads, dim, fp8):
     # a few rows behind a long cache: tiles of many columns whose positions are cut into chunks

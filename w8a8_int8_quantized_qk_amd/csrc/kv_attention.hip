@@ -94,7 +94,8 @@ __device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0
 }
 
 // Tiles of 16 columns: item = sequence * tiles + tile; longer sequences are
-// the other kernel's.
+// the other kernel's.  Partial results have room for the columns that max_q
+// rows have; rows beyond it, of which only the device knows, stay out of them.
 __device__ __forceinline__ Tile find_cols(const Params& p, unsigned item) {
   Tile t{};
   t.seq = static_cast<int>(item / static_cast<unsigned>(p.tiles));
@@ -107,8 +108,8 @@ __device__ __forceinline__ Tile find_cols(const Params& p, unsigned item) {
     if (first < 0 || t.rows <= 0 || t.rows > p.a.tokens - first) return t;
     if (static_cast<int64_t>(t.rows) * p.group > kSmall) return t;
   }
-  set_range(p, t, static_cast<int64_t>(item - static_cast<unsigned>(t.seq) * p.tiles) * kCols, kCols,
-            p.a.lens[t.seq]);
+  set_range(p, t, static_cast<int64_t>(item - static_cast<unsigned>(t.seq) * p.tiles) * kCols,
+            p.splits > 1 ? p.cols : kCols, p.a.lens[t.seq]);
   return t;
 }
 
