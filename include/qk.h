@@ -511,7 +511,8 @@ int qk_rms_norm_quant(int m, int k, const void *x, int64_t ldx, const void *resi
  * The cache is a pool of blocks of `block` positions (16, 32, 64 or 128):
  *   k_cache  [blocks][kv_heads][block][dim] codes
  *   v_cache  [blocks][kv_heads][dim][block] codes (positions innermost)
- *   k_scale, v_scale  [blocks][kv_heads] float: value = code * scale
+ *   k_scale, v_scale  [blocks][kv_heads] float: value = code * scale, for any
+ *            finite scale (0 where nothing was written into a fresh cache)
  * code is QK_CODE_I8 or QK_CODE_FP8; dim a multiple of 16 from 16 to 256.  A
  * sequence's position p lies in block table[s * ldt + p / block] at
  * p % block.  The caller hands out blocks; no block may belong to two

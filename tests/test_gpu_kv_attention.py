@@ -215,6 +215,61 @@ def test_scales_of_very_different_size():
     t.check(*t.run(return_lse=True))
 
 
+def _check_small(t, out, lse):
+    # as Setup.check, with what values below 2^-64 may lose beside the rest: 2^-88 each
+    host, cu = plain.Cache(t.cache, t.fp8), plain.offsets(t.counts)
+    for s, n in enumerate(t.lens):
+        r = slice(cu[s], cu[s + 1])
+        want, wl, bo, bl = plain.attention(plain.f32(t.q[r]), *host.values(t.table[s], n), n,
+                                           np.float64(np.float32(t.q.shape[2] ** -0.5)), 0)
+        ok = plain.within(out[r], want, bo + 2.0 ** -88)
+        assert ok.all(), f"sequence {s}: {(~ok).sum()} of {ok.size} outputs beyond the bound"
+        assert (np.abs(lse[r].cpu().numpy() - wl) <= bl).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,counts,dim", [([500, 130], [1, 1], 64), ([500, 130], [60, 33], 64), ([1400, 90], [1, 1], 128),
+                                             ([1500, 200], [70, 1], 128), ([300, 90], [2, 40], 256)])
+def test_scales_that_are_zero_negative_or_subnormal(lens, counts, dim, fp8):
+    t = Setup(25, lens, counts, 4, 2, dim, 32, fp8, "bf16")
+    k, v = t.cache.k_scale.clone(), t.cache.v_scale.clone()
+    # some blocks of each kind among ordinary ones; the first block of either sequence has every second kind
+    kinds = [0.0, -1.0, 1e-38, 1e-30, -1e-43, 1.0, 1.0, 1.0]
+    factor = np.asarray(kinds, np.float32)[t.rng.integers(0, 8, tuple(k.shape))]
+    factor[t.table[0, 0]], factor[t.table[1, 0]] = 0.0, -1.0
+    t.cache.v_scale.mul_(dev(factor))
+    t.cache.k_scale.mul_(dev(np.asarray([0.0, -1.0, 1e-38, 1.0], np.float32)[t.rng.integers(0, 4, tuple(k.shape))]))
+    _check_small(t, *t.run(return_lse=True))
+    # all of one kind
+    for fk, fv in ((-1.0, 1.0), (1.0, -1.0), (-1.0, 1e-38), (0.0, 1e-22), (1.0, -1e-43), (1.0, 0.0), (0.0, 0.0), (1.0, 1e13)):
+        t.cache.k_scale.copy_(k * fk)
+        t.cache.v_scale.copy_(v * fv)
+        out, lse = t.run(return_lse=True)
+        _check_small(t, out, lse)
+        if fv == 0.0:
+            assert not out.any()
+
+
+@pytest.mark.parametrize("counts", [[1, 1, 1], [3, 70, 1]])
+def test_a_fresh_cache_reads_as_zeros(counts):
+    lens = [20, 300, 1]
+    cache = qk.new_kv_cache(32, 2, 64, 16, device=DEV)
+    table, _ = plain.tables(np.random.default_rng(1), lens, 16)
+    q = torch.randn((sum(counts), 4, 64), device=DEV).to(torch.bfloat16)
+    out, lse = qk.kv_attention(q, cache, dev(table), dev(np.asarray(lens, np.int32)), dev(plain.offsets(counts)), return_lse=True)
+    assert not out.any()
+    seen = np.concatenate([np.arange(n - c, n) + 1 for n, c in zip(lens, counts)])
+    assert np.allclose(lse.cpu().numpy(), np.log(seen)[:, None], rtol=0, atol=2.0 ** -20)
+
+
+def test_the_largest_scales():
+    t = Setup(26, [90, 70], [1, 40], 2, 1, 64, 16, False, "bf16")
+    t.cache.v.view(torch.uint8).fill_(1)
+    t.cache.v_scale.fill_(2.0 ** 126.7)
+    t.cache.v_scale[::2] = 2.0 ** 125
+    t.check(*t.run(return_lse=True))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_non_finite_values_reach_only_rows_that_see_them(fp8):
     lens, counts = [80, 64], [40, 1]

@@ -24,6 +24,14 @@
 // every p is below 2^15.9 and normal in binary16 down to 2^-28 of the largest.
 // The sum l adds p / v_scale in binary32 from the unrounded p.  Rounding p to
 // 11 bits is the only rounding below binary32 before the output's.
+//
+// Scales may be any finite numbers.  Where K's is negative, or V's is outside
+// [2^-64, 2^126] (a fresh cache's is 0), the scores are multiplied out before
+// their maximum is taken, the exponent takes V's magnitude raised to 2^-64, and
+// the power of two (or sign, or 0) that is left multiplies p or the codes
+// before they are rounded to binary16, which costs values below 2^-64 an
+// absolute error of 2^-88 at most.  The sum l keeps binary32's precision as
+// long as the V scales that a row sees, so raised, lie within 2^92 of each other.
 #include <algorithm>
 #include <cmath>
 
@@ -46,6 +54,8 @@ constexpr int kWaves = 4;
 constexpr float kNone = -3.0e38f;  // a maximum over nothing
 constexpr float kLift = 14.0f;
 constexpr float kSlack = 1.9f;     // 2^(kLift + kSlack) < 65504
+constexpr float kLeastScale = 5.421010862427522e-20f;  // 2^-64: V scales from here ...
+constexpr float kMostScale = 8.507059173023462e37f;    // ... to 2^126 go into the exponent as they are
 constexpr int kJoinHere = 16;      // most chunks that a tile's last workgroup joins
 constexpr int kCounters = 16384;   // arrival counters at the front of the workspace
 
@@ -255,8 +265,33 @@ __device__ __forceinline__ float2 get2(const float* at) {
   return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
 }
 
+// m and log2 l may be large and of opposite signs (small V scales): l's exponent
+// is added to m first, as exactly as the two allow.
 __device__ __forceinline__ float lse_of(float m, float l) {
-  return l != 0.0f ? (m - kLift + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -__builtin_inff();
+  if (l == 0.0f) return -__builtin_inff();
+  const float whole = m - kLift + static_cast<float>(__builtin_amdgcn_frexp_expf(l));
+  return (whole + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(l))) * 0.6931471805599453f;
+}
+
+// Whether a block's scales need nothing of what split_scale does.
+__device__ __forceinline__ bool plain_scales(float ks, float vs) {
+  return ks >= 0.0f && vs >= kLeastScale && vs <= kMostScale;
+}
+
+// Any scale of V as held * rest: of `held`, positive and 2^-64 or more, the
+// exponent takes the logarithm and the sum the reciprocal (formed in two steps,
+// being subnormal beyond 2^126); `rest`, a power of two, its negative or 0, is
+// left to multiply p or the codes.  Infinity and NaN stay in `held`.
+struct SplitScale {
+  float log2, inv, rest;
+};
+__device__ __forceinline__ SplitScale split_scale(float vs) {
+  const float mag = __builtin_fabsf(vs);
+  const bool low = mag < kLeastScale;
+  const int up = low ? -63 - __builtin_amdgcn_frexp_expf(mag) : 0;
+  const float held = vs == 0.0f ? kLeastScale : __builtin_amdgcn_ldexpf(mag, up);
+  return SplitScale{__builtin_amdgcn_logf(held), __builtin_amdgcn_rcpf(held * 0.0625f) * 0.0625f,
+                    vs == 0.0f ? 0.0f : __builtin_copysignf(__builtin_amdgcn_ldexpf(1.0f, -up), vs)};
 }
 
 // One step of the running softmax over a lane's scores of one column: N
@@ -478,8 +513,14 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[0][i] = acc[i >> 2][i & 3];
     float c[1] = {c_col * ks[S]}, bias[1] = {__builtin_amdgcn_logf(vs[S])}, inv_vs[1] = {__builtin_amdgcn_rcpf(vs[S])};
-    if (t0 < t.lo || t0 + kGroup > t.len - t.rows || p.a.window > 0) {  // some column may not see all 64
+    const bool odd = __any(!plain_scales(ks[S], vs[S]));
+    if (t0 < t.lo || t0 + kGroup > t.len - t.rows || p.a.window > 0 || odd) {  // some column may not see all 64
       const int at = t0 + 16 * g;
+      if (odd) {
+        const SplitScale v = split_scale(vs[S]);
+        bias[0] = v.log2;
+        inv_vs[0] = v.inv;
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const bool seen = at + i >= col.see_lo && at + i < col.see_hi;
@@ -494,6 +535,11 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
 #pragma unroll
       for (int i = 0; i < VC; ++i) o[i] *= shrink;
     });
+    if (__any(!(vs[S] >= kLeastScale))) {
+      const float rest = split_scale(vs[S]).rest;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[0][i] *= rest;
+    }
     half8_t pf[2];
 #pragma unroll
     for (int i = 0; i < 16; ++i) pf[i >> 3][i & 7] = static_cast<_Float16>(s[0][i]);
@@ -716,6 +762,23 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
       lds_s[H][0][wave] = sk[S];
       lds_s[H][1][wave] = __builtin_amdgcn_logf(sv[S]);
       lds_s[H][2][wave] = __builtin_amdgcn_rcpf(sv[S]);
+    }
+    if (__any(!plain_scales(sk[S], sv[S]))) {  // the wave's 16 positions have one block's scales
+      const SplitScale v = split_scale(sv[S]);
+      const _Float16 turn = sk[S] < 0.0f ? -1.0f : 1.0f;
+#pragma unroll 1
+      for (int i = 0; i < 2 * NC; ++i) {
+        const int r = krow(i >> 1), row = (r & ~12) | ((r & 8) >> 1) | ((r & 4) << 1), d = lane + 64 * (i >> 1);
+        kl[row * KP + ((2 * kd + (i & 1)) ^ key_k(row))] *= turn;
+        half8_t& w = vl[d * 8 + ((2 * wave + (i & 1)) ^ (d & 7))];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = static_cast<_Float16>(static_cast<float>(w[e]) * v.rest);
+      }
+      if (lane == 0) {
+        lds_s[H][0][wave] = __builtin_fabsf(sk[S]);
+        lds_s[H][1][wave] = v.log2;
+        lds_s[H][2][wave] = v.inv;
+      }
     }
   };
   // the step at t0, in half H of LDS
