@@ -133,6 +133,31 @@ def test_non_finite_tokens_and_zero_tokens(block, fp8):
     assert torch.isfinite(cache.k_scale).all()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("block", [16, 64])
+def test_every_earlier_code_and_negative_and_zero_scales(block, fp8):
+    # a cache filled elsewhere: all 256 codes among the earlier tokens (-128 and NaN too), and scales that
+    # are tiny, negative (also beyond the new one in size) or 0 when a block is continued
+    rng = np.random.default_rng(block)
+    n = 12
+    table, blocks = plain.tables(rng, [block] * n, block)
+    cache = random_cache(rng, blocks, 1, 64, block, fp8)
+    factor = dev(np.resize(np.array([0.999, 0.5, -0.4, -30.0, 0.0, 1e-39], np.float32), (n, 1)))
+    top = 448 if fp8 else 127
+    for t in (cache.k_scale, cache.v_scale):
+        t[dev(table[:, 0].astype(np.int64))] = factor / top
+    want = plain.Cache(cache, fp8)
+    k, v = rows(rng, n, 1, 64, "f32")
+    k[:, 0, 0], v[:, 0, 0] = 4.0, -4.0                  # more than any other token: the new scale is 4 / top
+    cu = write(cache, k, v, table, [block - 2] * n, [1] * n)
+    want.write(plain.f32(k), plain.f32(v), table, [block - 2] * n, cu)
+    if fp8:                                             # which NaN a NaN becomes is not part of the format
+        for t in (cache.k, cache.v, want.k, want.v):
+            b = t.view(torch.uint8) if isinstance(t, torch.Tensor) else t
+            b[(b & 0x7F) == 0x7F] = 0x7F
+    same(cache, want)
+
+
 def test_many_sequences_and_slices_of_a_projection():
     # more sequences than a wave has lanes, rows of one fused projection
     rng = np.random.default_rng(8)

@@ -118,14 +118,23 @@ __device__ __forceinline__ void load2(const void* base, int64_t i, float& a, flo
   }
 }
 
-// Four earlier codes moved from scale s0 to s.
+// Four earlier codes moved from scale s0 to s.  The quotient is clamped, unlike
+// a new token's: a code of -128, or a negative s0 larger than s, exceeds the
+// range.  FP8 NaN codes stay NaN.
 template <bool FP8>
 __device__ __forceinline__ uint32_t moved4(uint32_t w, float s0, float s, float r) {
   float f[4];
   kv::codes4_to_float<FP8>(w, f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] *= s0;
-  return kv::codes4_of<FP8>(f, s, r);
+  if constexpr (FP8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f[i] != f[i] ? f[i] : qm::fp8_ratio(f[i], s, r);
+    return qm::pack4_fp8(f[0], f[1], f[2], f[3]);
+  } else {
+    return qm::pack4_low_bytes(qm::code_word_bounded(f[0], s, r), qm::code_word_bounded(f[1], s, r),
+                               qm::code_word_bounded(f[2], s, r), qm::code_word_bounded(f[3], s, r));
+  }
 }
 
 // DP: dim rounded up to 64, 128 or 256.
