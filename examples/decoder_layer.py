@@ -44,9 +44,10 @@ class Linear:
         size = 100 if fp8 else 73           # the codes' root mean square
         self.s = torch.full((n,), k ** -0.5 / size, device=device)
 
-    def __call__(self, q, s):
-        gemm = qk.gemm_fp8_scaled if q.dtype == torch.float8_e4m3fn else qk.gemm_i8_scaled
-        return gemm(q, self.w, s, self.s)
+    def __call__(self, q, s, workspace=None):
+        if q.dtype == torch.float8_e4m3fn:
+            return qk.gemm_fp8_scaled(q, self.w, s, self.s)
+        return qk.gemm_i8_scaled(q, self.w, s, self.s, workspace=workspace)
 
 
 @dataclass
@@ -58,6 +59,8 @@ class Step:
     cu: torch.Tensor        # [seqs + 1] rows of each sequence
     max_q: int
     max_kv: int
+    linear_workspace: torch.Tensor | None = None    # of a graph's own; None: the stream's
+    attention_workspace: torch.Tensor | None = None
 
 
 class Layer:
@@ -81,16 +84,17 @@ class Layer:
             q, s = qk.rms_norm_quant(x, self.norm1, c.eps, fp8=c.fp8)
         else:
             q, s, residual = qk.rms_norm_quant(x, self.norm1, c.eps, residual, c.fp8)
-        rows = self.qkv(q, s).view(n, c.heads + 2 * c.kv_heads, c.dim)
+        ws = step.linear_workspace
+        rows = self.qkv(q, s, ws).view(n, c.heads + 2 * c.kv_heads, c.dim)
         query, key, value = rows.split([c.heads, c.kv_heads, c.kv_heads], 1)
         qk.kv_cache_write(self.cache, key, value, step.table, step.start, step.cu)
         a = qk.kv_attention(query, self.cache, step.table, step.lens, step.cu if step.max_q > 1 else None,
-                            max_q=step.max_q, max_kv=step.max_kv)
+                            max_q=step.max_q, max_kv=step.max_kv, workspace=step.attention_workspace)
         quant, silu = ((qk.quant_per_token_fp8, qk.silu_mul_quant_per_token_fp8) if c.fp8
                        else (qk.quant_per_token, qk.silu_mul_quant_per_token))
-        x = self.o(*quant(a.view(n, c.heads * c.dim)))
+        x = self.o(*quant(a.view(n, c.heads * c.dim)), ws)
         q, s, residual = qk.rms_norm_quant(x, self.norm2, c.eps, residual, c.fp8)
-        return self.down(*silu(self.gate_up(q, s))), residual
+        return self.down(*silu(self.gate_up(q, s, ws)), ws), residual
 
 
 class Decoder:
@@ -104,8 +108,7 @@ class Decoder:
         self.layers = [Layer(shape, seqs * width, gen, device) for _ in range(layers)]
         self.lens = torch.zeros(seqs, dtype=torch.int32, device=device)
 
-    def run(self, x, start, lens, cu, max_q, max_kv):
-        step = Step(self.table, start, lens, cu, max_q, max_kv)
+    def run(self, x, step: Step):
         residual = None
         for layer in self.layers:
             x, residual = layer(x, residual, step)
@@ -117,22 +120,29 @@ class Decoder:
         cu = torch.zeros(len(counts) + 1, dtype=torch.int32, device=self.device)
         cu[1:] = new.cumsum(0)
         start, self.lens = self.lens, self.lens + new
-        return self.run(x, start, self.lens, cu, max(counts), self.longest)
+        return self.run(x, Step(self.table, start, self.lens, cu, max(counts), self.longest))
 
 
 class TokenGraph:
     """One row of every sequence per replay: from x, added to the caches, its
-    result in out.  Holds what the graph reads."""
+    result in out.  Holds what the graph reads and the workspaces that it uses,
+    so that a replay shares nothing with calls on other streams."""
 
     def __init__(self, dec: Decoder):
         seqs = dec.table.shape[0]
         self.x = torch.zeros((seqs, dec.shape.hidden), dtype=torch.bfloat16, device=dec.device)
         self.cu = torch.zeros(seqs + 1, dtype=torch.int32, device=dec.device)
         self.start, self.lens = dec.lens.clone(), dec.lens.clone()
+        c, layer = dec.shape, dec.layers[0]
+        linear = max(qk.gemm_workspace_size(seqs, m.w.shape[1], m.w.shape[0])
+                     for m in (layer.qkv, layer.o, layer.gate_up, layer.down))
+        attention = qk.kv_attention_workspace_size(seqs, seqs, c.heads, c.kv_heads, c.dim, dec.longest)
+        self.step = Step(dec.table, self.start, self.lens, self.cu, 1, dec.longest,
+                         *(qk.new_workspace(n, dec.device) for n in (linear, attention)))
         self.stream = torch.cuda.Stream()
         self.stream.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(self.stream):
-            self._step(dec)             # workspaces exist before the capture; no sequence has a row yet
+            self._step(dec)             # what happens on first use is out of the capture; no sequence has a row yet
             self.start.copy_(dec.lens)
             self.lens.copy_(dec.lens + 1)
             self.cu.copy_(torch.arange(seqs + 1))
@@ -142,7 +152,7 @@ class TokenGraph:
             self.out = self._step(dec)
 
     def _step(self, dec):
-        out = dec.run(self.x, self.start, self.lens, self.cu, 1, dec.longest)
+        out = dec.run(self.x, self.step)
         self.start.add_(1)
         self.lens.add_(1)
         return out

@@ -97,6 +97,34 @@ def test_replayed_tokens_are_the_eager_ones(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_a_token_graph_has_its_own_workspaces(fp8, monkeypatch):
+    shape = ex.Shape(hidden=256, heads=6, kv_heads=2, dim=64, inner=384, block=16, fp8=fp8)
+    dec = ex.Decoder(shape, 2, 3, 3000)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    dec.prompt(torch.randn((1200, shape.hidden), generator=g, device=DEV).to(torch.bfloat16), [700, 300, 200])
+    seen = []
+
+    def attend(*a, workspace=None, **kw):
+        seen.append(workspace)
+        return qk_attend(*a, workspace=workspace, **kw)
+
+    qk_attend = qk.kv_attention
+    monkeypatch.setattr(qk, "kv_attention", attend)
+    one, two = ex.TokenGraph(dec), ex.TokenGraph(dec)
+    half = len(seen) // 2
+    assert all(w is one.step.attention_workspace for w in seen[:half]) and one.step.attention_workspace is not None
+    assert all(w is two.step.attention_workspace for w in seen[half:])
+    assert one.step.attention_workspace.data_ptr() != two.step.attention_workspace.data_ptr()
+    if not fp8:
+        assert one.step.linear_workspace.data_ptr() != two.step.linear_workspace.data_ptr()
+    x = torch.randn((3, shape.hidden), generator=g, device=DEV).to(torch.bfloat16)
+    a = one(x).clone()
+    torch.cuda.synchronize()
+    b = two(x).clone()                           # both begin at the same position and write the same token
+    assert torch.equal(a, b) and a.isfinite().all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_a_prompt_in_pieces_of_whole_blocks_fills_the_same_cache(fp8):
     shape = _shape(fp8)
     one, two = (ex.Decoder(shape, 1, 2, 96, seed=9) for _ in range(2))

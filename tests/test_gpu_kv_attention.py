@@ -379,6 +379,54 @@ def test_graph_captured_before_any_eager_call_and_kept_past_larger_ones():
         torch.cuda.current_stream().wait_stream(stream)
 
 
+def test_graphs_share_no_workspace_with_other_calls(monkeypatch):
+    # captured on a stream that has a workspace already, twice: a replay on any stream may run beside the
+    # other graph and beside eager calls, so each call in a graph has a workspace of its own
+    made, of_package = [], qk._workspace_on
+
+    def spy(nbytes, index):
+        made.append(of_package(nbytes, index))
+        return made[-1]
+
+    monkeypatch.setattr(qk, "_workspace_on", spy)
+    qk._bind_to(qk.library())
+    try:
+        t = Setup(64, [5000, 64, 700], [1, 1, 1], 4, 2, 64, 64, False, "bf16")
+        big = Setup(65, [5000] * 8, [1] * 8, 32, 16, 64, 64, False, "bf16")
+        args, big_args = ((s.q, s.cache, dev(s.table), dev(np.asarray(s.lens, np.int32))) for s in (t, big))
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            qk.kv_attention(*big_args)           # the stream's workspace is large enough for all that follows
+            before = len(made)
+            want = qk.kv_attention(*args)
+            assert len(made) == before
+            torch.cuda.synchronize()
+            graphs, outs = [], []
+            for _ in range(2):
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g, stream=stream):
+                    outs.append(qk.kv_attention(*args))
+                graphs.append(g)
+            own = [w.data_ptr() for w in made[before:]]
+            assert len(set(own)) == 2 and not {w.data_ptr() for w in made[:before]} & set(own)
+            again = qk.kv_attention(*args)       # eager calls go on with the stream's
+            assert len(made) == before + 2
+        torch.cuda.synchronize()
+        assert torch.equal(again, want)
+        kept = [(w, w.clone()) for w in made[:before]]
+        for _ in range(3):
+            for g, out in zip(graphs, outs):
+                out.zero_()
+                g.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(out, want)
+        assert all(torch.equal(w, c) for w, c in kept)
+    finally:
+        monkeypatch.undo()
+        qk._bind_to(qk.library())
+
+
 def test_refusals():
     t = Setup(71, [20, 20], [1, 1], 4, 2, 64, 16, False, "bf16")
     table, lens, cu = dev(t.table), dev(np.array([20, 20], np.int32)), dev(np.array([0, 1, 2], np.int32))

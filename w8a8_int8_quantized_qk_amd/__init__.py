@@ -780,14 +780,12 @@ def gemm_i8_asym(a: torch.Tensor, zero_point: torch.Tensor, b: torch.Tensor, wsu
 _bound = None
 
 
-def _workspace_on(need: int, wanted: int, index: int):
-    """(a prepared workspace, whether later calls may use it).  In a capture its
-    preparation is part of the graph and has not run yet, so there it serves
-    its one call."""
-    device = torch.device("cuda", index)
-    with torch.cuda.device(device):
-        keep = not torch.cuda.is_current_stream_capturing()
-        return new_workspace(max(need, wanted) if keep else need, device), keep
+def _workspace_on(nbytes: int, index: int) -> torch.Tensor:
+    """A workspace of kv_attention, prepared on the current stream: only the
+    counters at its front have to be zero."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    workspace_init(ws[:KV_COUNTER_BYTES])
+    return ws
 
 
 def _bind_to(lib: ctypes.CDLL):
@@ -801,7 +799,7 @@ def _bind_to(lib: ctypes.CDLL):
     names = ("qk_rms_norm_quant", "qk_kv_cache_write", "qk_kv_cache_read", "qk_kv_attention_workspace_size",
              "qk_kv_attention")
     _qkbind.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names), _check,
-                 torch._C._cuda_getCurrentRawStream, _workspace_on)
+                 torch._C._cuda_getCurrentRawStream, _workspace_on, torch._C._cuda_isCurrentStreamCapturing)
     return _qkbind
 
 
@@ -833,6 +831,7 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
 
 
 KV_BLOCKS = (16, 32, 64, 128)
+KV_COUNTER_BYTES = 65536  # of a kv_attention workspace, zero between calls
 
 
 class KVCache(NamedTuple):
@@ -909,10 +908,16 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: tor
     sequence has one.  window > 0 limits a row to its last `window` positions.
     scale defaults to dim ** -0.5.  max_q and max_kv are bounds that the host
     knows on a sequence's rows and positions (by default all rows, and what the
-    table covers); tight ones save work.  A workspace of one's own has
-    kv_attention_workspace_size(...) bytes and comes from new_workspace.  Returns out [tokens, heads, dim], and
+    table covers); tight ones save work.  Returns out [tokens, heads, dim], and
     with return_lse the fp32 log-sum-exp [tokens, heads]; a row that sees no
     position gives 0 and -inf.
+
+    Calls that are cut into chunks use a workspace that is kept for the current
+    stream.  While that stream is being captured a call gets one of its own
+    instead, from the graph's memory and prepared within the graph, so that
+    replays share nothing with other calls.  A workspace of the caller's own
+    (kv_attention_workspace_size(...) bytes, from new_workspace) saves a graph
+    that preparation; calls that can run at the same time must not share it.
     """
     return _bind().kv_attention(q, cache, table, lens, cu, scale, window, max_q, max_kv, out, return_lse,
                                 workspace)

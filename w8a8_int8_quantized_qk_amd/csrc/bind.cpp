@@ -16,6 +16,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <map>
@@ -42,7 +43,8 @@ struct Lib {
 Lib lib;
 PyObject* py_check = nullptr;          // check(status): raises for a status other than 0
 PyObject* py_stream = nullptr;         // current stream of a device index, as a number
-PyObject* py_new_workspace = nullptr;  // (bytes needed, bytes wanted, device index) -> (workspace, whether to keep it)
+PyObject* py_new_workspace = nullptr;  // (bytes, device index) -> a workspace prepared on the current stream
+PyObject* py_capturing = nullptr;      // whether the current stream is being captured
 
 // A Python exception on its way out; Raised: it is set already.
 struct Raise {
@@ -383,9 +385,11 @@ PyObject* kv_cache_read(PyObject* const* a, Py_ssize_t n) {
 
 // ---- attention ----
 
-// One prepared workspace per device and stream.  None is freed, not even one
-// that became too small: a captured graph may hold its address.  Each is at
-// least twice the one before, so together they are at most twice the last.
+// One prepared workspace per device and stream, for calls that are not being
+// captured: a graph may be replayed on any stream, beside calls on the one it
+// was captured on.  None is freed, since calls on its stream may still be
+// running.  Each is at least twice the one before, so together they are at most
+// twice the last.
 std::map<std::pair<int, void*>, PyObject*>& workspaces() {
   static auto* all = new std::map<std::pair<int, void*>, PyObject*>;
   return *all;
@@ -453,19 +457,22 @@ PyObject* kv_attention(PyObject* const* a, Py_ssize_t n) {
   } else {
     const size_t need = lib.workspace(ns, nt, nh, c.heads, c.dim, ragged, static_cast<int>(max_q), static_cast<int>(max_kv), w);
     if (need > 0) {
+      PyObject* use = nullptr;
+      size_t had = 0;
+      const std::unique_ptr<PyObject, Release> capturing(PyObject_CallNoArgs(py_capturing));
+      if (!capturing) throw Raised{};
+      const bool keep = !truth(capturing.get());
       const auto at = workspaces().find(key);
-      PyObject* use = at != workspaces().end() ? at->second : nullptr;
-      const size_t had = use ? THPVariable_Unpack(use).nbytes() : 0;
+      if (keep && at != workspaces().end()) {
+        use = at->second;
+        had = THPVariable_Unpack(use).nbytes();
+      }
       if (had < need) {
-        PyObject* const made = PyObject_CallFunction(py_new_workspace, "nni", static_cast<Py_ssize_t>(need),
-                                                     static_cast<Py_ssize_t>(2 * had), static_cast<int>(dev.index()));
-        if (!made) throw Raised{};
-        use = PyTuple_GET_ITEM(made, 0);
-        if (PyTuple_GET_ITEM(made, 1) == Py_True) {
-          Py_INCREF(use);
-          workspaces()[key] = use;
-        }
-        own.reset(made);
+        use = PyObject_CallFunction(py_new_workspace, "ni", static_cast<Py_ssize_t>(std::max(need, 2 * had)),
+                                    static_cast<int>(dev.index()));
+        if (!use) throw Raised{};
+        own.reset(use);
+        if (keep) workspaces()[key] = own.release();
       }
       ws = THPVariable_Unpack(use).data_ptr();
       bytes = THPVariable_Unpack(use).nbytes();
@@ -499,9 +506,9 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return nullptr;
 }
 
-// (addresses of the five entry points, check, stream, new_workspace)
+// (addresses of the five entry points, check, stream, new_workspace, capturing)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 8);
+  need_args(n, 9);
   void* p[5];
   for (int i = 0; i < 5; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
@@ -515,8 +522,8 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   lib.read = reinterpret_cast<decltype(lib.read)>(p[2]);
   lib.workspace = reinterpret_cast<decltype(lib.workspace)>(p[3]);
   lib.attention = reinterpret_cast<decltype(lib.attention)>(p[4]);
-  PyObject** const hold[] = {&py_check, &py_stream, &py_new_workspace};
-  for (int i = 0; i < 3; ++i) {
+  PyObject** const hold[] = {&py_check, &py_stream, &py_new_workspace, &py_capturing};
+  for (int i = 0; i < 4; ++i) {
     Py_INCREF(a[5 + i]);
     Py_XDECREF(*hold[i]);
     *hold[i] = a[5 + i];
