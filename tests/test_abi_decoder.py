@@ -99,6 +99,23 @@ def test_binding_refuses_on_the_host():
         qk.kv_attention(None, cache, x, x)
 
 
+@pytest.mark.parametrize("seqs,tokens,heads,kv_heads,dim,max_q", [
+    (16, 28, 32, 8, 128, 28),        # 65 to 127 columns in all: at most one sequence has a prompt's
+    (40, 109, 32, 32, 128, 70), (1, 17, 32, 8, 128, 17), (3, 40, 8, 4, 256, 40),
+    (32, 32, 32, 8, 128, 32),        # single tokens, max_q left at all rows
+    (500, 520, 32, 8, 128, 520), (64, 4096, 32, 8, 128, 4096), (9, 1300, 16, 16, 256, 700),
+    (2048, 2048, 128, 8, 128, 1),    # 16384 tiles of single tokens
+    (1000, 4000, 64, 8, 256, 4),
+])
+@pytest.mark.parametrize("max_kv", [4096, 131072, 1 << 20])
+def test_attention_workspace_stays_small(seqs, tokens, heads, kv_heads, dim, max_q, max_kv):
+    size = qk.kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, max_kv, 0, True, max_q)
+    assert size <= (1 << 30) + (400 << 20)           # single tokens, prompts
+    if tokens * heads // kv_heads <= 64:
+        # no sequence can have a prompt's columns: as with the tight bound
+        assert size == qk.kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, max_kv, 0, True, 64 * kv_heads // heads)
+
+
 def test_attention_workspace_size():
     size = qk.kv_attention_workspace_size
     assert size(1, 1, 4, 2, 64, 64) == 0                     # one piece: nothing to join

@@ -164,6 +164,21 @@ def test_prompt_tiles_are_split(heads, kv_heads, dim, fp8):
         assert torch.equal(t.run(max_q=150), out)
 
 
+@pytest.mark.parametrize("long", [0, 3000])
+@pytest.mark.parametrize("heads,kv_heads", [(2, 2), (2, 1)])
+def test_prompts_among_short_sequences(heads, kv_heads, long):
+    # rows just at, above and below a tile's and the short sequences' columns, and many that have no tile;
+    # over a long cache the tiles are cut into chunks
+    counts = [1, 64, 0, 65, 1, 1, 127, 128, 3, 129, 32, 33, 1, 0, 191, 1] + [1] * 70 + [66, 2]
+    lens = [c + (5 * i) % 40 for i, c in enumerate(counts)]
+    lens[3] = max(lens[3], long)
+    t = Setup(14, lens, counts, heads, kv_heads, 32, 16, False, "f16")
+    out, lse = t.run(return_lse=True)
+    t.check(out, lse)
+    only = Setup(15, [n + long // 2 for n in (90, 5, 70)], [90, 5, 70], heads, kv_heads, 32, 16, True, "bf16")
+    only.check(*only.run(return_lse=True))
+
+
 def test_sharp_and_flat_rows():
     # scores of several hundred, equal scores, a scale of zero, large and tiny queries
     for spread, scale in ((300.0, None), (0.0, None), (1.0, 0.0), (1e30, 1e-30), (1e-30, 1e30), (1.0, -1.0)):

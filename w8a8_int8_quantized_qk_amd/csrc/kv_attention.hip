@@ -58,6 +58,10 @@ constexpr float kLeastScale = 5.421010862427522e-20f;  // 2^-64: V scales from h
 constexpr float kMostScale = 8.507059173023462e37f;    // ... to 2^126 go into the exponent as they are
 constexpr int kJoinHere = 16;      // most chunks that a tile's last workgroup joins
 constexpr int kCounters = 16384;   // arrival counters at the front of the workspace
+// Partial results of single tokens are held to this: chunks of thousands of
+// tiles over long ranges would take gigabytes, and that many tiles fill the
+// chip without them.
+constexpr int64_t kMostPartials = 1 << 30;
 
 struct Params {
   KvCacheView c;
@@ -66,7 +70,7 @@ struct Params {
   int group;        // heads per kv head
   int tiles;        // cols kernel: tiles per sequence
   unsigned items;
-  int small;        // tile kernel: columns of a sequence that the other kernel takes
+  int small;        // tile kernel: columns of a sequence that the other kernel takes (kSmall or 0)
   int chunk;        // positions per workgroup
   int splits;       // chunks of the longest range
   int cols;         // columns that the workspace holds per tile
@@ -123,16 +127,28 @@ __device__ __forceinline__ Tile find_cols(const Params& p, unsigned item) {
   return t;
 }
 
-// Tiles of 128 columns, laid over the ragged rows.
+// Tiles of 128 columns, laid over the ragged rows: sequence b, from `row` on,
+// owns items tile_base(row, b) .. tile_base(next row, b + 1).  n rows of it have
+// n * group columns and need ceil(n * group / 128) of them: the first term gives
+// floor(n * group / 128), the second, where sequences of up to `small` columns are
+// the other kernel's, at least one more to every longer sequence and at most
+// one for every small + 1 columns of the call, however many sequences there are.
+__host__ __device__ __forceinline__ int64_t tile_base(int64_t row, int group, int small, int b) {
+  const int64_t cols = row * group, many = cols / (kSmall + 1);
+  return cols / kTileCols + (small && many < b ? many : b);
+}
+
 __device__ __forceinline__ Tile find_tile(const Params& p, int64_t item) {
   Tile t{};
-  const kv::Owner o = kv::find_sequence(item, p.a.cu, p.a.lens, p.a.seqs, p.group, kTileCols, 1);
+  const kv::Owner o = kv::find_sequence(item, p.a.cu, p.a.lens, p.a.seqs, [&](int row, int seq) {
+    return tile_base(row, p.group, p.small, seq);
+  });
   t.seq = o.seq;
   t.rows = o.next - o.first;
   t.row0 = o.first;
   if (o.seq < 0 || o.first < 0 || t.rows <= 0 || t.rows > p.a.tokens - o.first) return t;
   if (static_cast<int64_t>(t.rows) * p.group <= p.small) return t;
-  set_range(p, t, (item - kv::item_base(t.row0, p.group, kTileCols, 1, t.seq)) * kTileCols, kTileCols, o.value);
+  set_range(p, t, (item - tile_base(t.row0, p.group, p.small, t.seq)) * kTileCols, kTileCols, o.value);
   return t;
 }
 
@@ -1007,7 +1023,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_tile_kernel(Par
   const unsigned pair = blockIdx.x * kWaves + wave, row_of = pair / heads;  // fewer than 2^31 pairs
   if (row_of >= static_cast<unsigned>(p.a.tokens)) return;
   const int row = static_cast<int>(row_of), h = static_cast<int>(pair - row_of * heads);
-  const kv::Owner o = kv::find_sequence(row, p.a.cu, p.a.lens, p.a.seqs, 1, 1, 0);
+  const kv::Owner o = kv::find_sequence(row, p.a.cu, p.a.lens, p.a.seqs, [](int first, int) { return first; });
   Tile t{};
   t.seq = o.seq;
   t.row0 = o.first;
@@ -1019,7 +1035,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_tile_kernel(Par
   const int k = static_cast<int>(col % kTileCols);
   set_range(p, t, col - k, kTileCols, o.value);
   if (t.splits <= 1) return;
-  const int64_t item = kv::item_base(o.first, p.group, kTileCols, 1, o.seq) + col / kTileCols;
+  const int64_t item = tile_base(o.first, p.group, p.small, o.seq) + col / kTileCols;
   float m, l;
   float4_t v;
   sum_chunks(p, (item * p.c.heads + head) * p.splits * p.cols + k, 0, t.splits, m, l, v);
@@ -1071,9 +1087,11 @@ Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q,
   int64_t chunks = 1;
   if (range > 640 && live < 256) chunks = 256 / live;
   if (range > 6144 && live >= 256) chunks = (range + 2047) / 2048;
+  const int64_t cols = std::min<int64_t>(most, kCols), each = items * kv_heads * cols * (dim + 2) * 4;
+  chunks = std::min(chunks, std::max<int64_t>(kMostPartials / each, 1));
   constexpr int64_t kStep = kWaves * kGroup;
   const int64_t chunk = ((range + chunks - 1) / chunks + kStep - 1) / kStep * kStep;
-  return cut_of(items, tiles, kv_heads, dim, static_cast<int>(std::min<int64_t>(most, kCols)), range, chunk);
+  return cut_of(items, tiles, kv_heads, dim, static_cast<int>(cols), range, chunk);
 }
 
 // Tiles of 128 columns, for the others: chunks, of 512 positions or more, only
@@ -1081,15 +1099,27 @@ Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q,
 // beyond dim 128) and the range is long.  Measured (us unsplit / split): 500
 // rows of 600 positions 24 / 35, 700 of 1400 47 / 30, 300 of 4000 123 / 38, 512
 // of 8192 220 / 112.
-Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window) {
+// Of the items, which all have room for partial results, few can be without
+// columns: at 128 columns, 512 chunks in all and dim 128 that is some 140 MB.
+Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window,
+             int small) {
   if (!ragged || static_cast<int64_t>(max_q) * group <= kSmall) return Cut{};
-  const int64_t cols = static_cast<int64_t>(tokens) * group;
-  const int64_t live = (cols / kTileCols + std::min<int64_t>(seqs, cols / kTileCols) / 2) * kv_heads;
+  const int64_t items = tile_base(tokens, group, small, seqs);
+  const int64_t full = static_cast<int64_t>(tokens) * group / kTileCols;
+  const int64_t live = std::max<int64_t>(full + std::min<int64_t>(seqs, full) / 2, 1) * kv_heads;
   const int64_t range = range_of(max_kv, window, kTileCols), wanted = dim > 128 ? 256 : 512;
   int64_t chunk = range;
   if (live < 192 && range > 1024) chunk = ((range * live + wanted - 1) / wanted + 255) / 256 * 256;
-  return cut_of(kv::item_base(tokens, group, kTileCols, 1, seqs), 1, kv_heads, dim, kTileCols, range,
-                std::max<int64_t>(chunk, 512));
+  return cut_of(items, 1, kv_heads, dim, kTileCols, range, std::max<int64_t>(chunk, 512));
+}
+
+struct Cuts {
+  Cut cols, tile;
+};
+Cuts cuts_of(int seqs, int tokens, int heads, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window) {
+  const int group = heads / kv_heads;
+  const Cut c = cut_cols(seqs, group, kv_heads, dim, ragged, max_q, max_kv, window);
+  return Cuts{c, cut_tile(seqs, tokens, group, kv_heads, dim, ragged, max_q, max_kv, window, c.items ? kSmall : 0)};
 }
 
 template <int DT, bool FP8, int DP>
@@ -1146,16 +1176,12 @@ size_t bytes_of(const Cut& cc, const Cut& ct) {
 
 size_t kv_attention_workspace_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, bool ragged, int max_q,
                                     int max_kv, int window) {
-  const int group = heads / kv_heads;
-  return bytes_of(cut_cols(seqs, group, kv_heads, dim, ragged, max_q, max_kv, window),
-                  cut_tile(seqs, tokens, group, kv_heads, dim, ragged, max_q, max_kv, window));
+  const Cuts c = cuts_of(seqs, tokens, heads, kv_heads, dim, ragged, max_q, max_kv, window);
+  return bytes_of(c.cols, c.tile);
 }
 
 hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, hipStream_t stream) {
-  const int group = a.heads / c.heads;
-  const bool ragged = a.cu != nullptr;
-  const Cut cc = cut_cols(a.seqs, group, c.heads, c.dim, ragged, a.max_q, a.max_kv, a.window);
-  const Cut ct = cut_tile(a.seqs, a.tokens, group, c.heads, c.dim, ragged, a.max_q, a.max_kv, a.window);
+  const auto [cc, ct] = cuts_of(a.seqs, a.tokens, a.heads, c.heads, c.dim, a.cu != nullptr, a.max_q, a.max_kv, a.window);
   const int64_t limit = 0x7fffffff;
   if (cc.items * c.heads * std::max(cc.splits, kCols) + ct.items * c.heads * ct.splits > limit ||
       static_cast<int64_t>(a.tokens) * a.heads > limit)
@@ -1164,7 +1190,7 @@ hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, h
   p.c = c;
   p.a = a;
   while (1 << p.block_shift < c.block) ++p.block_shift;
-  p.group = group;
+  p.group = a.heads / c.heads;
   p.scale2 = std::fabs(a.scale) * 1.4426950408889634f;
   p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
   p.arrived = static_cast<unsigned*>(a.workspace);

@@ -67,7 +67,9 @@ __device__ __forceinline__ Task find_task(const Params& p) {
   const int64_t item = ih / p.c.heads;
   t.head = static_cast<int>(ih - item * p.c.heads);
   if (item >= p.items) return t;
-  const kv::Owner o = kv::find_sequence(item, p.a.cu, p.a.start, p.a.seqs, 1, p.c.block, 2);
+  const kv::Owner o = kv::find_sequence(item, p.a.cu, p.a.start, p.a.seqs, [&](int row, int seq) {
+    return kv::item_base(row, 1, p.c.block, 2, seq);
+  });
   const int b = o.seq, first = o.first, n = o.next - o.first, start = o.value;
   if (b < 0 || first < 0 || n <= 0 || n > p.a.tokens - first || start < 0 || start > 0x7fffffff - n) return t;
   const int64_t at = start / p.c.block + (item - kv::item_base(first, 1, p.c.block, 2, b));

@@ -27,27 +27,28 @@ struct __attribute__((packed, aligned(ALIGN))) Raw4 {
 // uses the first of them.  base(b + 1) - base(b) >= floor(n * mul / size) +
 // extra for n rows, which covers the pieces of `size` that n * mul columns
 // have (extra = 1), or that n positions touch when they start inside a piece
-// (extra = 2).  The number of items is base(seqs).
+// (extra = 2).  The number of items is base(seqs).  (The attention's prompt tiles
+// have a base of their own, since short sequences have none.)
 __host__ __device__ __forceinline__ int64_t item_base(int64_t row, int mul, int size, int extra, int b) {
   return row * mul / size + static_cast<int64_t>(extra) * b;
 }
 
 // The sequence that owns `item`, its first row, the next one's, and its entry
-// of `each` (start or length): the last sequence whose base is at or below the
-// item.  The lanes of a wave look at 64 sequences at a time, each lane with its
+// of `each` (start or length): the last sequence whose base(first row, number)
+// is at or below the item.  The lanes of a wave look at 64 sequences at a time, each lane with its
 // sequence's numbers in hand, so that nothing has to be loaded again for the
 // one that is found; the result is uniform.  seq < 0: none.
 struct Owner {
   int seq, first, next, value;
 };
-__device__ __forceinline__ Owner find_sequence(int64_t item, const int* cu, const int* each, int seqs, int mul,
-                                               int size, int extra) {
+template <typename Base>
+__device__ __forceinline__ Owner find_sequence(int64_t item, const int* cu, const int* each, int seqs, Base base) {
   const int lane = threadIdx.x & 63;
   Owner o{-1, 0, 0, 0};
   for (int b0 = 0; b0 < seqs; b0 += 64) {
     const int b = min(b0 + lane, seqs - 1);
     const int first = cu[b], next = cu[b + 1], value = each[b];
-    const bool below = b0 + lane < seqs && item_base(first, mul, size, extra, b) <= item;
+    const bool below = b0 + lane < seqs && base(first, b) <= item;
     const int n = __popcll(__ballot(below));
     if (n == 0) break;
     o.seq = b0 + n - 1;
