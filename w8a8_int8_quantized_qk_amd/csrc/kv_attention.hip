@@ -28,9 +28,9 @@
 // Scales may be any finite numbers.  Where K's is negative, or V's is outside
 // [2^-64, 2^126] (a fresh cache's is 0), the scores are multiplied out before
 // their maximum is taken, the exponent takes V's magnitude raised to 2^-64, and
-// the power of two (or sign, or 0) that is left multiplies p or the codes
-// before they are rounded to binary16, which costs values below 2^-64 an
-// absolute error of 2^-88 at most.  The sum l keeps binary32's precision as
+// the power of two (or sign, or 0) that is left multiplies p, rounded, or the
+// codes in binary16: exact but for binary16's smallest numbers, which costs
+// values below 2^-64 an absolute error of 2^-88 at most.  The sum l keeps binary32's precision as
 // long as the V scales that a row sees, so raised, lie within 2^92 of each other.
 #include <algorithm>
 #include <cmath>
@@ -133,22 +133,29 @@ __device__ __forceinline__ Tile find_cols(const Params& p, unsigned item) {
 // floor(n * group / 128), the second, where sequences of up to `small` columns are
 // the other kernel's, at least one more to every longer sequence and at most
 // one for every small + 1 columns of the call, however many sequences there are.
-__host__ __device__ __forceinline__ int64_t tile_base(int64_t row, int group, int small, int b) {
-  const int64_t cols = row * group, many = cols / (kSmall + 1);
-  return cols / kTileCols + (small && many < b ? many : b);
+// A call's columns fit in 31 bits, which the host checks with Int = int64_t; the
+// device counts in 32 bits, where an offset outside the call may give any base:
+// it is the sequence's alone, and such a sequence is dropped.
+template <typename Int>
+__host__ __device__ __forceinline__ int64_t tile_base(Int row, int group, int small, Int b) {
+  const Int cols = row * static_cast<Int>(group), many = cols / (kSmall + 1);
+  return static_cast<int64_t>(cols / kTileCols + (small && many < b ? many : b));
+}
+__device__ __forceinline__ int64_t tile_base_of(const Params& p, int row, int b) {
+  return tile_base<uint32_t>(row, p.group, p.small, b);
 }
 
 __device__ __forceinline__ Tile find_tile(const Params& p, int64_t item) {
   Tile t{};
   const kv::Owner o = kv::find_sequence(item, p.a.cu, p.a.lens, p.a.seqs, [&](int row, int seq) {
-    return tile_base(row, p.group, p.small, seq);
+    return tile_base_of(p, row, seq);
   });
   t.seq = o.seq;
   t.rows = o.next - o.first;
   t.row0 = o.first;
   if (o.seq < 0 || o.first < 0 || t.rows <= 0 || t.rows > p.a.tokens - o.first) return t;
   if (static_cast<int64_t>(t.rows) * p.group <= p.small) return t;
-  set_range(p, t, (item - tile_base(t.row0, p.group, p.small, t.seq)) * kTileCols, kTileCols, o.value);
+  set_range(p, t, (item - tile_base_of(p, o.first, o.seq)) * kTileCols, kTileCols, o.value);
   return t;
 }
 
@@ -532,7 +539,7 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
     const bool odd = __any(!plain_scales(ks[S], vs[S]));
     if (t0 < t.lo || t0 + kGroup > t.len - t.rows || p.a.window > 0 || odd) {  // some column may not see all 64
       const int at = t0 + 16 * g;
-      if (odd) {
+      if (odd) [[unlikely]] {
         const SplitScale v = split_scale(vs[S]);
         bias[0] = v.log2;
         inv_vs[0] = v.inv;
@@ -551,14 +558,16 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
 #pragma unroll
       for (int i = 0; i < VC; ++i) o[i] *= shrink;
     });
-    if (__any(!(vs[S] >= kLeastScale))) {
-      const float rest = split_scale(vs[S]).rest;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[0][i] *= rest;
-    }
     half8_t pf[2];
 #pragma unroll
     for (int i = 0; i < 16; ++i) pf[i >> 3][i & 7] = static_cast<_Float16>(s[0][i]);
+    // after the rounding, where half as many registers are live (before it: 8
+    // spilled for FP8 at dim 128, and short FP8 calls took 1.04 times as long)
+    if (__any(!(vs[S] >= kLeastScale))) [[unlikely]] {
+      const float rest = split_scale(vs[S]).rest;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pf[i >> 3][i & 7] = static_cast<_Float16>(static_cast<float>(pf[i >> 3][i & 7]) * rest);
+    }
     if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) {
       const int have = t0 + 16 * g + 16 > t.lo ? t.len - (t0 + 16 * g) : 0;
 #pragma unroll
@@ -779,7 +788,7 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
       lds_s[H][1][wave] = __builtin_amdgcn_logf(sv[S]);
       lds_s[H][2][wave] = __builtin_amdgcn_rcpf(sv[S]);
     }
-    if (__any(!plain_scales(sk[S], sv[S]))) {  // the wave's 16 positions have one block's scales
+    if (__any(!plain_scales(sk[S], sv[S]))) [[unlikely]] {  // the wave's 16 positions have one block's scales
       const SplitScale v = split_scale(sv[S]);
       const _Float16 turn = sk[S] < 0.0f ? -1.0f : 1.0f;
 #pragma unroll 1
@@ -1035,7 +1044,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_tile_kernel(Par
   const int k = static_cast<int>(col % kTileCols);
   set_range(p, t, col - k, kTileCols, o.value);
   if (t.splits <= 1) return;
-  const int64_t item = tile_base(o.first, p.group, p.small, o.seq) + col / kTileCols;
+  const int64_t item = tile_base_of(p, o.first, o.seq) + col / kTileCols;
   float m, l;
   float4_t v;
   sum_chunks(p, (item * p.c.heads + head) * p.splits * p.cols + k, 0, t.splits, m, l, v);
@@ -1104,7 +1113,7 @@ Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q,
 Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window,
              int small) {
   if (!ragged || static_cast<int64_t>(max_q) * group <= kSmall) return Cut{};
-  const int64_t items = tile_base(tokens, group, small, seqs);
+  const int64_t items = tile_base<int64_t>(tokens, group, small, seqs);
   const int64_t full = static_cast<int64_t>(tokens) * group / kTileCols;
   const int64_t live = std::max<int64_t>(full + std::min<int64_t>(seqs, full) / 2, 1) * kv_heads;
   const int64_t range = range_of(max_kv, window, kTileCols), wanted = dim > 128 ? 256 : 512;
