@@ -116,6 +116,17 @@ def test_window(window, fp8):
     t.check(out, lse, window=window)
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 3, 2 ** 31 - 1, 2 ** 40])
+def test_a_window_without_bound(window):
+    # as no window, also where rows stand before position 0
+    lens, counts = [3, 70, 40, 0, 1], [9, 70, 100, 4, 1]
+    t = Setup(17, lens, counts, 4, 2, 64, 16, False, "bf16")
+    want, want_lse = t.run(return_lse=True)
+    t.check(want, want_lse)
+    out, lse = t.run(return_lse=True, window=window)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_long_cache_is_split(fp8, dtype):

@@ -92,6 +92,12 @@ struct Tile {
   int splits;
 };
 
+// The first position that a row at `pos` sees (a row before position 0 none,
+// whatever this says; held to 0 first, for windows close to 2^31).
+__device__ __forceinline__ int first_seen(const Params& p, int pos) {
+  return p.a.window > 0 ? max(max(pos, 0) - p.a.window + 1, 0) : 0;
+}
+
 // Columns col0 .. col0 + size of the sequence whose rows are already in t.
 __device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0, int size, int len) {
   const int64_t all = static_cast<int64_t>(t.rows) * p.group;
@@ -102,7 +108,7 @@ __device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0
   const int first_pos = t.len - t.rows + t.col0 / p.group;
   const int last_pos = t.len - t.rows + (t.col0 + t.ncols - 1) / p.group;
   t.hi = min(last_pos + 1, t.len);
-  t.lo = p.a.window > 0 ? max(first_pos - p.a.window + 1, 0) : 0;
+  t.lo = first_seen(p, first_pos);
   t.splits = t.hi > t.lo ? (t.hi - (t.lo & ~(kGroup - 1)) + p.chunk - 1) / p.chunk : 0;
   t.live = true;
 }
@@ -211,7 +217,7 @@ __device__ __forceinline__ Column column_of(const Params& p, const Tile& t, int 
   c.out_row = (t.row0 + row) * p.a.heads + h;
   c.q_at = (t.row0 + row) * p.a.ldq + static_cast<int64_t>(h) * p.c.dim;
   const int pos = t.len - t.rows + row;
-  c.see_lo = p.a.window > 0 ? max(pos - p.a.window + 1, 0) : 0;
+  c.see_lo = first_seen(p, pos);
   c.see_hi = c.valid ? min(pos + 1, t.len) : 0;
   return c;
 }
@@ -716,8 +722,7 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   const bool any = w0 < t.ncols;
   const int pos0 = t.len - t.rows + (t.col0 + w0) / p.group, pos1 = t.len - t.rows + (t.col0 + max(w1, 0)) / p.group;
   const int all_hi = min(pos0 + 1, t.len), any_hi = any ? min(pos1 + 1, t.len) : 0;
-  const int all_lo = p.a.window > 0 ? max(pos1 - p.a.window + 1, 0) : 0;
-  const int any_lo = p.a.window > 0 ? max(pos0 - p.a.window + 1, 0) : 0;
+  const int all_lo = first_seen(p, pos1), any_lo = first_seen(p, pos0);
 
   float16_t o[ND];
 #pragma unroll
