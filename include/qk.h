@@ -581,6 +581,7 @@ int qk_kv_cache_read(int seqs, int tokens, int kv_heads, int dim, void *k, int64
  *   max_q   a bound on every sequence's number of rows (a tight one saves work;
  *           rows of a sequence with more may be left unwritten).
  *   max_kv  a bound on lens, held to width * block; a length above it counts as it.
+ *           At most 2^30 - 128, so held.
  *   out  [tokens][heads][dim] of dtype, dense;  lse [tokens][heads] float or
  *        NULL.
  *   workspace  qk_kv_attention_workspace_size(...) bytes (ragged: whether cu is given;
@@ -594,6 +595,7 @@ int qk_kv_cache_read(int seqs, int tokens, int kv_heads, int dim, void *k, int64
  * products exactly, probabilities rounded to 11 bits.
  * Errors: as qk_kv_cache_write; heads not a multiple of kv_heads, cu NULL with tokens !=
  * seqs, scale not finite, negative window or bound, max_q < 1 (QK_ERR_INVALID_VALUE);
+ * max_kv beyond its limit (QK_ERR_UNSUPPORTED);
  * workspace missing, misaligned or short (QK_ERR_WORKSPACE).
  */
 size_t qk_kv_attention_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim, int ragged,

@@ -72,6 +72,11 @@ def test_rows(name, kw, status):
     (dict(scale=float("nan")), INVALID), (dict(q=FAKE_ODD), UNSUP), (dict(out=FAKE_ODD), UNSUP), (dict(lens=FAKE_ODD), UNSUP),
     (dict(lse=FAKE_ODD), UNSUP),
     (dict(ldt=1000, width=1000, max_kv=16000), WS),
+    # positions that 32-bit arithmetic has no room for, whatever the workspace; the bound as the table holds it counts
+    (dict(ldt=1 << 24, width=1 << 24, block=128, max_kv=(1 << 31) - 1), UNSUP),
+    (dict(ldt=1 << 24, width=1 << 24, block=128, max_kv=(1 << 30) - 127), UNSUP),
+    (dict(ldt=1 << 24, width=1 << 24, block=128, max_kv=(1 << 30) - 128), WS),
+    (dict(ldt=1000, width=1000, max_kv=(1 << 31) - 1), WS),
     (dict(ldt=1000, width=1000, max_kv=16000, workspace=FAKE, workspace_bytes=64), WS),
     (dict(ldt=1000, width=1000, max_kv=16000, workspace=ctypes.c_void_p(0x100010), workspace_bytes=1 << 30), WS),
 ])
@@ -123,4 +128,6 @@ def test_attention_workspace_size():
     assert size(0, 1, 4, 2, 64, 100000) == 0
     assert size(1, 1, 4, 3, 64, 100000) == 0                 # refused shapes need none
     assert size(1, 1, 4, 2, 64, 100000, window=100) == 0     # a window bounds the range
+    assert size(1, 1, 4, 2, 64, (1 << 30) - 128) > 0
+    assert size(1, 1, 4, 2, 64, (1 << 30) - 127) == 0
     assert size(1, 200, 4, 2, 64, 100000, ragged=True, max_q=200) > 0

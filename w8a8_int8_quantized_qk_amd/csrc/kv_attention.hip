@@ -1074,7 +1074,7 @@ Cut cut_of(int64_t items, int tiles, int kv_heads, int dim, int cols, int64_t ra
   Cut c{items, tiles, 0, 0, cols, 0};
   const int64_t all = items * kv_heads;
   if (chunk > range || all > kCounters) chunk = range;
-  c.chunk = static_cast<int>(std::min<int64_t>(chunk, 1 << 30));
+  c.chunk = static_cast<int>(chunk);  // at most 2^30, the range of kKvMostPositions
   c.splits = static_cast<int>((range + c.chunk - 1) / c.chunk);
   if (c.splits > 1) c.bytes = static_cast<size_t>(all) * c.splits * cols * (dim + 2) * sizeof(float);
   return c;

@@ -604,7 +604,7 @@ int qk_kv_cache_read(int seqs, int tokens, int kv_heads, int dim, void* k, int64
 size_t qk_kv_attention_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim, int ragged,
                                       int max_q, int max_kv, int window) {
   if (seqs <= 0 || tokens <= 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads != 0 || dim < 16 ||
-      dim > 256 || max_q < 1 || max_kv < 0 || window < 0)
+      dim > 256 || max_q < 1 || max_kv < 0 || max_kv > qk::kKvMostPositions || window < 0)
     return 0;
   return qk::kv_attention_workspace_bytes(seqs, tokens, heads, kv_heads, dim, ragged != 0, max_q, max_kv, window);
 }
@@ -626,6 +626,7 @@ int qk_kv_attention(int seqs, int tokens, int heads, int kv_heads, int dim, cons
   if (!aligned(q, 2) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(cu, 4)) return QK_ERR_UNSUPPORTED;
   const int64_t reach = static_cast<int64_t>(width) * block;
   if (reach < max_kv) max_kv = static_cast<int>(reach);
+  if (max_kv > qk::kKvMostPositions) return QK_ERR_UNSUPPORTED;
   const size_t need =
       qk::kv_attention_workspace_bytes(seqs, tokens, heads, kv_heads, dim, cu != nullptr, max_q, max_kv, window);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return QK_ERR_WORKSPACE;

@@ -205,7 +205,10 @@ struct KvRowsArgs {
 hipError_t launch_kv_cache_write(const KvCacheView& c, const KvRowsArgs& a, hipStream_t stream);
 hipError_t launch_kv_cache_read(const KvCacheView& c, const KvRowsArgs& a, hipStream_t stream);
 
-// Attention over the cache (kv_attention.hip).
+// Attention over the cache (kv_attention.hip).  The kernels count positions in
+// 32 bits, some steps of 64 beyond the last and in sums of two: max_kv is at
+// most kKvMostPositions.
+constexpr int kKvMostPositions = (1 << 30) - 128;
 struct KvAttentionArgs {
   int seqs, tokens, heads, dtype;
   const void* q;  // [tokens][heads][dim], row stride ldq
