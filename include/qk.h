@@ -545,8 +545,8 @@ int qk_rms_norm_quant(int m, int k, const void *x, int64_t ldx, const void *resi
  *   table [seqs][width] int, row stride ldt;  start [seqs];  cu [seqs + 1].
  * Errors: negative size, unknown type, code or block size, dim not a multiple
  * of 16 or out of range, short stride, NULL (QK_ERR_INVALID_VALUE); caches
- * not 16-byte aligned, others not aligned to their type, or more than 2^31
- * workgroups (QK_ERR_UNSUPPORTED).
+ * not 16-byte aligned, others not aligned to their type, or a grid of 2^32 work
+ * items and more, some 2^29 tokens times heads (QK_ERR_UNSUPPORTED).
  */
 int qk_kv_cache_write(int seqs, int tokens, int kv_heads, int dim, const void *k, int64_t ldk,
                       const void *v, int64_t ldv, int dtype, void *k_cache, void *v_cache,

@@ -45,6 +45,14 @@ def test_norm(kw, status):
     assert call(qk.library().qk_rms_norm_quant, NORM, **kw) == status
 
 
+@pytest.mark.parametrize("name", ["qk_kv_cache_write", "qk_kv_cache_read"])
+def test_grids_beyond_a_launch_are_refused_before_it(name):
+    assert call(getattr(qk.library(), name), ROWS, tokens=1 << 27, kv_heads=64, ldk=4096, ldv=4096) == UNSUP
+    many = dict(seqs=1 << 20, tokens=1 << 20, heads=64, kv_heads=64, ldq=4096, cu=NULL, max_q=1)
+    assert call(qk.library().qk_kv_attention, ATTEND, **many) == UNSUP
+    assert call(qk.library().qk_kv_attention, ATTEND, tokens=1 << 27, heads=64, kv_heads=64, ldq=4096, max_q=1 << 27) == UNSUP
+
+
 CACHE = [
     (dict(seqs=-1), INVALID), (dict(tokens=-1), INVALID), (dict(kv_heads=0), INVALID), (dict(dim=24), INVALID),
     (dict(dim=0), INVALID), (dict(dim=272), INVALID), (dict(block=8), INVALID), (dict(block=48), INVALID),

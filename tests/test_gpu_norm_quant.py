@@ -129,6 +129,18 @@ def test_on_another_stream():
         assert torch.equal(a, b)
 
 
+def test_more_rows_than_one_grid():
+    m, k = (1 << 24) + 5, 5                       # one workgroup a row
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.randn((m, k), generator=g, device=DEV, dtype=torch.float32).to(torch.bfloat16)
+    res = torch.randn((m, k + 1), generator=g, device=DEV, dtype=torch.float32).to(torch.bfloat16)[:, 1:]
+    w = torch.rand((k,), generator=g, device=DEV, dtype=torch.float32)
+    got = qk.rms_norm_quant(x, w, EPS, residual=res)
+    for at in (0, (1 << 23) - 3, (1 << 24) - 3):
+        rows = slice(at, at + 8)
+        _check(x[rows], w, res[rows], False, [t[rows] for t in got])
+
+
 def test_refusals():
     x, w, res = _inputs(2, 4, 64, "bf16")
     with pytest.raises(TypeError):

@@ -1196,10 +1196,9 @@ size_t kv_attention_workspace_bytes(int seqs, int tokens, int heads, int kv_head
 
 hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, hipStream_t stream) {
   const auto [cc, ct] = cuts_of(a.seqs, a.tokens, a.heads, c.heads, c.dim, a.cu != nullptr, a.max_q, a.max_kv, a.window);
-  const int64_t limit = 0x7fffffff;
-  if (cc.items * c.heads * std::max(cc.splits, kCols) + ct.items * c.heads * ct.splits > limit ||
-      static_cast<int64_t>(a.tokens) * a.heads > limit)
-    return hipErrorInvalidConfiguration;
+  if (!grid_fits((cc.items * cc.splits + ct.items * ct.splits) * c.heads, 64 * kWaves) ||
+      static_cast<int64_t>(a.tokens) * a.heads > 0x7fffffff)
+    return hipErrorInvalidConfiguration;  // the joins' grids are smaller: they are for few tiles
   Params p{};
   p.c = c;
   p.a = a;

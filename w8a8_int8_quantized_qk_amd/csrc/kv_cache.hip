@@ -387,7 +387,7 @@ hipError_t go(const Params& p, hipStream_t stream) {
   const int waves = p.c.block == 128 ? 8 : 4;
   const int64_t tasks = p.items * p.c.heads * 2;
   const int64_t groups = (tasks * (p.c.block / 16) + waves - 1) / waves;
-  if (groups > 0x7fffffff) return hipErrorInvalidConfiguration;
+  if (!grid_fits(groups, 64 * waves)) return hipErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(groups)), block(64 * waves);
   if constexpr (WRITE)
     return launch(kv_write_kernel<DT, FP8, DP>, grid, block, 0, stream, p);

@@ -26,6 +26,8 @@
 // 8192 rows of 8192 in 72 us (6.5 TB/s), 2048 of 4096 in 11 us (5.3 TB/s); 8
 // rows of 4096 in 6 us, which is the launch and one row's chain of a load and
 // two reductions.
+#include <algorithm>
+
 #include "quant_math.h"
 
 namespace qk {
@@ -455,12 +457,27 @@ hipError_t dispatch_dtype(const RmsNormQuantArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// More rows than a grid of one workgroup each may have go in several launches.
 hipError_t launch_rms_norm_quant(const RmsNormQuantArgs& a, hipStream_t stream) {
-  switch (a.dtype) {
-    case QK_F32: return dispatch_dtype<QK_F32>(a, stream);
-    case QK_BF16: return dispatch_dtype<QK_BF16>(a, stream);
-    default: return dispatch_dtype<QK_F16>(a, stream);
+  constexpr int kRows = 1 << 23;
+  static_assert(kRows <= 0xffffffffll / kBlock, "a launch's work items fit in 32 bits");
+  const int64_t bytes = a.dtype == QK_F32 ? 4 : 2;
+  for (int64_t row = 0; row < a.m; row += kRows) {
+    RmsNormQuantArgs s = a;
+    s.m = static_cast<int>(std::min<int64_t>(a.m - row, kRows));
+    s.x = static_cast<const char*>(a.x) + row * a.ldx * bytes;
+    if (a.residual) {
+      s.residual = static_cast<const char*>(a.residual) + row * a.ldr * bytes;
+      s.r_out = static_cast<char*>(a.r_out) + row * a.ldo * bytes;
+    }
+    s.q = a.q + row * a.k;
+    s.scale = a.scale + row;
+    const hipError_t e = a.dtype == QK_F32    ? dispatch_dtype<QK_F32>(s, stream)
+                         : a.dtype == QK_BF16 ? dispatch_dtype<QK_BF16>(s, stream)
+                                              : dispatch_dtype<QK_F16>(s, stream);
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 
 }  // namespace qk

@@ -30,6 +30,10 @@ hipError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t lds_by
       typed);
 }
 
+// Whether a grid of `groups` workgroups of `threads` is one that a launch takes:
+// fewer than 2^32 work items.
+inline bool grid_fits(int64_t groups, int threads) { return groups <= 0xffffffffll / threads; }
+
 // Split-K plan of the tiled INT8 GEMM (gemm_mfma.hip): splits > 1 when the
 // output has few tiles; `bytes` of workspace hold the INT32 partial sums.
 struct SplitKPlan {
