@@ -491,14 +491,15 @@ int qk_gemm_i8_asym(int m, int n, int k, const int8_t *a, const int32_t *zero_po
  * x, residual, residual_out  [m][k] of dtype (QK_F32, QK_BF16, QK_F16), rows
  *          ldx, ldr, ldo >= k elements apart.  residual NULL: no addition,
  *          residual_out is ignored; otherwise residual_out is required and
- *          may be residual or x itself (with the same row stride).
+ *          may be residual or x itself (with the same row stride).  Any other
+ *          overlap of its rows with theirs is an error.
  * weight   [k] of weight_dtype: dtype or QK_F32.
  * code     QK_CODE_I8 or QK_CODE_FP8;  q [m][k] dense;  scale [m].
  * A row whose max |y| is not finite (or whose sum is not) has that maximum as
  * its scale and codes 0.  k == 0 gives scale = 1e-12f / qmax.  Any alignment
  * of the element type, any k up to 2^30.
- * Errors: negative size, row stride below k, unknown type, negative or NaN eps, NULL
- * (QK_ERR_INVALID_VALUE); k above 2^30, misaligned (QK_ERR_UNSUPPORTED).
+ * Errors: negative size, row stride below k, unknown type, negative or NaN eps, NULL,
+ * overlapping rows (QK_ERR_INVALID_VALUE); k above 2^30, misaligned (QK_ERR_UNSUPPORTED).
  */
 int qk_rms_norm_quant(int m, int k, const void *x, int64_t ldx, const void *residual, int64_t ldr,
                       const void *weight, int dtype, int weight_dtype, double eps, int code,

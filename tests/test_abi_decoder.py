@@ -11,6 +11,10 @@ C = _header_constants()
 INVALID, UNSUP, WS = C["QK_ERR_INVALID_VALUE"], C["QK_ERR_UNSUPPORTED"], C["QK_ERR_WORKSPACE"]
 
 
+def at(offset):
+    return ctypes.c_void_p(FAKE.value + offset)
+
+
 def call(fn, defaults, **kw):
     args = dict(defaults)
     assert set(kw) <= set(args)
@@ -40,6 +44,12 @@ def test_constants():
     (dict(ldo=63), INVALID), (dict(x=FAKE_ODD), UNSUP), (dict(residual=FAKE_ODD), UNSUP), (dict(weight=FAKE_ODD), UNSUP),
     (dict(scale=FAKE_ODD), UNSUP), (dict(k=(1 << 30) + 1, ldx=1 << 31, ldr=1 << 31, ldo=1 << 31), UNSUP),
     (dict(m=0, x=NULL, q=NULL, scale=NULL), 0),
+    # rows of the sum that overlap rows of x or the residual: shifted by a row, within a row, by the last element,
+    # another stride from the same start, one row
+    (dict(residual_out=at(128)), INVALID), (dict(residual_out=at(2)), INVALID), (dict(x=at(2), residual=at(1 << 20)), INVALID),
+    (dict(x=at(1 << 20), residual_out=at(128), ldr=65, ldo=65), INVALID), (dict(x=at(1 << 20), residual_out=at(-126), ldr=100, ldo=100), INVALID),
+    (dict(x=at(1 << 20), ldo=65), INVALID), (dict(x=at(1 << 20), residual_out=at(128), ldo=128), INVALID),
+    (dict(m=1, residual_out=at(126)), INVALID),
 ])
 def test_norm(kw, status):
     assert call(qk.library().qk_rms_norm_quant, NORM, **kw) == status

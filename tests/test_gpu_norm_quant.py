@@ -129,6 +129,27 @@ def test_on_another_stream():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("m", [1, 6])
+def test_rows_side_by_side_in_one_buffer(m):
+    # x, residual and sum as columns of one buffer (also with a stride of two rows) share no element
+    k = 40
+    wide, w, _ = _inputs(3, 2 * m, 3 * k, "bf16", False)
+    w = w[:k].contiguous()
+    x, res = wide[:m, :k], wide[:m, k:2 * k]
+    for out in (wide[:m, 2 * k:], wide[::2, 2 * k:], wide[m:, k:2 * k]):
+        want = qk.rms_norm_quant(x, w, EPS, residual=res)
+        got = qk.rms_norm_quant(x, w, EPS, residual=res, residual_out=out)
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+    for inplace in (x.clone(), res.clone()):
+        pair = (inplace, res) if torch.equal(inplace, x) else (x, inplace)
+        got = qk.rms_norm_quant(pair[0], w, EPS, residual=pair[1], residual_out=inplace)
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+    with pytest.raises(qk.QKError, match="INVALID"):
+        qk.rms_norm_quant(x, w, EPS, residual=res, residual_out=wide[:m, k + 1:2 * k + 1])
+
+
 def test_more_rows_than_one_grid():
     m, k = (1 << 24) + 5, 5                       # one workgroup a row
     g = torch.Generator(device=DEV).manual_seed(6)

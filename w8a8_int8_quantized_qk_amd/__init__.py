@@ -822,7 +822,7 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     x [m, k] (fp32, bf16 or fp16), weight [k] of the same type or fp32.  With
     residual [m, k] the norm is taken of r = x + residual, and r, rounded to
     x's type, goes to residual_out (allocated when not given; may be residual
-    itself).  Rows of x, residual and residual_out may lie apart (slices).
+    or x itself, but not overlap their rows in another way).  Rows of x, residual and residual_out may lie apart (slices).
     Returns (q, scale), or (q, scale, residual_out) with a residual: q int8
     (float8_e4m3fn when fp8) [m, k], scale fp32 [m], ready for gemm_i8_scaled
     or gemm_fp8_scaled.

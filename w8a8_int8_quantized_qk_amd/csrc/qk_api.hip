@@ -504,6 +504,27 @@ int qk_gemm_i8_asym(int m, int n, int k, const int8_t* a, const int32_t* zero_po
   return status_of(qk::launch_gemm_asym(g, zero_point, wsum, stream));
 }
 
+// Whether some row of `in` (m rows of `row` bytes, ld_in bytes apart) overlaps a
+// row of `out` without being the same row in place.
+static bool rows_clash(const void* in, int64_t ld_in, const void* out, int64_t ld_out, int64_t m, int64_t row) {
+  const int64_t a = reinterpret_cast<intptr_t>(in), b = reinterpret_cast<intptr_t>(out);
+  if (row == 0 || a + (m - 1) * ld_in + row <= b || b + (m - 1) * ld_out + row <= a) return false;
+  if (m == 1) return a != b;
+  // rows i of `in` and j of `out` overlap where their distance is below `row`,
+  // which for each i can hold for the two j around it only
+  const int64_t last = ld_in == ld_out ? 1 : m;  // with one stride the distance depends on j - i alone
+  for (int64_t i = 0; i < last; ++i) {
+    const int64_t from = a + i * ld_in;
+    const int64_t near = (from - b) / ld_out - (from < b);
+    for (int64_t j = near; j <= near + 1; ++j) {
+      const bool there = ld_in == ld_out ? j > -m && j < m : j >= 0 && j < m;
+      const int64_t off = from - (b + j * ld_out);
+      if (there && off < row && off > -row && (off != 0 || i != j)) return true;
+    }
+  }
+  return false;
+}
+
 int qk_rms_norm_quant(int m, int k, const void* x, int64_t ldx, const void* residual, int64_t ldr,
                       const void* weight, int dtype, int weight_dtype, double eps, int code,
                       void* residual_out, int64_t ldo, void* q, float* scale, hipStream_t stream) {
@@ -519,6 +540,10 @@ int qk_rms_norm_quant(int m, int k, const void* x, int64_t ldx, const void* resi
   if (!aligned(x, e) || !aligned(weight, weight_dtype == QK_F32 ? 4 : 2) || !aligned(scale, 4))
     return QK_ERR_UNSUPPORTED;
   if (residual && (!aligned(residual, e) || !aligned(residual_out, e))) return QK_ERR_UNSUPPORTED;
+  const int64_t b = static_cast<int64_t>(e);
+  if (residual && (rows_clash(x, ldx * b, residual_out, ldo * b, m, k * b) ||
+                   rows_clash(residual, ldr * b, residual_out, ldo * b, m, k * b)))
+    return QK_ERR_INVALID_VALUE;
   const qk::RmsNormQuantArgs a{m,        k,          x,        ldx, residual,
                                ldr,      weight,     dtype,    weight_dtype == QK_F32,
                                eps,      residual_out, ldo,    code == QK_CODE_FP8,
