@@ -1113,17 +1113,24 @@ Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q,
 // beyond dim 128) and the range is long.  Measured (us unsplit / split): 500
 // rows of 600 positions 24 / 35, 700 of 1400 47 / 30, 300 of 4000 123 / 38, 512
 // of 8192 220 / 112.
+// A handful of rows (fewer columns than one tile) get short chunks, since the
+// bound on the range is mostly what the table covers and they are over before
+// it: 30 rows of 32 heads on 8 with a table of 131072, counted as a whole tile /
+// a half / a quarter: over 4000 positions 65 / 42 / 32 us, over 20000 69 / 57 /
+// 46, over all of them 106 / 126 / 135.
+//
 // Of the items, which all have room for partial results, few can be without
-// columns: at 128 columns, 512 chunks in all and dim 128 that is some 140 MB.
+// columns, so that the workspace stays below some 300 MB.
 Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window,
              int small) {
   if (!ragged || static_cast<int64_t>(max_q) * group <= kSmall) return Cut{};
   const int64_t items = tile_base<int64_t>(tokens, group, small, seqs);
   const int64_t full = static_cast<int64_t>(tokens) * group / kTileCols;
-  const int64_t live = std::max<int64_t>(full + std::min<int64_t>(seqs, full) / 2, 1) * kv_heads;
-  const int64_t range = range_of(max_kv, window, kTileCols), wanted = dim > 128 ? 256 : 512;
+  // in half tiles; a call without a full one counts as a quarter of one
+  const int64_t live = full ? 2 * (full + std::min<int64_t>(seqs, full) / 2) * kv_heads : (kv_heads + 1) / 2;
+  const int64_t range = range_of(max_kv, window, kTileCols), wanted = dim > 128 ? 512 : 1024;
   int64_t chunk = range;
-  if (live < 192 && range > 1024) chunk = ((range * live + wanted - 1) / wanted + 255) / 256 * 256;
+  if (live < 384 && range > 1024) chunk = ((range * live + wanted - 1) / wanted + 255) / 256 * 256;
   return cut_of(items, 1, kv_heads, dim, kTileCols, range, std::max<int64_t>(chunk, 512));
 }
 
