@@ -326,6 +326,26 @@ def test_non_finite_values_reach_only_rows_that_see_them(fp8):
     assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("lens,counts", [([80, 40], [1, 1]), ([80, 40], [5, 40]), ([80, 200], [70, 90]), ([5000, 90], [1, 1]),
+                                         ([2500, 90], [90, 1])])
+def test_scores_that_are_all_minus_infinity(lens, counts):
+    # 0 / 0 by the formula, unlike a row that sees nothing; the log of their sum is -infinity either way
+    t = Setup(33, lens, counts, 4, 2, 64, 16, False, "f16")
+    t.cache.k.view(torch.uint8)[:, :, :, 0] = 1
+    t.q[0, 1, 0] = -float("inf")
+    cu = plain.offsets(counts)
+    t.q[cu[1], 2, 0] = -float("inf")
+    out, lse = t.run(return_lse=True, max_q=max(counts))
+    for row, head in ((0, 1), (int(cu[1]), 2)):
+        assert torch.isnan(out[row, head]).all() and lse[row, head] == -float("inf")
+        t.q[row, head, 0] = out[row, head] = 0
+    other, other_lse = t.run(return_lse=True, max_q=max(counts))
+    for row, head in ((0, 1), (int(cu[1]), 2)):
+        other[row, head] = 0
+        lse[row, head] = other_lse[row, head]
+    assert torch.equal(out, other) and torch.equal(lse, other_lse)
+
+
 def test_table_entries_out_of_range_give_nan():
     t = Setup(32, [80, 200], [1, 1], 2, 1, 64, 16, False, "bf16")
     clean = t.run()

@@ -323,6 +323,11 @@ __device__ __forceinline__ SplitScale split_scale(float vs) {
                     vs == 0.0f ? 0.0f : __builtin_copysignf(__builtin_amdgcn_ldexpf(1.0f, -up), vs)};
 }
 
+// What a column's sums are multiplied by: 0 for a column that sees nothing, that
+// is, whose row stands before position 0; where the scores of one that does
+// are all -infinity, l and the sums are 0 and the products NaN.
+__device__ __forceinline__ float inverse_of(float l, bool sees) { return sees ? 1.0f / l : 0.0f; }
+
 // One step of the running softmax over a lane's scores of one column: N
 // pieces of E raw scores s, whose exponents are y = s c + b with c >= 0 and
 // b = log2 v_scale per piece.  Leaves p = 2^(y - m + 14) in s.  m is raised to
@@ -392,8 +397,9 @@ __device__ __forceinline__ void join_chunks(const Params& p, const Tile& t, int 
         b = __builtin_fmaf(b, f0, o[j].y * f1);
       }
     }
-    const int64_t out_row = column_of(p, t, head, k).out_row;
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    const Column col = column_of(p, t, head, k);
+    const int64_t out_row = col.out_row;
+    const float inv = inverse_of(l, col.see_hi > 0);
     *reinterpret_cast<kv::Raw4<2>*>(static_cast<char*>(p.a.out) + (out_row * p.c.dim + d) * 2) =
         kv::Raw4<2>{qm::pack2_narrow<DT>(a * inv, b * inv)};
     if (d == 0 && p.a.lse) p.a.lse[out_row] = lse_of(m, l);
@@ -644,8 +650,9 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
       b = __builtin_fmaf(v.y, f, b);
     }
     if (whole) {
-      const int64_t out_row = column_of(p, t, head, k).out_row;
-      const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
+      const Column c = column_of(p, t, head, k);
+      const int64_t out_row = c.out_row;
+      const float inv = inverse_of(ll, c.see_hi > 0);
       *reinterpret_cast<kv::Raw4<2>*>(static_cast<char*>(p.a.out) + (out_row * dim + d) * 2) =
           kv::Raw4<2>{qm::pack2_narrow<DT>(a * inv, b * inv)};
       if (d == 0 && p.a.lse) p.a.lse[out_row] = lse_of(mm, ll);
@@ -905,7 +912,9 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   l = column_sum<false>(l);
   // register 4 q + e of o[i] is element 32 i + 8 q + 4 h + e
   if (t.splits <= 1) {
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    // (with col kept for this, calls of few steps took 1.03 to 1.06 times as long)
+    if (__any(l == 0.0f)) [[unlikely]] inv = inverse_of(l, column_of(p, t, head, wave * 32 + n).see_hi > 0);
 #pragma unroll
     for (int i = 0; i < ND; ++i)
 #pragma unroll
@@ -986,9 +995,10 @@ __device__ __forceinline__ void sum_chunks(const Params& p, int64_t slot, int fi
 }
 
 template <int DT>
-__device__ __forceinline__ void store_row(const Params& p, int64_t out_row, float m, float l, const float4_t& v) {
+__device__ __forceinline__ void store_row(const Params& p, int64_t out_row, bool sees, float m, float l,
+                                          const float4_t& v) {
   const int lane = threadIdx.x & 63;
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  const float inv = inverse_of(l, sees);
   if (4 * lane < p.c.dim)
     *reinterpret_cast<kv::Raw8<2>*>(static_cast<char*>(p.a.out) + (out_row * p.c.dim + 4 * lane) * 2) =
         kv::Raw8<2>{{qm::pack2_narrow<DT>(v[0] * inv, v[1] * inv), qm::pack2_narrow<DT>(v[2] * inv, v[3] * inv)}};
@@ -1026,7 +1036,8 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_cols_kernel(Par
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(lds_o[w][4 * lane + e], f, v[e]);
   }
-  store_row<DT>(p, column_of(p, t, at.head, at.inner).out_row, m, l, v);
+  const Column col = column_of(p, t, at.head, at.inner);
+  store_row<DT>(p, col.out_row, col.see_hi > 0, m, l, v);
 }
 
 // Few chunks of many columns: one (row, head) pair per wave, over the rows as
@@ -1053,7 +1064,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_tile_kernel(Par
   float m, l;
   float4_t v;
   sum_chunks(p, (item * p.c.heads + head) * p.splits * p.cols + k, 0, t.splits, m, l, v);
-  store_row<DT>(p, pair, m, l, v);
+  store_row<DT>(p, pair, row - o.first >= t.rows - t.len, m, l, v);
 }
 
 // How a call is cut: which kernels run, their tiles and chunks of positions.
