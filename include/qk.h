@@ -592,12 +592,15 @@ int qk_kv_cache_read(int seqs, int tokens, int kv_heads, int dim, void *k, int64
  *        launch error; every successful call leaves them zero, so one buffer
  *        serves all calls issued in order on a stream.  Calls that can run at
  *        the same time must not share one.
+ * A row that sees positions, all with scores of -infinity, gives NaN.
  * Scores, maxima, sums and outputs are held in binary32; codes enter the
- * products exactly, probabilities rounded to 11 bits.
+ * products exactly, probabilities rounded to 11 bits.  FP8 NaN codes of V, which
+ * a write of tokens never makes (it makes the scale NaN and the codes 0), may
+ * also reach rows of the same sequence that do not see them.
  * Errors: as qk_kv_cache_write; heads not a multiple of kv_heads, cu NULL with tokens !=
  * seqs, scale not finite, negative window or bound, max_q < 1 (QK_ERR_INVALID_VALUE);
- * max_kv beyond its limit (QK_ERR_UNSUPPORTED);
- * workspace missing, misaligned or short (QK_ERR_WORKSPACE).
+ * max_kv beyond its limit (QK_ERR_UNSUPPORTED); workspace missing, misaligned or
+ * short (QK_ERR_WORKSPACE).
  */
 size_t qk_kv_attention_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim, int ragged,
                                       int max_q, int max_kv, int window);

@@ -688,8 +688,9 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
 // banks: 16 rows where a row of K has 16 pieces or more (eight only: 176 us for
 // 173 in the case below).
 //
-// 4096 rows of 32 heads on 8, dim 128, causal: 170-177 us, 790 TFLOP/s (a plain
-// binary16 matrix product of 8192^3 reaches 1280 here).  A wave's step is 1024
+// 4096 rows of 32 heads on 8, dim 128, causal: 170-178 us, 770 to 810 TFLOP/s (a
+// plain binary16 matrix product of 8192^3 reaches 1280 here), when some 200 calls
+// have run before; the first after a pause take 190 to 205.  A wave's step is 1024
 // cycles of matrix instructions and some 300 vector instructions (64 codes
 // converted, 32 exponentials), of which the two waves of a SIMD overlap a part.
 // Measured beside it: 64 columns per wave, which halves the reads of LDS but
