@@ -476,6 +476,103 @@ int qk_gemm_i8_asym(int m, int n, int k, const int8_t *a, const int32_t *zero_po
                     int b_layout, hipStream_t stream);
 
 /* ------------------------------------------------------------------ */
+/* Microscaled 4-bit floating point                                    */
+/* ------------------------------------------------------------------ */
+/*
+ * Rows in blocks of 32 consecutive values, each value a 4-bit code (E2M1: sign,
+ * two bits of exponent, one of mantissa) under its block's power of two (E8M0),
+ * as in the Open Compute Project's Microscaling Formats specification 1.0:
+ *   codes   [m][k / 2] bytes, dense: value 2 i in the low half of byte i.  Codes 0
+ *           .. 7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign.
+ *   scales  [m] rows of k / 32 bytes, lds bytes apart: byte b stands for
+ *           2^(b - 127), 255 for NaN.  lds is a multiple of 16, at least k / 32, and
+ *           a row can be read up to the next multiple of 16 (what lies past k / 32
+ *           is neither used nor written).
+ * k is a multiple of 32.  codes and scales are 16-byte aligned.
+ */
+
+/*
+ * Quantises rows.  Per block of 32 values:
+ *   scale = max(2^(floor(log2(max |x|)) - 2), 2^-127)      (0: 2^-127)
+ *   code  = x / scale to the nearest code, ties to the even one, at most 6
+ * A block that holds an infinity or a NaN gets the scale NaN and codes 0.
+ * The _silu_mul_ form quantises silu(gate) * up of h [m][2d], formed as in
+ * qk_silu_mul_quant_per_token.
+ *   x [m][k] of x_dtype, rows ldx >= k (h: ldh >= 2d) elements apart.
+ * Any alignment of the element type.  Errors: negative size, unknown type, short
+ * stride, NULL (QK_ERR_INVALID_VALUE); k (d) not a multiple of 32, misaligned,
+ * 2^35 values and more (QK_ERR_UNSUPPORTED).
+ */
+int qk_quant_mx4(int m, int k, const void *x, int64_t ldx, int x_dtype, uint8_t *q, uint8_t *scale,
+                 int64_t lds, hipStream_t stream);
+int qk_silu_mul_quant_mx4(int m, int d, const void *h, int64_t ldh, int h_dtype, uint8_t *q,
+                          uint8_t *scale, int64_t lds, hipStream_t stream);
+
+/*
+ * The values that codes and scales stand for, x[i][j] = code * scale, rounded
+ * to x_dtype, nearest even (exact but in fp16).  Arguments and errors as
+ * qk_quant_mx4, with x written.
+ */
+int qk_dequant_mx4(int m, int k, const uint8_t *q, const uint8_t *scale, int64_t lds, void *x,
+                   int64_t ldx, int x_dtype, hipStream_t stream);
+
+/*
+ * The product of two such operands:
+ *   out[i][j] = output_scale * sum_t A(i, t) * B(j, t)     (binary32 sums)
+ *   a [m][k / 2], scale_a (rows ldsa bytes apart); b [n][k / 2], scale_b (rows
+ *   ldsb bytes apart): the weight with k contiguous;  out [m][n] of out_dtype
+ *   (QK_F32, QK_BF16 or QK_F16), rounded once, nearest even.
+ * A NaN scale makes its row (column) NaN.  k == 0 gives zeros.  No workspace.
+ * Errors: negative size, unknown type, short stride, NULL (QK_ERR_INVALID_VALUE);
+ * k not a multiple of 32, misaligned, m or n above 2^24 (QK_ERR_UNSUPPORTED).
+ */
+int qk_gemm_mx4_scaled(int m, int n, int k, const uint8_t *a, const uint8_t *scale_a, int64_t ldsa,
+                       const uint8_t *b, const uint8_t *scale_b, int64_t ldsb, float output_scale,
+                       void *out, int out_dtype, hipStream_t stream);
+
+/*
+ * The 4-bit layer: qk_quant_mx4 of x into q_out / scale_out (rows lds_out bytes
+ * apart), then qk_gemm_mx4_scaled of those with the weight (two launches on
+ * `stream`).  Requirements and errors as the two calls.
+ */
+int qk_linear_mx4(int m, int n, int k, const void *x, int64_t ldx, int x_dtype, const uint8_t *b,
+                  const uint8_t *scale_b, int64_t ldsb, float output_scale, void *out, int out_dtype,
+                  uint8_t *q_out, uint8_t *scale_out, int64_t lds_out, hipStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Norm and rotation of queries and keys                               */
+/* ------------------------------------------------------------------ */
+/*
+ * What stands between the projections and the cache, for every head of every
+ * row in one launch: the root-mean-square norm over the head's elements and
+ * the rotation by the row's position.
+ *   y = (x * inv) * weight,  inv = 1 / sqrt(mean(x^2) + eps)   (binary32)
+ *   for i < rotary / 2, with (a, b) = (i, i + rotary / 2), or (2 i, 2 i + 1)
+ *   when interleaved:
+ *     out[a] = y[a] cos t - y[b] sin t,  out[b] = y[b] cos t + y[a] sin t,
+ *     t = position * freqs[i]            (angle and its whole turns in binary64)
+ *   out = y for elements past rotary; rounded once, nearest even.
+ * Sequence s's rows are cu[s] .. cu[s + 1] - 1, at positions start[s] and on; cu
+ * NULL: one row per sequence (tokens == seqs), at start[s].  Rows of no
+ * sequence are not written.
+ *   q [tokens][heads][dim], k [tokens][kv_heads][dim] of dtype, rows ldq and ldk
+ *     elements apart; q_out, k_out alike, rows ldqo and ldko apart.  An output
+ *     may be its own input (the same rows in place); any other overlap is an error.
+ *   q_weight, k_weight [dim] of weight_dtype (dtype or QK_F32), or NULL: no norm.
+ *   freqs [rotary / 2] double, on the device.
+ * dim is a multiple of 16 from 16 to 256, rotary even, from 0 to dim; heads or
+ * kv_heads may be 0 (its tensors are then not touched).
+ * Errors: negative size, unknown type, dim or rotary out of range, short stride,
+ * negative or NaN eps, NULL, overlapping rows (QK_ERR_INVALID_VALUE); misaligned,
+ * 2^24 rows and more (QK_ERR_UNSUPPORTED).
+ */
+int qk_norm_rope(int seqs, int tokens, int heads, int kv_heads, int dim, const void *q, int64_t ldq,
+                 const void *k, int64_t ldk, const void *q_weight, const void *k_weight, int dtype,
+                 int weight_dtype, float eps, const double *freqs, int rotary, int interleaved,
+                 const int *start, const int *cu, void *q_out, int64_t ldqo, void *k_out, int64_t ldko,
+                 hipStream_t stream);
+
+/* ------------------------------------------------------------------ */
 /* Root-mean-square norm with an 8-bit output                          */
 /* ------------------------------------------------------------------ */
 /*
@@ -610,6 +707,22 @@ int qk_kv_attention(int seqs, int tokens, int heads, int kv_heads, int dim, cons
                     const int *table, int64_t ldt, int width, const int *lens, const int *cu,
                     int max_q, int max_kv, float scale, int window, void *out, float *lse,
                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The same with the first `sinks` positions of every sequence visible beside
+ * the window: with window > 0 a row at position p sees j <= p with p - window < j
+ * or j < sinks.  (sinks 0, or window 0, which hides nothing: qk_kv_attention.)
+ * Blocks that hold neither may have been given back: their table entries are
+ * not used.  Negative sinks are QK_ERR_INVALID_VALUE.
+ */
+size_t qk_kv_attention_sinks_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim,
+                                            int ragged, int max_q, int max_kv, int window, int sinks);
+int qk_kv_attention_sinks(int seqs, int tokens, int heads, int kv_heads, int dim, const void *q,
+                          int64_t ldq, int dtype, const void *k_cache, const void *v_cache,
+                          const float *k_scale, const float *v_scale, int blocks, int block, int code,
+                          const int *table, int64_t ldt, int width, const int *lens, const int *cu,
+                          int max_q, int max_kv, float scale, int window, int sinks, void *out,
+                          float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

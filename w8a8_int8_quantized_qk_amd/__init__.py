@@ -16,11 +16,16 @@ and its FP8 (float8_e4m3fn) counterpart:
   q, s     = quant_per_token_fp8(x, scale_ub)   # or silu_mul_quant_per_token_fp8(h)
   out      = gemm_fp8_scaled(q, w8, s, s_ch)     # binary32 accumulate + dequant
   out      = linear_fp8(x, w8, s_ch)
+and in microscaled 4-bit floating point (blocks of 32 under a power of two):
+  q, s     = quant_mx4(x)                       # or silu_mul_quant_mx4(h); back: dequant_mx4(q, s)
+  out      = gemm_mx4_scaled(q, w4, s, s_w)      # w4, s_w = quant_mx4 of the weight [n, k]
+  out      = linear_mx4(x, w4, s_w)
 and what a decoder layer has between its linears, 8 bit as well:
   q, s, r  = rms_norm_quant(x, g, residual=r)    # r + x, norm, codes and scales
+  q, k     = norm_rope(q, k, start, freqs, cu)   # norm of heads and rotation by position
   cache    = new_kv_cache(blocks, kv_heads, dim) # a paged INT8 or FP8 cache
   kv_cache_write(cache, k, v, table, start, cu)  # quantised as it is written
-  out      = kv_attention(q, cache, table, lens) # attention over it
+  out      = kv_attention(q, cache, table, lens) # attention over it (window=, sinks=)
   k, v     = kv_cache_read(cache, table, start, cu, tokens)
 """
 from __future__ import annotations
@@ -58,6 +63,8 @@ EXPORTED = (
     "qk_quant_static_fp8", "qk_silu_mul_quant_static_fp8", "qk_quant_per_token_asym",
     "qk_weight_colsum", "qk_gemm_i8_asym", "qk_rms_norm_quant", "qk_kv_cache_write",
     "qk_kv_cache_read", "qk_kv_attention_workspace_size", "qk_kv_attention",
+    "qk_kv_attention_sinks_workspace_size", "qk_kv_attention_sinks", "qk_quant_mx4",
+    "qk_silu_mul_quant_mx4", "qk_dequant_mx4", "qk_gemm_mx4_scaled", "qk_linear_mx4", "qk_norm_rope",
 )
 
 
@@ -134,6 +141,22 @@ def _declare(lib):
     lib.qk_kv_attention.argtypes = [I, I, I, I, I, P, L, I, P, P, P, P, I, I, I, P, L, I, P, P, I, I, F, I, P,
                                     P, P, ctypes.c_size_t, P]
     lib.qk_kv_attention.restype = I
+    lib.qk_kv_attention_sinks_workspace_size.argtypes = [I] * 10
+    lib.qk_kv_attention_sinks_workspace_size.restype = ctypes.c_size_t
+    lib.qk_kv_attention_sinks.argtypes = [I, I, I, I, I, P, L, I, P, P, P, P, I, I, I, P, L, I, P, P, I, I, F, I, I,
+                                          P, P, P, ctypes.c_size_t, P]
+    lib.qk_kv_attention_sinks.restype = I
+    for name in ("qk_quant_mx4", "qk_silu_mul_quant_mx4"):
+        getattr(lib, name).argtypes = [I, I, P, L, I, P, P, L, P]
+        getattr(lib, name).restype = I
+    lib.qk_dequant_mx4.argtypes = [I, I, P, P, L, P, L, I, P]
+    lib.qk_dequant_mx4.restype = I
+    lib.qk_gemm_mx4_scaled.argtypes = [I, I, I, P, P, L, P, P, L, F, P, I, P]
+    lib.qk_gemm_mx4_scaled.restype = I
+    lib.qk_linear_mx4.argtypes = [I, I, I, P, L, I, P, P, L, F, P, I, P, P, L, P]
+    lib.qk_linear_mx4.restype = I
+    lib.qk_norm_rope.argtypes = [I, I, I, I, I, P, L, P, L, P, P, I, I, F, P, I, I, P, P, P, L, P, L, P]
+    lib.qk_norm_rope.restype = I
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -774,7 +797,7 @@ def gemm_i8_asym(a: torch.Tensor, zero_point: torch.Tensor, b: torch.Tensor, wsu
     return (out, c) if return_acc else out
 
 
-# ---- the operators between a decoder layer's linears ----
+# ---- the operators between a decoder layer's linears, and the 4-bit linear ----
 # These calls are short on the GPU: their checks and allocations are in C++
 # (csrc/bind.cpp, the module _qkbind) and raise the same exceptions.
 _bound = None
@@ -796,8 +819,9 @@ def _bind_to(lib: ctypes.CDLL):
         raise ImportError(
             f"{os.path.join(_HERE, '_qkbind.so')} is missing or was built for another torch: build it with "
             "`python -m w8a8_int8_quantized_qk_amd.build` (or __graft_entry__.build())") from e
-    names = ("qk_rms_norm_quant", "qk_kv_cache_write", "qk_kv_cache_read", "qk_kv_attention_workspace_size",
-             "qk_kv_attention")
+    names = ("qk_rms_norm_quant", "qk_kv_cache_write", "qk_kv_cache_read", "qk_kv_attention_sinks_workspace_size",
+             "qk_kv_attention_sinks", "qk_quant_mx4", "qk_silu_mul_quant_mx4", "qk_dequant_mx4", "qk_gemm_mx4_scaled",
+             "qk_linear_mx4", "qk_norm_rope")
     _qkbind.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names), _check,
                  torch._C._cuda_getCurrentRawStream, _workspace_on, torch._C._cuda_isCurrentStreamCapturing)
     return _qkbind
@@ -828,6 +852,81 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     or gemm_fp8_scaled.
     """
     return _bind().rms_norm_quant(x, weight, eps, residual, fp8, residual_out, q, scale)
+
+
+def norm_rope(q: torch.Tensor, k: torch.Tensor, start: torch.Tensor, freqs: torch.Tensor,
+              cu: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+              k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+              q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+    """Root-mean-square norm of every head's query and key, and their rotation by
+    position, one launch.
+
+    q [tokens, heads, dim], k [tokens, kv_heads, dim] (fp32, bf16 or fp16; rows
+    may lie apart, as slices of one projection); q_weight, k_weight [dim] of the
+    same type or fp32, None: no norm.  Sequence s's rows cu[s] .. cu[s + 1] - 1
+    stand at positions start[s], start[s] + 1, ... (int32 on the GPU); cu None:
+    one row per sequence.  freqs float64 [rotary / 2] on the GPU: the angle per
+    position of each pair of a head's first `rotary` elements, pairs (i, i +
+    rotary / 2), or (2 i, 2 i + 1) when interleaved; the others are not turned.
+    Returns (q_out, k_out), allocated when not given; each may be its own input.
+    Rows of no sequence are not written.
+    """
+    return _bind().norm_rope(q, k, start, freqs, cu, q_weight, k_weight, eps, interleaved, q_out, k_out)
+
+
+def new_mx4_scales(rows: int, k: int, device="cuda") -> torch.Tensor:
+    """An uninitialised tensor for the scales of `rows` microscaled rows of k
+    values: uint8 [rows, k / 32], rows beginning at multiples of 16 bytes."""
+    if k % 32 or k < 0 or rows < 0:
+        raise ValueError("k must be a multiple of 32, rows not negative")
+    return torch.empty((rows, -(-(k // 32) // 16) * 16), dtype=torch.uint8, device=device)[:, :k // 32]
+
+
+def quant_mx4(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """Microscaled 4-bit codes of x [m, k] (fp32, bf16 or fp16; rows may lie
+    apart; k a multiple of 32): blocks of 32 along k under one power of two.
+
+    Returns (q, scale): q uint8 [m, k / 2], two E2M1 codes to a byte, the lower k
+    in the lower half; scale uint8 [m, k / 32], the exponents + 127 (E8M0), its
+    rows at multiples of 16 bytes.  torch.float4_e2m1fn_x2 and
+    torch.float8_e8m0fnu views of them are taken wherever they are.  A block
+    with an infinity or NaN gets scale 255 (NaN).  The weight of gemm_mx4_scaled is
+    quantised the same way, from [n, k].
+    """
+    return _bind().quant_mx4(x, False, q, scale)
+
+
+def silu_mul_quant_mx4(h: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """quant_mx4 of silu(h[:, :d]) * h[:, d:], formed in binary32 as silu_mul does; d a multiple of 32."""
+    return _bind().quant_mx4(h, True, q, scale)
+
+
+def dequant_mx4(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                x: torch.Tensor | None = None) -> torch.Tensor:
+    """The values [m, k] that codes and scales stand for, in x's type when given, else dtype."""
+    if dtype not in _IN_DTYPES:
+        raise TypeError(f"dtype {dtype} not supported")
+    return _bind().dequant_mx4(q, scale, _IN_DTYPES[dtype], x)
+
+
+def gemm_mx4_scaled(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b: torch.Tensor,
+                    output_scale: float = 1.0, out_dtype: torch.dtype = torch.bfloat16,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """The product of two microscaled 4-bit operands, a [m, k / 2] and the weight
+    b [n, k / 2] (k contiguous) with the scales quant_mx4 gives: out [m, n] =
+    output_scale * sum_k A(i, k) B(j, k), binary32 sums, fp32, bf16 or fp16."""
+    if out_dtype not in _IN_DTYPES:
+        raise TypeError(f"out dtype {out_dtype} not supported")
+    return _bind().gemm_mx4_scaled(a, b, scale_a, scale_b, output_scale, _IN_DTYPES[out_dtype], out)
+
+
+def linear_mx4(x: torch.Tensor, w: torch.Tensor, scale_w: torch.Tensor, output_scale: float = 1.0,
+               out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The 4-bit layer: x [m, k] (fp32, bf16 or fp16) quantised as by quant_mx4,
+    times the weight w [n, k / 2] with its scales."""
+    if out_dtype not in _IN_DTYPES:
+        raise TypeError(f"out dtype {out_dtype} not supported")
+    return _bind().linear_mx4(x, w, scale_w, output_scale, _IN_DTYPES[out_dtype], out)
 
 
 KV_BLOCKS = (16, 32, 64, 128)
@@ -890,22 +989,23 @@ def kv_cache_read(cache: KVCache, table: torch.Tensor, start: torch.Tensor, cu: 
 
 
 def kv_attention_workspace_size(seqs: int, tokens: int, heads: int, kv_heads: int, dim: int, max_kv: int,
-                                window: int = 0, ragged: bool = False, max_q: int = 1) -> int:
+                                window: int = 0, ragged: bool = False, max_q: int = 1, sinks: int = 0) -> int:
     """Bytes of workspace of a kv_attention call (ragged: with cu); 0 if none."""
-    return int(library().qk_kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, ragged, max_q,
-                                                        max_kv, window))
+    return int(library().qk_kv_attention_sinks_workspace_size(seqs, tokens, heads, kv_heads, dim, ragged, max_q,
+                                                              max_kv, window, min(sinks, 2 ** 31 - 1)))
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
                  cu: torch.Tensor | None = None, scale: float | None = None, window: int = 0,
                  max_q: int | None = None, max_kv: int | None = None, out: torch.Tensor | None = None,
-                 return_lse: bool = False, workspace: torch.Tensor | None = None):
+                 return_lse: bool = False, workspace: torch.Tensor | None = None, sinks: int = 0):
     """Causal attention of q [tokens, heads, dim] (bf16 or fp16; rows may lie
     apart) over the cache.
 
     lens int32 [seqs]: positions of each sequence in the cache, its rows of q
     being the last of them; cu int32 [seqs + 1]: those rows, or None when every
-    sequence has one.  window > 0 limits a row to its last `window` positions.
+    sequence has one.  window > 0 limits a row to its last `window` positions
+    and, with sinks > 0, the sequence's first `sinks`, which stay visible.
     scale defaults to dim ** -0.5.  max_q and max_kv are bounds that the host
     knows on a sequence's rows and positions (by default all rows, and what the
     table covers); tight ones save work.  Returns out [tokens, heads, dim], and
@@ -920,4 +1020,4 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: tor
     that preparation; calls that can run at the same time must not share it.
     """
     return _bind().kv_attention(q, cache, table, lens, cu, scale, window, max_q, max_kv, out, return_lse,
-                                workspace)
+                                workspace, sinks)

@@ -26,7 +26,7 @@ LIB = os.path.join(PKG, "libqk.so")
 BIND = os.path.join(PKG, "_qkbind.so")
 SOURCES = ["qk_api.hip", "quant.hip", "quant_static.hip", "gemm_mfma.hip", "gemm_wide.hip",
            "gemm_spec.hip", "gemm_slice.hip", "gemv.hip", "norm_quant.hip", "kv_cache.hip",
-           "kv_attention.hip"]
+           "kv_attention.hip", "mx4_quant.hip", "mx4_gemm.hip", "norm_rope.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -1,5 +1,6 @@
 // Python module _qkbind: the checks and allocations of the calls that stand
-// between a decoder layer's linears (norm, cache, attention), in C++.
+// between a decoder layer's linears (norm, rotation, cache, attention) and of the
+// 4-bit linear, in C++.
 //
 // These kernels run for a few microseconds at decode sizes; the same checks in
 // Python took 7 to 10 us a call (about 0.6 us per checked tensor, 1.6 us per
@@ -35,11 +36,21 @@ struct Lib {
                int, int, int, const int*, int64_t, int, const int*, const int*, void*);
   int (*read)(int, int, int, int, void*, int64_t, void*, int64_t, int, const void*, const void*, const float*,
               const float*, int, int, int, const int*, int64_t, int, const int*, const int*, void*);
-  size_t (*workspace)(int, int, int, int, int, int, int, int, int);
+  size_t (*workspace)(int, int, int, int, int, int, int, int, int, int);
   int (*attention)(int, int, int, int, int, const void*, int64_t, int, const void*, const void*, const float*,
                    const float*, int, int, int, const int*, int64_t, int, const int*, const int*, int, int, float,
-                   int, void*, float*, void*, size_t, void*);
+                   int, int, void*, float*, void*, size_t, void*);
+  int (*quant4)(int, int, const void*, int64_t, int, uint8_t*, uint8_t*, int64_t, void*);
+  int (*silu_quant4)(int, int, const void*, int64_t, int, uint8_t*, uint8_t*, int64_t, void*);
+  int (*dequant4)(int, int, const uint8_t*, const uint8_t*, int64_t, void*, int64_t, int, void*);
+  int (*gemm4)(int, int, int, const uint8_t*, const uint8_t*, int64_t, const uint8_t*, const uint8_t*, int64_t, float,
+               void*, int, void*);
+  int (*linear4)(int, int, int, const void*, int64_t, int, const uint8_t*, const uint8_t*, int64_t, float, void*, int,
+                 uint8_t*, uint8_t*, int64_t, void*);
+  int (*rope)(int, int, int, int, int, const void*, int64_t, const void*, int64_t, const void*, const void*, int, int,
+              float, const double*, int, int, const int*, const int*, void*, int64_t, void*, int64_t, void*);
 };
+constexpr int kEntries = 11;
 Lib lib;
 PyObject* py_check = nullptr;          // check(status): raises for a status other than 0
 PyObject* py_stream = nullptr;         // current stream of a device index, as a number
@@ -63,6 +74,8 @@ std::string dtype_name(at::ScalarType t) {
     case at::kHalf: return "torch.float16";
     case at::kChar: return "torch.int8";
     case at::kInt: return "torch.int32";
+    case at::kByte: return "torch.uint8";
+    case at::kDouble: return "torch.float64";
     case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return std::string("torch.") + c10::toString(t);
   }
@@ -395,9 +408,9 @@ std::map<std::pair<int, void*>, PyObject*>& workspaces() {
   return *all;
 }
 
-// (q, cache, table, lens, cu, scale, window, max_q, max_kv, out, return_lse, workspace)
+// (q, cache, table, lens, cu, scale, window, max_q, max_kv, out, return_lse, workspace, sinks)
 PyObject* kv_attention(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 12);
+  need_args(n, 13);
   const at::Tensor& q = tensor(a[0], "q");
   const at::ScalarType dt = q.scalar_type();
   if (dt != at::kBFloat16 && dt != at::kHalf) type_error("q dtype " + dtype_name(dt) + " not supported");
@@ -437,6 +450,7 @@ PyObject* kv_attention(PyObject* const* a, Py_ssize_t n) {
   max_q = std::min(std::max<int64_t>(max_q, -1), top);
   max_kv = std::min(std::max<int64_t>(max_kv, -1), top);
   const int w = static_cast<int>(std::min(std::max<int64_t>(window, -1), top));
+  const int first = static_cast<int>(std::min(std::max<int64_t>(integer(a[12]), -1), top));
   const int ns = narrow(seqs, "sequences"), nt = narrow(tokens, "tokens"), nh = narrow(heads, "heads");
 
   const c10::DeviceGuard guard(dev);
@@ -455,7 +469,8 @@ PyObject* kv_attention(PyObject* const* a, Py_ssize_t n) {
     ws = t.data_ptr();
     bytes = t.nbytes();
   } else {
-    const size_t need = lib.workspace(ns, nt, nh, c.heads, c.dim, ragged, static_cast<int>(max_q), static_cast<int>(max_kv), w);
+    const size_t need = lib.workspace(ns, nt, nh, c.heads, c.dim, ragged, static_cast<int>(max_q), static_cast<int>(max_kv), w,
+                                      first);
     if (need > 0) {
       PyObject* use = nullptr;
       size_t had = 0;
@@ -482,12 +497,220 @@ PyObject* kv_attention(PyObject* const* a, Py_ssize_t n) {
       ns, nt, nh, c.heads, c.dim, q.data_ptr(), ldq, type_code(dt), c.k.data_ptr(), c.v.data_ptr(),
       static_cast<const float*>(c.ks.data_ptr()), static_cast<const float*>(c.vs.data_ptr()), c.blocks, c.block, c.code,
       c.table, c.ldt, c.width, static_cast<const int*>(lens.data_ptr()), cu, static_cast<int>(max_q),
-      static_cast<int>(max_kv), scale, w, out.data_ptr(), want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, ws,
+      static_cast<int>(max_kv), scale, w, first, out.data_ptr(), want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, ws,
       bytes, stream);
   if (status != 0 && status < 1000) workspaces().erase(key);  // part of the call may have run: a fresh one next time
   check(status);
   PyObject* const oo = a[9] != Py_None ? same(a[9]) : wrapped(out);
   return want_lse ? tuple_of({oo, wrapped(lse)}) : oo;
+}
+
+// ---- microscaled 4-bit rows ----
+
+at::ScalarType out_type(int64_t code) {
+  if (code < 0 || code > 2) type_error("dtype must be float32, bfloat16 or float16");
+  return code == 0 ? at::kFloat : code == 1 ? at::kBFloat16 : at::kHalf;
+}
+
+int64_t padded(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// Codes [rows, k / 2] and scales [rows, k / 32] of one operand: their bytes, and
+// the scales' row stride.
+struct Mx4 {
+  int64_t rows, k;
+  uint8_t *q, *scale;
+  int64_t lds;
+};
+Mx4 mx4_of(PyObject* qo, PyObject* so, const std::string& name, const c10::Device* want) {
+  const std::string sname = name == "q" ? "scale" : "scale_" + name;
+  const at::Tensor& q = tensor(qo, name.c_str());
+  const c10::Device dev = want ? *want : q.device();
+  on_device(q, name.c_str(), dev);
+  if (q.scalar_type() != at::kFloat4_e2m1fn_x2) has_type(q, name.c_str(), at::kByte);
+  has_dims(q, name.c_str(), 2);
+  if (!q.is_contiguous()) value_error(name + " must be contiguous");
+  const at::Tensor& s = tensor(so, sname.c_str());
+  on_device(s, sname.c_str(), dev);
+  if (s.scalar_type() != at::kFloat8_e8m0fnu) has_type(s, sname.c_str(), at::kByte);
+  int64_t lds = row_stride(s, sname.c_str(), 2);
+  const int64_t rows = q.size(0), k = 2 * q.size(1);
+  if (k % 32) value_error("k must be a multiple of 32");
+  if (s.size(0) != rows || s.size(1) != k / 32) value_error(sname + " must be [rows, k / 32] of " + name);
+  if (rows <= 1) lds = padded(k / 32);
+  if (rows && k) {
+    const int64_t end = s.storage_offset() + (rows - 1) * lds + padded(k / 32);
+    if (lds % 16 || end > static_cast<int64_t>(s.storage().nbytes()))
+      value_error("the rows of " + sname + " must begin at multiples of 16 bytes, the last one padded to 16 as well "
+                  "(new_mx4_scales makes such a tensor)");
+  }
+  return Mx4{rows, k, static_cast<uint8_t*>(q.data_ptr()), static_cast<uint8_t*>(s.data_ptr()), lds};
+}
+
+at::Tensor new_scales(int64_t rows, int64_t k, const c10::Device& dev) {
+  const int64_t n = k / 32, ld = padded(n);
+  if (ld == n) return make({rows, n}, at::kByte, dev);
+  return make({rows, ld}, at::kByte, dev).narrow(1, 0, n);
+}
+
+// (x, silu, q, scale)
+PyObject* quant_mx4(PyObject* const* a, Py_ssize_t n) {
+  need_args(n, 4);
+  const bool silu = truth(a[1]);
+  const char* const name = silu ? "h" : "x";
+  const at::Tensor& x = tensor(a[0], name);
+  const int code = type_code(x.scalar_type());
+  if (code < 0) type_error(std::string(name) + " dtype " + dtype_name(x.scalar_type()) + " not supported");
+  const c10::Device dev = x.device();
+  const int64_t ldx = row_stride(x, name, 2), m = x.size(0);
+  if (silu && x.size(1) % 2) value_error("h must have an even number of columns (gate | up)");
+  const int64_t k = silu ? x.size(1) / 2 : x.size(1);
+  if (k % 32) value_error(silu ? "d must be a multiple of 32" : "k must be a multiple of 32");
+  struct Ref {
+    PyObject* p = nullptr;
+    ~Ref() { Py_XDECREF(p); }
+  } q, scale;
+  const c10::DeviceGuard guard(dev);
+  q.p = a[2] != Py_None ? same(a[2]) : wrapped(make({m, k / 2}, at::kByte, dev));
+  scale.p = a[3] != Py_None ? same(a[3]) : wrapped(new_scales(m, k, dev));
+  const Mx4 to = mx4_of(q.p, scale.p, "q", &dev);
+  if (to.rows != m || to.k != k) value_error("q must be [m, k / 2] and scale [m, k / 32]");
+  check((silu ? lib.silu_quant4 : lib.quant4)(narrow(m, "rows"), narrow(k, "columns"), x.data_ptr(), ldx, code, to.q,
+                                              to.scale, to.lds, stream_of(dev)));
+  return tuple_of({same(q.p), same(scale.p)});
+}
+
+// (q, scale, dtype number, x)
+PyObject* dequant_mx4(PyObject* const* a, Py_ssize_t n) {
+  need_args(n, 4);
+  const Mx4 from = mx4_of(a[0], a[1], "q", nullptr);
+  const c10::Device dev = THPVariable_Unpack(a[0]).device();
+  at::Tensor x;
+  if (a[3] != Py_None) {
+    x = tensor(a[3], "x");
+    if (type_code(x.scalar_type()) < 0) type_error("x dtype " + dtype_name(x.scalar_type()) + " not supported");
+    on_device(x, "x", dev);
+  } else {
+    x = make({from.rows, from.k}, out_type(integer(a[2])), dev);
+  }
+  const int64_t ldx = row_stride(x, "x", 2);
+  if (x.size(0) != from.rows || x.size(1) != from.k) value_error("x must be [m, k]");
+  const c10::DeviceGuard guard(dev);
+  check(lib.dequant4(narrow(from.rows, "rows"), narrow(from.k, "columns"), from.q, from.scale, from.lds, x.data_ptr(), ldx,
+                     type_code(x.scalar_type()), stream_of(dev)));
+  return a[3] != Py_None ? same(a[3]) : wrapped(x);
+}
+
+// The output [m, n] of a product: the caller's, or a new one of the numbered type.
+at::Tensor product_out(PyObject* o, int64_t code, int64_t m, int64_t n, const c10::Device& dev) {
+  if (o == Py_None) return make({m, n}, out_type(code), dev);
+  const at::Tensor& out = tensor(o, "out");
+  if (type_code(out.scalar_type()) < 0) type_error("out dtype " + dtype_name(out.scalar_type()) + " not supported");
+  on_device(out, "out", dev);
+  if (!out.is_contiguous()) value_error("out must be contiguous");
+  if (out.dim() != 2 || out.size(0) != m || out.size(1) != n) value_error("out must be [m, n]");
+  return out;
+}
+
+// (a, b, scale_a, scale_b, output_scale, dtype number, out)
+PyObject* gemm_mx4_scaled(PyObject* const* a, Py_ssize_t n) {
+  need_args(n, 7);
+  const Mx4 x = mx4_of(a[0], a[2], "a", nullptr);
+  const c10::Device dev = THPVariable_Unpack(a[0]).device();
+  const Mx4 w = mx4_of(a[1], a[3], "b", &dev);
+  if (x.k != w.k) value_error("inner dimensions differ: a has k=" + std::to_string(x.k) + ", b has " + std::to_string(w.k));
+  const c10::DeviceGuard guard(dev);
+  const at::Tensor out = product_out(a[6], integer(a[5]), x.rows, w.rows, dev);
+  check(lib.gemm4(narrow(x.rows, "rows"), narrow(w.rows, "columns"), narrow(x.k, "k"), x.q, x.scale, x.lds, w.q, w.scale,
+                  w.lds, static_cast<float>(number(a[4])), out.data_ptr(), type_code(out.scalar_type()), stream_of(dev)));
+  return a[6] != Py_None ? same(a[6]) : wrapped(out);
+}
+
+// (x, w, scale_w, output_scale, dtype number, out)
+PyObject* linear_mx4(PyObject* const* a, Py_ssize_t n) {
+  need_args(n, 6);
+  const at::Tensor& x = tensor(a[0], "x");
+  const int code = type_code(x.scalar_type());
+  if (code < 0) type_error("x dtype " + dtype_name(x.scalar_type()) + " not supported");
+  const c10::Device dev = x.device();
+  const int64_t ldx = row_stride(x, "x", 2), m = x.size(0), k = x.size(1);
+  const Mx4 w = mx4_of(a[1], a[2], "w", &dev);
+  if (w.k != k) value_error("inner dimensions differ: x has k=" + std::to_string(k) + ", w has " + std::to_string(w.k));
+  const c10::DeviceGuard guard(dev);
+  const at::Tensor out = product_out(a[5], integer(a[4]), m, w.rows, dev);
+  const int64_t lds = padded(k / 32);
+  const at::Tensor codes = make({m * (k / 2 + lds)}, at::kByte, dev);  // and their scales behind them
+  uint8_t* const q = static_cast<uint8_t*>(codes.data_ptr());
+  check(lib.linear4(narrow(m, "rows"), narrow(w.rows, "columns"), narrow(k, "k"), x.data_ptr(), ldx, code, w.q, w.scale, w.lds,
+                    static_cast<float>(number(a[3])), out.data_ptr(), type_code(out.scalar_type()), q, q + m * (k / 2), lds,
+                    stream_of(dev)));
+  return a[5] != Py_None ? same(a[5]) : wrapped(out);
+}
+
+// ---- norm and rotation of queries and keys ----
+
+// (q, k, start, freqs, cu, q_weight, k_weight, eps, interleaved, q_out, k_out)
+PyObject* norm_rope(PyObject* const* a, Py_ssize_t n) {
+  need_args(n, 11);
+  const at::Tensor& q = tensor(a[0], "q");
+  const at::ScalarType dt = q.scalar_type();
+  const int code = type_code(dt);
+  if (code < 0) type_error("q dtype " + dtype_name(dt) + " not supported");
+  const c10::Device dev = q.device();
+  const int64_t ldq = row_stride(q, "q", 3), tokens = q.size(0), dim = q.size(2);
+  const at::Tensor& k = tensor(a[1], "k");
+  has_type(k, "k", dt);
+  on_device(k, "k", dev);
+  const int64_t ldk = row_stride(k, "k", 3);
+  if (k.size(0) != tokens || k.size(2) != dim) value_error("q and k must be [tokens, heads, dim] of the same tokens and dim");
+  const at::Tensor& start = dense(a[2], "start", at::kInt, 1, dev);
+  const at::Tensor& freqs = dense(a[3], "freqs", at::kDouble, 1, dev);
+  const int64_t seqs = start.size(0);
+  const int* cu = nullptr;
+  if (a[4] != Py_None) {
+    const at::Tensor& t = dense(a[4], "cu", at::kInt, 1, dev);
+    if (t.size(0) != seqs + 1) value_error("cu must have one entry more than start");
+    cu = static_cast<const int*>(t.data_ptr());
+  } else if (tokens != seqs) {
+    value_error("without cu every sequence has one row");
+  }
+  const void* weight[2] = {nullptr, nullptr};
+  int weight_code = code;
+  for (int i = 0; i < 2; ++i) {
+    if (a[5 + i] == Py_None) continue;
+    const char* const name = i ? "k_weight" : "q_weight";
+    const at::Tensor& w = tensor(a[5 + i], name);
+    if (w.scalar_type() != dt && w.scalar_type() != at::kFloat)
+      type_error(std::string(name) + " must be " + dtype_name(dt) + " or fp32, got " + dtype_name(w.scalar_type()));
+    on_device(w, name, dev);
+    if (!w.is_contiguous() || w.dim() != 1 || w.size(0) != dim) value_error(std::string(name) + " must be [dim]");
+    const int c = type_code(w.scalar_type());
+    if (i && weight[0] && c != weight_code) type_error("q_weight and k_weight must have one type");
+    weight_code = c;
+    weight[i] = w.data_ptr();
+  }
+  const c10::DeviceGuard guard(dev);
+  at::Tensor out[2];
+  int64_t ldo[2];
+  for (int i = 0; i < 2; ++i) {
+    const at::Tensor& in = i ? k : q;
+    const char* const name = i ? "k_out" : "q_out";
+    if (a[9 + i] != Py_None) {
+      out[i] = tensor(a[9 + i], name);
+      has_type(out[i], name, dt);
+      on_device(out[i], name, dev);
+      if (out[i].sizes() != in.sizes()) value_error(std::string(name) + " must have the shape of its input");
+    } else {
+      out[i] = make(in.sizes(), dt, dev);
+    }
+    ldo[i] = row_stride(out[i], name, 3);
+  }
+  check(lib.rope(narrow(seqs, "sequences"), narrow(tokens, "tokens"), narrow(q.size(1), "heads"), narrow(k.size(1), "kv_heads"),
+                 narrow(dim, "dim"), q.data_ptr(), ldq, k.data_ptr(), ldk, weight[0], weight[1], code, weight_code,
+                 static_cast<float>(number(a[7])), static_cast<const double*>(freqs.data_ptr()),
+                 narrow(2 * freqs.size(0), "rotary"), truth(a[8]), static_cast<const int*>(start.data_ptr()), cu,
+                 out[0].data_ptr(), ldo[0], out[1].data_ptr(), ldo[1], stream_of(dev)));
+  PyObject* const qo = a[9] != Py_None ? same(a[9]) : wrapped(out[0]);
+  return tuple_of({qo, a[10] != Py_None ? same(a[10]) : wrapped(out[1])});
 }
 
 // ---- module ----
@@ -506,11 +729,11 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return nullptr;
 }
 
-// (addresses of the five entry points, check, stream, new_workspace, capturing)
+// (addresses of the entry points, check, stream, new_workspace, capturing)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 9);
-  void* p[5];
-  for (int i = 0; i < 5; ++i) {
+  need_args(n, kEntries + 4);
+  void* p[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (PyErr_Occurred()) throw Raised{};
@@ -522,11 +745,17 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   lib.read = reinterpret_cast<decltype(lib.read)>(p[2]);
   lib.workspace = reinterpret_cast<decltype(lib.workspace)>(p[3]);
   lib.attention = reinterpret_cast<decltype(lib.attention)>(p[4]);
+  lib.quant4 = reinterpret_cast<decltype(lib.quant4)>(p[5]);
+  lib.silu_quant4 = reinterpret_cast<decltype(lib.silu_quant4)>(p[6]);
+  lib.dequant4 = reinterpret_cast<decltype(lib.dequant4)>(p[7]);
+  lib.gemm4 = reinterpret_cast<decltype(lib.gemm4)>(p[8]);
+  lib.linear4 = reinterpret_cast<decltype(lib.linear4)>(p[9]);
+  lib.rope = reinterpret_cast<decltype(lib.rope)>(p[10]);
   PyObject** const hold[] = {&py_check, &py_stream, &py_new_workspace, &py_capturing};
   for (int i = 0; i < 4; ++i) {
-    Py_INCREF(a[5 + i]);
+    Py_INCREF(a[kEntries + i]);
     Py_XDECREF(*hold[i]);
-    *hold[i] = a[5 + i];
+    *hold[i] = a[kEntries + i];
   }
   Py_RETURN_NONE;
 }
@@ -534,7 +763,9 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
 #define QK_METHOD(name) \
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<name>)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {QK_METHOD(bind),          QK_METHOD(rms_norm_quant), QK_METHOD(kv_cache_write),
-                         QK_METHOD(kv_cache_read), QK_METHOD(kv_attention),   {nullptr, nullptr, 0, nullptr}};
+                         QK_METHOD(kv_cache_read), QK_METHOD(kv_attention),   QK_METHOD(quant_mx4),
+                         QK_METHOD(dequant_mx4),   QK_METHOD(gemm_mx4_scaled), QK_METHOD(linear_mx4),
+                         QK_METHOD(norm_rope),     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qkbind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,6 +1,7 @@
 // Attention over the paged 8-bit cache for gfx950: softmax(scale q k^T) v with
 // a causal mask (the sequence's rows are its last positions), an optional
-// sliding window, and grouped heads.
+// sliding window, optional first positions that stay visible beside it (sinks),
+// and grouped heads.
 //
 // The (row, head) pairs of a sequence that share a kv head are the columns of
 // a tile: 16 in kv_attention_cols_kernel (sequences with up to 64 columns:
@@ -90,6 +91,9 @@ struct Tile {
   int col0, ncols;      // the tile's columns of the sequence's rows * group
   int lo, hi;           // positions that some column sees: [lo, hi)
   int splits;
+  // With sinks a tile's chunks are laid over the sinks, up to `turn`, and what
+  // lies from lo on, with the `gap` between them left out (multiples of 64).
+  int turn, gap;
 };
 
 // The first position that a row at `pos` sees (a row before position 0 none,
@@ -99,6 +103,7 @@ __device__ __forceinline__ int first_seen(const Params& p, int pos) {
 }
 
 // Columns col0 .. col0 + size of the sequence whose rows are already in t.
+template <bool SINKS>
 __device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0, int size, int len) {
   const int64_t all = static_cast<int64_t>(t.rows) * p.group;
   if (col0 >= all) return;
@@ -109,13 +114,41 @@ __device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0
   const int last_pos = t.len - t.rows + (t.col0 + t.ncols - 1) / p.group;
   t.hi = min(last_pos + 1, t.len);
   t.lo = first_seen(p, first_pos);
-  t.splits = t.hi > t.lo ? (t.hi - (t.lo & ~(kGroup - 1)) + p.chunk - 1) / p.chunk : 0;
+  if constexpr (SINKS) {
+    const int base = t.lo & ~(kGroup - 1), after = (max(min(p.a.sinks, t.hi), 0) + kGroup - 1) & ~(kGroup - 1);
+    t.turn = after;
+    t.gap = max(base - after, 0);
+    t.splits = t.hi > 0 ? (t.hi - t.gap + p.chunk - 1) / p.chunk : 0;
+  } else {
+    t.splits = t.hi > t.lo ? (t.hi - (t.lo & ~(kGroup - 1)) + p.chunk - 1) / p.chunk : 0;
+  }
   t.live = true;
+}
+
+// Where a chunk of a tile begins and ends, in the order in which its positions
+// are taken, and the position there.
+template <bool SINKS>
+__device__ __forceinline__ int range_begin(const Tile& t) { return SINKS ? 0 : t.lo & ~(kGroup - 1); }
+template <bool SINKS>
+__device__ __forceinline__ int range_end(const Tile& t) { return SINKS ? t.hi - t.gap : t.hi; }
+template <bool SINKS>
+__device__ __forceinline__ int position_of(const Tile& t, int v) { return SINKS && v >= t.turn ? v + t.gap : v; }
+
+// Whether a column that sees [lo, hi) sees position j, and whether it sees none
+// of the 16 from `at` on.
+template <bool SINKS>
+__device__ __forceinline__ bool sees(const Params& p, int lo, int hi, int j) {
+  return (j >= lo || (SINKS && j < p.a.sinks)) && j < hi;
+}
+template <bool SINKS>
+__device__ __forceinline__ bool sees_none16(const Params& p, int lo, int hi, int at) {
+  return (at + 16 <= lo && !(SINKS && at < p.a.sinks)) || at >= hi;
 }
 
 // Tiles of 16 columns: item = sequence * tiles + tile; longer sequences are
 // the other kernel's.  Partial results have room for the columns that max_q
 // rows have; rows beyond it, of which only the device knows, stay out of them.
+template <bool SINKS>
 __device__ __forceinline__ Tile find_cols(const Params& p, unsigned item) {
   Tile t{};
   t.seq = static_cast<int>(item / static_cast<unsigned>(p.tiles));
@@ -128,7 +161,7 @@ __device__ __forceinline__ Tile find_cols(const Params& p, unsigned item) {
     if (first < 0 || t.rows <= 0 || t.rows > p.a.tokens - first) return t;
     if (static_cast<int64_t>(t.rows) * p.group > kSmall) return t;
   }
-  set_range(p, t, static_cast<int64_t>(item - static_cast<unsigned>(t.seq) * p.tiles) * kCols,
+  set_range<SINKS>(p, t, static_cast<int64_t>(item - static_cast<unsigned>(t.seq) * p.tiles) * kCols,
             p.splits > 1 ? p.cols : kCols, p.a.lens[t.seq]);
   return t;
 }
@@ -151,6 +184,7 @@ __device__ __forceinline__ int64_t tile_base_of(const Params& p, int row, int b)
   return tile_base<uint32_t>(row, p.group, p.small, b);
 }
 
+template <bool SINKS>
 __device__ __forceinline__ Tile find_tile(const Params& p, int64_t item) {
   Tile t{};
   const kv::Owner o = kv::find_sequence(item, p.a.cu, p.a.lens, p.a.seqs, [&](int row, int seq) {
@@ -161,7 +195,7 @@ __device__ __forceinline__ Tile find_tile(const Params& p, int64_t item) {
   t.row0 = o.first;
   if (o.seq < 0 || o.first < 0 || t.rows <= 0 || t.rows > p.a.tokens - o.first) return t;
   if (static_cast<int64_t>(t.rows) * p.group <= p.small) return t;
-  set_range(p, t, (item - tile_base_of(p, o.first, o.seq)) * kTileCols, kTileCols, o.value);
+  set_range<SINKS>(p, t, (item - tile_base_of(p, o.first, o.seq)) * kTileCols, kTileCols, o.value);
   return t;
 }
 
@@ -423,7 +457,7 @@ constexpr int kLdsHalves = 4 * kGroup * DP;
 // sequences of about 115000, 64 heads, FP8, 88 us (5.4 TB/s); one of 771
 // positions 7 us: the launch, and a chain of table entry, keys, products and
 // join.
-template <int DT, bool FP8, int DP>
+template <int DT, bool FP8, int DP, bool SINKS>
 __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
   // the waves' outputs, [wave][column][element], elements exchanged in fours by
   // the column's number so that columns fall on different banks
@@ -444,11 +478,12 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
   // number so that no die gets the same one of each (64 requests of up to 8192
   // positions in four chunks: 153 us without, 128 with).
   const int head = at.head, split = static_cast<int>((at.inner + at.item + head) % static_cast<unsigned>(p.splits));
-  const Tile t = find_cols(p, at.item);
+  const Tile t = find_cols<SINKS>(p, at.item);
   if (!t.live) return;
   const int dim = p.c.dim, P = p.c.block;
-  const int begin = (t.lo & ~(kGroup - 1)) + split * p.chunk, end = min(begin + p.chunk, t.hi);
-  if (split > 0 && begin >= t.hi) return;  // split 0 stays, to write the rows that see nothing
+  const int stop = range_end<SINKS>(t);
+  const int begin = range_begin<SINKS>(t) + split * p.chunk, end = min(begin + p.chunk, stop);
+  if (split > 0 && begin >= stop) return;  // split 0 stays, to write the rows that see nothing
 
   const Column col = column_of(p, t, head, n);
   half8_t qf[DP / 32];
@@ -522,16 +557,18 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
   };
 
   constexpr int kStep = kWaves * kGroup;
-  // the group at t0, whose K and V are in registers or on their way; `more`:
+  auto pos_of = [&](int v) { return position_of<SINKS>(t, v); };
+  // the group at v, whose K and V are in registers or on their way; `more`:
   // ask for the next group's
-  auto group = [&](int t0, auto half, auto more) {
+  auto group = [&](int v, auto half, auto more) {
     constexpr int S = decltype(half)::value % kSets;
     constexpr std::integral_constant<int, 1 - decltype(half)::value> other{};
+    const int t0 = pos_of(v);
     if (kSets == 2 && more) {
       load_scales(other);
-      load_k(t0 + kStep, other);
-      load_v(t0 + kStep, other);
-      next_blocks(t0 + 2 * kStep);
+      load_k(pos_of(v + kStep), other);
+      load_v(pos_of(v + kStep), other);
+      next_blocks(pos_of(v + 2 * kStep));
     }
     float4_t acc[4];
 #pragma unroll
@@ -543,7 +580,7 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
         acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[S][i][c].z, kr[S][i][c].w), qf[2 * c + 1], acc[i], 0, 0, 0);
       }
     }
-    if (kSets == 1 && more) load_k(t0 + kStep, other);
+    if (kSets == 1 && more) load_k(pos_of(v + kStep), other);
     float s[1][16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[0][i] = acc[i >> 2][i & 3];
@@ -558,13 +595,13 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const bool seen = at + i >= col.see_lo && at + i < col.see_hi;
+        const bool seen = sees<SINKS>(p, col.see_lo, col.see_hi, at + i);
         s[0][i] = seen ? __builtin_fmaf(s[0][i], c[0], bias[0]) : -__builtin_inff();
       }
       c[0] = 1.0f;
       bias[0] = 0.0f;
       // a lane that sees none of these positions must not meet their scale
-      if (at + 16 <= col.see_lo || at >= col.see_hi) inv_vs[0] = 0.0f;
+      if (sees_none16<SINKS>(p, col.see_lo, col.see_hi, at)) inv_vs[0] = 0.0f;
     }
     softmax_step<1, 16, true>(s, c, bias, inv_vs, m, l, [&](float shrink) {
 #pragma unroll
@@ -581,7 +618,7 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
       for (int i = 0; i < 16; ++i) pf[i >> 3][i & 7] = static_cast<_Float16>(static_cast<float>(pf[i >> 3][i & 7]) * rest);
     }
     if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) {
-      const int have = t0 + 16 * g + 16 > t.lo ? t.len - (t0 + 16 * g) : 0;
+      const int have = t0 + 16 * g + 16 > t.lo || (SINKS && t0 + 16 * g < p.a.sinks) ? t.len - (t0 + 16 * g) : 0;
 #pragma unroll
       for (int i = 0; i < VC; ++i) keep_first(vr[S][i], have);
     }
@@ -592,19 +629,19 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
     }
     if (kSets == 1 && more) {
       load_scales(other);
-      load_v(t0 + kStep, other);
-      next_blocks(t0 + 2 * kStep);
+      load_v(pos_of(v + kStep), other);
+      next_blocks(pos_of(v + 2 * kStep));
     }
   };
   constexpr std::integral_constant<int, 0> even{};
   constexpr std::integral_constant<int, 1> odd{};
   int t0 = begin + wave * kGroup;
   if (t0 < end) {
-    next_blocks(t0);
+    next_blocks(pos_of(t0));
     load_scales(even);
-    load_k(t0, even);
-    load_v(t0, even);
-    next_blocks(t0 + kStep);
+    load_k(pos_of(t0), even);
+    load_v(pos_of(t0), even);
+    next_blocks(pos_of(t0 + kStep));
     if constexpr (kSets == 1) {
       for (; t0 < end; t0 += kStep) group(t0, even, t0 + kStep < end);
     } else {
@@ -698,7 +735,7 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
 // first product 471 (registers spill); conversion before the products 175;
 // a raised wave priority during the products 176; rescaling at every new
 // maximum 176.
-template <int DT, bool FP8, int DP>
+template <int DT, bool FP8, int DP, bool SINKS>
 __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   extern __shared__ __align__(16) _Float16 lds_all[];
   _Float16(*const lds_k)[kGroup * DP] = reinterpret_cast<_Float16(*)[kGroup * DP]>(lds_all);
@@ -715,11 +752,12 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   Place at = place_of(p, block, p.splits);
   at.item = p.items - 1 - at.item;  // later rows see more: the longest work first
   const int split = at.inner, head = at.head;
-  const Tile t = find_tile(p, at.item);
+  const Tile t = find_tile<SINKS>(p, at.item);
   if (!t.live) return;
   const int dim = p.c.dim, P = p.c.block;
-  const int begin = (t.lo & ~(kGroup - 1)) + split * p.chunk, end = min(begin + p.chunk, t.hi);
-  if (split > 0 && begin >= t.hi) return;
+  const int stop = range_end<SINKS>(t);
+  const int begin = range_begin<SINKS>(t) + split * p.chunk, end = min(begin + p.chunk, stop);
+  if (split > 0 && begin >= stop) return;
 
   const Column col = column_of(p, t, head, wave * 32 + n);
   half8_t qf[DP / 16];
@@ -757,9 +795,10 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   uint4 kr[kSets][NC], vr[kSets][NC];
   float sk[kSets], sv[kSets];
   int next_block = 0;  // of this wave's 16 positions of the step to load
-  auto load_block = [&](int t0) { next_block = entry(t0 + 16 * wave); };
-  auto load_step = [&](int t0, auto half) {
-    const int S = half % kSets;
+  auto pos_of = [&](int v) { return position_of<SINKS>(t, v); };
+  auto load_block = [&](int v) { next_block = entry(pos_of(v) + 16 * wave); };
+  auto load_step = [&](int v, auto half) {
+    const int S = half % kSets, t0 = pos_of(v);
     const bool ok = in_pool(next_block);
     const int64_t tile = static_cast<int64_t>(ok ? next_block : 0) * p.c.heads + head;
     const int pos = (t0 + 16 * wave) & (P - 1);
@@ -775,13 +814,13 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
     sv[S] = p.c.v_scale[tile];
     if (!ok) sk[S] = sv[S] = __builtin_nanf("");
   };
-  // the step at t0 into half H of LDS
-  auto put_step = [&](int t0, auto half) {
-    const int H = half, S = H % kSets;
+  // the step at v into half H of LDS
+  auto put_step = [&](int v, auto half) {
+    const int H = half, S = H % kSets, t0 = pos_of(v);
     half8_t* const kl = reinterpret_cast<half8_t*>(lds_k[H]);
     half8_t* const vl = reinterpret_cast<half8_t*>(lds_v[H]);
     if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) {
-      const int have = t0 + 16 * wave + 16 > t.lo ? t.len - (t0 + 16 * wave) : 0;
+      const int have = t0 + 16 * wave + 16 > t.lo || (SINKS && t0 + 16 * wave < p.a.sinks) ? t.len - (t0 + 16 * wave) : 0;
 #pragma unroll
       for (int i = 0; i < NC; ++i) keep_first(vr[S][i], have);
     }
@@ -819,10 +858,10 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
       }
     }
   };
-  // the step at t0, in half H of LDS
-  auto work = [&](int t0, auto half) {
-    const int H = half;
-    if (t0 >= any_hi || t0 + kGroup <= any_lo) return;
+  // the step at v, in half H of LDS
+  auto work = [&](int v, auto half) {
+    const int H = half, t0 = pos_of(v);
+    if (t0 >= any_hi || (t0 + kGroup <= any_lo && !(SINKS && t0 < p.a.sinks))) return;
     const half8_t* const kl = reinterpret_cast<const half8_t*>(lds_k[H]);
     const half8_t* const vl = reinterpret_cast<const half8_t*>(lds_v[H]);
     float16_t acc[2];
@@ -845,19 +884,19 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[b][e] = acc[b >> 1][8 * (b & 1) + e];
     }
-    if (t0 + kGroup > all_hi || t0 < all_lo) {
+    if (t0 + kGroup > all_hi || (t0 < all_lo && !(SINKS && t0 + kGroup <= p.a.sinks))) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int first = t0 + 16 * b;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int spot = first + 8 * h + e;
-          s[b][e] = spot >= col.see_lo && spot < col.see_hi ? __builtin_fmaf(s[b][e], c[b], bias[b]) : -__builtin_inff();
+          s[b][e] = sees<SINKS>(p, col.see_lo, col.see_hi, spot) ? __builtin_fmaf(s[b][e], c[b], bias[b]) : -__builtin_inff();
         }
         c[b] = 1.0f;
         bias[b] = 0.0f;
         // a column that sees none of these positions must not meet their scale
-        if (first + 16 <= col.see_lo || first >= col.see_hi) inv_vs[b] = 0.0f;
+        if (sees_none16<SINKS>(p, col.see_lo, col.see_hi, first)) inv_vs[b] = 0.0f;
       }
     }
     softmax_step<4, 8, false>(s, c, bias, inv_vs, m, l, [&](float shrink) {
@@ -942,25 +981,25 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   if (h == 0) *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(m, l);
 }
 
-template <int DT, bool FP8, int DP>
+template <int DT, bool FP8, int DP, bool SINKS>
 __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_cols_kernel(Params p) {
-  cols_body<DT, FP8, DP>(p, blockIdx.x);
+  cols_body<DT, FP8, DP, SINKS>(p, blockIdx.x);
 }
-template <int DT, bool FP8, int DP>
+template <int DT, bool FP8, int DP, bool SINKS>
 __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_tile_kernel(Params p) {
-  tile_body<DT, FP8, DP>(p, blockIdx.x);
+  tile_body<DT, FP8, DP, SINKS>(p, blockIdx.x);
 }
 // A call of both kinds of sequences in one launch, so that the two run side by
 // side: the first `tiles` workgroups (the longer ones) are tiles of 128
 // columns.  (16 requests of up to 4100 positions, one of them 509 rows, window
 // 1024: 37 us one after the other, 26 together.)
-template <int DT, bool FP8, int DP>
+template <int DT, bool FP8, int DP, bool SINKS>
 __global__ __launch_bounds__(64 * kWaves, DP > 128 ? 1 : 2) void kv_attention_both_kernel(Params pt, Params pc,
                                                                                          unsigned tiles) {
   if (blockIdx.x < tiles)
-    tile_body<DT, FP8, DP>(pt, blockIdx.x);
+    tile_body<DT, FP8, DP, SINKS>(pt, blockIdx.x);
   else
-    cols_body<DT, FP8, DP>(pc, blockIdx.x - tiles);
+    cols_body<DT, FP8, DP, SINKS>(pc, blockIdx.x - tiles);
 }
 
 // Sums chunks first .. last of one column into (m, l, v): the whole wave, four
@@ -1008,12 +1047,12 @@ __device__ __forceinline__ void store_row(const Params& p, int64_t out_row, bool
 
 // Joins chunks in a launch of its own.  Many chunks of few columns: one
 // workgroup per column, its waves a quarter of the chunks each.
-template <int DT>
+template <int DT, bool SINKS>
 __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_cols_kernel(Params p) {
   __shared__ float lds_o[kWaves][256];
   __shared__ float lds_m[kWaves], lds_l[kWaves];
   const Place at = place_of(p, blockIdx.x, p.cols);
-  const Tile t = find_cols(p, at.item);
+  const Tile t = find_cols<SINKS>(p, at.item);
   if (!t.live || t.splits <= 1 || at.inner >= t.ncols) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slot = (static_cast<int64_t>(at.item) * p.c.heads + at.head) * p.splits * p.cols + at.inner;
@@ -1043,7 +1082,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_cols_kernel(Par
 
 // Few chunks of many columns: one (row, head) pair per wave, over the rows as
 // they lie, so that no workgroup is without rows.
-template <int DT>
+template <int DT, bool SINKS>
 __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_tile_kernel(Params p) {
   const unsigned wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), heads = p.a.heads;
   const unsigned pair = blockIdx.x * kWaves + wave, row_of = pair / heads;  // fewer than 2^31 pairs
@@ -1059,7 +1098,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_tile_kernel(Par
   const int head = h / p.group;
   const int64_t col = static_cast<int64_t>(row - o.first) * p.group + h - head * p.group;
   const int k = static_cast<int>(col % kTileCols);
-  set_range(p, t, col - k, kTileCols, o.value);
+  set_range<SINKS>(p, t, col - k, kTileCols, o.value);
   if (t.splits <= 1) return;
   const int64_t item = tile_base_of(p, o.first, o.seq) + col / kTileCols;
   float m, l;
@@ -1075,10 +1114,23 @@ struct Cut {
   size_t bytes;   // of partial results
 };
 
-// The positions that one tile can see, from a multiple of 64 on.
-int64_t range_of(int max_kv, int window, int rows) {
+// What hides positions: with sinks up to the last position the window hides none.
+struct Mask {
+  int window, sinks;
+};
+Mask mask_of(int max_kv, int window, int sinks) {
+  if (window == 0 || sinks == 0) return Mask{window, 0};
+  return sinks >= max_kv ? Mask{0, 0} : Mask{window, sinks};
+}
+
+// The positions that one tile can see, from a multiple of 64 on: the window's
+// and, rounded up to whole groups of 64 on either side of the gap, the sinks.
+int64_t range_of(int max_kv, Mask mask, int rows) {
   int64_t range = max_kv;
-  if (window > 0) range = std::min<int64_t>(range, static_cast<int64_t>(window) + rows);
+  if (mask.window > 0) {
+    const int64_t first = mask.sinks > 0 ? (static_cast<int64_t>(mask.sinks) + 2 * kGroup - 1) / kGroup * kGroup : 0;
+    range = std::min<int64_t>(range, first + mask.window + rows);
+  }
   return (range + 2 * kGroup - 1) / kGroup * kGroup;
 }
 
@@ -1100,7 +1152,7 @@ Cut cut_of(int64_t items, int tiles, int kv_heads, int dim, int cols, int64_t ra
 // 121344 positions 652 / 336 / 178 / 105 / 89 / 91 / 96; 8 of 32768 172 / 92 /
 // 51 / 31 / 22 / 20 / 22; 128 of 7936 54 / 41 / 44 / 45 / 49; 512 of up to 8192
 // 131 / 139 / 128 / 128; 512 of 4096 94 / 102 / 109 / 113.
-Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window) {
+Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, Mask mask) {
   const int64_t most = ragged ? std::min<int64_t>(static_cast<int64_t>(max_q) * group, kSmall) : group;
   // wide groups, and a call of one long sequence, are the other kernel's alone
   if (ragged && (group > kSmall || (seqs == 1 && max_q * static_cast<int64_t>(group) > kSmall))) return Cut{};
@@ -1109,7 +1161,7 @@ Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q,
   // beside long sequences the others are mostly single tokens
   const bool mixed = ragged && static_cast<int64_t>(max_q) * group > kSmall;
   const int64_t live = (mixed ? static_cast<int64_t>(seqs) * ((group + kCols - 1) / kCols) : items) * kv_heads;
-  const int64_t range = range_of(max_kv, window, kCols);
+  const int64_t range = range_of(max_kv, mask, kCols);
   int64_t chunks = 1;
   if (range > 640 && live < 256) chunks = 256 / live;
   if (range > 6144 && live >= 256) chunks = (range + 2047) / 2048;
@@ -1133,14 +1185,14 @@ Cut cut_cols(int seqs, int group, int kv_heads, int dim, bool ragged, int max_q,
 //
 // Of the items, which all have room for partial results, few can be without
 // columns, so that the workspace stays below some 300 MB.
-Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window,
+Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged, int max_q, int max_kv, Mask mask,
              int small) {
   if (!ragged || static_cast<int64_t>(max_q) * group <= kSmall) return Cut{};
   const int64_t items = tile_base<int64_t>(tokens, group, small, seqs);
   const int64_t full = static_cast<int64_t>(tokens) * group / kTileCols;
   // in half tiles; a call without a full one counts as a quarter of one
   const int64_t live = full ? 2 * (full + std::min<int64_t>(seqs, full) / 2) * kv_heads : (kv_heads + 1) / 2;
-  const int64_t range = range_of(max_kv, window, kTileCols), wanted = dim > 128 ? 512 : 1024;
+  const int64_t range = range_of(max_kv, mask, kTileCols), wanted = dim > 128 ? 512 : 1024;
   int64_t chunk = range;
   if (live < 384 && range > 1024) chunk = ((range * live + wanted - 1) / wanted + 255) / 256 * 256;
   return cut_of(items, 1, kv_heads, dim, kTileCols, range, std::max<int64_t>(chunk, 512));
@@ -1149,13 +1201,13 @@ Cut cut_tile(int seqs, int tokens, int group, int kv_heads, int dim, bool ragged
 struct Cuts {
   Cut cols, tile;
 };
-Cuts cuts_of(int seqs, int tokens, int heads, int kv_heads, int dim, bool ragged, int max_q, int max_kv, int window) {
+Cuts cuts_of(int seqs, int tokens, int heads, int kv_heads, int dim, bool ragged, int max_q, int max_kv, Mask mask) {
   const int group = heads / kv_heads;
-  const Cut c = cut_cols(seqs, group, kv_heads, dim, ragged, max_q, max_kv, window);
-  return Cuts{c, cut_tile(seqs, tokens, group, kv_heads, dim, ragged, max_q, max_kv, window, c.items ? kSmall : 0)};
+  const Cut c = cut_cols(seqs, group, kv_heads, dim, ragged, max_q, max_kv, mask);
+  return Cuts{c, cut_tile(seqs, tokens, group, kv_heads, dim, ragged, max_q, max_kv, mask, c.items ? kSmall : 0)};
 }
 
-template <int DT, bool FP8, int DP>
+template <int DT, bool FP8, int DP, bool SINKS>
 hipError_t go(const Params& base, const Cut& cc, const Cut& ct, hipStream_t stream) {
   Params pc = base, pt = base;
   pc.tiles = cc.tiles;
@@ -1178,26 +1230,31 @@ hipError_t go(const Params& base, const Cut& cc, const Cut& ct, hipStream_t stre
   static_assert(lds_c <= lds_t, "the larger serves both");
   hipError_t e = hipSuccess;
   if (cc.items && ct.items)
-    e = launch(kv_attention_both_kernel<DT, FP8, DP>, dim3(blocks_t + blocks_c), block, lds_t, stream, pt, pc,
+    e = launch(kv_attention_both_kernel<DT, FP8, DP, SINKS>, dim3(blocks_t + blocks_c), block, lds_t, stream, pt, pc,
                blocks_t);
   else if (cc.items)
-    e = launch(kv_attention_cols_kernel<DT, FP8, DP>, dim3(blocks_c), block, lds_c, stream, pc);
+    e = launch(kv_attention_cols_kernel<DT, FP8, DP, SINKS>, dim3(blocks_c), block, lds_c, stream, pc);
   else if (ct.items)
-    e = launch(kv_attention_tile_kernel<DT, FP8, DP>, dim3(blocks_t), block, lds_t, stream, pt);
+    e = launch(kv_attention_tile_kernel<DT, FP8, DP, SINKS>, dim3(blocks_t), block, lds_t, stream, pt);
   if (e == hipSuccess && cc.items && pc.join_later)
-    e = launch(kv_attention_join_cols_kernel<DT>, dim3(static_cast<unsigned>(all_c * cc.cols)), block, 0, stream, pc);
+    e = launch(kv_attention_join_cols_kernel<DT, SINKS>, dim3(static_cast<unsigned>(all_c * cc.cols)), block, 0, stream, pc);
   if (e == hipSuccess && ct.items && ct.splits > 1) {
     const int64_t pairs = static_cast<int64_t>(base.a.tokens) * base.a.heads;
-    e = launch(kv_attention_join_tile_kernel<DT>, dim3(static_cast<unsigned>((pairs + kWaves - 1) / kWaves)), block, 0, stream, pt);
+    e = launch(kv_attention_join_tile_kernel<DT, SINKS>, dim3(static_cast<unsigned>((pairs + kWaves - 1) / kWaves)), block, 0, stream, pt);
   }
   return e;
 }
 
-template <int DT, bool FP8>
+template <int DT, bool FP8, bool SINKS>
 hipError_t by_dim(const Params& p, const Cut& cc, const Cut& ct, hipStream_t stream) {
-  if (p.c.dim <= 64) return go<DT, FP8, 64>(p, cc, ct, stream);
-  if (p.c.dim <= 128) return go<DT, FP8, 128>(p, cc, ct, stream);
-  return go<DT, FP8, 256>(p, cc, ct, stream);
+  if (p.c.dim <= 64) return go<DT, FP8, 64, SINKS>(p, cc, ct, stream);
+  if (p.c.dim <= 128) return go<DT, FP8, 128, SINKS>(p, cc, ct, stream);
+  return go<DT, FP8, 256, SINKS>(p, cc, ct, stream);
+}
+
+template <int DT, bool FP8>
+hipError_t by_mask(const Params& p, const Cut& cc, const Cut& ct, hipStream_t stream) {
+  return p.a.sinks > 0 ? by_dim<DT, FP8, true>(p, cc, ct, stream) : by_dim<DT, FP8, false>(p, cc, ct, stream);
 }
 
 size_t bytes_of(const Cut& cc, const Cut& ct) {
@@ -1208,27 +1265,30 @@ size_t bytes_of(const Cut& cc, const Cut& ct) {
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, bool ragged, int max_q,
-                                    int max_kv, int window) {
-  const Cuts c = cuts_of(seqs, tokens, heads, kv_heads, dim, ragged, max_q, max_kv, window);
+                                    int max_kv, int window, int sinks) {
+  const Cuts c = cuts_of(seqs, tokens, heads, kv_heads, dim, ragged, max_q, max_kv, mask_of(max_kv, window, sinks));
   return bytes_of(c.cols, c.tile);
 }
 
 hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, hipStream_t stream) {
-  const auto [cc, ct] = cuts_of(a.seqs, a.tokens, a.heads, c.heads, c.dim, a.cu != nullptr, a.max_q, a.max_kv, a.window);
+  const Mask mask = mask_of(a.max_kv, a.window, a.sinks);
+  const auto [cc, ct] = cuts_of(a.seqs, a.tokens, a.heads, c.heads, c.dim, a.cu != nullptr, a.max_q, a.max_kv, mask);
   if (!grid_fits((cc.items * cc.splits + ct.items * ct.splits) * c.heads, 64 * kWaves) ||
       static_cast<int64_t>(a.tokens) * a.heads > 0x7fffffff)
     return hipErrorInvalidConfiguration;  // the joins' grids are smaller: they are for few tiles
   Params p{};
   p.c = c;
   p.a = a;
+  p.a.window = mask.window;
+  p.a.sinks = mask.sinks;
   while (1 << p.block_shift < c.block) ++p.block_shift;
   p.group = a.heads / c.heads;
   p.scale2 = std::fabs(a.scale) * 1.4426950408889634f;
   p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
   p.arrived = static_cast<unsigned*>(a.workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounters * sizeof(unsigned));
-  if (a.dtype == QK_BF16) return c.fp8 ? by_dim<QK_BF16, true>(p, cc, ct, stream) : by_dim<QK_BF16, false>(p, cc, ct, stream);
-  return c.fp8 ? by_dim<QK_F16, true>(p, cc, ct, stream) : by_dim<QK_F16, false>(p, cc, ct, stream);
+  if (a.dtype == QK_BF16) return c.fp8 ? by_mask<QK_BF16, true>(p, cc, ct, stream) : by_mask<QK_BF16, false>(p, cc, ct, stream);
+  return c.fp8 ? by_mask<QK_F16, true>(p, cc, ct, stream) : by_mask<QK_F16, false>(p, cc, ct, stream);
 }
 
 }  // namespace qk

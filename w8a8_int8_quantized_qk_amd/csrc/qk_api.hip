@@ -504,25 +504,31 @@ int qk_gemm_i8_asym(int m, int n, int k, const int8_t* a, const int32_t* zero_po
   return status_of(qk::launch_gemm_asym(g, zero_point, wsum, stream));
 }
 
-// Whether some row of `in` (m rows of `row` bytes, ld_in bytes apart) overlaps a
-// row of `out` without being the same row in place.
-static bool rows_clash(const void* in, int64_t ld_in, const void* out, int64_t ld_out, int64_t m, int64_t row) {
+// Whether some row of `in` (m rows of `row_in` bytes, ld_in bytes apart) overlaps
+// a row of `out` (of `row_out` bytes), other than, with `own`, the same row in place.
+static bool rows_overlap(const void* in, int64_t ld_in, int64_t row_in, const void* out, int64_t ld_out,
+                         int64_t row_out, int64_t m, bool own) {
   const int64_t a = reinterpret_cast<intptr_t>(in), b = reinterpret_cast<intptr_t>(out);
-  if (row == 0 || a + (m - 1) * ld_in + row <= b || b + (m - 1) * ld_out + row <= a) return false;
-  if (m == 1) return a != b;
-  // rows i of `in` and j of `out` overlap where their distance is below `row`,
-  // which for each i can hold for the two j around it only
+  if (row_in == 0 || row_out == 0 || a + (m - 1) * ld_in + row_in <= b || b + (m - 1) * ld_out + row_out <= a)
+    return false;
+  if (m == 1) return !own || a != b;
+  // row i of `in` overlaps row j of `out` where j lies past its start less
+  // row_out and before its end; rows of either do not overlap each other, so with
+  // ld_out >= row_out there are few such j
   const int64_t last = ld_in == ld_out ? 1 : m;  // with one stride the distance depends on j - i alone
   for (int64_t i = 0; i < last; ++i) {
     const int64_t from = a + i * ld_in;
     const int64_t near = (from - b) / ld_out - (from < b);
-    for (int64_t j = near; j <= near + 1; ++j) {
+    for (int64_t j = near; j <= near + 1 || b + j * ld_out < from + row_in; ++j) {
       const bool there = ld_in == ld_out ? j > -m && j < m : j >= 0 && j < m;
       const int64_t off = from - (b + j * ld_out);
-      if (there && off < row && off > -row && (off != 0 || i != j)) return true;
+      if (there && off < row_out && off > -row_in && !(own && off == 0 && i == j)) return true;
     }
   }
   return false;
+}
+static bool rows_clash(const void* in, int64_t ld_in, const void* out, int64_t ld_out, int64_t m, int64_t row) {
+  return rows_overlap(in, ld_in, row, out, ld_out, row, m, true);
 }
 
 int qk_rms_norm_quant(int m, int k, const void* x, int64_t ldx, const void* residual, int64_t ldr,
@@ -626,23 +632,29 @@ int qk_kv_cache_read(int seqs, int tokens, int kv_heads, int dim, void* k, int64
                  blocks, block, code, table, ldt, width, start, cu, stream);
 }
 
-size_t qk_kv_attention_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim, int ragged,
-                                      int max_q, int max_kv, int window) {
+size_t qk_kv_attention_sinks_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim, int ragged,
+                                            int max_q, int max_kv, int window, int sinks) {
   if (seqs <= 0 || tokens <= 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads != 0 || dim < 16 ||
-      dim > 256 || max_q < 1 || max_kv < 0 || max_kv > qk::kKvMostPositions || window < 0)
+      dim > 256 || max_q < 1 || max_kv < 0 || max_kv > qk::kKvMostPositions || window < 0 || sinks < 0)
     return 0;
-  return qk::kv_attention_workspace_bytes(seqs, tokens, heads, kv_heads, dim, ragged != 0, max_q, max_kv, window);
+  return qk::kv_attention_workspace_bytes(seqs, tokens, heads, kv_heads, dim, ragged != 0, max_q, max_kv, window,
+                                          sinks);
 }
 
-int qk_kv_attention(int seqs, int tokens, int heads, int kv_heads, int dim, const void* q,
-                    int64_t ldq, int dtype, const void* k_cache, const void* v_cache,
-                    const float* k_scale, const float* v_scale, int blocks, int block, int code,
-                    const int* table, int64_t ldt, int width, const int* lens, const int* cu,
-                    int max_q, int max_kv, float scale, int window, void* out, float* lse,
-                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+size_t qk_kv_attention_workspace_size(int seqs, int tokens, int heads, int kv_heads, int dim, int ragged,
+                                      int max_q, int max_kv, int window) {
+  return qk_kv_attention_sinks_workspace_size(seqs, tokens, heads, kv_heads, dim, ragged, max_q, max_kv, window, 0);
+}
+
+int qk_kv_attention_sinks(int seqs, int tokens, int heads, int kv_heads, int dim, const void* q,
+                          int64_t ldq, int dtype, const void* k_cache, const void* v_cache,
+                          const float* k_scale, const float* v_scale, int blocks, int block, int code,
+                          const int* table, int64_t ldt, int width, const int* lens, const int* cu,
+                          int max_q, int max_kv, float scale, int window, int sinks, void* out,
+                          float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (dtype != QK_BF16 && dtype != QK_F16) return QK_ERR_INVALID_VALUE;
   if (kv_heads < 1 || heads < 1 || heads % kv_heads != 0) return QK_ERR_INVALID_VALUE;
-  if (max_q < 1 || max_kv < 0 || window < 0 || !(scale - scale == 0.0f)) return QK_ERR_INVALID_VALUE;
+  if (max_q < 1 || max_kv < 0 || window < 0 || sinks < 0 || !(scale - scale == 0.0f)) return QK_ERR_INVALID_VALUE;
   const int rc = kv_check(seqs, tokens, kv_heads, dim, k_cache, v_cache, k_scale, v_scale, blocks, block, code,
                           table, ldt, width, lens);
   if (rc != QK_OK || seqs == 0 || tokens == 0) return rc;
@@ -653,13 +665,145 @@ int qk_kv_attention(int seqs, int tokens, int heads, int kv_heads, int dim, cons
   if (reach < max_kv) max_kv = static_cast<int>(reach);
   if (max_kv > qk::kKvMostPositions) return QK_ERR_UNSUPPORTED;
   const size_t need =
-      qk::kv_attention_workspace_bytes(seqs, tokens, heads, kv_heads, dim, cu != nullptr, max_q, max_kv, window);
+      qk::kv_attention_workspace_bytes(seqs, tokens, heads, kv_heads, dim, cu != nullptr, max_q, max_kv, window, sinks);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return QK_ERR_WORKSPACE;
   const qk::KvCacheView c = kv_view(kv_heads, dim, k_cache, v_cache, k_scale, v_scale, blocks, block, code, table,
                                     ldt, width);
-  const qk::KvAttentionArgs a{seqs, tokens, heads, dtype, q, ldq, lens, cu, max_q, max_kv, scale, window, out, lse,
+  const qk::KvAttentionArgs a{seqs, tokens, heads, dtype, q, ldq, lens, cu, max_q, max_kv, scale, window, sinks, out, lse,
                               workspace, workspace_bytes};
   return status_of_cut(qk::launch_kv_attention(c, a, stream));
+}
+
+int qk_kv_attention(int seqs, int tokens, int heads, int kv_heads, int dim, const void* q,
+                    int64_t ldq, int dtype, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, int blocks, int block, int code,
+                    const int* table, int64_t ldt, int width, const int* lens, const int* cu,
+                    int max_q, int max_kv, float scale, int window, void* out, float* lse,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return qk_kv_attention_sinks(seqs, tokens, heads, kv_heads, dim, q, ldq, dtype, k_cache, v_cache, k_scale, v_scale,
+                               blocks, block, code, table, ldt, width, lens, cu, max_q, max_kv, scale, window, 0, out,
+                               lse, workspace, workspace_bytes, stream);
+}
+
+// ---- microscaled 4-bit rows ----
+
+constexpr int64_t kMx4Most = int64_t{1} << 35;  // values of one call, eight to a work item
+
+// Checks of one operand's codes and scales.
+static int mx4_operand(int64_t rows, int k, const uint8_t* q, const uint8_t* scale, int64_t lds) {
+  if (rows == 0 || k == 0) return QK_OK;
+  if (!q || !scale || lds < k / 32) return QK_ERR_INVALID_VALUE;
+  if (lds % 16 != 0 || !aligned(q, 16) || !aligned(scale, 16)) return QK_ERR_UNSUPPORTED;
+  return QK_OK;
+}
+
+static int mx4_rows(bool back, bool silu, int m, int k, void* x, int64_t ldx, int dtype, uint8_t* q, uint8_t* scale,
+                    int64_t lds, hipStream_t stream) {
+  if (m < 0 || k < 0 || !known_input_dtype(dtype)) return QK_ERR_INVALID_VALUE;
+  if (k % 32 != 0) return QK_ERR_UNSUPPORTED;
+  if (m == 0 || k == 0) return QK_OK;
+  if (!x || ldx < (silu ? 2 : 1) * static_cast<int64_t>(k)) return QK_ERR_INVALID_VALUE;
+  const int rc = mx4_operand(m, k, q, scale, lds);
+  if (rc != QK_OK) return rc;
+  if (!aligned(x, dtype == QK_F32 ? 4 : 2) || static_cast<int64_t>(m) * k >= kMx4Most) return QK_ERR_UNSUPPORTED;
+  return status_of_cut(qk::launch_mx4_rows(qk::Mx4RowsArgs{m, k, x, ldx, dtype, silu, q, scale, lds}, back, stream));
+}
+
+int qk_quant_mx4(int m, int k, const void* x, int64_t ldx, int x_dtype, uint8_t* q, uint8_t* scale, int64_t lds,
+                 hipStream_t stream) {
+  return mx4_rows(false, false, m, k, const_cast<void*>(x), ldx, x_dtype, q, scale, lds, stream);
+}
+
+int qk_silu_mul_quant_mx4(int m, int d, const void* h, int64_t ldh, int h_dtype, uint8_t* q, uint8_t* scale,
+                          int64_t lds, hipStream_t stream) {
+  return mx4_rows(false, true, m, d, const_cast<void*>(h), ldh, h_dtype, q, scale, lds, stream);
+}
+
+int qk_dequant_mx4(int m, int k, const uint8_t* q, const uint8_t* scale, int64_t lds, void* x, int64_t ldx,
+                   int x_dtype, hipStream_t stream) {
+  return mx4_rows(true, false, m, k, x, ldx, x_dtype, const_cast<uint8_t*>(q), const_cast<uint8_t*>(scale), lds,
+                  stream);
+}
+
+constexpr int kMx4MostRows = 1 << 24;
+
+int qk_gemm_mx4_scaled(int m, int n, int k, const uint8_t* a, const uint8_t* scale_a, int64_t ldsa, const uint8_t* b,
+                       const uint8_t* scale_b, int64_t ldsb, float output_scale, void* out, int out_dtype,
+                       hipStream_t stream) {
+  if (m < 0 || n < 0 || k < 0 || !known_input_dtype(out_dtype)) return QK_ERR_INVALID_VALUE;
+  if (k % 32 != 0) return QK_ERR_UNSUPPORTED;
+  if (m == 0 || n == 0) return QK_OK;
+  if (!out) return QK_ERR_INVALID_VALUE;
+  int rc = mx4_operand(m, k, a, scale_a, ldsa);
+  if (rc == QK_OK) rc = mx4_operand(n, k, b, scale_b, ldsb);
+  if (rc != QK_OK) return rc;
+  if (!aligned(out, out_dtype == QK_F32 ? 4 : 2) || m > kMx4MostRows || n > kMx4MostRows) return QK_ERR_UNSUPPORTED;
+  const qk::Mx4GemmArgs g{m, n, k, a, scale_a, ldsa, b, scale_b, ldsb, output_scale, out, out_dtype};
+  return status_of_cut(qk::launch_gemm_mx4(g, stream));
+}
+
+int qk_linear_mx4(int m, int n, int k, const void* x, int64_t ldx, int x_dtype, const uint8_t* b,
+                  const uint8_t* scale_b, int64_t ldsb, float output_scale, void* out, int out_dtype, uint8_t* q_out,
+                  uint8_t* scale_out, int64_t lds_out, hipStream_t stream) {
+  // the product's arguments are checked before anything is enqueued
+  if (m < 0 || n < 0 || k < 0 || !known_input_dtype(out_dtype)) return QK_ERR_INVALID_VALUE;
+  if (k % 32 != 0) return QK_ERR_UNSUPPORTED;
+  if (m > 0 && n > 0) {
+    if (!out) return QK_ERR_INVALID_VALUE;
+    const int rc = mx4_operand(n, k, b, scale_b, ldsb);
+    if (rc != QK_OK) return rc;
+    if (!aligned(out, out_dtype == QK_F32 ? 4 : 2) || m > kMx4MostRows || n > kMx4MostRows)
+      return QK_ERR_UNSUPPORTED;
+  }
+  const int rc = qk_quant_mx4(m, k, x, ldx, x_dtype, q_out, scale_out, lds_out, stream);
+  if (rc != QK_OK) return rc;
+  return qk_gemm_mx4_scaled(m, n, k, q_out, scale_out, lds_out, b, scale_b, ldsb, output_scale, out, out_dtype,
+                            stream);
+}
+
+// ---- norm and rotation of queries and keys ----
+
+int qk_norm_rope(int seqs, int tokens, int heads, int kv_heads, int dim, const void* q, int64_t ldq, const void* k,
+                 int64_t ldk, const void* q_weight, const void* k_weight, int dtype, int weight_dtype, float eps,
+                 const double* freqs, int rotary, int interleaved, const int* start, const int* cu, void* q_out,
+                 int64_t ldqo, void* k_out, int64_t ldko, hipStream_t stream) {
+  if (seqs < 0 || tokens < 0 || heads < 0 || kv_heads < 0 || !known_input_dtype(dtype)) return QK_ERR_INVALID_VALUE;
+  if (weight_dtype != dtype && weight_dtype != QK_F32) return QK_ERR_INVALID_VALUE;
+  if (dim < 16 || dim > 256 || dim % 16 != 0 || rotary < 0 || rotary > dim || rotary % 2 != 0)
+    return QK_ERR_INVALID_VALUE;
+  if (!(eps >= 0.0f)) return QK_ERR_INVALID_VALUE;
+  if (seqs == 0 || tokens == 0 || heads + static_cast<int64_t>(kv_heads) == 0) return QK_OK;
+  if (!start || (rotary > 0 && !freqs) || (!cu && tokens != seqs)) return QK_ERR_INVALID_VALUE;
+  const uintptr_t e = dtype == QK_F32 ? 4 : 2, we = weight_dtype == QK_F32 ? 4 : 2;
+  const int64_t b = static_cast<int64_t>(e);
+  struct Side {
+    int heads;
+    const void* x;
+    int64_t ldx;
+    const void* weight;
+    void* out;
+    int64_t ldo;
+  } sides[] = {{heads, q, ldq, q_weight, q_out, ldqo}, {kv_heads, k, ldk, k_weight, k_out, ldko}};
+  for (const Side& s : sides) {
+    const int64_t row = static_cast<int64_t>(s.heads) * dim;
+    if (row == 0) continue;
+    if (!s.x || !s.out || s.ldx < row || s.ldo < row) return QK_ERR_INVALID_VALUE;
+    if (!aligned(s.x, e) || !aligned(s.out, e) || !aligned(s.weight, we)) return QK_ERR_UNSUPPORTED;
+  }
+  if (!aligned(start, 4) || !aligned(cu, 4) || !aligned(freqs, 8)) return QK_ERR_UNSUPPORTED;
+  for (const Side& out : sides)
+    for (const Side& in : sides) {
+      const int64_t wo = static_cast<int64_t>(out.heads) * dim * b, wi = static_cast<int64_t>(in.heads) * dim * b;
+      if (wo == 0 || wi == 0) continue;
+      // each output against each input, and against the other output
+      const bool own = &out == &in;
+      if (rows_overlap(in.x, in.ldx * b, wi, out.out, out.ldo * b, wo, tokens, own)) return QK_ERR_INVALID_VALUE;
+      if (!own && rows_overlap(in.out, in.ldo * b, wi, out.out, out.ldo * b, wo, tokens, false))
+        return QK_ERR_INVALID_VALUE;
+    }
+  const qk::NormRopeArgs a{seqs, tokens, heads, kv_heads, dim, rotary, q, ldq, k, ldk, q_weight, k_weight, dtype,
+                           weight_dtype == QK_F32, eps, freqs, interleaved != 0, start, cu, q_out, ldqo, k_out, ldko};
+  return status_of_cut(qk::launch_norm_rope(a, stream));
 }
 
 }  // extern "C"

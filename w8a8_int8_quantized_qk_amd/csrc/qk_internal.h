@@ -181,6 +181,59 @@ struct RmsNormQuantArgs {
 };
 hipError_t launch_rms_norm_quant(const RmsNormQuantArgs& a, hipStream_t stream);
 
+// Microscaled 4-bit rows (mx4_quant.hip): x [m][k] to codes and scale bytes
+// (of silu(gate) * up of rows of 2 k with silu), or back.  ldx in elements, lds
+// in bytes.
+struct Mx4RowsArgs {
+  int m, k;
+  const void* x;  // written on the way back
+  int64_t ldx;
+  int dtype;
+  bool silu;
+  uint8_t* q;
+  uint8_t* scale;
+  int64_t lds;
+};
+hipError_t launch_mx4_rows(const Mx4RowsArgs& a, bool back, hipStream_t stream);
+
+// The product of two such operands (mx4_gemm.hip).
+struct Mx4GemmArgs {
+  int m, n, k;
+  const uint8_t* a;  // [m][k / 2]
+  const uint8_t* scale_a;
+  int64_t ldsa;
+  const uint8_t* b;  // [n][k / 2]
+  const uint8_t* scale_b;
+  int64_t ldsb;
+  float output_scale;
+  void* out;  // [m][n]
+  int out_dtype;
+};
+hipError_t launch_gemm_mx4(const Mx4GemmArgs& g, hipStream_t stream);
+
+// Norm of each head's query and key and their rotation (norm_rope.hip).  Row
+// strides in elements; null weights: no norm; cu null: one row per sequence.
+struct NormRopeArgs {
+  int seqs, tokens, heads, kv_heads, dim, rotary;
+  const void* q;
+  int64_t ldq;
+  const void* k;
+  int64_t ldk;
+  const void* q_weight;
+  const void* k_weight;
+  int dtype, weight_f32;
+  float eps;
+  const double* freqs;  // [rotary / 2]
+  bool interleaved;
+  const int* start;
+  const int* cu;
+  void* q_out;
+  int64_t ldqo;
+  void* k_out;
+  int64_t ldko;
+};
+hipError_t launch_norm_rope(const NormRopeArgs& a, hipStream_t stream);
+
 // A paged 8-bit key/value cache (qk.h, "Paged 8-bit key/value cache") and the
 // sequences that a call works on.
 struct KvCacheView {
@@ -221,14 +274,14 @@ struct KvAttentionArgs {
   const int* cu;    // [seqs + 1] rows of each sequence, or null: one each
   int max_q, max_kv;
   float scale;
-  int window;
+  int window, sinks;
   void* out;   // [tokens][heads][dim] dense
   float* lse;  // [tokens][heads] or null
   void* workspace;
   size_t workspace_bytes;
 };
 size_t kv_attention_workspace_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, bool ragged, int max_q,
-                                    int max_kv, int window);
+                                    int max_kv, int window, int sinks);
 hipError_t launch_kv_attention(const KvCacheView& c, const KvAttentionArgs& a, hipStream_t stream);
 
 }  // namespace qk
