@@ -97,33 +97,45 @@ hipError_t rows(const Mx4GemmArgs& g, hipStream_t stream) {
 
 // ---- many rows: tiles in LDS ----
 
-__device__ const uint4 kZeros = {0, 0, 0, 0};  // what a block past k is read from
-
-// lds_dma16 by all lanes (who = ~0) or none (0; a load by none counts as one that
-// has arrived).  Every lane is active before and after it.  A branch around the
-// load instead would let the compiler move the products of a whole loop behind
-// it, and their operands into scratch memory.
-__device__ __forceinline__ void lds_dma16_by(uint32_t who, const void* sbase, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\tglobal_load_lds_dwordx4 %0, %1\n\ts_mov_b64 exec, -1"
-               :
-               : "v"(voff), "s"(sbase), "s"(lds_base), "s"(who)
-               : "memory", "m0");
-}
-__device__ __forceinline__ void lds_dma16_by(uint32_t who, const void* from, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %2\n\tglobal_load_lds_dwordx4 %0, off\n\ts_mov_b64 exec, -1"
-               :
-               : "v"(from), "s"(lds_base), "s"(who)
-               : "memory", "m0");
+// lds_dma16_split by all lanes where i < n (both uniform), else by none, which
+// counts as a load that has arrived.  Every lane is active before and after it.  A
+// branch around the load instead would let the compiler move the products of a
+// whole loop behind it, and their operands into scratch memory.
+__device__ __forceinline__ void lds_dma16_below(int i, int n, const void* sbase, uint32_t voff, uint32_t lds_base) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\ts_cmp_lt_i32 %3, %4\n\ts_cselect_b64 exec, -1, 0\n\tglobal_load_lds_dwordx4 %0, %1\n\t"
+      "s_mov_b64 exec, -1"
+      :
+      : "v"(voff), "s"(sbase), "s"(lds_base), "s"(i), "s"(n)
+      : "memory", "m0", "scc");
 }
 
-// A workgroup has BM x BN outputs, a wave WTM x WTN of them, in steps of 64 k with
-// v_mfma_scale_f32_32x32x64_f8f6f4.  Slices of 128 k (64 bytes of a row, four
-// blocks) go from memory to LDS in a ring of four stages, three ahead of the one
-// that is multiplied; the scales of four slices (16 bytes of a row) in one of two
-// buffers.  Half h of a wave takes blocks 2 h and 2 h + 1 of a slice in its two
-// steps, for both operands, so that one 16-bit read brings the scales of both
-// steps, and the instruction picks the byte: no vector instruction is left
-// between the products.
+// A pointer that all lanes hold alike, in scalar registers.
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// A workgroup has BM x BN outputs, a wave WTM x WTN of them, with
+// v_mfma_scale_f32_16x16x128_f8f6f4 (measured alone, on random codes: 7.3
+// PFLOP/s, where 32x32x64 reaches 6.7; with all codes 0 both reach 9.5: the
+// power that the operands take holds the clock down).
+//
+// Slices of 128 k (64 bytes of a row, four blocks) go from memory to LDS in a
+// ring of four stages.  A stage is free as soon as every wave has read its
+// fragments, in the middle of the slice's products, and is then asked for slice
+// kt + 4: three slices are under way at a time.
+//
+// A lane's quarter of a wave is its block of a slice, and the byte of its scale
+// register that the instruction picks is the slice: the scales of four slices, 16
+// bytes of a row, have to be transposed as a 4 x 4 matrix of bytes for that.
+// Each thread does so for one row, 16 slices at a time, in place in LDS; a
+// fragment's scales are then one 32-bit read in four slices, and no vector
+// instruction stands between the products.  (64 bytes of a row are asked for at
+// a time because a transfer costs by the lines that it touches: with 16 bytes
+// of 64 rows in each, the scales cost a tenth of the kernel.)
 template <int DT, int BM, int BN, int WTM, int WTN, bool KTAIL>
 struct Mx4Tile {
   static constexpr int kStages = 4;
@@ -132,20 +144,25 @@ struct Mx4Tile {
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kRow = 64;                 // bytes of a row in a slice
   static constexpr int kStageA = BM * kRow, kStageB = BN * kRow;
-  static constexpr int kScales = kStages * (kStageA + kStageB);  // two buffers of them follow the ring
-  static constexpr int kScaleBuf = (BM + BN) * 16;
-  static constexpr int kSmem = kScales + 2 * kScaleBuf;
+  static constexpr int kScales = kStages * (kStageA + kStageB);  // rows of 64 bytes of scales follow the ring
+  // Half of a CU's LDS or all of it: workgroups of anything between were
+  // started one after the other, some 50 ns apart (2048 x 4096 x 4096 on tiles of
+  // 256 x 128, 256 of them, with 136 KiB each: 34.6 us; with 160: 23.8).
+  static constexpr int kUsed = kScales + kWaves * 64 * kRow;
+  static constexpr int kSmem = kUsed <= 81920 ? 81920 : 163840;
   static constexpr int kOps = (BM + BN) / 16 / kWaves;  // 1 KiB transfers of a slice per wave
-  static constexpr int FM = WTM / 32, FN = WTN / 32;
+  static constexpr int kPieces = (BM + BN) / 64;
+  static constexpr int FM = WTM / 16, FN = WTN / 16;
   static constexpr int kElem = DT == QK_F32 ? 4 : 2;
-  static_assert(kOps * kWaves * 16 == BM + BN && BM % 16 == 0, "whole transfers");
-  static_assert((BM + BN) / 64 <= kWaves, "one transfer of scales per wave");
-  static_assert(kSmem <= 163840 && kWaves * 16384 <= kSmem, "LDS; 16 KiB of it per wave for the results");
-  static_assert(3 * kStageA + 2048 * (FM - 1) < 65536 && 3 * kStageB + 2048 * (FN - 1) < 65536, "immediate offsets");
+  static_assert(kOps * kWaves * 16 == BM + BN && BM % 64 == 0 && BN % 64 == 0, "whole transfers");
+  static_assert(kPieces <= kWaves, "a thread for every row of scales");
+  static_assert(kUsed <= kSmem && kWaves * 16384 <= kSmem, "LDS; 16 KiB of it per wave for the results");
+  static_assert(3 * kStageA + 1024 * (FM - 1) < 65536 && 3 * kStageB + 1024 * (FN - 1) < 65536, "immediate offsets");
+  static_assert((FM == 8 || FM == 4) && FN == 4 && kOps <= 4, "the orders below");
 
-  typedef float v16f __attribute__((ext_vector_type(16)));
   typedef __attribute__((address_space(3))) const v4i* lds_v4i;
-  typedef __attribute__((address_space(3))) const uint16_t* lds_u16;
+  typedef __attribute__((address_space(3))) v4i* lds_v4i_out;
+  typedef __attribute__((address_space(3))) const int* lds_int;
 
   // 16-byte chunks of a row are exchanged by its number: 16 consecutive rows then
   // have a chunk in 16 different places of 256 bytes
@@ -160,116 +177,98 @@ struct Mx4Tile {
     const int KT = (blocks + 3) / 4;
     const uint32_t lds0 = lds_addr(smem);
 
+    // What is needed in few slices is formed where it is used, from a value that the
+    // compiler does not know there: kept over the loop it would cost the registers that
+    // the fragments need.
+    auto here = [](int x) {
+      asm volatile("" : "+v"(x));
+      return x;
+    };
+
     // ---- transfers ----
     // part p of a slice: 16 rows (A's, then B's); lane l brings a chunk of row l / 4
-    const uint8_t* const base_a = g.a + static_cast<int64_t>(m0) * row_bytes;
-    const uint8_t* const base_b = g.b + static_cast<int64_t>(n0) * row_bytes;
+    const uint8_t* const base_a = uniform(g.a + static_cast<int64_t>(m0) * row_bytes);
+    const uint8_t* const base_b = uniform(g.b + static_cast<int64_t>(n0) * row_bytes);
     uint32_t voff[kOps];
     const int part0 = wave * kOps;
-    auto chunk_of = [&](int row) { return (lane & 3) ^ ((row >> 2) & 3); };
+    const int chunk = (lane & 3) ^ ((lane >> 4) & 3);  // as row_offset has it, in every piece of 16 rows
 #pragma unroll
     for (int q = 0; q < kOps; ++q) {
       const bool is_a = (part0 + q) * 16 < BM;
       const int row = (part0 + q) * 16 - (is_a ? 0 : BM) + (lane >> 2);
       const int from = is_a ? min(m0 + row, g.m - 1) - m0 : min(n0 + row, g.n - 1) - n0;
-      voff[q] = static_cast<uint32_t>(from) * static_cast<uint32_t>(row_bytes) + 16 * chunk_of(row);
+      voff[q] = static_cast<uint32_t>(from) * static_cast<uint32_t>(row_bytes) + (KTAIL ? 0 : 16 * chunk);
     }
-    // slice s, if there is one
+    // slice s, if there is one; blocks past k are read from the row's last
     auto issue = [&](int s, int q) {
       const bool is_a = (part0 + q) * 16 < BM;
-      const uint32_t who = __builtin_amdgcn_readfirstlane(s < KT ? ~0u : 0u);
-      const uint32_t to = __builtin_amdgcn_readfirstlane(
-          lds0 + (is_a ? (s & 3) * kStageA : kStages * kStageA + (s & 3) * kStageB - BM * kRow) + (part0 + q) * 1024);
-      const uint8_t* const from = (is_a ? base_a : base_b) + static_cast<int64_t>(s) * kRow;
-      if constexpr (KTAIL) {  // blocks past k: A's are zeros, B's any
-        const int row = (part0 + q) * 16 - (is_a ? 0 : BM) + (lane >> 2);
-        const int past = 4 * s + chunk_of(row) - (blocks - 1);
-        const uint8_t* const src = from + voff[q];
-        const uint8_t* const other = is_a ? reinterpret_cast<const uint8_t*>(&kZeros) : src - 16 * past;
-        lds_dma16_by(who, past > 0 ? other : src, to);
-      } else {
-        lds_dma16_by(who, from, voff[q], to);
-      }
+      const uint32_t to =
+          lds0 + (is_a ? (s & 3) * kStageA : kStages * kStageA + (s & 3) * kStageB - BM * kRow) + (part0 + q) * 1024;
+      const uint8_t* const from = is_a ? base_a : base_b;
+      if constexpr (KTAIL)
+        lds_dma16_below(s, KT, from, voff[q] + 16 * min(4 * s + here(chunk), blocks - 1), to);
+      else
+        lds_dma16_below(s, KT, from + static_cast<int64_t>(s) * kRow, voff[q], to);
     };
-    // scales of slices 4 group .. 4 group + 3, 64 rows per wave; a wave beyond the
-    // rows brings some a second time
-    const int piece = wave % ((BM + BN) / 64);
-    const uint8_t* scale_from;
-    {
-      const int row = piece * 64 + lane;
-      scale_from = piece * 64 < BM ? g.scale_a + min(m0 + row, g.m - 1) * g.ldsa
-                                   : g.scale_b + min(n0 + row - BM, g.n - 1) * g.ldsb;
-    }
-    auto issue_scales = [&](int group) {
-      lds_dma16_by(__builtin_amdgcn_readfirstlane(4 * group < KT ? ~0u : 0u), scale_from + 16 * group,
-                   __builtin_amdgcn_readfirstlane(lds0 + kScales + (group & 1) * kScaleBuf + piece * 1024));
+    // Scales of 16 slices: 64 bytes (chunks of four slices' 16) of each of this
+    // wave's 64 rows, laid out and exchanged as a slice's.  Chunks past the row's
+    // last are read from that.  A wave past the rows has room of its own, and brings
+    // nothing.
+    const bool scales_a = wave * 64 < BM;
+    const uint8_t* const base_s = uniform(scales_a ? g.scale_a + m0 * g.ldsa : g.scale_b + n0 * g.ldsb);
+    const uint32_t lds_s = static_cast<uint32_t>(scales_a ? g.ldsa : g.ldsb);
+    const int rows_s = (scales_a ? g.m - m0 : g.n - n0) - 1, row_s = wave * 64 - (scales_a ? 0 : BM);
+    const int last_chunk = (KT - 1) >> 2;
+    const uint32_t wave_scales = lds0 + kScales + wave * 64 * kRow;
+    auto issue_scales = [&](int batch, int q) {
+      const int l = here(lane), c = (l & 3) ^ ((l >> 4) & 3);
+      const uint32_t row = static_cast<uint32_t>(min(row_s + q * 16 + (l >> 2), rows_s));
+      lds_dma16_below(wave < kPieces ? 16 * batch : KT, KT, base_s, row * lds_s + 16 * min(4 * batch + c, last_chunk),
+                   wave_scales + q * 1024);
+    };
+    auto own_scales = [&](int x) { return wave_scales + here(lane) * kRow + 16 * x; };  // of this thread's row
+    auto raw_scales = [&](int x) { return *reinterpret_cast<lds_v4i>(own_scales(x)); };
+    auto put_scales = [&](int batch, int x, v4i w) {
+      // Those of blocks past k, where anything may lie, become 2^-127 in both
+      // operands: products of codes are then 2^-247 at most, nothing in binary32.
+      if constexpr (KTAIL) {
+        const int left = blocks - 16 * (4 * batch + (x ^ ((here(lane) >> 2) & 3)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int have = left - 4 * i;
+          const uint32_t keep = have >= 4 ? ~0u : have <= 0 ? 0u : (1u << (8 * have)) - 1u;
+          w[i] = static_cast<int>(static_cast<uint32_t>(w[i]) & keep);
+        }
+      }
+      uint32_t t[4];
+      tile::transpose4x4(w[0], w[1], w[2], w[3], t[0], t[1], t[2], t[3]);
+      *reinterpret_cast<lds_v4i_out>(own_scales(x)) =
+          v4i{static_cast<int>(t[0]), static_cast<int>(t[1]), static_cast<int>(t[2]), static_cast<int>(t[3])};
     };
 
     // ---- fragments ----
     const int wm = wave / kWavesN, wn = wave % kWavesN;
-    const int i32 = lane & 31, h = lane >> 5;
+    const int i16 = lane & 15, c4 = lane >> 4;
     auto opaque = [](uint32_t x) {
       asm("" : "+v"(x));
       return x;
     };
-    uint32_t a_base[2], b_base[2];  // [step]
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      a_base[s] = opaque(lds0 + row_offset(wm * WTM + i32, 2 * h + s));
-      b_base[s] = opaque(lds0 + kStages * kStageA + row_offset(wn * WTN + i32, 2 * h + s));
-    }
-    const uint32_t sa_base = opaque(lds0 + kScales + (wm * WTM + i32) * 16 + 2 * h);
-    const uint32_t sb_base = opaque(lds0 + kScales + (BM + wn * WTN + i32) * 16 + 2 * h);
-    auto read_a = [&](int S, int i, int s) { return *reinterpret_cast<lds_v4i>(a_base[s] + S * kStageA + 2048 * i); };
-    auto read_b = [&](int S, int j, int s) { return *reinterpret_cast<lds_v4i>(b_base[s] + S * kStageB + 2048 * j); };
-    // S8: the slice's number modulo 8
-    auto read_sa = [&](int S8, int i) -> int {
-      return *reinterpret_cast<lds_u16>(sa_base + (S8 >> 2) * kScaleBuf + (S8 & 3) * 4 + 512 * i);
-    };
-    auto read_sb = [&](int S8, int j) -> int {
-      return *reinterpret_cast<lds_u16>(sb_base + (S8 >> 2) * kScaleBuf + (S8 & 3) * 4 + 512 * j);
-    };
-    // the scales of blocks past k become 1: whatever lies there may be NaN
-    int keep = 0xffff, fill = 0;
-    if (KTAIL) {
-      const int valid = blocks - 4 * (KT - 1);
-      if (2 * h >= valid) keep &= 0xff00, fill |= kOne;
-      if (2 * h + 1 >= valid) keep &= 0x00ff, fill |= kOne << 8;
-    }
-
-    v16f acc[FM][FN];
+    const uint32_t a_base = opaque(lds0 + row_offset(wm * WTM + i16, c4));
+    const uint32_t b_base = opaque(lds0 + kStages * kStageA + row_offset(wn * WTN + i16, c4));
+    const uint32_t sa_base = opaque(lds0 + kScales + row_offset(wm * WTM + i16, 0) + 4 * c4);
+    const uint32_t sb_base = opaque(lds0 + kScales + row_offset(BM + wn * WTN + i16, 0) + 4 * c4);
+    auto read_a = [&](int S, int i) { return *reinterpret_cast<lds_v4i>(a_base + S * kStageA + 1024 * i); };
+    auto read_b = [&](int S, int j) { return *reinterpret_cast<lds_v4i>(b_base + S * kStageB + 1024 * j); };
+    v4f acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    v4i fa[2][FM], fb[2][FN];
-    int sa[FM], sb[FN], na[FM], nb[FN];
-    auto settle = [&](int kt) {  // the scales just read are slice kt's
-      if constexpr (KTAIL) {
-        const int k = kt == KT - 1 ? keep : 0xffff, f = kt == KT - 1 ? fill : 0;
-#pragma unroll
-        for (int i = 0; i < FM; ++i) sa[i] = (sa[i] & k) | f;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) sb[j] = (sb[j] & k) | f;
-      }
-    };
-
-    if (KT > 0) {
-      issue_scales(0);
-#pragma unroll
-      for (int s = 0; s < 3; ++s)
-#pragma unroll
-        for (int q = 0; q < kOps; ++q) issue(s, q);
-      wait_vmcnt<2 * kOps>();
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < FN; ++j) fb[0][j] = read_b(0, j, 0), sb[j] = read_sb(0, j);
-#pragma unroll
-      for (int i = 0; i < FM; ++i) fa[0][i] = read_a(0, i, 0), sa[i] = read_sa(0, i);
-      settle(0);
-    }
+      for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+    v4i fa[FM], fb[FN];
+    int sa[FM], sb[FN];  // of four slices
+    int ta[FM], tb[FN];  // small tiles: of the next four
+    auto scale_a = [&](int chunk, int i) { return *reinterpret_cast<lds_int>((sa_base ^ (chunk << 4)) + 1024 * i); };
+    auto scale_b = [&](int chunk, int j) { return *reinterpret_cast<lds_int>((sb_base ^ (chunk << 4)) + 1024 * j); };
     auto barrier = [] {
       __builtin_amdgcn_sched_barrier(0);
       asm volatile("" ::: "memory");
@@ -278,47 +277,183 @@ struct Mx4Tile {
       __builtin_amdgcn_sched_barrier(0);
     };
     auto pin = [] { __builtin_amdgcn_sched_barrier(0); };
-    // Slice kt, S8 its number modulo 8.  While step 0 is multiplied step 1's
-    // fragments are read; then slice kt + 1 has landed, and slice kt - 1's stage is
-    // free, for every wave; while step 1 is multiplied the next slice's step 0
-    // is read and slice kt + 3 asked for.
-    auto slice = [&](int S8, int kt) __attribute__((always_inline)) {
-      const int S = S8 & 3, N8 = (S8 + 1) & 7;
+
+    if (KT > 0) {
 #pragma unroll
-      for (int n = 0; n < FM * FN; ++n) {
-        const int i = n / FN, j = n % FN;
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(fb[0][j]), operand(fa[0][i]), acc[i][j], kFp4,
-                                                                   kFp4, 0, sb[j], 0, sa[i]);
-        pin();
-        if (n < FN) fb[1][n] = read_b(S, n, 1);
-        if (n < FM) fa[1][n] = read_a(S, n, 1);
-        pin();
-      }
-      wait_vmcnt<kOps>();  // what may still be under way is slice kt + 2
+      for (int q = 0; q < 4; ++q) issue_scales(0, q);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int q = 0; q < kOps; ++q) issue(s, q);
+      wait_vmcnt<3 * kOps>();
+#pragma unroll
+      for (int x = 0; x < 4; ++x) put_scales(0, x, raw_scales(x));
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sb[j] = scale_b(0, j), fb[j] = read_b(0, j);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) sa[i] = scale_a(0, i), fa[i] = read_a(0, i);
+    }
+
+    // Slice kt, X its number modulo 16 (a constant wherever it is used).  At the
+    // barrier slice kt + 1 has landed, for every wave, and every wave has read the last
+    // of slice kt; what may still be under way is slices kt + 2 and kt + 3.  The
+    // last scales of a batch are read in slice 11, so the next batch may come
+    // over it from slice 12's barrier on; asked for before slice 16's data, it is
+    // there at slice 14's barrier, transposed behind it, and read in slice 15.
+    auto meet = [&] {
+      wait_vmcnt<2 * kOps>();
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
       barrier();
-#pragma unroll
-      for (int n = 0; n < FM * FN; ++n) {
-        const int i = n / FN, j = n % FN;
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(fb[1][j]), operand(fa[1][i]), acc[i][j], kFp4,
-                                                                   kFp4, 1, sb[j], 1, sa[i]);
+    };
+    auto slice = [&](int X, int kt) __attribute__((always_inline)) {
+      const int S = X & 3, SN = (X + 1) & 3;
+      const int next = (kt >> 4) + 1;  // the next batch of scales
+      auto mfma = [&](int i, int j) {
+        // the byte's number is part of the instruction
+        if (S == 0) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 0, sb[j], 0, sa[i]);
+        if (S == 1) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 1, sb[j], 1, sa[i]);
+        if (S == 2) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 2, sb[j], 2, sa[i]);
+        if (S == 3) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 3, sb[j], 3, sa[i]);
         pin();
+      };
+      auto dma = [&](int q) {
+        if (X == 12) issue_scales(next, q);
+        pin();
+      };
+      auto data = [&](int q) {
+        if (q < kOps) issue(kt + 4, q);
+        pin();
+      };
+      v4i raw[2];
+      auto scales = [&](int part) {  // work on scales between the last products: 12 parts
+        const int chunk = ((X + 1) >> 2) & 3;
+        if ((X & 3) == 3 && FM == 8) {  // the first half's; the others are still in use
+          if (part >= 6 && part < 10) sa[part - 6] = scale_a(chunk, part - 6);
+          if (part >= 10) sb[part - 10] = scale_b(chunk, part - 10);
+        }
+        if ((X & 3) == 3 && FM == 4) {
+          if (part < FN) tb[part] = scale_b(chunk, part);
+          else if (part < FN + FM) ta[part - FN] = scale_a(chunk, part - FN);
+        }
+        if (X == 14 && (part == 0 || part == 1 || part == 6 || part == 7)) raw[part & 1] = raw_scales(part < 6 ? part : part - 4);
+        if (X == 14 && (part == 4 || part == 5 || part == 10 || part == 11))
+          put_scales(next, part < 6 ? part - 4 : part - 8, raw[part & 1]);
+        pin();
+      };
+      if constexpr (FM == 8) {
+        // Each fragment is read several products before its first use, and the
+        // slice's last well before the barrier.  In hand: A 0 .. 3, B 0 .. 1.
+        mfma(0, 0);
+        fa[4] = read_a(S, 4);
+        fa[5] = read_a(S, 5);
+        mfma(0, 1);
+        fa[6] = read_a(S, 6);
+        fa[7] = read_a(S, 7);
+        mfma(1, 0);
+        fb[2] = read_b(S, 2);
+        fb[3] = read_b(S, 3);
+        mfma(1, 1);
+        if (S == 0) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sa[4 + x] = scale_a(X >> 2, 4 + x);
+          sb[2] = scale_b(X >> 2, 2);
+          sb[3] = scale_b(X >> 2, 3);
+          pin();
+        }
+        mfma(2, 0);
+        mfma(2, 1);
+        mfma(3, 0);
+        mfma(3, 1);
+        meet();
+        if (X == 12) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) dma(q);
+        }
         // after the last slice these come from a stage that is there and are not used
-        if (n < FN) fb[0][n] = read_b(N8 & 3, n, 0), nb[n] = read_sb(N8, n);
-        if (n < FM) fa[0][n] = read_a(N8 & 3, n, 0), na[n] = read_sa(N8, n);
-        if (n == 0 && (S8 & 3) == 1) issue_scales((kt + 3) >> 2);
-        if (n < kOps) issue(kt + 3, n);
-        pin();
+        v4i na[4], nb[2];
+        mfma(4, 0);
+        scales(0);
+        mfma(5, 0);
+        data(0);
+        mfma(6, 0);
+        scales(1);
+        mfma(7, 0);
+        nb[0] = read_b(SN, 0);
+        mfma(4, 1);
+        scales(2);
+        mfma(5, 1);
+        data(1);
+        mfma(6, 1);
+        scales(3);
+        mfma(7, 1);
+        nb[1] = read_b(SN, 1);
+        mfma(0, 2);
+        scales(4);
+        mfma(0, 3);
+        na[0] = read_a(SN, 0);
+        mfma(1, 2);
+        data(2);
+        mfma(1, 3);
+        na[1] = read_a(SN, 1);
+        mfma(2, 2);
+        scales(5);
+        mfma(2, 3);
+        na[2] = read_a(SN, 2);
+        mfma(3, 2);
+        data(3);
+        mfma(3, 3);
+        na[3] = read_a(SN, 3);
+        mfma(4, 2);
+        scales(6);
+        mfma(4, 3);
+        scales(7);
+        mfma(5, 2);
+        scales(8);
+        mfma(5, 3);
+        scales(9);
+        mfma(6, 2);
+        scales(10);
+        mfma(6, 3);
+        scales(11);
+        mfma(7, 2);
+        mfma(7, 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fa[i] = na[i];
+        fb[0] = nb[0];
+        fb[1] = nb[1];
+      } else {
+        // Small sets of fragments are held twice: after the barrier the next slice's
+        // are read while this one's, read before it, are multiplied.
+        meet();
+        if (X == 12) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) dma(q);
+        }
+        v4i na[FM], nb[FN];
+#pragma unroll
+        for (int x = 0; x < FM * FN; ++x) {
+          mfma(x / FN, x % FN);
+          if (x < FN) nb[x] = read_b(SN, x);
+          else if (x < FN + FM) na[x - FN] = read_a(SN, x - FN);
+          if (x % 2 == 1 && x / 2 < 4) data(x / 2);
+          scales(x < 12 ? x : 99);
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fa[i] = na[i];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[j] = nb[j];
+        if (S == 3) {
+#pragma unroll
+          for (int i = 0; i < FM; ++i) sa[i] = ta[i];
+#pragma unroll
+          for (int j = 0; j < FN; ++j) sb[j] = tb[j];
+        }
       }
-      static_assert(FM * FN >= kOps && FM * FN >= FM && FM * FN >= FN, "a place for every read and transfer");
-#pragma unroll
-      for (int i = 0; i < FM; ++i) sa[i] = na[i];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) sb[j] = nb[j];
-      settle(kt + 1);
     };
     int kt = 0;
-    for (; kt + 8 <= KT; kt += 8) {
-      slice(0, kt);
+    for (; kt + 16 <= KT; kt += 16) {
+      slice(0, kt + 0);
       slice(1, kt + 1);
       slice(2, kt + 2);
       slice(3, kt + 3);
@@ -326,23 +461,39 @@ struct Mx4Tile {
       slice(5, kt + 5);
       slice(6, kt + 6);
       slice(7, kt + 7);
+      slice(8, kt + 8);
+      slice(9, kt + 9);
+      slice(10, kt + 10);
+      slice(11, kt + 11);
+      slice(12, kt + 12);
+      slice(13, kt + 13);
+      slice(14, kt + 14);
+      slice(15, kt + 15);
     }
-    if (kt < KT) slice(0, kt);
+    if (kt + 0 < KT) slice(0, kt + 0);
     if (kt + 1 < KT) slice(1, kt + 1);
     if (kt + 2 < KT) slice(2, kt + 2);
     if (kt + 3 < KT) slice(3, kt + 3);
     if (kt + 4 < KT) slice(4, kt + 4);
     if (kt + 5 < KT) slice(5, kt + 5);
     if (kt + 6 < KT) slice(6, kt + 6);
+    if (kt + 7 < KT) slice(7, kt + 7);
+    if (kt + 8 < KT) slice(8, kt + 8);
+    if (kt + 9 < KT) slice(9, kt + 9);
+    if (kt + 10 < KT) slice(10, kt + 10);
+    if (kt + 11 < KT) slice(11, kt + 11);
+    if (kt + 12 < KT) slice(12, kt + 12);
+    if (kt + 13 < KT) slice(13, kt + 13);
+    if (kt + 14 < KT) slice(14, kt + 14);
 
     // ---- results ----
-    // register 4 q + e of a fragment is row (of out) i32, column 8 q + 4 h + e.  A wave
-    // puts rows of WTN results into its 16 KiB of LDS, as many at a time as fit,
-    // and stores them 16 bytes per lane.
+    // register e of a fragment is row (of out) i16, column 4 c4 + e.  A wave puts
+    // rows of WTN results into its 16 KiB of LDS, as many at a time as fit, and
+    // stores them 16 bytes per lane.
     __syncthreads();
     constexpr int kRowOut = WTN * kElem;                   // bytes
     constexpr int kChunks = kRowOut / 16;
-    constexpr int kFrags = 16384 / (32 * kRowOut) < FM ? 16384 / (32 * kRowOut) : FM;  // fragments of rows at a time
+    constexpr int kFrags = 16384 / (16 * kRowOut) < FM ? 16384 / (16 * kRowOut) : FM;  // fragments of rows at a time
     char* const stage = smem + wave * 16384;
     auto place = [](int row, int chunk) { return row * kRowOut + ((chunk ^ (row & (kChunks - 1))) << 4); };
 #pragma unroll
@@ -351,27 +502,23 @@ struct Mx4Tile {
 #pragma unroll
       for (int ii = 0; ii < kFrags; ++ii)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = acc[i0 + ii][j][4 * q + e] * g.output_scale;
-            const int row = ii * 32 + i32, col = j * 32 + 8 * q + 4 * h;
-            if constexpr (DT == QK_F32)
-              *reinterpret_cast<float4*>(stage + place(row, col / 4)) = make_float4(v[0], v[1], v[2], v[3]);
-            else
-              *reinterpret_cast<uint2*>(stage + place(row, col / 8) + (col & 4) * 2) =
-                  make_uint2(qm::pack2_narrow<DT>(v[0], v[1]), qm::pack2_narrow<DT>(v[2], v[3]));
-          }
+        for (int j = 0; j < FN; ++j) {
+          const v4f v = acc[i0 + ii][j] * g.output_scale;
+          const int row = ii * 16 + i16, col = j * 16 + 4 * c4;
+          if constexpr (DT == QK_F32)
+            *reinterpret_cast<v4f*>(stage + place(row, col / 4)) = v;
+          else
+            *reinterpret_cast<uint2*>(stage + place(row, col / 8) + (col & 4) * 2) =
+                make_uint2(qm::pack2_narrow<DT>(v[0], v[1]), qm::pack2_narrow<DT>(v[2], v[3]));
+        }
       __builtin_amdgcn_wave_barrier();
       constexpr int kRowsAt = 64 / kChunks;  // rows that the wave's lanes take together
       const int chunk = lane % kChunks, col = n0 + wn * WTN + chunk * (16 / kElem);
 #pragma unroll 4
-      for (int r = lane / kChunks; r < kFrags * 32; r += kRowsAt) {
+      for (int r = lane / kChunks; r < kFrags * 16; r += kRowsAt) {
         typedef unsigned v4u __attribute__((ext_vector_type(4)));
         const v4u w = *reinterpret_cast<const v4u*>(stage + place(r, chunk));
-        const int row = m0 + wm * WTM + i0 * 32 + r;
+        const int row = m0 + wm * WTM + i0 * 16 + r;
         if (row >= g.m || col >= g.n) continue;
         char* const to = static_cast<char*>(g.out) + (static_cast<int64_t>(row) * g.n + col) * kElem;
         if (col + 16 / kElem <= g.n && reinterpret_cast<uintptr_t>(to) % 16 == 0) {
@@ -409,12 +556,20 @@ hipError_t tiles(const Mx4GemmArgs& g, hipStream_t stream) {
   return launch(mx4_gemm_tile_kernel<Whole>, grid, block, 0, stream, g, tm, tn);
 }
 
+// Which tile: the least estimated time.  A round of 256 large tiles takes 0.97 us
+// for a slice, of 256 of 256 x 128 0.58, of 512 of 128 x 128 (two to a CU) 0.65, of
+// up to 256 of them 0.33 (measured with k from 4096 to 16384).
 template <int DT>
 hipError_t by_size(const Mx4GemmArgs& g, hipStream_t stream) {
   if (g.m <= 16) return rows<DT, 1, 4>(g, stream);
   if (g.m <= 64) return rows<DT, 4, 4>(g, stream);
-  const int64_t large = static_cast<int64_t>((g.m + 255) / 256) * ((g.n + 255) / 256);
-  if (large >= 256) return tiles<DT, 256, 256, 128, 64>(g, stream);
+  auto count = [&](int bm, int bn) { return static_cast<int64_t>((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn); };
+  auto rounds = [](int64_t t, int at) { return static_cast<double>((t + at - 1) / at); };
+  const double large = rounds(count(256, 256), 256) * 0.97, wide = rounds(count(256, 128), 256) * 0.58;
+  const int64_t few = count(128, 128);
+  const double small = static_cast<double>(few / 512) * 0.65 + (few % 512 == 0 ? 0 : few % 512 <= 256 ? 0.33 : 0.65);
+  if (large <= wide && large <= small) return tiles<DT, 256, 256, 128, 64>(g, stream);
+  if (wide <= small) return tiles<DT, 256, 128, 64, 64>(g, stream);
   return tiles<DT, 128, 128, 64, 64>(g, stream);
 }
 
