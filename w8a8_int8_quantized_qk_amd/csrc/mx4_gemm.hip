@@ -9,6 +9,9 @@
 //
 // The weight's rows are the first operand: a lane's four sums are then four
 // consecutive columns of one output row.
+#include <algorithm>
+#include <cmath>
+
 #include "gemm_tile.h"
 #include "quant_math.h"
 
@@ -19,7 +22,6 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4;       // the instruction's number of the element type
-constexpr uint32_t kOne = 127;  // the scale byte of 1
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ v8i operand(const v4i& w) { return v8i{w[0], w[1], w[2], w[3], 0, 0, 0, 0}; }
@@ -33,54 +35,105 @@ __device__ __forceinline__ void put(void* out, int64_t at, float v) {
     static_cast<uint16_t*>(out)[at] = static_cast<uint16_t>(qm::pack2_narrow<DT>(v, 0.0f));
 }
 
-// Few rows: bound by the weight's bytes.  A workgroup has 16 columns (rows of
-// the weight) and 16 F rows of A, its W waves a part of k each; their sums meet
-// in LDS in the order of the waves.  Operands come straight from memory: each
-// lane's 16 bytes are what the instruction wants from it.
-template <int DT, int F, int W>
-__global__ __launch_bounds__(64 * W) void mx4_gemm_rows_kernel(Mx4GemmArgs g, int steps_each) {
-  __shared__ v4f sums[W][F][64];
+// ---- few rows ----
+
+// Bound by the weight's bytes.  A workgroup has 16 R columns (rows of the weight)
+// and 16 F rows of A; its W waves take stretches of S slices of 128 k in turn, and
+// their sums meet in LDS in the order of the waves.  A wave brings its own operands
+// through LDS of its own, 64 S bytes of a row at a time: loaded straight into the
+// registers that the instruction wants (16 bytes of 16 rows from neighbouring lanes)
+// they came at a quarter of the rate.  Nothing is shared until the end, so no wave
+// waits for another, and several workgroups of a CU keep the weight coming.
+template <int DT, int F, int R, int W, int S>
+__global__ __launch_bounds__(64 * W) void mx4_gemm_rows_kernel(Mx4GemmArgs g, unsigned tiles_n) {
+  constexpr int kRow = 64 * S, kChunks = 4 * S;  // bytes, and 16-byte chunks, of a row in a stretch
+  constexpr int kTile = 16 * kRow;               // 16 rows
+  constexpr int kOps = kTile / 1024;
+  constexpr int kRowsAt = 64 / kChunks;          // rows of one transfer
+  constexpr int kWave = (F + R) * kTile;
+  static_assert(W * kWave <= 81920 && F * R * 1024 <= kWave, "LDS: two workgroups or more on a CU; the sums");
+  __shared__ __attribute__((aligned(1024))) char smem[W * kWave];
+  typedef __attribute__((address_space(3))) const v4i* lds_v4i;
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * F;
-  const int blocks = g.k / 32;
+  const unsigned tile_m = blockIdx.x / tiles_n;
+  const int n0 = (blockIdx.x - tile_m * tiles_n) * 16 * R, m0 = tile_m * 16 * F;
+  const int blocks = g.k / 32, stretches = (blocks + kChunks - 1) / kChunks;
   const int64_t row_bytes = g.k / 2;
-  const uint8_t* const b = g.b + min(n0 + r, g.n - 1) * row_bytes;
-  const uint8_t* const sb = g.scale_b + min(n0 + r, g.n - 1) * g.ldsb;
-  const uint8_t* a[F];
-  const uint8_t* sa[F];
+  const uint32_t own = lds_addr(smem) + wave * kWave;
+  const uint8_t *sb[R], *sa[F];
 #pragma unroll
-  for (int f = 0; f < F; ++f) {
-    a[f] = g.a + min(m0 + 16 * f + r, g.m - 1) * row_bytes;
-    sa[f] = g.scale_a + min(m0 + 16 * f + r, g.m - 1) * g.ldsa;
-  }
-  v4f acc[F];
+  for (int i = 0; i < R; ++i) sb[i] = g.scale_b + min(n0 + 16 * i + r, g.n - 1) * g.ldsb;
 #pragma unroll
-  for (int f = 0; f < F; ++f) acc[f] = v4f{0, 0, 0, 0};
-  const int first = wave * steps_each, last = min(first + steps_each, (blocks + 3) / 4);
-#pragma unroll 4
-  for (int s = first; s < last; ++s) {
-    const int at = 4 * s + c;  // the lane's block
-    const bool in = at < blocks;
-    const int here = in ? at : blocks - 1;
-    const v4i w = *reinterpret_cast<const v4i*>(b + 16 * here);
-    const uint32_t ws = in ? sb[here] : kOne;
+  for (int f = 0; f < F; ++f) sa[f] = g.scale_a + min(m0 + 16 * f + r, g.m - 1) * g.ldsa;
+  v4f acc[F][R];
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
-      v4i x = *reinterpret_cast<const v4i*>(a[f] + 16 * here);
-      if (!in) x = v4i{0, 0, 0, 0};
-      const uint32_t xs = in ? sa[f][here] : kOne;
-      acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(x), acc[f], kFp4, kFp4, 0,
-                                                               static_cast<int>(ws), 0, static_cast<int>(xs));
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int i = 0; i < R; ++i) acc[f][i] = v4f{0, 0, 0, 0};
+  // Chunks of a row are exchanged by its number, so that a chunk of 16 rows lies in 16
+  // different places of 256 bytes (8 where a row has 8 chunks).
+  auto key = [](int row) { return kChunks == 16 ? row & 15 : (row >> 1) & 7; };
+  for (int t = wave; t < stretches; t += W) {
+    // Blocks past k are read from the row's last one, and their scales become
+    // 2^-127 in both operands: products of codes are then 2^-247 at most, nothing in
+    // binary32.
+    auto bring = [&](const uint8_t* base, int row0, int rows, uint32_t to) {
+#pragma unroll
+      for (int q = 0; q < kOps; ++q) {
+        const int row = q * kRowsAt + lane / kChunks;
+        const int chunk = min(t * kChunks + ((lane % kChunks) ^ key(row)), blocks - 1);
+        lds_dma16(base + min(row0 + row, rows - 1) * row_bytes + 16 * chunk, to + 1024 * q);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < R; ++i) bring(g.b, n0 + 16 * i, g.n, own + i * kTile);
+#pragma unroll
+    for (int f = 0; f < F; ++f) bring(g.a, m0 + 16 * f, g.m, own + (R + f) * kTile);
+    uint32_t ws[R][S], xs[F][S];
+    auto scales = [&](const uint8_t* from, uint32_t (&v)[S]) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) v[s] = reinterpret_cast<const uint32_t*>(from)[t * S + s];
+    };
+#pragma unroll
+    for (int i = 0; i < R; ++i) scales(sb[i], ws[i]);
+#pragma unroll
+    for (int f = 0; f < F; ++f) scales(sa[f], xs[f]);
+    wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const bool past = t * kChunks + 4 * s + c >= blocks;
+      auto at = [&](int tile) { return *reinterpret_cast<lds_v4i>(own + tile * kTile + r * kRow + (((4 * s + c) ^ key(r)) << 4)); };
+      auto scale = [&](uint32_t w) { return static_cast<int>(past ? 0u : w >> (8 * c)); };
+      v4i w[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) w[i] = at(i);
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const v4i x = at(R + f);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          acc[f][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[i]), operand(x), acc[f][i], kFp4, kFp4, 0,
+                                                                      scale(ws[i][s]), 0, scale(xs[f][s]));
+      }
     }
+    // the next stretch's transfers come over what has been read
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
   }
+  v4f* const sums = reinterpret_cast<v4f*>(smem + wave * kWave);
 #pragma unroll
-  for (int f = 0; f < F; ++f) sums[wave][f][lane] = acc[f];
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int i = 0; i < R; ++i) sums[(f * R + i) * 64 + lane] = acc[f][i];
   __syncthreads();
-  for (int f = wave; f < F; f += W) {
-    v4f v = sums[0][f][lane];
-    for (int w = 1; w < W; ++w) v += sums[w][f][lane];
-    const int row = m0 + 16 * f + r, col = n0 + 4 * c;
+  for (int x = wave; x < F * R; x += W) {
+    auto of = [&](int w) { return reinterpret_cast<const v4f*>(smem + w * kWave)[x * 64 + lane]; };
+    v4f v = of(0);
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += of(w);
+    const int row = m0 + 16 * (x / R) + r, col = n0 + 16 * (x % R) + 4 * c;
     if (row >= g.m) continue;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -88,11 +141,12 @@ __global__ __launch_bounds__(64 * W) void mx4_gemm_rows_kernel(Mx4GemmArgs g, in
   }
 }
 
-template <int DT, int F, int W>
+template <int DT, int F, int R, int W, int S>
 hipError_t rows(const Mx4GemmArgs& g, hipStream_t stream) {
-  const int steps = (g.k / 32 + 3) / 4;
-  const dim3 grid(static_cast<unsigned>((g.n + 15) / 16), static_cast<unsigned>((g.m + 16 * F - 1) / (16 * F)));
-  return launch(mx4_gemm_rows_kernel<DT, F, W>, grid, dim3(64 * W), 0, stream, g, (steps + W - 1) / W);
+  const int64_t gn = (g.n + 16 * R - 1) / (16 * R), groups = gn * ((g.m + 16 * F - 1) / (16 * F));
+  if (!grid_fits(groups, 64 * W)) return hipErrorInvalidConfiguration;
+  return launch(mx4_gemm_rows_kernel<DT, F, R, W, S>, dim3(static_cast<unsigned>(groups)), dim3(64 * W), 0, stream, g,
+                static_cast<unsigned>(gn));
 }
 
 // ---- many rows: tiles in LDS ----
@@ -556,28 +610,42 @@ hipError_t tiles(const Mx4GemmArgs& g, hipStream_t stream) {
   return launch(mx4_gemm_tile_kernel<Whole>, grid, block, 0, stream, g, tm, tn);
 }
 
-// Which tile: the least estimated time.  A round of 256 large tiles takes 0.97 us
-// for a slice, of 256 of 256 x 128 0.58, of 512 of 128 x 128 (two to a CU) 0.65, of
-// up to 256 of them 0.33 (measured with k from 4096 to 16384).
+// Up to 32 rows: as many columns to a workgroup as leave enough of them (28672,
+// 14336 and 4096 columns in 64 / 32 / 16: one row of 4096 k 7.9 / 6.9 / 7.4 us with
+// 14336, 16 rows of 8192 k 28.6 / 29.8 / 30.2 with 28672, of 4096 k 5.9 / 4.6 / 3.8
+// with 4096; 24 rows of 4096 k 8.9 in 32 and 9.6 in 16 with 14336).
+//
+// Beyond, the least estimated time, in us, from what was measured with k from
+// 1024 to 16384 (rows in 32 x 32 / rows in 64 x 64 / tiles of 128 x 128: 64 x 4096 x
+// 4096 5.7 / 10.8 / 12.2; 128 x 14336 x 4096 23.9 / 19.9 / 14.0; 256 x 4096 x 14336
+// 31.3 / 23.8 / 35.4; 512 x 4096 x 4096 23.3 / 18.9 / 13.3.  Tiles of 128 x 128 / 256 x
+// 128 / 256 x 256: 2048 x 4096 x 4096 25.0 / 23.8 / 28.7; 4096 x 4096 x 14336
+// 154 / 144 / 109).  A workgroup's time grows with k; a CU takes one after the other.
 template <int DT>
 hipError_t by_size(const Mx4GemmArgs& g, hipStream_t stream) {
-  if (g.m <= 16) return rows<DT, 1, 4>(g, stream);
-  if (g.m <= 64) return rows<DT, 4, 4>(g, stream);
-  auto count = [&](int bm, int bn) { return static_cast<int64_t>((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn); };
-  auto rounds = [](int64_t t, int at) { return static_cast<double>((t + at - 1) / at); };
-  const double large = rounds(count(256, 256), 256) * 0.97, wide = rounds(count(256, 128), 256) * 0.58;
-  const int64_t few = count(128, 128);
-  const double small = static_cast<double>(few / 512) * 0.65 + (few % 512 == 0 ? 0 : few % 512 <= 256 ? 0.33 : 0.65);
-  if (large <= wide && large <= small) return tiles<DT, 256, 256, 128, 64>(g, stream);
-  if (wide <= small) return tiles<DT, 256, 128, 64, 64>(g, stream);
-  return tiles<DT, 128, 128, 64, 64>(g, stream);
+  if (g.m <= 16) {
+    if (g.n >= 64 * 400) return rows<DT, 1, 4, 4, 4>(g, stream);
+    if (g.n >= 32 * 400) return rows<DT, 1, 2, 4, 4>(g, stream);
+    return rows<DT, 1, 1, 8, 4>(g, stream);
+  }
+  if (g.m <= 32) return g.n >= 32 * 400 ? rows<DT, 2, 2, 4, 4>(g, stream) : rows<DT, 2, 1, 4, 4>(g, stream);
+  auto count = [&](int bm, int bn) { return static_cast<double>((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn); };
+  const double slices = (g.k + 127) / 128, waves22 = std::max(count(32, 32) / 256, 1.0), waves44 = std::max(count(64, 64) / 256, 1.0);
+  const double rounds1 = std::floor(count(128, 128) / 512), left1 = count(128, 128) - 512 * rounds1;
+  const double rows22 = 3.0 + 0.075 * slices * waves22, rows44 = 3.5 + 0.24 * slices * waves44;
+  const double tile1 = 5.0 + slices * (0.62 * rounds1 + (left1 > 256 ? 0.62 : left1 > 0 ? 0.25 : 0.0));
+  const double tile2 = 5.5 + slices * 0.58 * std::ceil(count(256, 128) / 256);
+  const double tile4 = 8.0 + slices * 0.97 * std::ceil(count(256, 256) / 256);
+  const double best = std::min({rows22, rows44, tile1, tile2, tile4});
+  if (best == tile4) return tiles<DT, 256, 256, 128, 64>(g, stream);
+  if (best == tile2) return tiles<DT, 256, 128, 64, 64>(g, stream);
+  if (best == tile1) return tiles<DT, 128, 128, 64, 64>(g, stream);
+  return best == rows44 ? rows<DT, 4, 4, 4, 2>(g, stream) : rows<DT, 2, 2, 4, 4>(g, stream);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_mx4(const Mx4GemmArgs& g, hipStream_t stream) {
-  const int64_t groups = static_cast<int64_t>((g.n + 15) / 16) * ((g.m + 15) / 16);
-  if (!grid_fits(groups, 256) || (g.m + 15) / 16 > 65535) return hipErrorInvalidConfiguration;
   switch (g.out_dtype) {
     case QK_F32: return by_size<QK_F32>(g, stream);
     case QK_BF16: return by_size<QK_BF16>(g, stream);
