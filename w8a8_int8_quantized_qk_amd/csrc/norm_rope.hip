@@ -10,7 +10,10 @@
 // is exact and at most an eighth of a turn, and loses nothing when it is rounded to
 // binary32 (t is off by 2^-52 of itself: 2^-25 of a turn at position 2^29).
 // Sine and cosine of at most pi / 4 are their Taylor sums in binary32, up to
-// x^9 and x^10 (the next terms are below 2^-28 and 2^-33).
+// x^9 and x^10 (the next terms are below 2^-29 and 2^-33).
+#include <algorithm>
+#include <type_traits>
+
 #include "kv_common.h"
 
 namespace qk {
@@ -21,6 +24,7 @@ using qm::Elem;
 constexpr int kBlock = 256;
 constexpr int kWaves = kBlock / 64;
 constexpr int kMostPairs = 128;
+constexpr int64_t kFill = 4096;  // waves that keep the memory busy
 
 struct Turn {
   float cos, sin;
@@ -93,119 +97,190 @@ __device__ __forceinline__ void store(char* p, const float* f) {
   }
 }
 
-// One workgroup per row (token); a head is L lanes of a wave, a lane has P
-// pairs of it: two pieces of P elements r / 2 apart, or one of 2 P (pairs side
-// by side, and the elements past r).  P = 4 where r is a multiple of 8;
-// otherwise P = 1 and a lane takes U pairs, L apart.
-template <int DT, int P, int L, int U, bool SIDE>
-__global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a) {
-  constexpr int B = Elem<DT>::kBytes;
-  constexpr int kHeads = 64 / L;  // heads that a wave has at a time
-  __shared__ Turn turns[kMostPairs];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = blockIdx.x;
-  int pos;
-  if (a.cu) {
-    const kv::Owner o = kv::find_sequence(row, a.cu, a.start, a.seqs, [](int first, int) { return first; });
-    if (o.seq < 0 || o.first < 0 || row >= o.next) return;  // uniform over the workgroup
-    pos = static_cast<int>(static_cast<uint32_t>(o.value) + static_cast<uint32_t>(row - o.first));
-  } else {
-    pos = a.start[row];
+// Sum over the L neighbouring lanes that hold a head.
+template <int L>
+__device__ __forceinline__ float head_sum(float v) {
+  auto from = [&](auto ctrl) {
+    return __uint_as_float(static_cast<uint32_t>(
+        __builtin_amdgcn_mov_dpp(static_cast<int>(__float_as_uint(v)), decltype(ctrl)::value, 0xF, 0xF, false)));
+  };
+  v += from(std::integral_constant<int, 0xB1>{});                         // lane ^ 1
+  v += from(std::integral_constant<int, 0x4E>{});                         // lane ^ 2
+  if constexpr (L >= 8) v += from(std::integral_constant<int, 0x141>{});  // the other four of eight
+  if constexpr (L >= 16) v += from(std::integral_constant<int, 0x140>{}); // the other eight of 16
+  if constexpr (L >= 32) {
+    const uint32_t b = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
-  if (static_cast<int>(threadIdx.x) < a.rotary / 2) turns[threadIdx.x] = turn_of(pos, a.freqs[threadIdx.x]);
-  __syncthreads();
+  if constexpr (L >= 64) {
+    const uint32_t b = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
 
+// A wave has a row's position, the sines and cosines of its pairs (a pair or two
+// per lane, handed round through LDS of its own) and `groups` of its heads, 64 / L
+// of them at a time: L lanes to a head, P pairs to a lane, that is two pieces of P
+// elements r / 2 apart, or one of 2 P (pairs side by side, and the elements past
+// r).  P is 8 where r is a multiple of 16, so that a 16-bit piece is 16 bytes; 4 where it
+// is one of 8; else 1, and a lane takes U pairs, L apart.
+template <int DT, int P, int L, int U, bool SIDE>
+__global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int parts, int groups) {
+  constexpr int B = Elem<DT>::kBytes;
+  constexpr int kHeads = 64 / L;  // of a group
+  constexpr int G = P == 1 ? 1 : 2;  // groups whose loads are in flight together
+  __shared__ Turn all_turns[kWaves][kMostPairs];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned item = blockIdx.x * kWaves + wave;
+  const unsigned of_row = item / static_cast<unsigned>(parts);
+  if (of_row >= static_cast<unsigned>(a.tokens)) return;
+  const int row = static_cast<int>(of_row), part = static_cast<int>(item - of_row * parts);
+  Turn* const turns = all_turns[wave];
   const int within = lane % L, pairs = a.dim / 2, half = a.rotary / 2;
-  const int all = a.heads + a.kv_heads;
-  for (int h0 = wave * kHeads; h0 < all; h0 += kWaves * kHeads) {
-    const int h = h0 + lane / L;
-    const bool is_q = h < a.heads, live = h < all;
-    const int64_t at = is_q ? row * a.ldq + static_cast<int64_t>(h) * a.dim : row * a.ldk + static_cast<int64_t>(h - a.heads) * a.dim;
-    const int64_t to = is_q ? row * a.ldqo + static_cast<int64_t>(h) * a.dim : row * a.ldko + static_cast<int64_t>(h - a.heads) * a.dim;
-    const char* const from = static_cast<const char*>(is_q ? a.q : a.k) + at * B;
-    char* const dst = static_cast<char*>(is_q ? a.q_out : a.k_out) + to * B;
-    const void* const weight = is_q ? a.q_weight : a.k_weight;
-    float x[U][2 * P];
-    float sum = 0.0f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = (within + u * L) * P;  // the first pair
-#pragma unroll
-      for (int e = 0; e < 2 * P; ++e) x[u][e] = 0.0f;
-      if (!live || i >= pairs) continue;
-      if (!SIDE && i < half) {
-        load<DT, P>(from + i * B, x[u]);
-        load<DT, P>(from + (half + i) * B, x[u] + P);
-      } else if constexpr (P > 1) {
-        load<DT, 2 * P>(from + 2 * i * B, x[u]);
-      } else {
-        load<DT, 1>(from + 2 * i * B, x[u]);
-        load<DT, 1>(from + (2 * i + 1) * B, x[u] + 1);
-      }
-#pragma unroll
-      for (int e = 0; e < 2 * P; ++e) sum = __builtin_fmaf(x[u][e], x[u][e], sum);
+  const int q_groups = (a.heads + kHeads - 1) / kHeads, last = q_groups + (a.kv_heads + kHeads - 1) / kHeads;
+  const int g0 = part * groups, g1 = min(g0 + groups, last);
+
+  bool ready = false;  // the row's turns
+  bool mine = true;    // some sequence's row
+  auto prepare = [&] {
+    if (ready) return;
+    ready = true;
+    int pos;
+    if (a.cu) {
+      const kv::Owner o = kv::find_sequence(row, a.cu, a.start, a.seqs, [](int first, int) { return first; });
+      mine = o.seq >= 0 && o.first >= 0 && row < o.next;
+      pos = static_cast<int>(static_cast<uint32_t>(o.value) + static_cast<uint32_t>(row - o.first));
+    } else {
+      pos = a.start[row];
     }
-    if (weight) {
+    for (int i = lane; i < half; i += 64) turns[i] = turn_of(pos, a.freqs[i]);
+    __builtin_amdgcn_wave_barrier();
+  };
+
+  // heads of one tensor, groups first .. end of it
+  auto side = [&](int first, int end, const void* in, int64_t ld, int heads, const void* weight, void* out, int64_t ldo) {
+    if (first >= end) return;
+    const char* const from_row = static_cast<const char*>(in) + row * ld * B;
+    char* const to_row = static_cast<char*>(out) + row * ldo * B;
+    float w[U][2 * P];
 #pragma unroll
-      for (int d = 1; d < L; d <<= 1) sum += __shfl_xor(sum, d);
-      const float inv = 1.0f / __builtin_sqrtf(sum / static_cast<float>(a.dim) + a.eps);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 2 * P; ++e) w[u][e] = 1.0f;
+    if (weight) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = (within + u * L) * P;
         if (i >= pairs) continue;
+        const bool apart = !SIDE && i < half;
+        const int at = apart ? i : 2 * i, other = apart ? half + i : 2 * i + P;
+        if (a.weight_f32) {
+          const float* const f = static_cast<const float*>(weight);
 #pragma unroll
-        for (int e = 0; e < 2 * P; ++e) {
-          const int d = !SIDE && i < half ? (e < P ? i + e : half + i + e - P) : 2 * i + e;
-          const float w = a.weight_f32 ? static_cast<const float*>(weight)[d] : Elem<DT>::load(weight, d);
-          x[u][e] = (x[u][e] * inv) * w;
+          for (int e = 0; e < P; ++e) w[u][e] = f[at + e], w[u][P + e] = f[other + e];
+        } else {
+          load<DT, P>(static_cast<const char*>(weight) + at * B, w[u]);
+          load<DT, P>(static_cast<const char*>(weight) + other * B, w[u] + P);
         }
       }
     }
+    for (int base = first; base < end; base += G) {
+      float x[G][U][2 * P];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = (within + u * L) * P;
-      if (!live || i >= pairs) continue;
-      if (i < half) {
+      for (int g = 0; g < G; ++g) {
+        const int h = (base + g) * kHeads + lane / L;
+        const char* const from = from_row + h * a.dim * B;
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const Turn t = turns[i + p];
-          const int ia = SIDE ? 2 * p : p, ib = SIDE ? 2 * p + 1 : P + p;
-          const float ya = x[u][ia], yb = x[u][ib];
-          x[u][ia] = __builtin_fmaf(ya, t.cos, -(yb * t.sin));
-          x[u][ib] = __builtin_fmaf(yb, t.cos, ya * t.sin);
+        for (int u = 0; u < U; ++u) {
+          const int i = (within + u * L) * P;  // the first pair
+#pragma unroll
+          for (int e = 0; e < 2 * P; ++e) x[g][u][e] = 0.0f;
+          if (base + g >= end || h >= heads || i >= pairs) continue;
+          const bool apart = !SIDE && i < half;
+          load<DT, P>(from + (apart ? i : 2 * i) * B, x[g][u]);
+          load<DT, P>(from + (apart ? half + i : 2 * i + P) * B, x[g][u] + P);
         }
       }
-      if (!SIDE && i < half) {
-        store<DT, P>(dst + i * B, x[u]);
-        store<DT, P>(dst + (half + i) * B, x[u] + P);
-      } else if constexpr (P > 1) {
-        store<DT, 2 * P>(dst + 2 * i * B, x[u]);
-      } else {
-        store<DT, 1>(dst + 2 * i * B, x[u]);
-        store<DT, 1>(dst + (2 * i + 1) * B, x[u] + 1);
+      prepare();
+      if (!mine) return;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int h = (base + g) * kHeads + lane / L;
+        if (weight) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 2 * P; ++e) sum = __builtin_fmaf(x[g][u][e], x[g][u][e], sum);
+          sum = head_sum<L>(sum);
+          const float inv = 1.0f / __builtin_sqrtf(sum / static_cast<float>(a.dim) + a.eps);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 2 * P; ++e) x[g][u][e] = (x[g][u][e] * inv) * w[u][e];
+        }
+        char* const to = to_row + h * a.dim * B;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = (within + u * L) * P;
+          if (base + g >= end || h >= heads || i >= pairs) continue;
+          const bool apart = !SIDE && i < half;
+          if (i < half) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              const Turn t = turns[i + p];
+              const int ia = SIDE ? 2 * p : p, ib = SIDE ? 2 * p + 1 : P + p;
+              const float ya = x[g][u][ia], yb = x[g][u][ib];
+              x[g][u][ia] = __builtin_fmaf(ya, t.cos, -(yb * t.sin));
+              x[g][u][ib] = __builtin_fmaf(yb, t.cos, ya * t.sin);
+            }
+          }
+          store<DT, P>(to + (apart ? i : 2 * i) * B, x[g][u]);
+          store<DT, P>(to + (apart ? half + i : 2 * i + P) * B, x[g][u] + P);
+        }
       }
     }
-  }
+  };
+  side(g0, min(g1, q_groups), a.q, a.ldq, a.heads, a.q_weight, a.q_out, a.ldqo);
+  side(max(g0, q_groups) - q_groups, g1 - q_groups, a.k, a.ldk, a.kv_heads, a.k_weight, a.k_out, a.ldko);
 }
 
 template <int DT, int P, int L, int U>
 hipError_t go(const NormRopeArgs& a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.tokens)), block(kBlock);
-  return a.interleaved ? launch(norm_rope_kernel<DT, P, L, U, true>, grid, block, 0, stream, a)
-                       : launch(norm_rope_kernel<DT, P, L, U, false>, grid, block, 0, stream, a);
+  constexpr int kHeads = 64 / L;
+  const int groups = (a.heads + kHeads - 1) / kHeads + (a.kv_heads + kHeads - 1) / kHeads;
+  // a wave per row where there are enough rows, else as many as there are groups
+  const int wanted = static_cast<int>(std::min<int64_t>(groups, std::max<int64_t>(1, kFill / a.tokens)));
+  const int each = (groups + wanted - 1) / wanted, parts = (groups + each - 1) / each;
+  const int64_t blocks = (static_cast<int64_t>(a.tokens) * parts + kWaves - 1) / kWaves;
+  if (!grid_fits(blocks, kBlock)) return hipErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kBlock);
+  return a.interleaved ? launch(norm_rope_kernel<DT, P, L, U, true>, grid, block, 0, stream, a, parts, each)
+                       : launch(norm_rope_kernel<DT, P, L, U, false>, grid, block, 0, stream, a, parts, each);
 }
 
 template <int DT>
 hipError_t by_size(const NormRopeArgs& a, hipStream_t stream) {
-  if (a.rotary % 8 != 0) return go<DT, 1, 64, 2>(a, stream);
-  if (a.dim <= 64) return go<DT, 4, 8, 1>(a, stream);
-  if (a.dim <= 128) return go<DT, 4, 16, 1>(a, stream);
-  return go<DT, 4, 32, 1>(a, stream);
+  if (a.rotary % 16 == 0) {
+    if (a.dim <= 64) return go<DT, 8, 4, 1>(a, stream);
+    if (a.dim <= 128) return go<DT, 8, 8, 1>(a, stream);
+    return go<DT, 8, 16, 1>(a, stream);
+  }
+  if (a.rotary % 8 == 0) {
+    if (a.dim <= 64) return go<DT, 4, 8, 1>(a, stream);
+    if (a.dim <= 128) return go<DT, 4, 16, 1>(a, stream);
+    return go<DT, 4, 32, 1>(a, stream);
+  }
+  return go<DT, 1, 64, 2>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_norm_rope(const NormRopeArgs& a, hipStream_t stream) {
-  if (!grid_fits(a.tokens, kBlock)) return hipErrorInvalidConfiguration;
+  if (a.tokens >= 1 << 24) return hipErrorInvalidConfiguration;
   switch (a.dtype) {
     case QK_F32: return by_size<QK_F32>(a, stream);
     case QK_BF16: return by_size<QK_BF16>(a, stream);
