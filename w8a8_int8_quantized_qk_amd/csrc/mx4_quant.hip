@@ -19,7 +19,10 @@
 //
 // Bound by memory: four lanes share a block, eight values (16 or 32 bytes)
 // each, so a wave reads 1 KiB of 16-bit rows in one piece and writes 256 bytes
-// of codes and 16 of scales.
+// of codes and 16 of scales.  bf16, 4096 x 14336 there 28.1 us (5.3 TB/s), back 18.3
+// (8.1, its last stores still on their way), one after the other 49.2 (6.0);
+// 8 x 4096 2.0 us either way.  Reading past the caches there gains nothing (27.7);
+// the values of large calls are stored past them on the way back (29.4 without).
 #include "kv_common.h"
 
 namespace qk {
@@ -30,6 +33,7 @@ using qm::Elem;
 
 constexpr int kBlock = 256;
 constexpr int kEach = 8;  // values per lane, a quarter of a block
+constexpr int64_t kPastCaches = 8 << 20;  // bytes of values that are stored past the caches
 
 // Eight values at any alignment the element type allows.
 template <int DT>
@@ -81,7 +85,7 @@ __global__ __launch_bounds__(kBlock) void mx4_quant_kernel(const char* __restric
   if ((at & 3) == 0) scale[row * lds + (at >> 2)] = static_cast<uint8_t>(byte);
 }
 
-template <int DT>
+template <int DT, bool PAST>
 __global__ __launch_bounds__(kBlock) void mx4_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                                                              int64_t lds, int64_t items, uint32_t per_row,
                                                              char* __restrict__ x, int64_t ldx) {
@@ -100,15 +104,21 @@ __global__ __launch_bounds__(kBlock) void mx4_dequant_kernel(const uint8_t* __re
     for (int e = 0; e < kEach; ++e) v[e] = __builtin_nanf("");
   }
   constexpr int B = Elem<DT>::kBytes;
-  Raw16<B>* const to = reinterpret_cast<Raw16<B>*>(x + (row * ldx + static_cast<int64_t>(at) * kEach) * B);
-  if constexpr (DT == QK_F32) {
+  kv::Loose16* const to = reinterpret_cast<kv::Loose16*>(x + (row * ldx + static_cast<int64_t>(at) * kEach) * B);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      to[h] = Raw16<B>{{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
-                        __float_as_uint(v[4 * h + 3])}};
-  } else {
-    to[0] = Raw16<B>{{qm::pack2_narrow<DT>(v[0], v[1]), qm::pack2_narrow<DT>(v[2], v[3]), qm::pack2_narrow<DT>(v[4], v[5]),
-                      qm::pack2_narrow<DT>(v[6], v[7])}};
+  for (int h = 0; h < kEach * B / 16; ++h) {
+    kv::Loose16 out;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (DT == QK_F32)
+        out[e] = __float_as_uint(v[4 * h + e]);
+      else
+        out[e] = qm::pack2_narrow<DT>(v[2 * e], v[2 * e + 1]);
+    }
+    if constexpr (PAST)
+      __builtin_nontemporal_store(out, to + h);
+    else
+      to[h] = out;
   }
 }
 
@@ -125,8 +135,9 @@ hipError_t quant(const Mx4RowsArgs& a, int64_t items, uint32_t per_row, hipStrea
 
 template <int DT>
 hipError_t dequant(const Mx4RowsArgs& a, int64_t items, uint32_t per_row, hipStream_t stream) {
-  return launch(mx4_dequant_kernel<DT>, grid_of(items), dim3(kBlock), 0, stream, a.q, a.scale, a.lds, items, per_row,
-                static_cast<char*>(const_cast<void*>(a.x)), a.ldx);
+  const bool past = items * kEach * Elem<DT>::kBytes > kPastCaches;
+  return launch(past ? mx4_dequant_kernel<DT, true> : mx4_dequant_kernel<DT, false>, grid_of(items), dim3(kBlock), 0, stream,
+                a.q, a.scale, a.lds, items, per_row, static_cast<char*>(const_cast<void*>(a.x)), a.ldx);
 }
 
 }  // namespace

@@ -24,7 +24,10 @@ using qm::Elem;
 constexpr int kBlock = 256;
 constexpr int kWaves = kBlock / 64;
 constexpr int kMostPairs = 128;
-constexpr int64_t kFill = 4096;  // waves that keep the memory busy
+constexpr int64_t kFill = 16384;  // waves that keep the memory busy (4096: 29.2 us for 27.3 in the case below)
+// Outputs beyond this are stored past the caches, which do not hold them until they
+// are read.
+constexpr int64_t kPastCaches = 8 << 20;
 
 struct Turn {
   float cos, sin;
@@ -69,7 +72,7 @@ __device__ __forceinline__ void load(const char* p, float* f) {
     f[0] = Elem<DT>::load(p, 0);
   }
 }
-template <int DT, int N>
+template <int DT, int N, bool PAST>
 __device__ __forceinline__ void store(char* p, const float* f) {
   constexpr int B = Elem<DT>::kBytes;
   if constexpr (N == 1) {
@@ -91,8 +94,13 @@ __device__ __forceinline__ void store(char* p, const float* f) {
       *reinterpret_cast<kv::Raw8<B>*>(p) = kv::Raw8<B>{{w[0], w[1]}};
     } else {
 #pragma unroll
-      for (int i = 0; i < W / 4; ++i)
-        *reinterpret_cast<kv::Raw16<B>*>(p + 16 * i) = kv::Raw16<B>{{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]}};
+      for (int i = 0; i < W / 4; ++i) {
+        const kv::Loose16 v = {w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+        if constexpr (PAST)
+          __builtin_nontemporal_store(v, reinterpret_cast<kv::Loose16*>(p + 16 * i));
+        else
+          *reinterpret_cast<kv::Loose16*>(p + 16 * i) = v;
+      }
     }
   }
 }
@@ -127,11 +135,14 @@ __device__ __forceinline__ float head_sum(float v) {
 // elements r / 2 apart, or one of 2 P (pairs side by side, and the elements past
 // r).  P is 8 where r is a multiple of 16, so that a 16-bit piece is 16 bytes; 4 where it
 // is one of 8; else 1, and a lane takes U pairs, L apart.
-template <int DT, int P, int L, int U, bool SIDE>
+//
+// Bound by memory: 7690 rows of 32 + 8 heads of 128, bf16, 27 us (5.8 TB/s; 37 with
+// plain stores, 28.6 with two groups in flight per wave); r = 64 side by side 33 us;
+// one row 3.0 us, 64 rows 3.3.
+template <int DT, int P, int L, int U, bool SIDE, bool PAST>
 __global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int parts, int groups) {
   constexpr int B = Elem<DT>::kBytes;
   constexpr int kHeads = 64 / L;  // of a group
-  constexpr int G = P == 1 ? 1 : 2;  // groups whose loads are in flight together
   __shared__ Turn all_turns[kWaves][kMostPairs];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned item = blockIdx.x * kWaves + wave;
@@ -187,60 +198,53 @@ __global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int p
         }
       }
     }
-    for (int base = first; base < end; base += G) {
-      float x[G][U][2 * P];
+    for (int group = first; group < end; ++group) {
+      const int h = group * kHeads + lane / L;
+      const char* const from = from_row + h * a.dim * B;
+      float x[U][2 * P];
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int h = (base + g) * kHeads + lane / L;
-        const char* const from = from_row + h * a.dim * B;
+      for (int u = 0; u < U; ++u) {
+        const int i = (within + u * L) * P;  // the first pair
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = (within + u * L) * P;  // the first pair
-#pragma unroll
-          for (int e = 0; e < 2 * P; ++e) x[g][u][e] = 0.0f;
-          if (base + g >= end || h >= heads || i >= pairs) continue;
-          const bool apart = !SIDE && i < half;
-          load<DT, P>(from + (apart ? i : 2 * i) * B, x[g][u]);
-          load<DT, P>(from + (apart ? half + i : 2 * i + P) * B, x[g][u] + P);
-        }
+        for (int e = 0; e < 2 * P; ++e) x[u][e] = 0.0f;
+        if (h >= heads || i >= pairs) continue;
+        const bool apart = !SIDE && i < half;
+        load<DT, P>(from + (apart ? i : 2 * i) * B, x[u]);
+        load<DT, P>(from + (apart ? half + i : 2 * i + P) * B, x[u] + P);
       }
       prepare();
       if (!mine) return;
+      if (weight) {
+        float sum = 0.0f;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int h = (base + g) * kHeads + lane / L;
-        if (weight) {
-          float sum = 0.0f;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int u = 0; u < U; ++u)
+          for (int e = 0; e < 2 * P; ++e) sum = __builtin_fmaf(x[u][e], x[u][e], sum);
+        sum = head_sum<L>(sum);
+        const float inv = 1.0f / __builtin_sqrtf(sum / static_cast<float>(a.dim) + a.eps);
 #pragma unroll
-            for (int e = 0; e < 2 * P; ++e) sum = __builtin_fmaf(x[g][u][e], x[g][u][e], sum);
-          sum = head_sum<L>(sum);
-          const float inv = 1.0f / __builtin_sqrtf(sum / static_cast<float>(a.dim) + a.eps);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int u = 0; u < U; ++u)
+          for (int e = 0; e < 2 * P; ++e) x[u][e] = (x[u][e] * inv) * w[u][e];
+      }
+      char* const to = to_row + h * a.dim * B;
 #pragma unroll
-            for (int e = 0; e < 2 * P; ++e) x[g][u][e] = (x[g][u][e] * inv) * w[u][e];
-        }
-        char* const to = to_row + h * a.dim * B;
+      for (int u = 0; u < U; ++u) {
+        const int i = (within + u * L) * P;
+        if (h >= heads || i >= pairs) continue;
+        const bool apart = !SIDE && i < half;
+        if (i < half) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = (within + u * L) * P;
-          if (base + g >= end || h >= heads || i >= pairs) continue;
-          const bool apart = !SIDE && i < half;
-          if (i < half) {
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-              const Turn t = turns[i + p];
-              const int ia = SIDE ? 2 * p : p, ib = SIDE ? 2 * p + 1 : P + p;
-              const float ya = x[g][u][ia], yb = x[g][u][ib];
-              x[g][u][ia] = __builtin_fmaf(ya, t.cos, -(yb * t.sin));
-              x[g][u][ib] = __builtin_fmaf(yb, t.cos, ya * t.sin);
-            }
+          for (int p = 0; p < P; ++p) {
+            const Turn t = turns[i + p];
+            const int ia = SIDE ? 2 * p : p, ib = SIDE ? 2 * p + 1 : P + p;
+            const float ya = x[u][ia], yb = x[u][ib];
+            x[u][ia] = __builtin_fmaf(ya, t.cos, -(yb * t.sin));
+            x[u][ib] = __builtin_fmaf(yb, t.cos, ya * t.sin);
           }
-          store<DT, P>(to + (apart ? i : 2 * i) * B, x[g][u]);
-          store<DT, P>(to + (apart ? half + i : 2 * i + P) * B, x[g][u] + P);
         }
+        store<DT, P, PAST>(to + (apart ? i : 2 * i) * B, x[u]);
+        store<DT, P, PAST>(to + (apart ? half + i : 2 * i + P) * B, x[u] + P);
       }
     }
   };
@@ -258,8 +262,14 @@ hipError_t go(const NormRopeArgs& a, hipStream_t stream) {
   const int64_t blocks = (static_cast<int64_t>(a.tokens) * parts + kWaves - 1) / kWaves;
   if (!grid_fits(blocks, kBlock)) return hipErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kBlock);
-  return a.interleaved ? launch(norm_rope_kernel<DT, P, L, U, true>, grid, block, 0, stream, a, parts, each)
-                       : launch(norm_rope_kernel<DT, P, L, U, false>, grid, block, 0, stream, a, parts, each);
+  if constexpr (P == 8) {
+    const int64_t bytes = static_cast<int64_t>(a.tokens) * (a.heads + a.kv_heads) * a.dim * Elem<DT>::kBytes;
+    if (bytes > kPastCaches)
+      return a.interleaved ? launch(norm_rope_kernel<DT, P, L, U, true, true>, grid, block, 0, stream, a, parts, each)
+                           : launch(norm_rope_kernel<DT, P, L, U, false, true>, grid, block, 0, stream, a, parts, each);
+  }
+  return a.interleaved ? launch(norm_rope_kernel<DT, P, L, U, true, false>, grid, block, 0, stream, a, parts, each)
+                       : launch(norm_rope_kernel<DT, P, L, U, false, false>, grid, block, 0, stream, a, parts, each);
 }
 
 template <int DT>
