@@ -92,7 +92,8 @@ struct Tile {
   int lo, hi;           // positions that some column sees: [lo, hi)
   int splits;
   // With sinks a tile's chunks are laid over the sinks, up to `turn`, and what
-  // lies from lo on, with the `gap` between them left out (multiples of 64).
+  // lies from lo on, with the `gap` between them left out.  Both are multiples of 16,
+  // the positions that a step takes as one piece: 4 sinks then cost 16 positions.
   int turn, gap;
 };
 
@@ -115,7 +116,7 @@ __device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0
   t.hi = min(last_pos + 1, t.len);
   t.lo = first_seen(p, first_pos);
   if constexpr (SINKS) {
-    const int base = t.lo & ~(kGroup - 1), after = (max(min(p.a.sinks, t.hi), 0) + kGroup - 1) & ~(kGroup - 1);
+    const int base = t.lo & ~15, after = (max(min(p.a.sinks, t.hi), 0) + 15) & ~15;
     t.turn = after;
     t.gap = max(base - after, 0);
     t.splits = t.hi > 0 ? (t.hi - t.gap + p.chunk - 1) / p.chunk : 0;
@@ -125,8 +126,8 @@ __device__ __forceinline__ void set_range(const Params& p, Tile& t, int64_t col0
   t.live = true;
 }
 
-// Where a chunk of a tile begins and ends, in the order in which its positions
-// are taken, and the position there.
+// Where a tile's positions begin and end, in the order in which they are taken, and
+// the position at a multiple of 16 of that order.
 template <bool SINKS>
 __device__ __forceinline__ int range_begin(const Tile& t) { return SINKS ? 0 : t.lo & ~(kGroup - 1); }
 template <bool SINKS>
@@ -134,12 +135,36 @@ __device__ __forceinline__ int range_end(const Tile& t) { return SINKS ? t.hi - 
 template <bool SINKS>
 __device__ __forceinline__ int position_of(const Tile& t, int v) { return SINKS && v >= t.turn ? v + t.gap : v; }
 
-// Whether a column that sees [lo, hi) sees position j, and whether it sees none
-// of the 16 from `at` on.
+// The same for a lane's piece of the group of 64 at v, k = 0, 16, 32 or 48 past it: in
+// all groups but the one that the sinks end in, the shift is the group's.
 template <bool SINKS>
-__device__ __forceinline__ bool sees(const Params& p, int lo, int hi, int j) {
-  return (j >= lo || (SINKS && j < p.a.sinks)) && j < hi;
+__device__ __forceinline__ int piece_position(const Tile& t, int v, int k) {
+  int at = position_of<SINKS>(t, v) + k;
+  if constexpr (SINKS) {
+    if (v < t.turn && v + 48 >= t.turn) [[unlikely]] at += v + k >= t.turn ? t.gap : 0;
+  }
+  return at;
 }
+
+// Which of the N positions from `at` on a column that sees [lo, hi), and with sinks
+// what lies before it of those, sees: a bit for each, or the two ends.  (With bits,
+// sinks cost a step some ten instructions; tested position by position, two for each.)
+template <int N, bool SINKS>
+struct Seen {
+  int at, lo, hi;
+  uint32_t bits;
+  __device__ __forceinline__ Seen(const Params& p, int at, int lo, int hi) : at(at), lo(lo), hi(hi), bits(0) {
+    if constexpr (SINKS) {
+      auto below = [&](int end) { return (1u << min(max(end - at, 0), N)) - 1u; };
+      bits = below(hi) & (~below(lo) | below(p.a.sinks));
+    }
+  }
+  __device__ __forceinline__ bool operator[](int i) const {
+    if constexpr (SINKS) return bits & (1u << i);
+    return at + i >= lo && at + i < hi;
+  }
+};
+// Whether it sees none of the 16 from `at` on.
 template <bool SINKS>
 __device__ __forceinline__ bool sees_none16(const Params& p, int lo, int hi, int at) {
   return (at + 16 <= lo && !(SINKS && at < p.a.sinks)) || at >= hi;
@@ -514,13 +539,14 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
   constexpr int kSets = DP > 128 ? 1 : 2;
   uint4 kr[kSets][4][KC], vr[kSets][VC];
   float ks[kSets], vs[kSets];
+  auto pos_of = [&](int v) { return position_of<SINKS>(t, v); };
   // The blocks of the next group's four pieces of 16 positions.
   int nb0 = 0, nb1 = 0, nb2 = 0, nb3 = 0;
-  auto next_blocks = [&](int t0) {
-    nb0 = entry(t0);
-    nb1 = entry(t0 + 16);
-    nb2 = entry(t0 + 32);
-    nb3 = entry(t0 + 48);
+  auto next_blocks = [&](int v) {
+    nb0 = entry(pos_of(v));
+    nb1 = entry(pos_of(v + 16));
+    nb2 = entry(pos_of(v + 32));
+    nb3 = entry(pos_of(v + 48));
   };
   auto pick = [&](int j) {
     const int lo = j & 1 ? nb1 : nb0, hi = j & 1 ? nb3 : nb2;
@@ -532,11 +558,11 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
   int kpart[KC];
 #pragma unroll
   for (int c = 0; c < KC; ++c) kpart[c] = 64 * c + 16 * g < dim ? 64 * c + 16 * g : 0;
-  // K: the lane's row n of tile i is position t0 + 16 (n / 4) + 4 i + n % 4
-  auto load_k = [&](int t0, auto half) {
+  // K: the lane's row n of tile i is n % 4 + 4 i past the position of piece n / 4
+  auto load_k = [&](int v, auto half) {
     constexpr int S = decltype(half)::value % kSets;
     const uint8_t* const row =
-        p.c.k + tile_of(pick(n >> 2)) * head_bytes + (((t0 + 16 * (n >> 2)) & (P - 1)) + (n & 3)) * dim;
+        p.c.k + tile_of(pick(n >> 2)) * head_bytes + ((piece_position<SINKS>(t, v, 16 * (n >> 2)) & (P - 1)) + (n & 3)) * dim;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -549,15 +575,14 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
     vs[S] = p.c.v_scale[tile_of(b)];
     if (!in_pool(b)) ks[S] = vs[S] = __builtin_nanf("");
   };
-  auto load_v = [&](int t0, auto half) {
+  auto load_v = [&](int v, auto half) {
     constexpr int S = decltype(half)::value % kSets;
-    const uint8_t* const row = p.c.v + tile_of(pick(g)) * head_bytes + n * P + ((t0 + 16 * g) & (P - 1));
+    const uint8_t* const row = p.c.v + tile_of(pick(g)) * head_bytes + n * P + (piece_position<SINKS>(t, v, 16 * g) & (P - 1));
 #pragma unroll
     for (int i = 0; i < VC; ++i) vr[S][i] = *reinterpret_cast<const uint4*>(row + (16 * i < dim ? 16 * i : 0) * P);
   };
 
   constexpr int kStep = kWaves * kGroup;
-  auto pos_of = [&](int v) { return position_of<SINKS>(t, v); };
   // the group at v, whose K and V are in registers or on their way; `more`:
   // ask for the next group's
   auto group = [&](int v, auto half, auto more) {
@@ -566,9 +591,9 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
     const int t0 = pos_of(v);
     if (kSets == 2 && more) {
       load_scales(other);
-      load_k(pos_of(v + kStep), other);
-      load_v(pos_of(v + kStep), other);
-      next_blocks(pos_of(v + 2 * kStep));
+      load_k(v + kStep, other);
+      load_v(v + kStep, other);
+      next_blocks(v + 2 * kStep);
     }
     float4_t acc[4];
 #pragma unroll
@@ -580,23 +605,23 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
         acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kv::codes8_to_half<FP8>(kr[S][i][c].z, kr[S][i][c].w), qf[2 * c + 1], acc[i], 0, 0, 0);
       }
     }
-    if (kSets == 1 && more) load_k(pos_of(v + kStep), other);
+    if (kSets == 1 && more) load_k(v + kStep, other);
     float s[1][16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[0][i] = acc[i >> 2][i & 3];
     float c[1] = {c_col * ks[S]}, bias[1] = {__builtin_amdgcn_logf(vs[S])}, inv_vs[1] = {__builtin_amdgcn_rcpf(vs[S])};
     const bool odd = __any(!plain_scales(ks[S], vs[S]));
     if (t0 < t.lo || t0 + kGroup > t.len - t.rows || p.a.window > 0 || odd) {  // some column may not see all 64
-      const int at = t0 + 16 * g;
+      const int at = piece_position<SINKS>(t, v, 16 * g);
       if (odd) [[unlikely]] {
         const SplitScale v = split_scale(vs[S]);
         bias[0] = v.log2;
         inv_vs[0] = v.inv;
       }
+      const Seen<16, SINKS> seen(p, at, col.see_lo, col.see_hi);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const bool seen = sees<SINKS>(p, col.see_lo, col.see_hi, at + i);
-        s[0][i] = seen ? __builtin_fmaf(s[0][i], c[0], bias[0]) : -__builtin_inff();
+        s[0][i] = seen[i] ? __builtin_fmaf(s[0][i], c[0], bias[0]) : -__builtin_inff();
       }
       c[0] = 1.0f;
       bias[0] = 0.0f;
@@ -617,8 +642,9 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) pf[i >> 3][i & 7] = static_cast<_Float16>(static_cast<float>(pf[i >> 3][i & 7]) * rest);
     }
-    if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) {
-      const int have = t0 + 16 * g + 16 > t.lo || (SINKS && t0 + 16 * g < p.a.sinks) ? t.len - (t0 + 16 * g) : 0;
+    // (with sinks every piece has a position that some column sees, or ends the sequence)
+    if (FP8 && (SINKS ? pos_of(v + 48) + 16 > t.len : t0 + kGroup > t.len || t0 < t.lo)) {
+      const int at = piece_position<SINKS>(t, v, 16 * g), have = SINKS || at + 16 > t.lo ? t.len - at : 0;
 #pragma unroll
       for (int i = 0; i < VC; ++i) keep_first(vr[S][i], have);
     }
@@ -629,19 +655,19 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
     }
     if (kSets == 1 && more) {
       load_scales(other);
-      load_v(pos_of(v + kStep), other);
-      next_blocks(pos_of(v + 2 * kStep));
+      load_v(v + kStep, other);
+      next_blocks(v + 2 * kStep);
     }
   };
   constexpr std::integral_constant<int, 0> even{};
   constexpr std::integral_constant<int, 1> odd{};
   int t0 = begin + wave * kGroup;
   if (t0 < end) {
-    next_blocks(pos_of(t0));
+    next_blocks(t0);
     load_scales(even);
-    load_k(pos_of(t0), even);
-    load_v(pos_of(t0), even);
-    next_blocks(pos_of(t0 + kStep));
+    load_k(t0, even);
+    load_v(t0, even);
+    next_blocks(t0 + kStep);
     if constexpr (kSets == 1) {
       for (; t0 < end; t0 += kStep) group(t0, even, t0 + kStep < end);
     } else {
@@ -796,12 +822,12 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   float sk[kSets], sv[kSets];
   int next_block = 0;  // of this wave's 16 positions of the step to load
   auto pos_of = [&](int v) { return position_of<SINKS>(t, v); };
-  auto load_block = [&](int v) { next_block = entry(pos_of(v) + 16 * wave); };
+  auto load_block = [&](int v) { next_block = entry(pos_of(v + 16 * wave)); };
   auto load_step = [&](int v, auto half) {
-    const int S = half % kSets, t0 = pos_of(v);
+    const int S = half % kSets;
     const bool ok = in_pool(next_block);
     const int64_t tile = static_cast<int64_t>(ok ? next_block : 0) * p.c.heads + head;
-    const int pos = (t0 + 16 * wave) & (P - 1);
+    const int pos = pos_of(v + 16 * wave) & (P - 1);
     const uint8_t* const from_k = p.c.k + tile * head_bytes + pos * dim;
     const uint8_t* const from_v = p.c.v + tile * head_bytes + pos;
 #pragma unroll
@@ -816,11 +842,11 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   };
   // the step at v into half H of LDS
   auto put_step = [&](int v, auto half) {
-    const int H = half, S = H % kSets, t0 = pos_of(v);
+    const int H = half, S = H % kSets, at = pos_of(v + 16 * wave);
     half8_t* const kl = reinterpret_cast<half8_t*>(lds_k[H]);
     half8_t* const vl = reinterpret_cast<half8_t*>(lds_v[H]);
-    if (FP8 && (t0 + kGroup > t.len || t0 < t.lo)) {
-      const int have = t0 + 16 * wave + 16 > t.lo || (SINKS && t0 + 16 * wave < p.a.sinks) ? t.len - (t0 + 16 * wave) : 0;
+    if (FP8 && (SINKS ? at + 16 > t.len : v + kGroup > t.len || v < t.lo)) {
+      const int have = SINKS || at + 16 > t.lo ? t.len - at : 0;
 #pragma unroll
       for (int i = 0; i < NC; ++i) keep_first(vr[S][i], have);
     }
@@ -860,8 +886,8 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   };
   // the step at v, in half H of LDS
   auto work = [&](int v, auto half) {
-    const int H = half, t0 = pos_of(v);
-    if (t0 >= any_hi || (t0 + kGroup <= any_lo && !(SINKS && t0 < p.a.sinks))) return;
+    const int H = half, t0 = pos_of(v), stop0 = SINKS ? pos_of(v + 48) + 16 : v + kGroup;
+    if (t0 >= any_hi || (stop0 <= any_lo && !(SINKS && t0 < p.a.sinks))) return;
     const half8_t* const kl = reinterpret_cast<const half8_t*>(lds_k[H]);
     const half8_t* const vl = reinterpret_cast<const half8_t*>(lds_v[H]);
     float16_t acc[2];
@@ -884,14 +910,14 @@ __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[b][e] = acc[b >> 1][8 * (b & 1) + e];
     }
-    if (t0 + kGroup > all_hi || (t0 < all_lo && !(SINKS && t0 + kGroup <= p.a.sinks))) {
+    if (stop0 > all_hi || t0 < all_lo) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int first = t0 + 16 * b;
+        const int first = pos_of(v + 16 * b);
+        const Seen<8, SINKS> seen(p, first + 8 * h, col.see_lo, col.see_hi);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int spot = first + 8 * h + e;
-          s[b][e] = sees<SINKS>(p, col.see_lo, col.see_hi, spot) ? __builtin_fmaf(s[b][e], c[b], bias[b]) : -__builtin_inff();
+          s[b][e] = seen[e] ? __builtin_fmaf(s[b][e], c[b], bias[b]) : -__builtin_inff();
         }
         c[b] = 1.0f;
         bias[b] = 0.0f;
@@ -1124,11 +1150,11 @@ Mask mask_of(int max_kv, int window, int sinks) {
 }
 
 // The positions that one tile can see, from a multiple of 64 on: the window's
-// and, rounded up to whole groups of 64 on either side of the gap, the sinks.
+// and, in whole pieces of 16 on either side of the gap, the sinks.
 int64_t range_of(int max_kv, Mask mask, int rows) {
   int64_t range = max_kv;
   if (mask.window > 0) {
-    const int64_t first = mask.sinks > 0 ? (static_cast<int64_t>(mask.sinks) + 2 * kGroup - 1) / kGroup * kGroup : 0;
+    const int64_t first = mask.sinks > 0 ? (static_cast<int64_t>(mask.sinks) + 31) / 16 * 16 : 0;
     range = std::min<int64_t>(range, first + mask.window + rows);
   }
   return (range + 2 * kGroup - 1) / kGroup * kGroup;
