@@ -12,8 +12,9 @@ template <int ALIGN>
 struct __attribute__((packed, aligned(ALIGN))) Raw16 {
   uint32_t w[4];
 };
-// (and as a vector, for accesses past the caches)
+// (and as vectors, for accesses past the caches)
 typedef uint32_t Loose16 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t Loose8 __attribute__((ext_vector_type(2), aligned(2)));
 template <int ALIGN>
 struct __attribute__((packed, aligned(ALIGN))) Raw8 {
   uint32_t w[2];

@@ -91,7 +91,11 @@ __device__ __forceinline__ void store(char* p, const float* f) {
         w[i] = qm::pack2_narrow<DT>(f[2 * i], f[2 * i + 1]);
     }
     if constexpr (W == 2) {
-      *reinterpret_cast<kv::Raw8<B>*>(p) = kv::Raw8<B>{{w[0], w[1]}};
+      const kv::Loose8 v = {w[0], w[1]};
+      if constexpr (PAST)
+        __builtin_nontemporal_store(v, reinterpret_cast<kv::Loose8*>(p));
+      else
+        *reinterpret_cast<kv::Loose8*>(p) = v;
     } else {
 #pragma unroll
       for (int i = 0; i < W / 4; ++i) {
@@ -131,10 +135,11 @@ __device__ __forceinline__ float head_sum(float v) {
 
 // A wave has a row's position, the sines and cosines of its pairs (a pair or two
 // per lane, handed round through LDS of its own) and `groups` of its heads, 64 / L
-// of them at a time: L lanes to a head, P pairs to a lane, that is two pieces of P
-// elements r / 2 apart, or one of 2 P (pairs side by side, and the elements past
-// r).  P is 8 where r is a multiple of 16, so that a 16-bit piece is 16 bytes; 4 where it
-// is one of 8; else 1, and a lane takes U pairs, L apart.
+// of them at a time: L lanes to a head, P pairs to a lane.  Those are one piece of
+// 2 P elements where pairs lie side by side, else two pieces of P, r / 2 apart, or,
+// past r, half of what is left apart.  A piece is 16 bytes, next to its neighbour's, where r
+// allows it (32 bytes per lane in two halves took up to twice as long); where r is no
+// multiple of 8 (4 for binary32 side by side) P is 1, and a lane takes U pairs, L apart.
 //
 // Bound by memory: 7690 rows of 32 + 8 heads of 128, bf16, 27 us (5.8 TB/s; 37 with
 // plain stores, 28.6 with two groups in flight per wave); r = 64 side by side 33 us;
@@ -151,6 +156,9 @@ __global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int p
   const int row = static_cast<int>(of_row), part = static_cast<int>(item - of_row * parts);
   Turn* const turns = all_turns[wave];
   const int within = lane % L, pairs = a.dim / 2, half = a.rotary / 2;
+  // elements of the P pairs from pair i on
+  auto first_of = [&](int i) { return SIDE ? 2 * i : i < half ? i : half + i; };
+  auto second_of = [&](int i) { return SIDE ? 2 * i + P : i < half ? half + i : pairs + i; };
   const int q_groups = (a.heads + kHeads - 1) / kHeads, last = q_groups + (a.kv_heads + kHeads - 1) / kHeads;
   const int g0 = part * groups, g1 = min(g0 + groups, last);
 
@@ -186,15 +194,19 @@ __global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int p
       for (int u = 0; u < U; ++u) {
         const int i = (within + u * L) * P;
         if (i >= pairs) continue;
-        const bool apart = !SIDE && i < half;
-        const int at = apart ? i : 2 * i, other = apart ? half + i : 2 * i + P;
+        const int at = first_of(i), other = second_of(i);
         if (a.weight_f32) {
           const float* const f = static_cast<const float*>(weight);
 #pragma unroll
           for (int e = 0; e < P; ++e) w[u][e] = f[at + e], w[u][P + e] = f[other + e];
         } else {
-          load<DT, P>(static_cast<const char*>(weight) + at * B, w[u]);
-          load<DT, P>(static_cast<const char*>(weight) + other * B, w[u] + P);
+          const char* const f = static_cast<const char*>(weight);
+          if constexpr (SIDE && P > 1) {
+            load<DT, 2 * P>(f + at * B, w[u]);
+          } else {
+            load<DT, P>(f + at * B, w[u]);
+            load<DT, P>(f + other * B, w[u] + P);
+          }
         }
       }
     }
@@ -208,9 +220,12 @@ __global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int p
 #pragma unroll
         for (int e = 0; e < 2 * P; ++e) x[u][e] = 0.0f;
         if (h >= heads || i >= pairs) continue;
-        const bool apart = !SIDE && i < half;
-        load<DT, P>(from + (apart ? i : 2 * i) * B, x[u]);
-        load<DT, P>(from + (apart ? half + i : 2 * i + P) * B, x[u] + P);
+        if constexpr (SIDE && P > 1) {
+          load<DT, 2 * P>(from + first_of(i) * B, x[u]);
+        } else {
+          load<DT, P>(from + first_of(i) * B, x[u]);
+          load<DT, P>(from + second_of(i) * B, x[u] + P);
+        }
       }
       prepare();
       if (!mine) return;
@@ -232,7 +247,6 @@ __global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int p
       for (int u = 0; u < U; ++u) {
         const int i = (within + u * L) * P;
         if (h >= heads || i >= pairs) continue;
-        const bool apart = !SIDE && i < half;
         if (i < half) {
 #pragma unroll
           for (int p = 0; p < P; ++p) {
@@ -243,8 +257,12 @@ __global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int p
             x[u][ib] = __builtin_fmaf(yb, t.cos, ya * t.sin);
           }
         }
-        store<DT, P, PAST>(to + (apart ? i : 2 * i) * B, x[u]);
-        store<DT, P, PAST>(to + (apart ? half + i : 2 * i + P) * B, x[u] + P);
+        if constexpr (SIDE && P > 1) {
+          store<DT, 2 * P, PAST>(to + first_of(i) * B, x[u]);
+        } else {
+          store<DT, P, PAST>(to + first_of(i) * B, x[u]);
+          store<DT, P, PAST>(to + second_of(i) * B, x[u] + P);
+        }
       }
     }
   };
@@ -252,7 +270,7 @@ __global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int p
   side(max(g0, q_groups) - q_groups, g1 - q_groups, a.k, a.ldk, a.kv_heads, a.k_weight, a.k_out, a.ldko);
 }
 
-template <int DT, int P, int L, int U>
+template <int DT, int P, int L, int U, bool SIDE>
 hipError_t go(const NormRopeArgs& a, hipStream_t stream) {
   constexpr int kHeads = 64 / L;
   const int groups = (a.heads + kHeads - 1) / kHeads + (a.kv_heads + kHeads - 1) / kHeads;
@@ -262,29 +280,32 @@ hipError_t go(const NormRopeArgs& a, hipStream_t stream) {
   const int64_t blocks = (static_cast<int64_t>(a.tokens) * parts + kWaves - 1) / kWaves;
   if (!grid_fits(blocks, kBlock)) return hipErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kBlock);
-  if constexpr (P == 8) {
+  if constexpr (P > 1) {
     const int64_t bytes = static_cast<int64_t>(a.tokens) * (a.heads + a.kv_heads) * a.dim * Elem<DT>::kBytes;
-    if (bytes > kPastCaches)
-      return a.interleaved ? launch(norm_rope_kernel<DT, P, L, U, true, true>, grid, block, 0, stream, a, parts, each)
-                           : launch(norm_rope_kernel<DT, P, L, U, false, true>, grid, block, 0, stream, a, parts, each);
+    if (bytes > kPastCaches) return launch(norm_rope_kernel<DT, P, L, U, SIDE, true>, grid, block, 0, stream, a, parts, each);
   }
-  return a.interleaved ? launch(norm_rope_kernel<DT, P, L, U, true, false>, grid, block, 0, stream, a, parts, each)
-                       : launch(norm_rope_kernel<DT, P, L, U, false, false>, grid, block, 0, stream, a, parts, each);
+  return launch(norm_rope_kernel<DT, P, L, U, SIDE, false>, grid, block, 0, stream, a, parts, each);
+}
+
+template <int DT, int P, bool SIDE>
+hipError_t by_dim(const NormRopeArgs& a, hipStream_t stream) {
+  if (a.dim <= 64) return go<DT, P, 32 / P, 1, SIDE>(a, stream);
+  if (a.dim <= 128) return go<DT, P, 64 / P, 1, SIDE>(a, stream);
+  return go<DT, P, 128 / P, 1, SIDE>(a, stream);
 }
 
 template <int DT>
 hipError_t by_size(const NormRopeArgs& a, hipStream_t stream) {
-  if (a.rotary % 16 == 0) {
-    if (a.dim <= 64) return go<DT, 8, 4, 1>(a, stream);
-    if (a.dim <= 128) return go<DT, 8, 8, 1>(a, stream);
-    return go<DT, 8, 16, 1>(a, stream);
+  constexpr int kSide = Elem<DT>::kPerUnit / 2;  // pairs in 16 bytes
+  if (a.interleaved) {
+    if (a.rotary % (2 * kSide) == 0) return by_dim<DT, kSide, true>(a, stream);
+    return go<DT, 1, 64, 2, true>(a, stream);
   }
-  if (a.rotary % 8 == 0) {
-    if (a.dim <= 64) return go<DT, 4, 8, 1>(a, stream);
-    if (a.dim <= 128) return go<DT, 4, 16, 1>(a, stream);
-    return go<DT, 4, 32, 1>(a, stream);
+  if constexpr (DT != QK_F32) {
+    if (a.rotary % 16 == 0) return by_dim<DT, 8, false>(a, stream);
   }
-  return go<DT, 1, 64, 2>(a, stream);
+  if (a.rotary % 8 == 0) return by_dim<DT, 4, false>(a, stream);
+  return go<DT, 1, 64, 2, false>(a, stream);
 }
 
 }  // namespace
