@@ -1,12 +1,15 @@
 """A decoder layer in 8 bits, over a paged 8-bit cache: prompts, then tokens.
 
-    norm + quantization -> QKV GEMM -> cache write -> attention -> quantization
-    -> output GEMM -> residual + norm + quantization -> gate/up GEMM
-    -> silu(gate) * up + quantization -> down GEMM
+    norm + quantization -> QKV GEMM -> (norm of heads + rotation) -> cache write
+    -> attention -> quantization -> output GEMM -> residual + norm + quantization
+    -> gate/up GEMM -> silu(gate) * up + quantization -> down GEMM
 
 Every step is a call of the framework; between two of them activations are
-either 8-bit codes with per-token scales or bf16.  Positional encoding is left
-out.  `python -m examples.decoder_layer` runs prompts of mixed lengths through
+either 8-bit codes with per-token scales, microscaled 4-bit codes, or bf16.
+With `mx4` the output and down projections, whose inputs are not a norm's, are
+held and multiplied in 4 bits; `rope` norms and rotates queries and keys;
+`window` and `sinks` bound what a row sees.
+`python -m examples.decoder_layer` runs prompts of mixed lengths through
 a few layers, then single tokens replayed from a HIP graph, and prints times.
 """
 from __future__ import annotations
@@ -30,6 +33,10 @@ class Shape:
     block: int = 64
     fp8: bool = False       # both the linears' codes and the cache
     eps: float = 1e-6
+    mx4: bool = False       # the output and down projections in microscaled 4 bits
+    rope: float = 0.0       # the rotation's base; 0: neither norm of heads nor rotation
+    window: int = 0         # positions that a row sees; 0: all before it
+    sinks: int = 0          # and first ones that stay visible beside the window
 
 
 class Linear:
@@ -48,6 +55,16 @@ class Linear:
         if q.dtype == torch.float8_e4m3fn:
             return qk.gemm_fp8_scaled(q, self.w, s, self.s)
         return qk.gemm_i8_scaled(q, self.w, s, self.s, workspace=workspace)
+
+
+class Linear4:
+    """A weight of k inputs and n outputs in microscaled 4 bits, random."""
+
+    def __init__(self, k, n, gen, device):
+        self.w, self.s = qk.quant_mx4(torch.randn((n, k), generator=gen, device=device) * k ** -0.5)
+
+    def __call__(self, q, s, workspace=None):
+        return qk.gemm_mx4_scaled(q, self.w, s, self.s)
 
 
 @dataclass
@@ -70,9 +87,12 @@ class Layer:
         self.norm2 = torch.ones(c.hidden, dtype=torch.bfloat16, device=device)
         wide = (c.heads + 2 * c.kv_heads) * c.dim
         self.qkv = Linear(c.hidden, wide, c.fp8, gen, device)
-        self.o = Linear(c.heads * c.dim, c.hidden, c.fp8, gen, device)
+        self.o = Linear4(c.heads * c.dim, c.hidden, gen, device) if c.mx4 else Linear(c.heads * c.dim, c.hidden, c.fp8, gen, device)
         self.gate_up = Linear(c.hidden, 2 * c.inner, c.fp8, gen, device)
-        self.down = Linear(c.inner, c.hidden, c.fp8, gen, device)
+        self.down = Linear4(c.inner, c.hidden, gen, device) if c.mx4 else Linear(c.inner, c.hidden, c.fp8, gen, device)
+        if c.rope:
+            self.q_norm, self.k_norm = (torch.ones(c.dim, dtype=torch.bfloat16, device=device) for _ in range(2))
+            self.freqs = c.rope ** (-torch.arange(0, c.dim, 2, dtype=torch.float64, device=device) / c.dim)
         self.cache = qk.new_kv_cache(blocks, c.kv_heads, c.dim, c.block, c.fp8, device)
 
     def __call__(self, x, residual, step: Step):
@@ -87,10 +107,14 @@ class Layer:
         ws = step.linear_workspace
         rows = self.qkv(q, s, ws).view(n, c.heads + 2 * c.kv_heads, c.dim)
         query, key, value = rows.split([c.heads, c.kv_heads, c.kv_heads], 1)
+        cu = step.cu if step.max_q > 1 else None
+        if c.rope:
+            query, key = qk.norm_rope(query, key, step.start, self.freqs, cu, self.q_norm, self.k_norm, c.eps)
         qk.kv_cache_write(self.cache, key, value, step.table, step.start, step.cu)
-        a = qk.kv_attention(query, self.cache, step.table, step.lens, step.cu if step.max_q > 1 else None,
-                            max_q=step.max_q, max_kv=step.max_kv, workspace=step.attention_workspace)
-        quant, silu = ((qk.quant_per_token_fp8, qk.silu_mul_quant_per_token_fp8) if c.fp8
+        a = qk.kv_attention(query, self.cache, step.table, step.lens, cu, window=c.window, max_q=step.max_q,
+                            max_kv=step.max_kv, workspace=step.attention_workspace, sinks=c.sinks)
+        quant, silu = ((qk.quant_mx4, qk.silu_mul_quant_mx4) if c.mx4
+                       else (qk.quant_per_token_fp8, qk.silu_mul_quant_per_token_fp8) if c.fp8
                        else (qk.quant_per_token, qk.silu_mul_quant_per_token))
         x = self.o(*quant(a.view(n, c.heads * c.dim)), ws)
         q, s, residual = qk.rms_norm_quant(x, self.norm2, c.eps, residual, c.fp8)
@@ -135,8 +159,8 @@ class TokenGraph:
         self.start, self.lens = dec.lens.clone(), dec.lens.clone()
         c, layer = dec.shape, dec.layers[0]
         linear = max(qk.gemm_workspace_size(seqs, m.w.shape[1], m.w.shape[0])
-                     for m in (layer.qkv, layer.o, layer.gate_up, layer.down))
-        attention = qk.kv_attention_workspace_size(seqs, seqs, c.heads, c.kv_heads, c.dim, dec.longest)
+                     for m in (layer.qkv, layer.o, layer.gate_up, layer.down) if isinstance(m, Linear))
+        attention = qk.kv_attention_workspace_size(seqs, seqs, c.heads, c.kv_heads, c.dim, dec.longest, c.window, sinks=c.sinks)
         self.step = Step(dec.table, self.start, self.lens, self.cu, 1, dec.longest,
                          *(qk.new_workspace(n, dec.device) for n in (linear, attention)))
         self.stream = torch.cuda.Stream()
@@ -169,8 +193,12 @@ def main():
     ap.add_argument("--prompts", type=int, nargs="+", default=[37, 2048, 700, 301])
     ap.add_argument("--tokens", type=int, default=64)
     ap.add_argument("--fp8", action="store_true")
+    ap.add_argument("--mx4", action="store_true", help="output and down projections in microscaled 4 bits")
+    ap.add_argument("--rope", type=float, default=0.0, help="base of the rotation of queries and keys, which are normed too (0: neither)")
+    ap.add_argument("--window", type=int, default=0)
+    ap.add_argument("--sinks", type=int, default=0)
     a = ap.parse_args()
-    shape = Shape(fp8=a.fp8)
+    shape = Shape(fp8=a.fp8, mx4=a.mx4, rope=a.rope, window=a.window, sinks=a.sinks)
     dec = Decoder(shape, a.layers, len(a.prompts), max(a.prompts) + a.tokens)
     x = torch.randn((sum(a.prompts), shape.hidden), device="cuda").to(torch.bfloat16)
     empty = dec.lens
