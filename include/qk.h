@@ -531,9 +531,12 @@ int qk_gemm_mx4_scaled(int m, int n, int k, const uint8_t *a, const uint8_t *sca
                        void *out, int out_dtype, hipStream_t stream);
 
 /*
- * The 4-bit layer: qk_quant_mx4 of x into q_out / scale_out (rows lds_out bytes
- * apart), then qk_gemm_mx4_scaled of those with the weight (two launches on
- * `stream`).  Requirements and errors as the two calls.
+ * The 4-bit layer: qk_quant_mx4 of x, then qk_gemm_mx4_scaled of that with the
+ * weight; the result is that of the two calls.  A call of up to 16 rows and a
+ * small weight (n k <= 2^24), with the address of x and its row stride multiples of 16
+ * bytes, is one launch; others are two, with the codes in q_out and scale_out
+ * (rows lds_out bytes apart), which the one launch neither needs nor writes.
+ * Requirements and errors as the two calls.
  */
 int qk_linear_mx4(int m, int n, int k, const void *x, int64_t ldx, int x_dtype, const uint8_t *b,
                   const uint8_t *scale_b, int64_t ldsb, float output_scale, void *out, int out_dtype,

@@ -13,7 +13,7 @@ QUANT = dict(m=4, k=64, x=FAKE, ldx=64, dtype=1, q=FAKE, scale=FAKE, lds=16, str
 BACK = dict(m=4, k=64, q=FAKE, scale=FAKE, lds=16, x=FAKE, ldx=64, dtype=1, stream=NULL)
 GEMM = dict(m=4, n=5, k=64, a=FAKE, scale_a=FAKE, ldsa=16, b=FAKE, scale_b=FAKE, ldsb=16, output_scale=1.0, out=FAKE, out_dtype=1,
             stream=NULL)
-LINEAR = dict(m=4, n=5, k=64, x=FAKE, ldx=64, x_dtype=1, b=FAKE, scale_b=FAKE, ldsb=16, output_scale=1.0, out=FAKE, out_dtype=1, q=FAKE,
+LINEAR = dict(m=40, n=5, k=64, x=FAKE, ldx=64, x_dtype=1, b=FAKE, scale_b=FAKE, ldsb=16, output_scale=1.0, out=FAKE, out_dtype=1, q=FAKE,
               scale=FAKE, lds=16, stream=NULL)
 ROPE = dict(seqs=2, tokens=5, heads=4, kv_heads=2, dim=64, q=FAKE, ldq=512, k=at(512), ldk=512, q_weight=NULL, k_weight=NULL, dtype=1,
             weight_dtype=1, eps=1e-6, freqs=FAKE, rotary=64, interleaved=0, start=FAKE, cu=FAKE, q_out=at(1 << 20), ldqo=256,
@@ -54,7 +54,8 @@ def test_product(kw, status):
     (dict(m=-1), INVALID), (dict(k=40), UNSUP), (dict(x=NULL), INVALID), (dict(b=NULL), INVALID), (dict(out=NULL), INVALID),
     (dict(q=NULL), INVALID), (dict(scale=NULL), INVALID), (dict(lds=8), UNSUP), (dict(ldsb=8), UNSUP), (dict(ldx=60), INVALID),
     (dict(x_dtype=5), INVALID), (dict(out_dtype=5), INVALID), (dict(out=FAKE_ODD), UNSUP), (dict(n=(1 << 24) + 1), UNSUP),
-    (dict(m=0, x=NULL), 0)])
+    (dict(m=0, x=NULL), 0), (dict(m=4, x=at(8), q=NULL), INVALID), (dict(m=4, ldx=68, q=NULL), INVALID), (dict(m=4, x=NULL), INVALID),
+    (dict(m=4, b=NULL), INVALID), (dict(m=4, ldx=60), INVALID), (dict(m=4, x=FAKE_ODD), UNSUP), (dict(m=4, out=FAKE_ODD), UNSUP)])
 def test_linear(kw, status):
     assert call(qk.library().qk_linear_mx4, LINEAR, **kw) == status
 

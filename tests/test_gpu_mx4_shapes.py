@@ -79,3 +79,39 @@ def test_a_run_of_products_on_two_streams():
     torch.cuda.synchronize()
     for got in outs:
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (16, 1001, 2720), (5, 12801, 544), (16, 26001, 1056), (2, 16, 32), (15, 333, 14336),
+                                   (7, 13000, 96), (1, 30000, 160), (17, 500, 512), (3, 4096, 2016)])
+def test_few_rows_of_a_linear_are_the_two_calls(m, n, k, dtype):
+    # rows that are quantised within the product, and the same rows where they cannot be (a row stride or a place
+    # that is no multiple of 16 bytes): the same codes, the same order of sums
+    gen = torch.Generator(device=DEV).manual_seed(m * k + n)
+    x = torch.randn((m, k), generator=gen, device=DEV).to(TORCH[dtype])
+    x[m // 2, k // 2] = 300
+    w, sw = qk.quant_mx4(torch.randn((n, k), generator=gen, device=DEV))
+    q, s = qk.quant_mx4(x)
+    want = qk.gemm_mx4_scaled(q, w, s, sw, 0.5, torch.float32)
+    assert torch.equal(qk.linear_mx4(x, w, sw, 0.5, torch.float32), want)
+    apart = torch.zeros((m, k + 16), dtype=TORCH[dtype], device=DEV)[:, 8:8 + k]
+    odd = torch.zeros((m, k + 17), dtype=TORCH[dtype], device=DEV)[:, 3:3 + k]
+    for t in (apart, odd):
+        t.copy_(x)
+        assert torch.equal(qk.linear_mx4(t, w, sw, 0.5, torch.float32), want)
+    for out in ("bf16", "f16"):
+        assert torch.equal(qk.linear_mx4(x, w, sw, 0.5, TORCH[out]), want.to(TORCH[out]))
+
+
+@pytest.mark.parametrize("k", [32, 96, 2048, 2720])
+def test_special_values_in_few_rows_of_a_linear(k):
+    gen = torch.Generator(device=DEV).manual_seed(k)
+    x = torch.randn((6, k), generator=gen, device=DEV)
+    x[1, k - 1], x[2, 0], x[3] = float("nan"), float("inf"), 0.0
+    x[4] *= 2.0 ** -140
+    w, sw = qk.quant_mx4(torch.randn((77, k), generator=gen, device=DEV))
+    out = qk.linear_mx4(x, w, sw, out_dtype=torch.float32)
+    q, s = qk.quant_mx4(x)
+    want = qk.gemm_mx4_scaled(q, w, s, sw, out_dtype=torch.float32)
+    assert out[1:3].isnan().all() and not out[3].any() and out[[0, 3, 4, 5]].isfinite().all()
+    assert torch.equal(out.nan_to_num(7e20), want.nan_to_num(7e20))

@@ -638,10 +638,14 @@ PyObject* linear_mx4(PyObject* const* a, Py_ssize_t n) {
   const c10::DeviceGuard guard(dev);
   const at::Tensor out = product_out(a[5], integer(a[4]), m, w.rows, dev);
   const int64_t lds = padded(k / 32);
-  const at::Tensor codes = make({m * (k / 2 + lds)}, at::kByte, dev);  // and their scales behind them
-  uint8_t* const q = static_cast<uint8_t*>(codes.data_ptr());
+  // up to 16 aligned rows are quantised within the product of a small weight
+  const int64_t row = ldx * x.element_size();
+  const bool at_once = m <= 16 && k > 0 && w.rows * k <= 1 << 24 && reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0 && (m <= 1 || row % 16 == 0);
+  at::Tensor codes;  // and their scales behind them
+  if (!at_once) codes = make({m * (k / 2 + lds)}, at::kByte, dev);
+  uint8_t* const q = at_once ? nullptr : static_cast<uint8_t*>(codes.data_ptr());
   check(lib.linear4(narrow(m, "rows"), narrow(w.rows, "columns"), narrow(k, "k"), x.data_ptr(), ldx, code, w.q, w.scale, w.lds,
-                    static_cast<float>(number(a[3])), out.data_ptr(), type_code(out.scalar_type()), q, q + m * (k / 2), lds,
+                    static_cast<float>(number(a[3])), out.data_ptr(), type_code(out.scalar_type()), q, at_once ? nullptr : q + m * (k / 2), lds,
                     stream_of(dev)));
   return a[5] != Py_None ? same(a[5]) : wrapped(out);
 }

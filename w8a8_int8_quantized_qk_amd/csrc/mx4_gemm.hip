@@ -13,7 +13,7 @@
 #include <cmath>
 
 #include "gemm_tile.h"
-#include "quant_math.h"
+#include "mx4.h"
 
 namespace qk {
 namespace {
@@ -36,6 +36,9 @@ __device__ __forceinline__ void put(void* out, int64_t at, float v) {
 }
 
 // ---- few rows ----
+
+// Columns from which a workgroup of few rows has 64, or 32, of them: 400 workgroups.
+constexpr int kCols64 = 64 * 400, kCols32 = 32 * 400;
 
 // Bound by the weight's bytes.  A workgroup has 16 R columns (rows of the weight)
 // and 16 F rows of A; its W waves take stretches of S slices of 128 k in turn, and
@@ -147,6 +150,117 @@ hipError_t rows(const Mx4GemmArgs& g, hipStream_t stream) {
   if (!grid_fits(groups, 64 * W)) return hipErrorInvalidConfiguration;
   return launch(mx4_gemm_rows_kernel<DT, F, R, W, S>, dim3(static_cast<unsigned>(groups)), dim3(64 * W), 0, stream, g,
                 static_cast<unsigned>(gn));
+}
+
+// The same for up to 16 rows that are not quantised yet: one launch for a whole
+// linear layer.  A lane's operand is one block of one row, so it quantises its 32 values
+// by itself, into the registers and the scale byte that the instruction wants.  The
+// values come through LDS too, 128 B k at a time (512 bytes of a row), and every
+// workgroup quantises them again.  Stretches, waves and the order of the sums are those of
+// mx4_gemm_rows_kernel, and so are the results.
+template <int DT, int XT, int R, int W>
+__global__ __launch_bounds__(64 * W) void mx4_linear_rows_kernel(Mx4GemmArgs g, const char* x, int64_t ldx) {
+  constexpr int XB = qm::Elem<XT>::kBytes;
+  constexpr int B = 4 / XB;                      // slices at a time
+  constexpr int kRowX = 128 * B * XB, kChunksX = kRowX / 16;  // of a row of values
+  constexpr int kRowW = 64 * B, kChunksW = 4 * B;
+  constexpr int kTileX = 16 * kRowX, kTileW = 16 * kRowW;
+  constexpr int kWave = kTileX + R * kTileW;
+  static_assert(W * kWave <= 81920 && R * 1024 <= kWave, "LDS: two workgroups or more on a CU; the sums");
+  __shared__ __attribute__((aligned(1024))) char smem[W * kWave];
+  typedef __attribute__((address_space(3))) const v4i* lds_v4i;
+  const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16 * R;
+  const int blocks = g.k / 32, pieces = (blocks + kChunksW - 1) / kChunksW;
+  const int64_t row_bytes = g.k / 2;
+  const uint32_t own = lds_addr(smem) + wave * kWave;
+  const uint8_t* sb[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) sb[i] = g.scale_b + min(n0 + 16 * i + r, g.n - 1) * g.ldsb;
+  v4f acc[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) acc[i] = v4f{0, 0, 0, 0};
+  auto key_w = [](int row) { return kChunksW == 8 ? (row >> 1) & 7 : (row >> 2) & 3; };
+  // piece p: B slices; a wave's stretches of four slices are those of the other kernel
+  for (int p = wave * (4 / B); p < pieces; p = p % (4 / B) == 4 / B - 1 ? p + 1 + (W - 1) * (4 / B) : p + 1) {
+#pragma unroll
+    for (int q = 0; q < kTileX / 1024; ++q) {
+      const int row = q * (64 / kChunksX) + lane / kChunksX;
+      if (q * (64 / kChunksX) >= g.m) break;  // rows that are not there: any values, in columns of their own
+      const int chunk = min(p * kChunksX + ((lane % kChunksX) ^ row), blocks * 2 * XB - 1);
+      lds_dma16(x + min(row, g.m - 1) * ldx * XB + 16 * static_cast<int64_t>(chunk), own + 1024 * q);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int q = 0; q < kTileW / 1024; ++q) {
+        const int row = q * (64 / kChunksW) + lane / kChunksW;
+        const int chunk = min(p * kChunksW + ((lane % kChunksW) ^ key_w(row)), blocks - 1);
+        lds_dma16(g.b + min(n0 + 16 * i + row, g.n - 1) * row_bytes + 16 * chunk, own + kTileX + i * kTileW + 1024 * q);
+      }
+    uint32_t ws[R][B];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int s = 0; s < B; ++s) ws[i][s] = reinterpret_cast<const uint32_t*>(sb[i])[p * B + s];
+    wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int s = 0; s < B; ++s) {
+      const bool past = (p * B + s) * 4 + c >= blocks;
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 2 * XB; ++j) {
+        const v4i u = *reinterpret_cast<lds_v4i>(own + r * kRowX + ((((4 * s + c) * 2 * XB + j) ^ r) << 4));
+        qm::Elem<XT>::unpack(make_uint4(u[0], u[1], u[2], u[3]), v + j * qm::Elem<XT>::kPerUnit);
+      }
+      const mx4::Block b = mx4::quantised(v);
+      const v4i a = {static_cast<int>(b.codes[0]), static_cast<int>(b.codes[1]), static_cast<int>(b.codes[2]), static_cast<int>(b.codes[3])};
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const v4i w = *reinterpret_cast<lds_v4i>(own + kTileX + i * kTileW + r * kRowW + (((4 * s + c) ^ key_w(r)) << 4));
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a), acc[i], kFp4, kFp4, 0,
+                                                                 static_cast<int>(past ? 0u : ws[i][s] >> (8 * c)), 0,
+                                                                 static_cast<int>(past ? 0u : b.scale));
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the next piece comes over what has been read
+    asm volatile("" ::: "memory");
+  }
+  v4f* const sums = reinterpret_cast<v4f*>(smem + wave * kWave);
+#pragma unroll
+  for (int i = 0; i < R; ++i) sums[i * 64 + lane] = acc[i];
+  __syncthreads();
+  for (int i = wave; i < R; i += W) {
+    auto of = [&](int w) { return reinterpret_cast<const v4f*>(smem + w * kWave)[i * 64 + lane]; };
+    v4f v = of(0);
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += of(w);
+    const int col = n0 + 16 * i + 4 * c;
+    if (r >= g.m) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < g.n) put<DT>(g.out, static_cast<int64_t>(r) * g.n + col + e, v[e] * g.output_scale);
+  }
+}
+
+template <int DT, int XT>
+hipError_t linear_rows(const Mx4GemmArgs& g, const void* x, int64_t ldx, hipStream_t stream) {
+  const char* const from = static_cast<const char*>(x);
+  auto grid = [&](int cols) { return dim3(static_cast<unsigned>((g.n + cols - 1) / cols)); };
+  if (g.n >= kCols64) return launch(mx4_linear_rows_kernel<DT, XT, 4, 4>, grid(64), dim3(256), 0, stream, g, from, ldx);
+  if (g.n >= kCols32) return launch(mx4_linear_rows_kernel<DT, XT, 2, 4>, grid(32), dim3(256), 0, stream, g, from, ldx);
+  return launch(mx4_linear_rows_kernel<DT, XT, 1, 8>, grid(16), dim3(512), 0, stream, g, from, ldx);
+}
+
+template <int DT>
+hipError_t linear_by_type(const Mx4GemmArgs& g, const void* x, int64_t ldx, int x_dtype, hipStream_t stream) {
+  switch (x_dtype) {
+    case QK_F32: return linear_rows<DT, QK_F32>(g, x, ldx, stream);
+    case QK_BF16: return linear_rows<DT, QK_BF16>(g, x, ldx, stream);
+    default: return linear_rows<DT, QK_F16>(g, x, ldx, stream);
+  }
 }
 
 // ---- many rows: tiles in LDS ----
@@ -624,11 +738,11 @@ hipError_t tiles(const Mx4GemmArgs& g, hipStream_t stream) {
 template <int DT>
 hipError_t by_size(const Mx4GemmArgs& g, hipStream_t stream) {
   if (g.m <= 16) {
-    if (g.n >= 64 * 400) return rows<DT, 1, 4, 4, 4>(g, stream);
-    if (g.n >= 32 * 400) return rows<DT, 1, 2, 4, 4>(g, stream);
+    if (g.n >= kCols64) return rows<DT, 1, 4, 4, 4>(g, stream);
+    if (g.n >= kCols32) return rows<DT, 1, 2, 4, 4>(g, stream);
     return rows<DT, 1, 1, 8, 4>(g, stream);
   }
-  if (g.m <= 32) return g.n >= 32 * 400 ? rows<DT, 2, 2, 4, 4>(g, stream) : rows<DT, 2, 1, 4, 4>(g, stream);
+  if (g.m <= 32) return g.n >= kCols32 ? rows<DT, 2, 2, 4, 4>(g, stream) : rows<DT, 2, 1, 4, 4>(g, stream);
   auto count = [&](int bm, int bn) { return static_cast<double>((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn); };
   const double slices = (g.k + 127) / 128, waves22 = std::max(count(32, 32) / 256, 1.0), waves44 = std::max(count(64, 64) / 256, 1.0);
   const double rounds1 = std::floor(count(128, 128) / 512), left1 = count(128, 128) - 512 * rounds1;
@@ -650,6 +764,23 @@ hipError_t launch_gemm_mx4(const Mx4GemmArgs& g, hipStream_t stream) {
     case QK_F32: return by_size<QK_F32>(g, stream);
     case QK_BF16: return by_size<QK_BF16>(g, stream);
     default: return by_size<QK_F16>(g, stream);
+  }
+}
+
+// Where the weight is small.  One launch / two, from a graph, and called one by one
+// (where a second launch costs the host 3 us): 1 x 4096 x 4096 4.7 / 4.7 and 4.7 / 7.9 us;
+// 16 x 4096 x 4096 5.8 / 5.4 and 5.7 / 7.8; 1 x 14336 x 4096 10.0 / 9.0 and 9.7 / 8.7; 16 x 4096
+// x 14336 13.5 / 9.3 and 13.2 / 9.1: quantising again in every workgroup grows with n k.
+bool linear_mx4_rows_applies(const Mx4GemmArgs& g, const void* x, int64_t ldx, int x_dtype) {
+  const int64_t b = x_dtype == QK_F32 ? 4 : 2;
+  return g.m <= 16 && g.k > 0 && static_cast<int64_t>(g.n) * g.k <= 1 << 24 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && (g.m == 1 || ldx * b % 16 == 0);
+}
+
+hipError_t launch_linear_mx4_rows(const Mx4GemmArgs& g, const void* x, int64_t ldx, int x_dtype, hipStream_t stream) {
+  switch (g.out_dtype) {
+    case QK_F32: return linear_by_type<QK_F32>(g, x, ldx, x_dtype, stream);
+    case QK_BF16: return linear_by_type<QK_BF16>(g, x, ldx, x_dtype, stream);
+    default: return linear_by_type<QK_F16>(g, x, ldx, x_dtype, stream);
   }
 }
 

@@ -12,11 +12,6 @@
 // field of max |x| as binary32, less 2.  A block with an infinity or a NaN has
 // the byte 255, which stands for NaN, and codes 0.
 //
-// gfx950 converts with v_cvt_scalef32_pk_fp4_f32: it divides by the power of
-// two in its scale operand's exponent field, rounds as above and saturates
-// (checked over all 65536 bf16 and fp16 values and over binary32 around every
-// border, subnormals among them).
-//
 // Bound by memory: four lanes share a block, eight values (16 or 32 bytes)
 // each, so a wave reads 1 KiB of 16-bit rows in one piece and writes 256 bytes
 // of codes and 16 of scales.  bf16, 4096 x 14336 there 28.1 us (5.3 TB/s), back 18.3
@@ -24,6 +19,7 @@
 // 8 x 4096 2.0 us either way.  Reading past the caches there gains nothing (27.7);
 // the values of large calls are stored past them on the way back (29.4 without).
 #include "kv_common.h"
+#include "mx4.h"
 
 namespace qk {
 namespace {
@@ -71,17 +67,9 @@ __global__ __launch_bounds__(kBlock) void mx4_quant_kernel(const char* __restric
   }
   uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) top = qm::max_u32(top, __float_as_uint(v[e]) & 0x7fffffffu);
-  top = quad_max(top) >> 23;
-  const bool bad = top == 255;
-  const uint32_t byte = bad ? 255 : top > 2 ? top - 2 : 0;
-  const float s = __uint_as_float(byte << 23);
-  uint32_t w = 0;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], s, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], s, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], s, 2);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], s, 3);
-  reinterpret_cast<uint32_t*>(q)[i] = bad ? 0 : w;
+  for (int e = 0; e < kEach; ++e) top = qm::max_u32(top, mx4::magnitude_bits(v[e]));
+  const uint32_t byte = mx4::scale_byte(quad_max(top));
+  reinterpret_cast<uint32_t*>(q)[i] = mx4::codes8(v, byte);
   if ((at & 3) == 0) scale[row * lds + (at >> 2)] = static_cast<uint8_t>(byte);
 }
 

@@ -745,18 +745,22 @@ int qk_gemm_mx4_scaled(int m, int n, int k, const uint8_t* a, const uint8_t* sca
 int qk_linear_mx4(int m, int n, int k, const void* x, int64_t ldx, int x_dtype, const uint8_t* b,
                   const uint8_t* scale_b, int64_t ldsb, float output_scale, void* out, int out_dtype, uint8_t* q_out,
                   uint8_t* scale_out, int64_t lds_out, hipStream_t stream) {
-  // the product's arguments are checked before anything is enqueued
-  if (m < 0 || n < 0 || k < 0 || !known_input_dtype(out_dtype)) return QK_ERR_INVALID_VALUE;
+  // everything is checked before anything is enqueued
+  if (m < 0 || n < 0 || k < 0 || !known_input_dtype(x_dtype) || !known_input_dtype(out_dtype))
+    return QK_ERR_INVALID_VALUE;
   if (k % 32 != 0) return QK_ERR_UNSUPPORTED;
-  if (m > 0 && n > 0) {
-    if (!out) return QK_ERR_INVALID_VALUE;
-    const int rc = mx4_operand(n, k, b, scale_b, ldsb);
-    if (rc != QK_OK) return rc;
-    if (!aligned(out, out_dtype == QK_F32 ? 4 : 2) || m > kMx4MostRows || n > kMx4MostRows)
-      return QK_ERR_UNSUPPORTED;
-  }
-  const int rc = qk_quant_mx4(m, k, x, ldx, x_dtype, q_out, scale_out, lds_out, stream);
+  if (m == 0 || n == 0) return QK_OK;
+  if (!out || (k > 0 && (!x || ldx < k))) return QK_ERR_INVALID_VALUE;
+  const int rc = mx4_operand(n, k, b, scale_b, ldsb);
   if (rc != QK_OK) return rc;
+  if (!aligned(x, x_dtype == QK_F32 ? 4 : 2) || !aligned(out, out_dtype == QK_F32 ? 4 : 2) || m > kMx4MostRows ||
+      n > kMx4MostRows)
+    return QK_ERR_UNSUPPORTED;
+  const qk::Mx4GemmArgs g{m, n, k, q_out, scale_out, lds_out, b, scale_b, ldsb, output_scale, out, out_dtype};
+  if (qk::linear_mx4_rows_applies(g, x, ldx, x_dtype))
+    return status_of_cut(qk::launch_linear_mx4_rows(g, x, ldx, x_dtype, stream));
+  const int quantised = qk_quant_mx4(m, k, x, ldx, x_dtype, q_out, scale_out, lds_out, stream);
+  if (quantised != QK_OK) return quantised;
   return qk_gemm_mx4_scaled(m, n, k, q_out, scale_out, lds_out, b, scale_b, ldsb, output_scale, out, out_dtype,
                             stream);
 }
