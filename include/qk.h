@@ -524,7 +524,8 @@ int qk_dequant_mx4(int m, int k, const uint8_t *q, const uint8_t *scale, int64_t
  *   (QK_F32, QK_BF16 or QK_F16), rounded once, nearest even.
  * A NaN scale makes its row (column) NaN.  k == 0 gives zeros.  No workspace.
  * Errors: negative size, unknown type, short stride, NULL (QK_ERR_INVALID_VALUE);
- * k not a multiple of 32, misaligned, m or n above 2^24 (QK_ERR_UNSUPPORTED).
+ * k not a multiple of 32, misaligned, m, n or k above 2^24, scale rows more than 2^23
+ * bytes apart (QK_ERR_UNSUPPORTED).
  */
 int qk_gemm_mx4_scaled(int m, int n, int k, const uint8_t *a, const uint8_t *scale_a, int64_t ldsa,
                        const uint8_t *b, const uint8_t *scale_b, int64_t ldsb, float output_scale,
@@ -567,7 +568,7 @@ int qk_linear_mx4(int m, int n, int k, const void *x, int64_t ldx, int x_dtype, 
  * kv_heads may be 0 (its tensors are then not touched).
  * Errors: negative size, unknown type, dim or rotary out of range, short stride,
  * negative or NaN eps, NULL, overlapping rows (QK_ERR_INVALID_VALUE); misaligned,
- * 2^24 rows and more (QK_ERR_UNSUPPORTED).
+ * 2^24 rows and more, more than 2^24 elements to a row (QK_ERR_UNSUPPORTED).
  */
 int qk_norm_rope(int seqs, int tokens, int heads, int kv_heads, int dim, const void *q, int64_t ldq,
                  const void *k, int64_t ldk, const void *q_weight, const void *k_weight, int dtype,

@@ -45,6 +45,7 @@ def test_silu_rows_hold_both_halves():
     (dict(ldsa=1), INVALID), (dict(ldsb=1), INVALID), (dict(ldsa=8), UNSUP), (dict(ldsb=20), UNSUP), (dict(a=OFF16), UNSUP),
     (dict(b=OFF16), UNSUP), (dict(scale_a=OFF16), UNSUP), (dict(scale_b=OFF16), UNSUP), (dict(out=FAKE_ODD), UNSUP),
     (dict(out=at(2), out_dtype=0), UNSUP), (dict(m=(1 << 24) + 1), UNSUP), (dict(n=(1 << 24) + 1), UNSUP),
+    (dict(k=(1 << 24) + 32, ldsa=1 << 20, ldsb=1 << 20), UNSUP), (dict(ldsa=(1 << 23) + 16), UNSUP), (dict(ldsb=1 << 40), UNSUP),
     (dict(m=0, a=NULL), 0), (dict(n=0, b=NULL), 0)])
 def test_product(kw, status):
     assert call(qk.library().qk_gemm_mx4_scaled, GEMM, **kw) == status
@@ -53,7 +54,7 @@ def test_product(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(m=-1), INVALID), (dict(k=40), UNSUP), (dict(x=NULL), INVALID), (dict(b=NULL), INVALID), (dict(out=NULL), INVALID),
     (dict(q=NULL), INVALID), (dict(scale=NULL), INVALID), (dict(lds=8), UNSUP), (dict(ldsb=8), UNSUP), (dict(ldx=60), INVALID),
-    (dict(x_dtype=5), INVALID), (dict(out_dtype=5), INVALID), (dict(out=FAKE_ODD), UNSUP), (dict(n=(1 << 24) + 1), UNSUP),
+    (dict(x_dtype=5), INVALID), (dict(out_dtype=5), INVALID), (dict(lds=(1 << 23) + 16), UNSUP), (dict(m=4, ldsb=1 << 40), UNSUP), (dict(out=FAKE_ODD), UNSUP), (dict(n=(1 << 24) + 1), UNSUP),
     (dict(m=0, x=NULL), 0), (dict(m=4, x=at(8), q=NULL), INVALID), (dict(m=4, ldx=68, q=NULL), INVALID), (dict(m=4, x=NULL), INVALID),
     (dict(m=4, b=NULL), INVALID), (dict(m=4, ldx=60), INVALID), (dict(m=4, x=FAKE_ODD), UNSUP), (dict(m=4, out=FAKE_ODD), UNSUP)])
 def test_linear(kw, status):
@@ -69,6 +70,7 @@ def test_linear(kw, status):
     (dict(ldko=127), INVALID), (dict(q=FAKE_ODD), UNSUP), (dict(k_out=FAKE_ODD), UNSUP), (dict(q_weight=FAKE_ODD), UNSUP),
     (dict(freqs=at(4)), UNSUP), (dict(start=FAKE_ODD), UNSUP), (dict(tokens=0), 0), (dict(seqs=0), 0), (dict(heads=0, kv_heads=0), 0),
     (dict(tokens=1 << 24, q_out=at(1 << 40), k_out=at(1 << 41)), UNSUP),
+    (dict(heads=(1 << 18) + 1, ldq=1 << 25, ldqo=1 << 25, q_out=at(1 << 40), k_out=at(1 << 41)), UNSUP),
     # outputs over inputs: shifted in place, over the other input, over each other
     (dict(q_out=at(2), ldqo=512), INVALID), (dict(q_out=at(1024), ldqo=512), INVALID), (dict(q_out=FAKE, ldqo=256), INVALID),
     (dict(k_out=FAKE), INVALID), (dict(k_out=at(384), ldko=512), INVALID), (dict(q_out=at(512), ldqo=512), INVALID),

@@ -725,7 +725,12 @@ int qk_dequant_mx4(int m, int k, const uint8_t* q, const uint8_t* scale, int64_t
                   stream);
 }
 
-constexpr int kMx4MostRows = 1 << 24;
+// The product's kernels reach 256 rows from a base with 32-bit offsets.
+constexpr int kMx4MostRows = 1 << 24, kMx4MostK = 1 << 24;
+constexpr int64_t kMx4MostStride = 1 << 23;
+static bool mx4_fits(int m, int n, int k, int64_t ldsa, int64_t ldsb) {
+  return m <= kMx4MostRows && n <= kMx4MostRows && k <= kMx4MostK && ldsa <= kMx4MostStride && ldsb <= kMx4MostStride;
+}
 
 int qk_gemm_mx4_scaled(int m, int n, int k, const uint8_t* a, const uint8_t* scale_a, int64_t ldsa, const uint8_t* b,
                        const uint8_t* scale_b, int64_t ldsb, float output_scale, void* out, int out_dtype,
@@ -737,7 +742,7 @@ int qk_gemm_mx4_scaled(int m, int n, int k, const uint8_t* a, const uint8_t* sca
   int rc = mx4_operand(m, k, a, scale_a, ldsa);
   if (rc == QK_OK) rc = mx4_operand(n, k, b, scale_b, ldsb);
   if (rc != QK_OK) return rc;
-  if (!aligned(out, out_dtype == QK_F32 ? 4 : 2) || m > kMx4MostRows || n > kMx4MostRows) return QK_ERR_UNSUPPORTED;
+  if (!aligned(out, out_dtype == QK_F32 ? 4 : 2) || !mx4_fits(m, n, k, ldsa, ldsb)) return QK_ERR_UNSUPPORTED;
   const qk::Mx4GemmArgs g{m, n, k, a, scale_a, ldsa, b, scale_b, ldsb, output_scale, out, out_dtype};
   return status_of_cut(qk::launch_gemm_mx4(g, stream));
 }
@@ -753,12 +758,13 @@ int qk_linear_mx4(int m, int n, int k, const void* x, int64_t ldx, int x_dtype, 
   if (!out || (k > 0 && (!x || ldx < k))) return QK_ERR_INVALID_VALUE;
   const int rc = mx4_operand(n, k, b, scale_b, ldsb);
   if (rc != QK_OK) return rc;
-  if (!aligned(x, x_dtype == QK_F32 ? 4 : 2) || !aligned(out, out_dtype == QK_F32 ? 4 : 2) || m > kMx4MostRows ||
-      n > kMx4MostRows)
+  if (!aligned(x, x_dtype == QK_F32 ? 4 : 2) || !aligned(out, out_dtype == QK_F32 ? 4 : 2) ||
+      !mx4_fits(m, n, k, 0, ldsb))
     return QK_ERR_UNSUPPORTED;
   const qk::Mx4GemmArgs g{m, n, k, q_out, scale_out, lds_out, b, scale_b, ldsb, output_scale, out, out_dtype};
   if (qk::linear_mx4_rows_applies(g, x, ldx, x_dtype))
     return status_of_cut(qk::launch_linear_mx4_rows(g, x, ldx, x_dtype, stream));
+  if (lds_out > kMx4MostStride) return QK_ERR_UNSUPPORTED;
   const int quantised = qk_quant_mx4(m, k, x, ldx, x_dtype, q_out, scale_out, lds_out, stream);
   if (quantised != QK_OK) return quantised;
   return qk_gemm_mx4_scaled(m, n, k, q_out, scale_out, lds_out, b, scale_b, ldsb, output_scale, out, out_dtype,
@@ -795,6 +801,7 @@ int qk_norm_rope(int seqs, int tokens, int heads, int kv_heads, int dim, const v
     if (!aligned(s.x, e) || !aligned(s.out, e) || !aligned(s.weight, we)) return QK_ERR_UNSUPPORTED;
   }
   if (!aligned(start, 4) || !aligned(cu, 4) || !aligned(freqs, 8)) return QK_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>((heads > kv_heads ? heads : kv_heads)) * dim > 1 << 24) return QK_ERR_UNSUPPORTED;
   for (const Side& out : sides)
     for (const Side& in : sides) {
       const int64_t wo = static_cast<int64_t>(out.heads) * dim * b, wi = static_cast<int64_t>(in.heads) * dim * b;
