@@ -181,14 +181,16 @@ __global__ __launch_bounds__(64 * W) void mx4_linear_rows_kernel(Mx4GemmArgs g, 
   v4f acc[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) acc[i] = v4f{0, 0, 0, 0};
-  auto key_w = [](int row) { return kChunksW == 8 ? (row >> 1) & 7 : (row >> 2) & 3; };
+  // as in Mx4Tile; the values' rows are two or four times 256 bytes
+  auto key_w = [](int row) { return kChunksW == 8 ? row & 7 : (row >> 1) & 3; };
+  auto key_x = [](int row) { return row >> 2 | (row & 3) << 2; };
   // piece p: B slices; a wave's stretches of four slices are those of the other kernel
   for (int p = wave * (4 / B); p < pieces; p = p % (4 / B) == 4 / B - 1 ? p + 1 + (W - 1) * (4 / B) : p + 1) {
 #pragma unroll
     for (int q = 0; q < kTileX / 1024; ++q) {
       const int row = q * (64 / kChunksX) + lane / kChunksX;
       if (q * (64 / kChunksX) >= g.m) break;  // rows that are not there: any values, in columns of their own
-      const int chunk = min(p * kChunksX + ((lane % kChunksX) ^ row), blocks * 2 * XB - 1);
+      const int chunk = min(p * kChunksX + ((lane % kChunksX) ^ key_x(row)), blocks * 2 * XB - 1);
       lds_dma16(x + min(row, g.m - 1) * ldx * XB + 16 * static_cast<int64_t>(chunk), own + 1024 * q);
     }
 #pragma unroll
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(64 * W) void mx4_linear_rows_kernel(Mx4GemmArgs g, 
       float v[32];
 #pragma unroll
       for (int j = 0; j < 2 * XB; ++j) {
-        const v4i u = *reinterpret_cast<lds_v4i>(own + r * kRowX + ((((4 * s + c) * 2 * XB + j) ^ r) << 4));
+        const v4i u = *reinterpret_cast<lds_v4i>(own + r * kRowX + ((((4 * s + c) * 2 * XB + j) ^ key_x(r)) << 4));
         qm::Elem<XT>::unpack(make_uint4(u[0], u[1], u[2], u[3]), v + j * qm::Elem<XT>::kPerUnit);
       }
       const mx4::Block b = mx4::quantised(v);
@@ -291,10 +293,16 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 // PFLOP/s, where 32x32x64 reaches 6.7; with all codes 0 both reach 9.5: the
 // power that the operands take holds the clock down).
 //
-// Slices of 128 k (64 bytes of a row, four blocks) go from memory to LDS in a
-// ring of four stages.  A stage is free as soon as every wave has read its
-// fragments, in the middle of the slice's products, and is then asked for slice
-// kt + 4: three slices are under way at a time.
+// Slices of 128 k (64 bytes of a row, four blocks) go from memory to LDS, into a
+// ring that holds four.  In large tiles two come together, so that a transfer touches
+// 8 whole lines of 128 bytes and not 16 halves (8192 x 28672 x 8192: 837 us for 898;
+// 2048 x 4096 x 14336: 60.5 for 69), in small ones, of which few are under way at a time,
+// one by one (512 x 4096 x 4096: 13.2 us for 14.8).  A part of the ring is free as soon as
+// every wave has read its fragments, and is then asked for what comes four slices on.
+//
+// Figures: 8192 x 28672 x 8192 837 us (4.6 PFLOP/s; the products alone, from LDS that
+// nothing is brought to, 718; the stores, while which nothing is multiplied, 84 of
+// both), 4096 x 4096 x 14336 97, 2048 x 4096 x 4096 23.2 (21.6 and 4).
 //
 // A lane's quarter of a wave is its block of a slice, and the byte of its scale
 // register that the instruction picks is the slice: the scales of four slices, 16
@@ -306,35 +314,41 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 // of 64 rows in each, the scales cost a tenth of the kernel.)
 template <int DT, int BM, int BN, int WTM, int WTN, bool KTAIL>
 struct Mx4Tile {
-  static constexpr int kStages = 4;
   static constexpr int kWavesN = BN / WTN;
   static constexpr int kWaves = (BM / WTM) * kWavesN;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kRow = 64;                 // bytes of a row in a slice
+  static constexpr int kUnit = BM * BN > 128 * 128 ? 2 : 1;  // slices that come together
+  static constexpr int kRing = 4 / kUnit;
+  static constexpr int kRow = 64 * kUnit;                    // bytes of a row in a unit
   static constexpr int kStageA = BM * kRow, kStageB = BN * kRow;
-  static constexpr int kScales = kStages * (kStageA + kStageB);  // rows of 64 bytes of scales follow the ring
+  static constexpr int kScales = kRing * (kStageA + kStageB);  // rows of 64 bytes of scales follow the ring
   // Half of a CU's LDS or all of it: workgroups of anything between were
   // started one after the other, some 50 ns apart (2048 x 4096 x 4096 on tiles of
   // 256 x 128, 256 of them, with 136 KiB each: 34.6 us; with 160: 23.8).
-  static constexpr int kUsed = kScales + kWaves * 64 * kRow;
+  static constexpr int kUsed = kScales + kWaves * 64 * 64;
   static constexpr int kSmem = kUsed <= 81920 ? 81920 : 163840;
-  static constexpr int kOps = (BM + BN) / 16 / kWaves;  // 1 KiB transfers of a slice per wave
+  static constexpr int kRowsAt = 1024 / kRow;             // rows of a transfer
+  static constexpr int kOps = (BM + BN) / kRowsAt / kWaves;  // transfers of a unit per wave
   static constexpr int kPieces = (BM + BN) / 64;
   static constexpr int FM = WTM / 16, FN = WTN / 16;
   static constexpr int kElem = DT == QK_F32 ? 4 : 2;
-  static_assert(kOps * kWaves * 16 == BM + BN && BM % 64 == 0 && BN % 64 == 0, "whole transfers");
+  static_assert(kOps * kWaves * kRowsAt == BM + BN && BM % 64 == 0 && BN % 64 == 0, "whole transfers");
   static_assert(kPieces <= kWaves, "a thread for every row of scales");
   static_assert(kUsed <= kSmem && kWaves * 16384 <= kSmem, "LDS; 16 KiB of it per wave for the results");
-  static_assert(3 * kStageA + 1024 * (FM - 1) < 65536 && 3 * kStageB + 1024 * (FN - 1) < 65536, "immediate offsets");
-  static_assert((FM == 8 || FM == 4) && FN == 4 && kOps <= 4, "the orders below");
+  static_assert((kRing - 1) * kStageA + 16 * kRow * (FM - 1) < 65536 && (kRing - 1) * kStageB + 16 * kRow * (FN - 1) < 65536, "immediate offsets");
+  static_assert((FM == 8 || FM == 4) && FN == 4 && kOps <= 4 * kUnit, "the orders below");
 
   typedef __attribute__((address_space(3))) const v4i* lds_v4i;
   typedef __attribute__((address_space(3))) v4i* lds_v4i_out;
   typedef __attribute__((address_space(3))) const int* lds_int;
 
-  // 16-byte chunks of a row are exchanged by its number: 16 consecutive rows then
-  // have a chunk in 16 different places of 256 bytes
-  __device__ static int row_offset(int row, int chunk) { return row * kRow + ((chunk ^ ((row >> 2) & 3)) << 4); }
+  // 16-byte chunks of a row are exchanged by its number.  The 64 lanes' reads of a
+  // fragment (chunk c of rows 0 .. 15, c = 0 .. 3) go in sets of 16 that take half of their rows
+  // from one chunk and half from the next; those fall on 16 different places of 256 bytes
+  // with this key and not with, say, row / 4 of 64-byte rows, which took twice as long.
+  __device__ static int key(int row) { return kUnit == 2 ? row & 7 : (row >> 1) & 3; }
+  __device__ static int row_offset(int row, int chunk) { return row * kRow + ((chunk ^ key(row)) << 4); }
+  __device__ static int scale_offset(int row, int chunk) { return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4); }
 
   __device__ static __forceinline__ void run(const Mx4GemmArgs& g, int tm, int tn) {
     __shared__ __attribute__((aligned(1024))) char smem[kSmem];
@@ -354,29 +368,30 @@ struct Mx4Tile {
     };
 
     // ---- transfers ----
-    // part p of a slice: 16 rows (A's, then B's); lane l brings a chunk of row l / 4
+    // part p of a unit: some rows (A's, then B's); the lanes bring their chunks
     const uint8_t* const base_a = uniform(g.a + static_cast<int64_t>(m0) * row_bytes);
     const uint8_t* const base_b = uniform(g.b + static_cast<int64_t>(n0) * row_bytes);
     uint32_t voff[kOps];
     const int part0 = wave * kOps;
-    const int chunk = (lane & 3) ^ ((lane >> 4) & 3);  // as row_offset has it, in every piece of 16 rows
+    const int row_at = lane / (4 * kUnit), chunk = lane % (4 * kUnit) ^ key(row_at);  // as row_offset has it
 #pragma unroll
     for (int q = 0; q < kOps; ++q) {
-      const bool is_a = (part0 + q) * 16 < BM;
-      const int row = (part0 + q) * 16 - (is_a ? 0 : BM) + (lane >> 2);
+      const bool is_a = (part0 + q) * kRowsAt < BM;
+      const int row = (part0 + q) * kRowsAt - (is_a ? 0 : BM) + row_at;
       const int from = is_a ? min(m0 + row, g.m - 1) - m0 : min(n0 + row, g.n - 1) - n0;
       voff[q] = static_cast<uint32_t>(from) * static_cast<uint32_t>(row_bytes) + (KTAIL ? 0 : 16 * chunk);
     }
-    // slice s, if there is one; blocks past k are read from the row's last
+    // the unit from slice s on, if there is s; blocks past k are read from the row's last
     auto issue = [&](int s, int q) {
-      const bool is_a = (part0 + q) * 16 < BM;
+      const bool is_a = (part0 + q) * kRowsAt < BM;
+      const int at = s / kUnit & (kRing - 1);
       const uint32_t to =
-          lds0 + (is_a ? (s & 3) * kStageA : kStages * kStageA + (s & 3) * kStageB - BM * kRow) + (part0 + q) * 1024;
+          lds0 + (is_a ? at * kStageA : kRing * kStageA + at * kStageB - BM * kRow) + (part0 + q) * 1024;
       const uint8_t* const from = is_a ? base_a : base_b;
       if constexpr (KTAIL)
         lds_dma16_below(s, KT, from, voff[q] + 16 * min(4 * s + here(chunk), blocks - 1), to);
       else
-        lds_dma16_below(s, KT, from + static_cast<int64_t>(s) * kRow, voff[q], to);
+        lds_dma16_below(s, KT, from + static_cast<int64_t>(s) * 64, voff[q], to);
     };
     // Scales of 16 slices: 64 bytes (chunks of four slices' 16) of each of this
     // wave's 64 rows, laid out and exchanged as a slice's.  Chunks past the row's
@@ -387,20 +402,20 @@ struct Mx4Tile {
     const uint32_t lds_s = static_cast<uint32_t>(scales_a ? g.ldsa : g.ldsb);
     const int rows_s = (scales_a ? g.m - m0 : g.n - n0) - 1, row_s = wave * 64 - (scales_a ? 0 : BM);
     const int last_chunk = (KT - 1) >> 2;
-    const uint32_t wave_scales = lds0 + kScales + wave * 64 * kRow;
+    const uint32_t wave_scales = lds0 + kScales + wave * 64 * 64;
     auto issue_scales = [&](int batch, int q) {
-      const int l = here(lane), c = (l & 3) ^ ((l >> 4) & 3);
+      const int l = here(lane), c = (l & 3) ^ ((l >> 3) & 3);
       const uint32_t row = static_cast<uint32_t>(min(row_s + q * 16 + (l >> 2), rows_s));
       lds_dma16_below(wave < kPieces ? 16 * batch : KT, KT, base_s, row * lds_s + 16 * min(4 * batch + c, last_chunk),
                    wave_scales + q * 1024);
     };
-    auto own_scales = [&](int x) { return wave_scales + here(lane) * kRow + 16 * x; };  // of this thread's row
+    auto own_scales = [&](int x) { return wave_scales + here(lane) * 64 + 16 * x; };  // of this thread's row
     auto raw_scales = [&](int x) { return *reinterpret_cast<lds_v4i>(own_scales(x)); };
     auto put_scales = [&](int batch, int x, v4i w) {
       // Those of blocks past k, where anything may lie, become 2^-127 in both
       // operands: products of codes are then 2^-247 at most, nothing in binary32.
       if constexpr (KTAIL) {
-        const int left = blocks - 16 * (4 * batch + (x ^ ((here(lane) >> 2) & 3)));
+        const int left = blocks - 16 * (4 * batch + (x ^ ((here(lane) >> 1) & 3)));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int have = left - 4 * i;
@@ -422,11 +437,12 @@ struct Mx4Tile {
       return x;
     };
     const uint32_t a_base = opaque(lds0 + row_offset(wm * WTM + i16, c4));
-    const uint32_t b_base = opaque(lds0 + kStages * kStageA + row_offset(wn * WTN + i16, c4));
-    const uint32_t sa_base = opaque(lds0 + kScales + row_offset(wm * WTM + i16, 0) + 4 * c4);
-    const uint32_t sb_base = opaque(lds0 + kScales + row_offset(BM + wn * WTN + i16, 0) + 4 * c4);
-    auto read_a = [&](int S, int i) { return *reinterpret_cast<lds_v4i>(a_base + S * kStageA + 1024 * i); };
-    auto read_b = [&](int S, int j) { return *reinterpret_cast<lds_v4i>(b_base + S * kStageB + 1024 * j); };
+    const uint32_t b_base = opaque(lds0 + kRing * kStageA + row_offset(wn * WTN + i16, c4));
+    const uint32_t sa_base = opaque(lds0 + kScales + scale_offset(wm * WTM + i16, 0) + 4 * c4);
+    const uint32_t sb_base = opaque(lds0 + kScales + scale_offset(BM + wn * WTN + i16, 0) + 4 * c4);
+    // of slice S of the ring's four
+    auto read_a = [&](int S, int i) { return *reinterpret_cast<lds_v4i>((a_base ^ (S % kUnit) << 6) + S / kUnit * kStageA + 16 * kRow * i); };
+    auto read_b = [&](int S, int j) { return *reinterpret_cast<lds_v4i>((b_base ^ (S % kUnit) << 6) + S / kUnit * kStageB + 16 * kRow * j); };
     v4f acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -450,10 +466,10 @@ struct Mx4Tile {
 #pragma unroll
       for (int q = 0; q < 4; ++q) issue_scales(0, q);
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < 4; s += kUnit)
 #pragma unroll
         for (int q = 0; q < kOps; ++q) issue(s, q);
-      wait_vmcnt<3 * kOps>();
+      wait_vmcnt<(kRing - 1) * kOps>();
 #pragma unroll
       for (int x = 0; x < 4; ++x) put_scales(0, x, raw_scales(x));
       __syncthreads();
@@ -464,13 +480,18 @@ struct Mx4Tile {
     }
 
     // Slice kt, X its number modulo 16 (a constant wherever it is used).  At the
-    // barrier slice kt + 1 has landed, for every wave, and every wave has read the last
-    // of slice kt; what may still be under way is slices kt + 2 and kt + 3.  The
-    // last scales of a batch are read in slice 11, so the next batch may come
-    // over it from slice 12's barrier on; asked for before slice 16's data, it is
-    // there at slice 14's barrier, transposed behind it, and read in slice 15.
-    auto meet = [&] {
-      wait_vmcnt<2 * kOps>();
+    // barrier in a unit's last slice the next unit has landed, for every wave, and every
+    // wave has read the last of this one, whose part of the ring is then asked for a
+    // unit four slices on.  The last scales of a batch are read in slice 11, so the next
+    // batch may come over it from slice 12's barrier on; in slice 14 it is there, each thread
+    // transposes what its own wave brought, and it is read behind slice 15's barrier.
+    // (Loads arrive in order: the waits count those that may still be under way, in
+    // slice 13 of pairs the scales.)
+    auto meet = [&](int X) {
+      if (X % kUnit != kUnit - 1 && X != 12) return;
+      if (kUnit == 1) wait_vmcnt<2 * kOps>();
+      else if (X == 13) wait_vmcnt<4>();
+      else if (X != 12) wait_vmcnt<0>();
       __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
       barrier();
     };
@@ -490,7 +511,9 @@ struct Mx4Tile {
         pin();
       };
       auto data = [&](int q) {
-        if (q < kOps) issue(kt + 4, q);
+#pragma unroll
+        for (int j = 0; j < kUnit; ++j)
+          if (X % kUnit == kUnit - 1 && kUnit * q + j < kOps) issue(kt + 5 - kUnit, kUnit * q + j);
         pin();
       };
       v4i raw[2];
@@ -503,6 +526,10 @@ struct Mx4Tile {
         if ((X & 3) == 3 && FM == 4) {
           if (part < FN) tb[part] = scale_b(chunk, part);
           else if (part < FN + FM) ta[part - FN] = scale_a(chunk, part - FN);
+        }
+        if (kUnit == 2 && X == 14 && part == 0) {
+          wait_vmcnt<kOps>();
+          asm volatile("" ::: "memory");
         }
         if (X == 14 && (part == 0 || part == 1 || part == 6 || part == 7)) raw[part & 1] = raw_scales(part < 6 ? part : part - 4);
         if (X == 14 && (part == 4 || part == 5 || part == 10 || part == 11))
@@ -533,7 +560,7 @@ struct Mx4Tile {
         mfma(2, 1);
         mfma(3, 0);
         mfma(3, 1);
-        meet();
+        meet(X);
         if (X == 12) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) dma(q);
@@ -593,7 +620,7 @@ struct Mx4Tile {
       } else {
         // Small sets of fragments are held twice: after the barrier the next slice's
         // are read while this one's, read before it, are multiplied.
-        meet();
+        meet(X);
         if (X == 12) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) dma(q);
@@ -720,7 +747,7 @@ hipError_t tiles(const Mx4GemmArgs& g, hipStream_t stream) {
   const int tm = (g.m + BM - 1) / BM, tn = (g.n + BN - 1) / BN;
   const dim3 grid(static_cast<unsigned>(tm) * static_cast<unsigned>(tn)), block(Whole::kThreads);
   if (!grid_fits(static_cast<int64_t>(tm) * tn, Whole::kThreads)) return hipErrorInvalidConfiguration;
-  if (g.k % 128) return launch(mx4_gemm_tile_kernel<Tail>, grid, block, 0, stream, g, tm, tn);
+  if (g.k % (128 * Whole::kUnit)) return launch(mx4_gemm_tile_kernel<Tail>, grid, block, 0, stream, g, tm, tn);
   return launch(mx4_gemm_tile_kernel<Whole>, grid, block, 0, stream, g, tm, tn);
 }
 
@@ -733,8 +760,8 @@ hipError_t tiles(const Mx4GemmArgs& g, hipStream_t stream) {
 // 1024 to 16384 (rows in 32 x 32 / rows in 64 x 64 / tiles of 128 x 128: 64 x 4096 x
 // 4096 5.7 / 10.8 / 12.2; 128 x 14336 x 4096 23.9 / 19.9 / 14.0; 256 x 4096 x 14336
 // 31.3 / 23.8 / 35.4; 512 x 4096 x 4096 23.3 / 18.9 / 13.3.  Tiles of 128 x 128 / 256 x
-// 128 / 256 x 256: 2048 x 4096 x 4096 25.0 / 23.8 / 28.7; 4096 x 4096 x 14336
-// 154 / 144 / 109).  A workgroup's time grows with k; a CU takes one after the other.
+// 128 / 256 x 256: 2048 x 4096 x 4096 25.1 / 23.2 / 26.8; 4096 x 4096 x 14336
+// 154 / 139 / 97).  A workgroup's time grows with k; a CU takes one after the other.
 template <int DT>
 hipError_t by_size(const Mx4GemmArgs& g, hipStream_t stream) {
   if (g.m <= 16) {
@@ -748,8 +775,8 @@ hipError_t by_size(const Mx4GemmArgs& g, hipStream_t stream) {
   const double rounds1 = std::floor(count(128, 128) / 512), left1 = count(128, 128) - 512 * rounds1;
   const double rows22 = 3.0 + 0.075 * slices * waves22, rows44 = 3.5 + 0.24 * slices * waves44;
   const double tile1 = 5.0 + slices * (0.62 * rounds1 + (left1 > 256 ? 0.62 : left1 > 0 ? 0.25 : 0.0));
-  const double tile2 = 5.5 + slices * 0.58 * std::ceil(count(256, 128) / 256);
-  const double tile4 = 8.0 + slices * 0.97 * std::ceil(count(256, 256) / 256);
+  const double tile2 = 4.0 + (4.0 + slices * 0.47) * std::ceil(count(256, 128) / 256);
+  const double tile4 = 4.0 + (5.0 + slices * 0.80) * std::ceil(count(256, 256) / 256);
   const double best = std::min({rows22, rows44, tile1, tile2, tile4});
   if (best == tile4) return tiles<DT, 256, 256, 128, 64>(g, stream);
   if (best == tile2) return tiles<DT, 256, 128, 64, 64>(g, stream);
