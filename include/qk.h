@@ -8,7 +8,9 @@
  *   3. a dequant epilogue  out = acc * scale_a[row] * scale_b[col] * output_scale.
  * and the same layer with float8_e4m3fn codes (per-token FP8 quantization
  * with an optional scale bound, an FP8 x FP8 product accumulated in
- * binary32, the same epilogue).
+ * binary32, the same epilogue), or with microscaled 4-bit floating point on
+ * both sides.  Beside the layer stands what a decoder has between two of them:
+ * norms, the rotation by position, a paged 8-bit cache and the attention over it.
  *
  * Sources, cited by page title and section:
  *   "16. Deploying Custom Kernels", C++ Kernel Interface: the GEMM problem

@@ -47,6 +47,7 @@ constexpr int kCols64 = 64 * 400, kCols32 = 32 * 400;
 // registers that the instruction wants (16 bytes of 16 rows from neighbouring lanes)
 // they came at a quarter of the rate.  Nothing is shared until the end, so no wave
 // waits for another, and several workgroups of a CU keep the weight coming.
+// 1 x 14336 x 4096 (m, n, k) 6.9 us (4.5 TB/s, the launch included; loaded straight 10.6), 24 rows 8.8.
 template <int DT, int F, int R, int W, int S>
 __global__ __launch_bounds__(64 * W) void mx4_gemm_rows_kernel(Mx4GemmArgs g, unsigned tiles_n) {
   constexpr int kRow = 64 * S, kChunks = 4 * S;  // bytes, and 16-byte chunks, of a row in a stretch

@@ -142,7 +142,7 @@ __device__ __forceinline__ float head_sum(float v) {
 // multiple of 8 (4 for binary32 side by side) P is 1, and a lane takes U pairs, L apart.
 //
 // Bound by memory: 7690 rows of 32 + 8 heads of 128, bf16, 27 us (5.8 TB/s; 37 with
-// plain stores, 28.6 with two groups in flight per wave); r = 64 side by side 33 us;
+// plain stores, 28.6 with two groups in flight per wave); r = 64 side by side 26;
 // one row 3.0 us, 64 rows 3.3.
 template <int DT, int P, int L, int U, bool SIDE, bool PAST>
 __global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int parts, int groups) {
