@@ -65,6 +65,12 @@ def test_every_remainder_of_k(m, n, k):
     check(m, n, k, "f32")
 
 
+@pytest.mark.parametrize("k", [32, 224, 256, 384, 992, 1024, 1280, 1536, 1792, 1920, 2048, 2176, 2304, 3840, 4096, 4352, 6176, 8192])
+@pytest.mark.parametrize("m,n", [(2000, 4000), (700, 4096), (3100, 4096)])
+def test_every_number_of_slices_in_the_rings(m, n, k):
+    check(m, n, k, "bf16")
+
+
 def test_a_run_of_products_on_two_streams():
     # nothing is shared between calls
     gen = torch.Generator(device=DEV).manual_seed(1)

@@ -294,16 +294,18 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 // PFLOP/s, where 32x32x64 reaches 6.7; with all codes 0 both reach 9.5: the
 // power that the operands take holds the clock down).
 //
-// Slices of 128 k (64 bytes of a row, four blocks) go from memory to LDS, into a
-// ring that holds four.  In large tiles two come together, so that a transfer touches
-// 8 whole lines of 128 bytes and not 16 halves (8192 x 28672 x 8192: 837 us for 898;
-// 2048 x 4096 x 14336: 60.5 for 69), in small ones, of which few are under way at a time,
-// one by one (512 x 4096 x 4096: 13.2 us for 14.8).  A part of the ring is free as soon as
-// every wave has read its fragments, and is then asked for what comes four slices on.
+// Slices of 128 k (64 bytes of a row, four blocks) go from memory to LDS in pairs,
+// so that a transfer touches 8 whole lines of 128 bytes and not 16 halves (8192 x 28672 x
+// 8192: 837 us for 898; 2048 x 4096 x 14336: 60.5 for 69), into a ring of as many pairs
+// as LDS holds: two, or in 128 x 128 tiles four (512 x 4096 x 14336: 32.5 us; 35.9 with two
+// such workgroups on a CU and slices one by one, 39.7 with two of two pairs each).  A part of
+// the ring is free as soon as every wave has read its fragments, and is then asked for the
+// next pair.
 //
 // Figures: 8192 x 28672 x 8192 837 us (4.6 PFLOP/s; the products alone, from LDS that
 // nothing is brought to, 718; the stores, while which nothing is multiplied, 84 of
-// both), 4096 x 4096 x 14336 97, 2048 x 4096 x 4096 23.2 (21.6 and 4).
+// both), 4096 x 4096 x 14336 97, 2048 x 4096 x 4096 21.7 to 23.1 (of which stores 4),
+// 512 x 4096 x 4096 13.4.
 //
 // A lane's quarter of a wave is its block of a slice, and the byte of its scale
 // register that the instruction picks is the slice: the scales of four slices, 16
@@ -318,18 +320,17 @@ struct Mx4Tile {
   static constexpr int kWavesN = BN / WTN;
   static constexpr int kWaves = (BM / WTM) * kWavesN;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kUnit = BM * BN > 128 * 128 ? 2 : 1;  // slices that come together
-  static constexpr int kRing = 4 / kUnit;
-  static constexpr int kRow = 64 * kUnit;                    // bytes of a row in a unit
+  static constexpr int kRing = BM * BN > 128 * 128 ? 2 : 4;  // pairs of slices
+  static constexpr int kRow = 128;                           // bytes of a row in a pair
   static constexpr int kStageA = BM * kRow, kStageB = BN * kRow;
   static constexpr int kScales = kRing * (kStageA + kStageB);  // rows of 64 bytes of scales follow the ring
-  // Half of a CU's LDS or all of it: workgroups of anything between were
-  // started one after the other, some 50 ns apart (2048 x 4096 x 4096 on tiles of
-  // 256 x 128, 256 of them, with 136 KiB each: 34.6 us; with 160: 23.8).
   static constexpr int kUsed = kScales + kWaves * 64 * 64;
-  static constexpr int kSmem = kUsed <= 81920 ? 81920 : 163840;
+  // All of a CU's LDS, or half of it: workgroups of anything between were
+  // started one after the other, some 50 ns apart (2048 x 4096 x 4096 on 256 tiles,
+  // with 136 KiB each: 34.6 us; with 160: 23.8).
+  static constexpr int kSmem = 163840;
   static constexpr int kRowsAt = 1024 / kRow;             // rows of a transfer
-  static constexpr int kOps = (BM + BN) / kRowsAt / kWaves;  // transfers of a unit per wave
+  static constexpr int kOps = (BM + BN) / kRowsAt / kWaves;  // transfers of a pair per wave
   static constexpr int kPieces = (BM + BN) / 64;
   static constexpr int FM = WTM / 16, FN = WTN / 16;
   static constexpr int kElem = DT == QK_F32 ? 4 : 2;
@@ -337,7 +338,7 @@ struct Mx4Tile {
   static_assert(kPieces <= kWaves, "a thread for every row of scales");
   static_assert(kUsed <= kSmem && kWaves * 16384 <= kSmem, "LDS; 16 KiB of it per wave for the results");
   static_assert((kRing - 1) * kStageA + 16 * kRow * (FM - 1) < 65536 && (kRing - 1) * kStageB + 16 * kRow * (FN - 1) < 65536, "immediate offsets");
-  static_assert((FM == 8 || FM == 4) && FN == 4 && kOps <= 4 * kUnit, "the orders below");
+  static_assert((FM == 8 || FM == 4) && FN == 4 && kOps <= 8, "the orders below");
 
   typedef __attribute__((address_space(3))) const v4i* lds_v4i;
   typedef __attribute__((address_space(3))) v4i* lds_v4i_out;
@@ -347,7 +348,7 @@ struct Mx4Tile {
   // fragment (chunk c of rows 0 .. 15, c = 0 .. 3) go in sets of 16 that take half of their rows
   // from one chunk and half from the next; those fall on 16 different places of 256 bytes
   // with this key and not with, say, row / 4 of 64-byte rows, which took twice as long.
-  __device__ static int key(int row) { return kUnit == 2 ? row & 7 : (row >> 1) & 3; }
+  __device__ static int key(int row) { return row & 7; }
   __device__ static int row_offset(int row, int chunk) { return row * kRow + ((chunk ^ key(row)) << 4); }
   __device__ static int scale_offset(int row, int chunk) { return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4); }
 
@@ -369,12 +370,12 @@ struct Mx4Tile {
     };
 
     // ---- transfers ----
-    // part p of a unit: some rows (A's, then B's); the lanes bring their chunks
+    // part p of a pair: 8 rows (A's, then B's); the lanes bring their chunks
     const uint8_t* const base_a = uniform(g.a + static_cast<int64_t>(m0) * row_bytes);
     const uint8_t* const base_b = uniform(g.b + static_cast<int64_t>(n0) * row_bytes);
     uint32_t voff[kOps];
     const int part0 = wave * kOps;
-    const int row_at = lane / (4 * kUnit), chunk = lane % (4 * kUnit) ^ key(row_at);  // as row_offset has it
+    const int row_at = lane / 8, chunk = lane % 8 ^ key(row_at);  // as row_offset has it
 #pragma unroll
     for (int q = 0; q < kOps; ++q) {
       const bool is_a = (part0 + q) * kRowsAt < BM;
@@ -382,10 +383,10 @@ struct Mx4Tile {
       const int from = is_a ? min(m0 + row, g.m - 1) - m0 : min(n0 + row, g.n - 1) - n0;
       voff[q] = static_cast<uint32_t>(from) * static_cast<uint32_t>(row_bytes) + (KTAIL ? 0 : 16 * chunk);
     }
-    // the unit from slice s on, if there is s; blocks past k are read from the row's last
+    // slices s and s + 1 (s even), if there is s; blocks past k are read from the row's last
     auto issue = [&](int s, int q) {
       const bool is_a = (part0 + q) * kRowsAt < BM;
-      const int at = s / kUnit & (kRing - 1);
+      const int at = s / 2 & (kRing - 1);
       const uint32_t to =
           lds0 + (is_a ? at * kStageA : kRing * kStageA + at * kStageB - BM * kRow) + (part0 + q) * 1024;
       const uint8_t* const from = is_a ? base_a : base_b;
@@ -441,9 +442,9 @@ struct Mx4Tile {
     const uint32_t b_base = opaque(lds0 + kRing * kStageA + row_offset(wn * WTN + i16, c4));
     const uint32_t sa_base = opaque(lds0 + kScales + scale_offset(wm * WTM + i16, 0) + 4 * c4);
     const uint32_t sb_base = opaque(lds0 + kScales + scale_offset(BM + wn * WTN + i16, 0) + 4 * c4);
-    // of slice S of the ring's four
-    auto read_a = [&](int S, int i) { return *reinterpret_cast<lds_v4i>((a_base ^ (S % kUnit) << 6) + S / kUnit * kStageA + 16 * kRow * i); };
-    auto read_b = [&](int S, int j) { return *reinterpret_cast<lds_v4i>((b_base ^ (S % kUnit) << 6) + S / kUnit * kStageB + 16 * kRow * j); };
+    // of slice S of the ring's
+    auto read_a = [&](int S, int i) { return *reinterpret_cast<lds_v4i>((a_base ^ (S % 2) << 6) + S / 2 * kStageA + 16 * kRow * i); };
+    auto read_b = [&](int S, int j) { return *reinterpret_cast<lds_v4i>((b_base ^ (S % 2) << 6) + S / 2 * kStageB + 16 * kRow * j); };
     v4f acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -467,7 +468,7 @@ struct Mx4Tile {
 #pragma unroll
       for (int q = 0; q < 4; ++q) issue_scales(0, q);
 #pragma unroll
-      for (int s = 0; s < 4; s += kUnit)
+      for (int s = 0; s < 2 * kRing; s += 2)
 #pragma unroll
         for (int q = 0; q < kOps; ++q) issue(s, q);
       wait_vmcnt<(kRing - 1) * kOps>();
@@ -481,30 +482,29 @@ struct Mx4Tile {
     }
 
     // Slice kt, X its number modulo 16 (a constant wherever it is used).  At the
-    // barrier in a unit's last slice the next unit has landed, for every wave, and every
-    // wave has read the last of this one, whose part of the ring is then asked for a
-    // unit four slices on.  The last scales of a batch are read in slice 11, so the next
-    // batch may come over it from slice 12's barrier on; in slice 14 it is there, each thread
+    // barrier in an odd slice the next pair has landed, for every wave, and every wave
+    // has read the last of this one, whose part of the ring is then asked for the next
+    // pair but kRing - 1.  The last scales of a batch are read in slice 11, so the next batch
+    // may come over it from slice 12's barrier on; in slice 14 it is there, each thread
     // transposes what its own wave brought, and it is read behind slice 15's barrier.
     // (Loads arrive in order: the waits count those that may still be under way, in
-    // slice 13 of pairs the scales.)
+    // slice 13 the scales among them.)
     auto meet = [&](int X) {
-      if (X % kUnit != kUnit - 1 && X != 12) return;
-      if (kUnit == 1) wait_vmcnt<2 * kOps>();
-      else if (X == 13) wait_vmcnt<4>();
-      else if (X != 12) wait_vmcnt<0>();
+      if (X % 2 == 0 && X != 12) return;
+      if (X == 13) wait_vmcnt<(kRing - 2) * kOps + 4>();
+      else if (X != 12) wait_vmcnt<(kRing - 2) * kOps>();
       __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
       barrier();
     };
     auto slice = [&](int X, int kt) __attribute__((always_inline)) {
-      const int S = X & 3, SN = (X + 1) & 3;
+      const int S = X & (2 * kRing - 1), SN = (X + 1) & (2 * kRing - 1);
       const int next = (kt >> 4) + 1;  // the next batch of scales
       auto mfma = [&](int i, int j) {
         // the byte's number is part of the instruction
-        if (S == 0) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 0, sb[j], 0, sa[i]);
-        if (S == 1) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 1, sb[j], 1, sa[i]);
-        if (S == 2) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 2, sb[j], 2, sa[i]);
-        if (S == 3) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 3, sb[j], 3, sa[i]);
+        if ((X & 3) == 0) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 0, sb[j], 0, sa[i]);
+        if ((X & 3) == 1) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 1, sb[j], 1, sa[i]);
+        if ((X & 3) == 2) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 2, sb[j], 2, sa[i]);
+        if ((X & 3) == 3) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[j]), operand(fa[i]), acc[i][j], kFp4, kFp4, 3, sb[j], 3, sa[i]);
         pin();
       };
       auto dma = [&](int q) {
@@ -513,8 +513,8 @@ struct Mx4Tile {
       };
       auto data = [&](int q) {
 #pragma unroll
-        for (int j = 0; j < kUnit; ++j)
-          if (X % kUnit == kUnit - 1 && kUnit * q + j < kOps) issue(kt + 5 - kUnit, kUnit * q + j);
+        for (int j = 0; j < 2; ++j)
+          if (X % 2 == 1 && 2 * q + j < kOps) issue(kt + 2 * kRing - 1, 2 * q + j);
         pin();
       };
       v4i raw[2];
@@ -528,7 +528,7 @@ struct Mx4Tile {
           if (part < FN) tb[part] = scale_b(chunk, part);
           else if (part < FN + FM) ta[part - FN] = scale_a(chunk, part - FN);
         }
-        if (kUnit == 2 && X == 14 && part == 0) {
+        if (X == 14 && part == 0) {
           wait_vmcnt<kOps>();
           asm volatile("" ::: "memory");
         }
@@ -550,7 +550,7 @@ struct Mx4Tile {
         fb[2] = read_b(S, 2);
         fb[3] = read_b(S, 3);
         mfma(1, 1);
-        if (S == 0) {
+        if ((X & 3) == 0) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) sa[4 + x] = scale_a(X >> 2, 4 + x);
           sb[2] = scale_b(X >> 2, 2);
@@ -639,7 +639,7 @@ struct Mx4Tile {
         for (int i = 0; i < FM; ++i) fa[i] = na[i];
 #pragma unroll
         for (int j = 0; j < FN; ++j) fb[j] = nb[j];
-        if (S == 3) {
+        if ((X & 3) == 3) {
 #pragma unroll
           for (int i = 0; i < FM; ++i) sa[i] = ta[i];
 #pragma unroll
@@ -748,7 +748,7 @@ hipError_t tiles(const Mx4GemmArgs& g, hipStream_t stream) {
   const int tm = (g.m + BM - 1) / BM, tn = (g.n + BN - 1) / BN;
   const dim3 grid(static_cast<unsigned>(tm) * static_cast<unsigned>(tn)), block(Whole::kThreads);
   if (!grid_fits(static_cast<int64_t>(tm) * tn, Whole::kThreads)) return hipErrorInvalidConfiguration;
-  if (g.k % (128 * Whole::kUnit)) return launch(mx4_gemm_tile_kernel<Tail>, grid, block, 0, stream, g, tm, tn);
+  if (g.k % 256) return launch(mx4_gemm_tile_kernel<Tail>, grid, block, 0, stream, g, tm, tn);
   return launch(mx4_gemm_tile_kernel<Whole>, grid, block, 0, stream, g, tm, tn);
 }
 
@@ -759,10 +759,12 @@ hipError_t tiles(const Mx4GemmArgs& g, hipStream_t stream) {
 //
 // Beyond, the least estimated time, in us, from what was measured with k from
 // 1024 to 16384 (rows in 32 x 32 / rows in 64 x 64 / tiles of 128 x 128: 64 x 4096 x
-// 4096 5.7 / 10.8 / 12.2; 128 x 14336 x 4096 23.9 / 19.9 / 14.0; 256 x 4096 x 14336
-// 31.3 / 23.8 / 35.4; 512 x 4096 x 4096 23.3 / 18.9 / 13.3.  Tiles of 128 x 128 / 256 x
-// 128 / 256 x 256: 2048 x 4096 x 4096 25.1 / 23.2 / 26.8; 4096 x 4096 x 14336
-// 154 / 139 / 97).  A workgroup's time grows with k; a CU takes one after the other.
+// 4096 5.7 / 10.8 / 12.2; 128 x 14336 x 4096 23.9 / 19.9 / 13.8; 256 x 4096 x 14336
+// 31.3 / 23.8 / 32; 512 x 4096 x 4096 23.3 / 18.9 / 13.4.  Tiles of 128 x 128 / 128 x
+// 256 / 256 x 256: 1024 x 4096 x 4096 15.1 / 20.2 / 26; 1500 x 4096 x 4096 26.7 / 20.8 / 27.4;
+// 2048 x 4096 x 4096 29.2 / 23.1 / 27.4; 4096 x 4096 x 4096 - / 44.6 / 36.8.  256 x 128 took
+// 23.7 and 46.2 for 23.1 and 44.6: shorter rows of results).  A workgroup's time grows
+// with k; a CU takes one after the other.
 template <int DT>
 hipError_t by_size(const Mx4GemmArgs& g, hipStream_t stream) {
   if (g.m <= 16) {
@@ -773,14 +775,13 @@ hipError_t by_size(const Mx4GemmArgs& g, hipStream_t stream) {
   if (g.m <= 32) return g.n >= kCols32 ? rows<DT, 2, 2, 4, 4>(g, stream) : rows<DT, 2, 1, 4, 4>(g, stream);
   auto count = [&](int bm, int bn) { return static_cast<double>((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn); };
   const double slices = (g.k + 127) / 128, waves22 = std::max(count(32, 32) / 256, 1.0), waves44 = std::max(count(64, 64) / 256, 1.0);
-  const double rounds1 = std::floor(count(128, 128) / 512), left1 = count(128, 128) - 512 * rounds1;
   const double rows22 = 3.0 + 0.075 * slices * waves22, rows44 = 3.5 + 0.24 * slices * waves44;
-  const double tile1 = 5.0 + slices * (0.62 * rounds1 + (left1 > 256 ? 0.62 : left1 > 0 ? 0.25 : 0.0));
-  const double tile2 = 4.0 + (4.0 + slices * 0.47) * std::ceil(count(256, 128) / 256);
-  const double tile4 = 4.0 + (5.0 + slices * 0.80) * std::ceil(count(256, 256) / 256);
+  auto rounds = [&](int bm, int bn) { return std::ceil(count(bm, bn) / 256); };
+  const double tile1 = 3.4 + (2.4 + slices * 0.24) * rounds(128, 128), tile2 = 3.5 + (3.8 + slices * 0.49) * rounds(128, 256);
+  const double tile4 = 4.0 + (5.0 + slices * 0.80) * rounds(256, 256);
   const double best = std::min({rows22, rows44, tile1, tile2, tile4});
   if (best == tile4) return tiles<DT, 256, 256, 128, 64>(g, stream);
-  if (best == tile2) return tiles<DT, 256, 128, 64, 64>(g, stream);
+  if (best == tile2) return tiles<DT, 128, 256, 64, 64>(g, stream);
   if (best == tile1) return tiles<DT, 128, 128, 64, 64>(g, stream);
   return best == rows44 ? rows<DT, 4, 4, 4, 2>(g, stream) : rows<DT, 2, 2, 4, 4>(g, stream);
 }
