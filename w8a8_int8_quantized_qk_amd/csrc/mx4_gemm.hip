@@ -47,7 +47,7 @@ constexpr int kCols64 = 64 * 400, kCols32 = 32 * 400;
 // registers that the instruction wants (16 bytes of 16 rows from neighbouring lanes)
 // they came at a quarter of the rate.  Nothing is shared until the end, so no wave
 // waits for another, and several workgroups of a CU keep the weight coming.
-// 1 x 14336 x 4096 (m, n, k) 6.9 us (4.5 TB/s, the launch included; loaded straight 10.6), 24 rows 8.8.
+// 1 x 14336 x 4096 (m, n, k) 6.9 us (4.5 TB/s, the launch included; loaded straight 10.6), 24 rows 8.0.
 template <int DT, int F, int R, int W, int S>
 __global__ __launch_bounds__(64 * W) void mx4_gemm_rows_kernel(Mx4GemmArgs g, unsigned tiles_n) {
   constexpr int kRow = 64 * S, kChunks = 4 * S;  // bytes, and 16-byte chunks, of a row in a stretch
@@ -755,7 +755,8 @@ hipError_t tiles(const Mx4GemmArgs& g, hipStream_t stream) {
 // Up to 32 rows: as many columns to a workgroup as leave enough of them (28672,
 // 14336 and 4096 columns in 64 / 32 / 16: one row of 4096 k 7.9 / 6.9 / 7.4 us with
 // 14336, 16 rows of 8192 k 28.6 / 29.8 / 30.2 with 28672, of 4096 k 5.9 / 4.6 / 3.8
-// with 4096; 24 rows of 4096 k 8.9 in 32 and 9.6 in 16 with 14336).
+// with 4096; 24 rows of 4096 k 8.0 in 32 by two waves, 9.0 by four, 9.7 in 16 with 14336;
+// 32 rows of 8192 k 34.2 / 35.2 / 39.5 with 28672; 24 of 4096 k 5.8 / 5.2 / 4.7 with 4096).
 //
 // Beyond, the least estimated time, in us, from what was measured with k from
 // 1024 to 16384 (rows in 32 x 32 / rows in 64 x 64 / tiles of 128 x 128: 64 x 4096 x
@@ -772,7 +773,7 @@ hipError_t by_size(const Mx4GemmArgs& g, hipStream_t stream) {
     if (g.n >= kCols32) return rows<DT, 1, 2, 4, 4>(g, stream);
     return rows<DT, 1, 1, 8, 4>(g, stream);
   }
-  if (g.m <= 32) return g.n >= kCols32 ? rows<DT, 2, 2, 4, 4>(g, stream) : rows<DT, 2, 1, 4, 4>(g, stream);
+  if (g.m <= 32) return g.n >= kCols32 ? rows<DT, 2, 2, 2, 4>(g, stream) : rows<DT, 2, 1, 4, 4>(g, stream);
   auto count = [&](int bm, int bn) { return static_cast<double>((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn); };
   const double slices = (g.k + 127) / 128, waves22 = std::max(count(32, 32) / 256, 1.0), waves44 = std::max(count(64, 64) / 256, 1.0);
   const double rows22 = 3.0 + 0.075 * slices * waves22, rows44 = 3.5 + 0.24 * slices * waves44;
