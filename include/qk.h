@@ -552,7 +552,8 @@ int qk_linear_mx4(int m, int n, int k, const void *x, int64_t ldx, int x_dtype, 
  * What stands between the projections and the cache, for every head of every
  * row in one launch: the root-mean-square norm over the head's elements and
  * the rotation by the row's position.
- *   y = (x * inv) * weight,  inv = 1 / sqrt(mean(x^2) + eps)   (binary32)
+ *   y = (x * inv) * weight,  inv = 1 / sqrt(mean(x^2) + eps)   (binary32; the mean
+ *   of any finite head, its squares in binary64 where binary32 does not hold them)
  *   for i < rotary / 2, with (a, b) = (i, i + rotary / 2), or (2 i, 2 i + 1)
  *   when interleaved:
  *     out[a] = y[a] cos t - y[b] sin t,  out[b] = y[b] cos t + y[a] sin t,

@@ -1,6 +1,7 @@
 // Root-mean-square norm of every head's query and key and the rotation by its
 // position, in one pass, for gfx950:
-//   y = (x * inv) * w,  inv = 1 / sqrt(mean(x^2) + eps)    (binary32; y = x without w)
+//   y = (x * inv) * w,  inv = 1 / sqrt(mean(x^2) + eps)    (binary32, and the mean in
+//                       binary64 where its squares leave that; y = x without w)
 //   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)
 // for the pairs (a, b) = (i, i + r / 2), or (2 i, 2 i + 1), of a head's first r
 // elements, at the angle position * freqs[i]; the other elements keep y.
@@ -28,6 +29,9 @@ constexpr int64_t kFill = 16384;  // waves that keep the memory busy (4096: 29.2
 // Outputs beyond this are stored past the caches, which do not hold them until they
 // are read.
 constexpr int64_t kPastCaches = 8 << 20;
+// A mean (with eps) from here on has lost nothing to squares below binary32's range:
+// those of a head of 256 are less than 2^-141 together.
+constexpr float kLeastMean = 0x1p-100f;
 
 struct Turn {
   float cos, sin;
@@ -109,26 +113,36 @@ __device__ __forceinline__ void store(char* p, const float* f) {
   }
 }
 
+// A value of the lane that `move` names for each half of its bits: of binary32
+// in one exchange, of binary64 in two.
+template <typename F>
+__device__ __forceinline__ float exchanged(float v, F move) { return __uint_as_float(move(__float_as_uint(v))); }
+template <typename F>
+__device__ __forceinline__ double exchanged(double v, F move) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
+  const uint32_t lo = move(static_cast<uint32_t>(b)), hi = move(static_cast<uint32_t>(b >> 32));
+  return __longlong_as_double(static_cast<long long>(static_cast<uint64_t>(hi) << 32 | lo));
+}
+
 // Sum over the L neighbouring lanes that hold a head.
-template <int L>
-__device__ __forceinline__ float head_sum(float v) {
+template <int L, typename T>
+__device__ __forceinline__ T head_sum(T v) {
   auto from = [&](auto ctrl) {
-    return __uint_as_float(static_cast<uint32_t>(
-        __builtin_amdgcn_mov_dpp(static_cast<int>(__float_as_uint(v)), decltype(ctrl)::value, 0xF, 0xF, false)));
+    return exchanged(v, [](uint32_t b) {
+      return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(b), decltype(ctrl)::value, 0xF, 0xF, false));
+    });
   };
   v += from(std::integral_constant<int, 0xB1>{});                         // lane ^ 1
   v += from(std::integral_constant<int, 0x4E>{});                         // lane ^ 2
   if constexpr (L >= 8) v += from(std::integral_constant<int, 0x141>{});  // the other four of eight
   if constexpr (L >= 16) v += from(std::integral_constant<int, 0x140>{}); // the other eight of 16
   if constexpr (L >= 32) {
-    const uint32_t b = __float_as_uint(v);
-    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    v = exchanged(v, [](uint32_t b) { return __builtin_amdgcn_permlane16_swap(b, b, false, false)[0]; }) +
+        exchanged(v, [](uint32_t b) { return __builtin_amdgcn_permlane16_swap(b, b, false, false)[1]; });
   }
   if constexpr (L >= 64) {
-    const uint32_t b = __float_as_uint(v);
-    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    v = exchanged(v, [](uint32_t b) { return __builtin_amdgcn_permlane32_swap(b, b, false, false)[0]; }) +
+        exchanged(v, [](uint32_t b) { return __builtin_amdgcn_permlane32_swap(b, b, false, false)[1]; });
   }
   return v;
 }
@@ -143,9 +157,11 @@ __device__ __forceinline__ float head_sum(float v) {
 //
 // Bound by memory: 7690 rows of 32 + 8 heads of 128, bf16, 27 us (5.8 TB/s; 37 with
 // plain stores, 28.6 with two groups in flight per wave); r = 64 side by side 26;
-// one row 3.0 us, 64 rows 3.3.
+// one row 3.0 us, 64 rows 3.3.  (Eight waves a SIMD are asked for where that costs no
+// scratch: 27.4 us for 26.3 at r = 64 side by side, 34.6 for 31.9 at 4000 rows of 40 heads of 80 where P is 1; with P = 8
+// values went to scratch, 9.7 for 7.9 us at 4000 rows of 40 heads of 64.)
 template <int DT, int P, int L, int U, bool SIDE, bool PAST>
-__global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int parts, int groups) {
+__global__ __launch_bounds__(kBlock, SIDE || P == 1 ? 8 : 1) void norm_rope_kernel(NormRopeArgs a, int parts, int groups) {
   constexpr int B = Elem<DT>::kBytes;
   constexpr int kHeads = 64 / L;  // of a group
   __shared__ Turn all_turns[kWaves][kMostPairs];
@@ -235,8 +251,30 @@ __global__ __launch_bounds__(kBlock) void norm_rope_kernel(NormRopeArgs a, int p
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int e = 0; e < 2 * P; ++e) sum = __builtin_fmaf(x[u][e], x[u][e], sum);
-        sum = head_sum<L>(sum);
-        const float inv = 1.0f / __builtin_sqrtf(sum / static_cast<float>(a.dim) + a.eps);
+        const float mean = head_sum<L>(sum) / static_cast<float>(a.dim) + a.eps;
+        float inv = 1.0f / __builtin_sqrtf(mean);
+        // Squares that left binary32's range (beyond it, or too small beside eps): the
+        // sum again in binary64, and a power of two in x where the quotient has no
+        // binary32 of full precision.  Heads in range keep what they have; binary16's
+        // squares are all in range.
+        const bool out_of_range = h < heads && !(mean >= kLeastMean && mean < __builtin_inff());
+        if (DT != QK_F16 && __any(out_of_range)) [[unlikely]] {
+          double wide = 0.0;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 2 * P; ++e) {
+              const double d = static_cast<double>(x[u][e]);
+              wide = __builtin_fma(d, d, wide);
+            }
+          wide = 1.0 / sqrt(head_sum<L>(wide) / static_cast<double>(a.dim) + static_cast<double>(a.eps));
+          const float raise = !out_of_range ? 1.0f : wide > 0x1p126 ? 0x1p32f : wide < 0x1p-126 ? 0x1p-8f : 1.0f;
+          if (out_of_range) inv = static_cast<float>(wide / static_cast<double>(raise));
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 2 * P; ++e) x[u][e] *= raise;
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
