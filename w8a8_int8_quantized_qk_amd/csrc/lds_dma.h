@@ -13,9 +13,11 @@ namespace qk {
 // LDS read as possibly aliasing the transfer (which makes it wait for all
 // outstanding loads before each read); completion is tracked explicitly with
 // wait_vmcnt before the data is read.  The instruction
-// has no register results.  m0 is written here and nowhere else in the kernel.
+// has no register results.  m0 is written here and nowhere else in the kernel;
+// between a scalar write of m0 and a load that takes its LDS address from it the
+// hardware wants one wait state, which the compiler adds to its own code but not here.
 __device__ __forceinline__ void lds_dma16(const void* g, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :
                : "v"(g), "s"(lds_base)
                : "memory", "m0");
@@ -25,7 +27,7 @@ __device__ __forceinline__ void lds_dma16(const void* g, uint32_t lds_base) {
 // scalar registers and this lane's unsigned 32-bit offset: advancing the base
 // is then scalar arithmetic, not a 64-bit vector add per instruction.
 __device__ __forceinline__ void lds_dma16_split(const void* sbase, uint32_t voff, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
                : "v"(voff), "s"(sbase), "s"(lds_base)
                : "memory", "m0");
