@@ -25,6 +25,8 @@
 #include <string>
 #include <utility>
 
+#include "mx4_rule.h"
+
 namespace {
 
 // libqk's entry points (include/qk.h), as addresses handed over by the
@@ -638,9 +640,7 @@ PyObject* linear_mx4(PyObject* const* a, Py_ssize_t n) {
   const c10::DeviceGuard guard(dev);
   const at::Tensor out = product_out(a[5], integer(a[4]), m, w.rows, dev);
   const int64_t lds = padded(k / 32);
-  // up to 16 aligned rows are quantised within the product of a small weight
-  const int64_t row = ldx * x.element_size();
-  const bool at_once = m <= 16 && k > 0 && w.rows * k <= 1 << 24 && reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0 && (m <= 1 || row % 16 == 0);
+  const bool at_once = qk::mx4_linear_at_once(m, w.rows, k, x.data_ptr(), ldx * x.element_size());
   at::Tensor codes;  // and their scales behind them
   if (!at_once) codes = make({m * (k / 2 + lds)}, at::kByte, dev);
   uint8_t* const q = at_once ? nullptr : static_cast<uint8_t*>(codes.data_ptr());

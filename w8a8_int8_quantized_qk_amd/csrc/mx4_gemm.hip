@@ -797,15 +797,6 @@ hipError_t launch_gemm_mx4(const Mx4GemmArgs& g, hipStream_t stream) {
   }
 }
 
-// Where the weight is small.  One launch / two, from a graph, and called one by one
-// (where a second launch costs the host 3 us): 1 x 4096 x 4096 4.7 / 4.7 and 4.7 / 7.9 us;
-// 16 x 4096 x 4096 5.8 / 5.4 and 5.7 / 7.8; 1 x 14336 x 4096 10.0 / 9.0 and 9.7 / 8.7; 16 x 4096
-// x 14336 13.5 / 9.3 and 13.2 / 9.1: quantising again in every workgroup grows with n k.
-bool linear_mx4_rows_applies(const Mx4GemmArgs& g, const void* x, int64_t ldx, int x_dtype) {
-  const int64_t b = x_dtype == QK_F32 ? 4 : 2;
-  return g.m <= 16 && g.k > 0 && static_cast<int64_t>(g.n) * g.k <= 1 << 24 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && (g.m == 1 || ldx * b % 16 == 0);
-}
-
 hipError_t launch_linear_mx4_rows(const Mx4GemmArgs& g, const void* x, int64_t ldx, int x_dtype, hipStream_t stream) {
   switch (g.out_dtype) {
     case QK_F32: return linear_by_type<QK_F32>(g, x, ldx, x_dtype, stream);

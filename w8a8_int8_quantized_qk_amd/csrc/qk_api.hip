@@ -3,6 +3,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "mx4_rule.h"
 #include "qk_internal.h"
 
 #define QK_STR2(x) #x
@@ -762,7 +763,7 @@ int qk_linear_mx4(int m, int n, int k, const void* x, int64_t ldx, int x_dtype, 
       !mx4_fits(m, n, k, 0, ldsb))
     return QK_ERR_UNSUPPORTED;
   const qk::Mx4GemmArgs g{m, n, k, q_out, scale_out, lds_out, b, scale_b, ldsb, output_scale, out, out_dtype};
-  if (qk::linear_mx4_rows_applies(g, x, ldx, x_dtype))
+  if (qk::mx4_linear_at_once(m, n, k, x, ldx * (x_dtype == QK_F32 ? 4 : 2)))
     return status_of_cut(qk::launch_linear_mx4_rows(g, x, ldx, x_dtype, stream));
   if (lds_out > kMx4MostStride) return QK_ERR_UNSUPPORTED;
   const int quantised = qk_quant_mx4(m, k, x, ldx, x_dtype, q_out, scale_out, lds_out, stream);

@@ -210,8 +210,8 @@ struct Mx4GemmArgs {
   int out_dtype;
 };
 hipError_t launch_gemm_mx4(const Mx4GemmArgs& g, hipStream_t stream);
-// Few rows of x [m][k] quantised within the product (a and scale_a are not used).
-bool linear_mx4_rows_applies(const Mx4GemmArgs& g, const void* x, int64_t ldx, int x_dtype);
+// Few rows of x [m][k] quantised within the product (a and scale_a are not used),
+// where mx4_linear_at_once (mx4_rule.h) says so.
 hipError_t launch_linear_mx4_rows(const Mx4GemmArgs& g, const void* x, int64_t ldx, int x_dtype, hipStream_t stream);
 
 // Norm of each head's query and key and their rotation (norm_rope.hip).  Row
