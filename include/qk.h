@@ -54,7 +54,7 @@
 extern "C" {
 #endif
 
-#define QK_ABI_VERSION 8
+#define QK_ABI_VERSION 9
 
 /* element types */
 #define QK_F32 0
