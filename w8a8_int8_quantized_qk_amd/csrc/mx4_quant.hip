@@ -14,10 +14,12 @@
 //
 // Bound by memory: four lanes share a block, eight values (16 or 32 bytes)
 // each, so a wave reads 1 KiB of 16-bit rows in one piece and writes 256 bytes
-// of codes and 16 of scales.  bf16, 4096 x 14336 there 28.1 us (5.3 TB/s), back 18.3
-// (8.1, its last stores still on their way), one after the other 49.2 (6.0);
-// 8 x 4096 2.0 us either way.  Reading past the caches there gains nothing (27.7);
-// the values of large calls are stored past them on the way back (29.4 without).
+// of codes and 16 of scales.  bf16, 4096 x 14336 there 27.1 us (5.5 TB/s), back 21.6
+// (6.9), one after the other 48.8 (6.1); of silu(gate) * up 56 (4.7); 8 x 4096 2.3 us
+// either way.  Reading past the caches there gains nothing (27.7).  On the way back the
+// 16-bit values of large calls are stored past them (22.5 us without, and 29.8 for 21.6
+// where three outputs take turns; 2048 x 4096 3.9 for 4.8), binary32's, of which a lane
+// has two pieces, not (88 us for 51).
 #include "kv_common.h"
 #include "mx4.h"
 
@@ -29,7 +31,7 @@ using qm::Elem;
 
 constexpr int kBlock = 256;
 constexpr int kEach = 8;  // values per lane, a quarter of a block
-constexpr int64_t kPastCaches = 8 << 20;  // bytes of values that are stored past the caches
+constexpr int64_t kPastCaches = 8 << 20;  // bytes of 16-bit values that are stored past the caches
 
 // Eight values at any alignment the element type allows.
 template <int DT>
@@ -87,27 +89,29 @@ __global__ __launch_bounds__(kBlock) void mx4_dequant_kernel(const uint8_t* __re
   const pair_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1),
                c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
   v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
-  if (byte == 255) {
+  constexpr int B = Elem<DT>::kBytes, W = kEach * B / 4;  // words
+  constexpr uint32_t kNaN = DT == QK_F32 ? 0x7fc00000u : DT == QK_BF16 ? 0x7fc07fc0u : 0x7e007e00u;
+  uint32_t out[W];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) v[e] = __builtin_nanf("");
-  }
-  constexpr int B = Elem<DT>::kBytes;
-  kv::Loose16* const to = reinterpret_cast<kv::Loose16*>(x + (row * ldx + static_cast<int64_t>(at) * kEach) * B);
-#pragma unroll
-  for (int h = 0; h < kEach * B / 16; ++h) {
-    kv::Loose16 out;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (DT == QK_F32)
-        out[e] = __float_as_uint(v[4 * h + e]);
-      else
-        out[e] = qm::pack2_narrow<DT>(v[2 * e], v[2 * e + 1]);
-    }
-    if constexpr (PAST)
-      __builtin_nontemporal_store(out, to + h);
+  for (int i = 0; i < W; ++i) {
+    if constexpr (DT == QK_F32)
+      out[i] = __float_as_uint(v[i]);
     else
-      to[h] = out;
+      out[i] = qm::pack2_narrow<DT>(v[2 * i], v[2 * i + 1]);
+    out[i] = byte == 255 ? kNaN : out[i];
   }
+  kv::Loose16* const to = reinterpret_cast<kv::Loose16*>(x + (row * ldx + static_cast<int64_t>(at) * kEach) * B);
+  // (not in a loop: out of one of a single turn the compiler moved the store, and
+  // that went through the caches)
+  auto put = [&](int h) {
+    const kv::Loose16 piece = {out[4 * h], out[4 * h + 1], out[4 * h + 2], out[4 * h + 3]};
+    if constexpr (PAST)
+      __builtin_nontemporal_store(piece, to + h);
+    else
+      to[h] = piece;
+  };
+  put(0);
+  if constexpr (W == 8) put(1);
 }
 
 dim3 grid_of(int64_t items) { return dim3(static_cast<unsigned>((items + kBlock - 1) / kBlock)); }
@@ -123,9 +127,14 @@ hipError_t quant(const Mx4RowsArgs& a, int64_t items, uint32_t per_row, hipStrea
 
 template <int DT>
 hipError_t dequant(const Mx4RowsArgs& a, int64_t items, uint32_t per_row, hipStream_t stream) {
-  const bool past = items * kEach * Elem<DT>::kBytes > kPastCaches;
-  return launch(past ? mx4_dequant_kernel<DT, true> : mx4_dequant_kernel<DT, false>, grid_of(items), dim3(kBlock), 0, stream,
-                a.q, a.scale, a.lds, items, per_row, static_cast<char*>(const_cast<void*>(a.x)), a.ldx);
+  char* const x = static_cast<char*>(const_cast<void*>(a.x));
+  if constexpr (DT != QK_F32) {
+    if (items * kEach * Elem<DT>::kBytes > kPastCaches)
+      return launch(mx4_dequant_kernel<DT, true>, grid_of(items), dim3(kBlock), 0, stream, a.q, a.scale, a.lds, items,
+                    per_row, x, a.ldx);
+  }
+  return launch(mx4_dequant_kernel<DT, false>, grid_of(items), dim3(kBlock), 0, stream, a.q, a.scale, a.lds, items, per_row,
+                x, a.ldx);
 }
 
 }  // namespace
