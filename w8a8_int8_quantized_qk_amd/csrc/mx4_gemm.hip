@@ -9,11 +9,9 @@
 //
 // The weight's rows are the first operand: a lane's four sums are then four
 // consecutive columns of one output row.
-#include <algorithm>
-#include <cmath>
-
 #include "gemm_tile.h"
 #include "mx4.h"
+#include "mx4_rule.h"
 
 namespace qk {
 namespace {
@@ -36,9 +34,6 @@ __device__ __forceinline__ void put(void* out, int64_t at, float v) {
 }
 
 // ---- few rows ----
-
-// Columns from which a workgroup of few rows has 64, or 32, of them: 400 workgroups.
-constexpr int kCols64 = 64 * 400, kCols32 = 32 * 400;
 
 // Bound by the weight's bytes.  A workgroup has 16 R columns (rows of the weight)
 // and 16 F rows of A; its W waves take stretches of S slices of 128 k in turn, and
@@ -252,8 +247,8 @@ template <int DT, int XT>
 hipError_t linear_rows(const Mx4GemmArgs& g, const void* x, int64_t ldx, hipStream_t stream) {
   const char* const from = static_cast<const char*>(x);
   auto grid = [&](int cols) { return dim3(static_cast<unsigned>((g.n + cols - 1) / cols)); };
-  if (g.n >= kCols64) return launch(mx4_linear_rows_kernel<DT, XT, 4, 4>, grid(64), dim3(256), 0, stream, g, from, ldx);
-  if (g.n >= kCols32) return launch(mx4_linear_rows_kernel<DT, XT, 2, 4>, grid(32), dim3(256), 0, stream, g, from, ldx);
+  if (g.n >= kMx4Cols64) return launch(mx4_linear_rows_kernel<DT, XT, 4, 4>, grid(64), dim3(256), 0, stream, g, from, ldx);
+  if (g.n >= kMx4Cols32) return launch(mx4_linear_rows_kernel<DT, XT, 2, 4>, grid(32), dim3(256), 0, stream, g, from, ldx);
   return launch(mx4_linear_rows_kernel<DT, XT, 1, 8>, grid(16), dim3(512), 0, stream, g, from, ldx);
 }
 
@@ -752,39 +747,20 @@ hipError_t tiles(const Mx4GemmArgs& g, hipStream_t stream) {
   return launch(mx4_gemm_tile_kernel<Whole>, grid, block, 0, stream, g, tm, tn);
 }
 
-// Up to 32 rows: as many columns to a workgroup as leave enough of them (28672,
-// 14336 and 4096 columns in 64 / 32 / 16: one row of 4096 k 7.9 / 6.9 / 7.4 us with
-// 14336, 16 rows of 8192 k 28.6 / 29.8 / 30.2 with 28672, of 4096 k 5.9 / 4.6 / 3.8
-// with 4096; 24 rows of 4096 k 8.0 in 32 by two waves, 9.0 by four, 9.7 in 16 with 14336;
-// 32 rows of 8192 k 34.2 / 35.2 / 39.5 with 28672; 24 of 4096 k 5.8 / 5.2 / 4.7 with 4096).
-//
-// Beyond, the least estimated time, in us, from what was measured with k from
-// 1024 to 16384 (rows in 32 x 32 / rows in 64 x 64 / tiles of 128 x 128: 64 x 4096 x
-// 4096 5.7 / 10.8 / 12.2; 128 x 14336 x 4096 23.9 / 19.9 / 13.8; 256 x 4096 x 14336
-// 31.3 / 23.8 / 32; 512 x 4096 x 4096 23.3 / 18.9 / 13.4.  Tiles of 128 x 128 / 128 x
-// 256 / 256 x 256: 1024 x 4096 x 4096 15.1 / 20.2 / 26; 1500 x 4096 x 4096 26.7 / 20.8 / 27.4;
-// 2048 x 4096 x 4096 29.2 / 23.1 / 27.4; 4096 x 4096 x 4096 - / 44.6 / 36.8.  256 x 128 took
-// 23.7 and 46.2 for 23.1 and 44.6: shorter rows of results).  A workgroup's time grows
-// with k; a CU takes one after the other.
 template <int DT>
 hipError_t by_size(const Mx4GemmArgs& g, hipStream_t stream) {
-  if (g.m <= 16) {
-    if (g.n >= kCols64) return rows<DT, 1, 4, 4, 4>(g, stream);
-    if (g.n >= kCols32) return rows<DT, 1, 2, 4, 4>(g, stream);
-    return rows<DT, 1, 1, 8, 4>(g, stream);
+  switch (mx4_kernel_of(g.m, g.n, g.k)) {
+    case Mx4Kernel::kRows16x64: return rows<DT, 1, 4, 4, 4>(g, stream);
+    case Mx4Kernel::kRows16x32: return rows<DT, 1, 2, 4, 4>(g, stream);
+    case Mx4Kernel::kRows16x16: return rows<DT, 1, 1, 8, 4>(g, stream);
+    case Mx4Kernel::kRows32x32: return rows<DT, 2, 2, 2, 4>(g, stream);
+    case Mx4Kernel::kRows32x16: return rows<DT, 2, 1, 4, 4>(g, stream);
+    case Mx4Kernel::kManyRows32: return rows<DT, 2, 2, 4, 4>(g, stream);
+    case Mx4Kernel::kManyRows64: return rows<DT, 4, 4, 4, 2>(g, stream);
+    case Mx4Kernel::kTile128: return tiles<DT, 128, 128, 64, 64>(g, stream);
+    case Mx4Kernel::kTile128x256: return tiles<DT, 128, 256, 64, 64>(g, stream);
+    default: return tiles<DT, 256, 256, 128, 64>(g, stream);
   }
-  if (g.m <= 32) return g.n >= kCols32 ? rows<DT, 2, 2, 2, 4>(g, stream) : rows<DT, 2, 1, 4, 4>(g, stream);
-  auto count = [&](int bm, int bn) { return static_cast<double>((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn); };
-  const double slices = (g.k + 127) / 128, waves22 = std::max(count(32, 32) / 256, 1.0), waves44 = std::max(count(64, 64) / 256, 1.0);
-  const double rows22 = 3.0 + 0.075 * slices * waves22, rows44 = 3.5 + 0.24 * slices * waves44;
-  auto rounds = [&](int bm, int bn) { return std::ceil(count(bm, bn) / 256); };
-  const double tile1 = 3.4 + (2.4 + slices * 0.24) * rounds(128, 128), tile2 = 3.5 + (3.8 + slices * 0.49) * rounds(128, 256);
-  const double tile4 = 4.0 + (5.0 + slices * 0.80) * rounds(256, 256);
-  const double best = std::min({rows22, rows44, tile1, tile2, tile4});
-  if (best == tile4) return tiles<DT, 256, 256, 128, 64>(g, stream);
-  if (best == tile2) return tiles<DT, 128, 256, 64, 64>(g, stream);
-  if (best == tile1) return tiles<DT, 128, 128, 64, 64>(g, stream);
-  return best == rows44 ? rows<DT, 4, 4, 4, 2>(g, stream) : rows<DT, 2, 2, 4, 4>(g, stream);
 }
 
 }  // namespace
