@@ -481,8 +481,8 @@ constexpr int kLdsHalves = 4 * kGroup * DP;
 // (5.0 TB/s; a plain copy reaches 4.9 and a read-only stream 6.1); two
 // sequences of about 115000, 64 heads, FP8, 88 us (5.4 TB/s); one of 771
 // positions 7 us: the launch, and a chain of table entry, keys, products and
-// join.  The 64 sequences with a window of 1024 29.6 us, and with 4 sinks 29.8; two of
-// about 115000, window 32768, 33.5 and with 128 sinks 35.
+// join.  The 64 sequences with a window of 1024 27.5 us, and with 4 sinks 27.6; two of
+// about 115000, window 32768, 31.9 and with 128 sinks 33.
 template <int DT, bool FP8, int DP, bool SINKS>
 __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
   // the waves' outputs, [wave][column][element], elements exchanged in fours by
@@ -761,7 +761,7 @@ __device__ __forceinline__ void cols_body(const Params& p, unsigned block) {
 // leaves one wave per SIMD, 319 us; the next step's conversion within the
 // first product 471 (registers spill); conversion before the products 175;
 // a raised wave priority during the products 176; rescaling at every new
-// maximum 176.  With a window of 1024 93 us, and with 4 sinks 97.
+// maximum 176.  With a window of 1024 91.3 us, and with 4 sinks 92.4; FP8 88.8 and 89.8.
 template <int DT, bool FP8, int DP, bool SINKS>
 __device__ __forceinline__ void tile_body(const Params& p, unsigned block) {
   extern __shared__ __align__(16) _Float16 lds_all[];

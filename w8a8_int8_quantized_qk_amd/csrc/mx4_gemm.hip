@@ -177,7 +177,8 @@ __global__ __launch_bounds__(64 * W) void mx4_linear_rows_kernel(Mx4GemmArgs g, 
   v4f acc[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) acc[i] = v4f{0, 0, 0, 0};
-  // as in Mx4Tile; the values' rows are two or four times 256 bytes
+  // Chunks of a row are exchanged by its number, as in the other kernel; a row of the
+  // weight has 64 or 128 bytes here, one of the values 512.
   auto key_w = [](int row) { return kChunksW == 8 ? row & 7 : (row >> 1) & 3; };
   auto key_x = [](int row) { return row >> 2 | (row & 3) << 2; };
   // piece p: B slices; a wave's stretches of four slices are those of the other kernel
@@ -297,10 +298,13 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 // the ring is free as soon as every wave has read its fragments, and is then asked for the
 // next pair.
 //
-// Figures: 8192 x 28672 x 8192 837 us (4.6 PFLOP/s; the products alone, from LDS that
-// nothing is brought to, 718; the stores, while which nothing is multiplied, 84 of
-// both), 4096 x 4096 x 14336 97, 2048 x 4096 x 4096 21.7 to 23.1 (of which stores 4),
-// 512 x 4096 x 4096 13.4.
+// Figures: 8192 x 28672 x 8192 840 to 865 us (4.4 to 4.6 PFLOP/s; the products alone, from
+// LDS that nothing is brought to, 718; the stores, while which nothing is multiplied, 84
+// of both), 4096 x 4096 x 14336 97 to 101, 2048 x 4096 x 4096 21.7 to 23.1 (of which stores
+// 4), 512 x 4096 x 4096 13.2.  Columns that are no multiple of 16 bytes of results are
+// stored one by one and through the caches: 2048 x 4097 x 4096 42, 8192 x 28671 x 8192 1120.
+// With 16-bit results 16 bytes of the arguments lie in scratch memory per lane, written
+// ahead of the loop and read behind it.
 //
 // A lane's quarter of a wave is its block of a slice, and the byte of its scale
 // register that the instruction picks is the slice: the scales of four slices, 16
@@ -479,9 +483,10 @@ struct Mx4Tile {
     // Slice kt, X its number modulo 16 (a constant wherever it is used).  At the
     // barrier in an odd slice the next pair has landed, for every wave, and every wave
     // has read the last of this one, whose part of the ring is then asked for the next
-    // pair but kRing - 1.  The last scales of a batch are read in slice 11, so the next batch
-    // may come over it from slice 12's barrier on; in slice 14 it is there, each thread
-    // transposes what its own wave brought, and it is read behind slice 15's barrier.
+    // pair but kRing - 1.  The last scales of a batch are read in slice 11 or, half of them
+    // where FM is 8, in slice 12 ahead of its barrier, so the next batch may come over it
+    // from that barrier on; in slice 14 it is there, each thread transposes what its own
+    // wave brought, and it is read behind slice 15's barrier.
     // (Loads arrive in order: the waits count those that may still be under way, in
     // slice 13 the scales among them.)
     auto meet = [&](int X) {

@@ -9,7 +9,8 @@
 // The angle of a far position has many whole turns, so it is formed and its
 // turns are taken off in binary64: t = position * (freqs[i] / 2 pi), t - rint(4 t) / 4
 // is exact and at most an eighth of a turn, and loses nothing when it is rounded to
-// binary32 (t is off by 2^-52 of itself: 2^-25 of a turn at position 2^29).
+// binary32 (t is off by less than 2^-51 of itself, three roundings: 2^-25 of a turn at
+// position 2^29).
 // Sine and cosine of at most pi / 4 are their Taylor sums in binary32, up to
 // x^9 and x^10 (the next terms are below 2^-29 and 2^-33).
 #include <algorithm>
@@ -155,11 +156,13 @@ __device__ __forceinline__ T head_sum(T v) {
 // allows it (32 bytes per lane in two halves took up to twice as long); where r is no
 // multiple of 8 (4 for binary32 side by side) P is 1, and a lane takes U pairs, L apart.
 //
-// Bound by memory: 7690 rows of 32 + 8 heads of 128, bf16, 27 us (5.8 TB/s; 37 with
-// plain stores, 28.6 with two groups in flight per wave); r = 64 side by side 26;
-// one row 3.0 us, 64 rows 3.3.  (Eight waves a SIMD are asked for where that costs no
-// scratch: 27.4 us for 26.3 at r = 64 side by side, 34.6 for 31.9 at 4000 rows of 40 heads of 80 where P is 1; with P = 8
-// values went to scratch, 9.7 for 7.9 us at 4000 rows of 40 heads of 64.)
+// Bound by memory: 7690 rows of 32 + 8 heads of 128, bf16, the outputs of three calls in
+// turn, 26.6 us (5.9 TB/s; 34.6 with plain stores; 28.6 with two groups in flight per wave,
+// for 27); r = 64 side by side 28.9 (36.0); in place 27 to 30 either way; with P = 1, dim 80
+// and r = 20 56.  One row 3.3 us, 64 rows 3.5.  (Eight waves a SIMD are asked for where that costs no
+// scratch: without it 27.4 us for 26.3 at r = 64 side by side, one output, and 34.6 for 31.9
+// at 4000 rows of 40 heads of 80 where P is 1; with P = 8 values went to scratch, 9.7 us for
+// 7.9 at 4000 rows of 40 heads of 64.)
 template <int DT, int P, int L, int U, bool SIDE, bool PAST>
 __global__ __launch_bounds__(kBlock, SIDE || P == 1 ? 8 : 1) void norm_rope_kernel(NormRopeArgs a, int parts, int groups) {
   constexpr int B = Elem<DT>::kBytes;
